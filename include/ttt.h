@@ -1,7 +1,8 @@
 /*
  * ttt.h -- C ABI of libttt.so, the MI355X (gfx950) TTT (test-time training)
  * sequence layer: the forward of TTT-Linear and TTT-MLP and the backward of
- * TTT-Linear, mini-batch dual form.
+ * TTT-Linear, mini-batch dual form; linear attention with a decay per head; and
+ * rotary positions.
  *
  * Pages: [TTT] = news article "大模型最强架构TTT问世！斯坦福UCSD等5年磨一剑，
  * 一夜推翻Transformer" (aharts.cn / itmax.cn).
@@ -59,9 +60,10 @@ typedef enum {
   TTT_ERR_DTYPE = 3,       /* dtype code is not a ttt_dtype                      */
   TTT_ERR_UNSUPPORTED = 4, /* valid request, but no kernel built for it          */
   TTT_ERR_ALIAS = 5,       /* an output overlaps an input in a forbidden way     */
-  TTT_ERR_ALIGN = 6,       /* a pointer is not aligned as required               */
+  TTT_ERR_ALIGN = 6,       /* a pointer or stride is not aligned as required     */
   TTT_ERR_HIP = 7,         /* the HIP runtime rejected the launch                */
-  TTT_ERR_STRIDE = 8,      /* negative eta stride, or w0 stride not 0 / H*d*d    */
+  TTT_ERR_STRIDE = 8,      /* negative stride, w0 stride not 0 / H*d*d, output   */
+                           /* strides that overlap                               */
   TTT_ERR_FLAGS = 9,       /* unknown bit set in flags                           */
   TTT_ERR_POS = 10,        /* negative decode position                           */
   TTT_ERR_WORKSPACE = 11,  /* workspace missing, misaligned or too small         */
@@ -544,6 +546,153 @@ ttt_status ttt_mlp_ln_decode_validate(const ttt_mlp_desc* desc, const void* Q, c
                                       const float* eta, const float* gamma, const float* beta, float eps,
                                       const void* Z, const float* W1, const float* W2, const float* W1b,
                                       const float* W2b, int64_t pos);
+
+/*
+ * Linear attention with a decay per head ([TTT] 03 §8: TTT with a linear f and
+ * batch gradient descent is linear attention; here the state also forgets).
+ * Per (sequence bi, head h), lambda = exp(log_decay[h]), token t:
+ *     W_t = lambda W_{t-1} + v_t k_t^T,     z_t = scale W_t q_t
+ * with the state laid out as TTT-Linear's (z = W q, row i = output i).
+ *
+ * Conventions of the linear-attention and rotary entry points, where they
+ * differ from those above
+ *  - q, z (and dq, dz) have H heads, k and v (dk, dv) have Hkv, H a multiple of
+ *    Hkv: query head h reads key / value head h / (H / Hkv).
+ *  - Tensors are strided: element (bi, h, t, i) is at bi*b + h*h' + t*t' + i with
+ *    the ttt_strides {b, h', t'} in elements.  Strides must be >= 0 and, for
+ *    outputs, keep elements apart (TTT_ERR_STRIDE); strides of dimensions of size
+ *    1 are not looked at.  Inputs may repeat (stride 0).  For ttt_linear_attn_fwd
+ *    and _bwd every base address and stride is a multiple of 16 bytes
+ *    (TTT_ERR_ALIGN), for the others of the element's size.
+ *  - Outputs share no element with an input or another output (TTT_ERR_ALIAS);
+ *    slices of the same rows ([B, T, 3, H, d]) are apart.
+ *  - lens: [B] int32 on the device, the tokens of each sequence (taken into
+ *    [0, T]), or NULL for T each.  Rows behind the last token are not read; their
+ *    outputs and gradients are written as zero; the state is that after the last
+ *    token.
+ *  - log_decay: [H] fp32 on the device; 0 keeps everything, -inf nothing.
+ *  - 0 <= T <= 2^30.
+ *  - Finite values: a NaN or infinity reaches only tokens at or after its own, but
+ *    for V (and dZ in the backward) also the others of its 16-token block.
+ */
+typedef struct {
+  int64_t b, h, t; /* elements between sequences, heads, tokens */
+} ttt_strides;
+
+typedef struct {
+  int32_t B, H, Hkv, T, d;
+  int32_t in_dtype;         /* ttt_dtype of Q, K, V                                   */
+  int32_t out_dtype;        /* ttt_dtype of Z; in the backward of dZ, dQ, dK, dV      */
+  uint32_t flags;           /* must be 0                                              */
+  float scale;              /* finite                                                 */
+  int32_t reserved;         /* must be 0                                              */
+  int64_t w0_batch_stride;  /* 0 (shared, [H,d,d]) or H*d*d (per sequence, [B,H,d,d]) */
+  ttt_strides q, k, v, z;   /* z: Z, or dZ                                            */
+  ttt_strides dq, dk, dv;   /* the backward's outputs (the others do not look)        */
+} ttt_linear_attn_desc;
+
+/*
+ * Linear attention, forward (prompts): Z for all tokens and the last state.
+ *   W0 : fp32, see w0_batch_stride, or NULL for a zero state
+ *   W_final : [B,H,d,d] fp32; may be exactly W0 when W0 is per sequence
+ *   workspace : ttt_linear_attn_workspace_bytes(desc, 0) bytes, 16-byte aligned
+ *       (TTT_ERR_WORKSPACE), overlapping nothing else; unspecified on return.
+ * Chunks of 32 tokens as matrix products; where there are few (sequence, head)
+ * chains a sequence is walked in segments at the same time, whose start states a
+ * first launch computes.  d in {16, 32, 64, 128}; bf16 inputs on the bf16 matrix
+ * cores (fp32 operands split into bf16 parts), fp32 inputs on the fp32 ones.
+ */
+ttt_status ttt_linear_attn_fwd(const ttt_linear_attn_desc* desc, const void* Q, const void* K, const void* V,
+                               const float* log_decay, const float* W0, const int32_t* lens, void* Z, float* W_final,
+                               void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Runs every host-side check of ttt_linear_attn_fwd and launches nothing. */
+ttt_status ttt_linear_attn_fwd_validate(const ttt_linear_attn_desc* desc, const void* Q, const void* K, const void* V,
+                                        const float* log_decay, const float* W0, const int32_t* lens, const void* Z,
+                                        const float* W_final, const void* workspace, int64_t workspace_bytes);
+
+/*
+ * Linear attention, backward: with L any scalar whose gradients with respect to
+ * Z and W_final are dZ and dW_final (NULL for zero), its gradients with respect to
+ * every input of ttt_linear_attn_fwd, from the inputs alone:
+ *   dQ [B,H,T,d]; dK, dV [B,Hkv,T,d] (summed over the query heads that share them)
+ *   dlog_decay : [B,H] fp32 per sequence (sum over B for the [H] parameter)
+ *   dW0        : [B,H,d,d] fp32 per sequence (sum over B for a shared W0)
+ * workspace as for the forward, ttt_linear_attn_workspace_bytes(desc, 1) bytes.
+ * Outputs overlap no input, no other output and not the workspace (TTT_ERR_ALIAS).
+ * The same inputs give the same bits: no atomics.
+ */
+ttt_status ttt_linear_attn_bwd(const ttt_linear_attn_desc* desc, const void* Q, const void* K, const void* V,
+                               const float* log_decay, const float* W0, const int32_t* lens, const void* dZ,
+                               const float* dW_final, void* dQ, void* dK, void* dV, float* dlog_decay, float* dW0,
+                               void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Runs every host-side check of ttt_linear_attn_bwd and launches nothing. */
+ttt_status ttt_linear_attn_bwd_validate(const ttt_linear_attn_desc* desc, const void* Q, const void* K, const void* V,
+                                        const float* log_decay, const float* W0, const int32_t* lens, const void* dZ,
+                                        const float* dW_final, const void* dQ, const void* dK, const void* dV,
+                                        const float* dlog_decay, const float* dW0, const void* workspace,
+                                        int64_t workspace_bytes);
+
+/* Workspace bytes of the forward (backward = 0) or the backward (1); 0 where none is needed, -1 for an invalid desc. */
+int64_t ttt_linear_attn_workspace_bytes(const ttt_linear_attn_desc* desc, int32_t backward);
+
+/* Rotary positions of a row's first rot elements (ttt_rotary, ttt_linear_attn_decode). */
+typedef struct {
+  const int64_t* pos;    /* device: position of (bi, t) at pos[bi*pos_stride_b + t*pos_stride_t]; NULL: 0 */
+  int64_t pos_stride_b;  /* elements, >= 0 (TTT_ERR_STRIDE)                                               */
+  int64_t pos_stride_t;  /* elements, >= 0; 0: the position is that of token 0, token t is t further      */
+  int64_t pos_offset;    /* added to every position                                                       */
+  const double* freqs;   /* device, [rot / 2]: radians per position of each pair                          */
+  int32_t rot;           /* even, 0 <= rot <= d (TTT_ERR_SHAPE)                                           */
+  int32_t interleaved;   /* 1: pair i is elements (2i, 2i+1); 0: (i, i + rot/2)                           */
+  float scale;           /* factor on the turned elements, finite                                         */
+  int32_t reserved;      /* must be 0                                                                     */
+} ttt_rope;
+
+/*
+ * Linear attention, decode: continues B*H sequences by desc->T new tokens (often
+ * 1), the state W [B,H,d,d] fp32 read and written in place; with lens, sequences
+ * of length 0 keep their state.  rope (or NULL): q and k are turned by it on the
+ * way, in fp32 and not rounded in between.  w0_batch_stride must be 0.  Decoding T
+ * tokens from W = W0 gives the Z and W_final of ttt_linear_attn_fwd (to rounding).
+ * One launch.
+ */
+ttt_status ttt_linear_attn_decode(const ttt_linear_attn_desc* desc, const void* Q, const void* K, const void* V,
+                                  const float* log_decay, const int32_t* lens, const ttt_rope* rope, void* Z, float* W,
+                                  void* stream);
+
+/* Runs every host-side check of ttt_linear_attn_decode and launches nothing. */
+ttt_status ttt_linear_attn_decode_validate(const ttt_linear_attn_desc* desc, const void* Q, const void* K,
+                                           const void* V, const float* log_decay, const int32_t* lens,
+                                           const ttt_rope* rope, const void* Z, const float* W);
+
+/* q and k of ttt_rotary. */
+typedef struct {
+  int32_t B, H, Hkv, T, d;  /* Hkv = 0: no k                         */
+  int32_t dtype;            /* ttt_dtype of all four tensors         */
+  uint32_t flags;           /* 0, or TTT_FLAG_INVERSE                */
+  int32_t reserved;         /* must be 0                             */
+  ttt_strides q, k, q_out, k_out;
+} ttt_rotary_desc;
+
+#define TTT_FLAG_INVERSE 1u /* ttt_rotary: turn back by the same angles (with the same scale: the gradient) */
+
+/*
+ * Rotary positions for the q and k views of a sequence layer: each pair (x1, x2)
+ * of a row's first rot elements becomes
+ *     scale (x1 cos a - x2 sin a, x1 sin a + x2 cos a),   a = position * freqs[i]
+ * (angles in 64 bits, values in fp32, one rounding); the other elements are passed
+ * on.  Any d >= 1.  q_out may be exactly q and k_out exactly k (same address and
+ * strides); outputs overlap nothing else.  With TTT_FLAG_INVERSE the angle's sign
+ * is turned: applied to the gradients of the outputs it gives those of the inputs.
+ */
+ttt_status ttt_rotary(const ttt_rotary_desc* desc, const ttt_rope* rope, const void* q, const void* k, void* q_out,
+                      void* k_out, void* stream);
+
+/* Runs every host-side check of ttt_rotary and launches nothing. */
+ttt_status ttt_rotary_validate(const ttt_rotary_desc* desc, const ttt_rope* rope, const void* q, const void* k,
+                               const void* q_out, const void* k_out);
 
 /* Human-readable text of a status code (never NULL). */
 const char* ttt_status_str(int status);

@@ -1,4 +1,5 @@
-"""MI355X (gfx950) TTT sequence layer (forward, and the TTT-Linear backward) -- Python binding.
+"""MI355X (gfx950) TTT sequence layer (forward, and the TTT-Linear backward), linear
+attention with a decay per head, and rotary positions -- Python binding.
 
 Thin ctypes layer over libttt.so (C ABI in include/ttt.h).  It only checks and
 marshals arguments: torch supplies device memory and the current HIP stream,
@@ -10,6 +11,9 @@ no CPU or PyTorch fallback: if libttt.so is missing, importing the ops raises.
     z, w1_final, w2_final = ttt.mlp_fwd(q, k, v, w1, w2, eta, b=16)
     z, w_final, e = ttt.linear_fwd_save(q, k, v, w0, eta, b=16)          # training
     dq, dk, dv, deta, dw0 = ttt.linear_bwd(q, k, eta, w_final, e, dz, b=16)
+    q, k = ttt.rotary(q, k, pos=0, freqs=freqs)
+    z, w_final = ttt.linear_attn_fwd(q, k, v, log_decay)
+    z = ttt.linear_attn_decode(q1, k1, v1, log_decay, w_final, rope=(pos, freqs))
 
 Pages: [TTT] = news article "大模型最强架构TTT问世！斯坦福UCSD等5年磨一剑，一夜推翻Transformer"
 (aharts.cn / itmax.cn), part 03 §1-§9 (the TTT layer, mini-batch GD, the dual
@@ -17,7 +21,9 @@ form, TTT-Linear and TTT-MLP).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 from typing import Optional, Tuple
 
@@ -28,6 +34,7 @@ TTT_OK = 0
 TTT_F32, TTT_BF16 = 0, 1
 TTT_FLAG_GENERIC = 1
 TTT_FLAG_PRIMAL = 2
+TTT_FLAG_INVERSE = 1  # ttt_rotary
 TTT_FLAG_ROWS = {1: 4, 2: 8, 4: 16}  # row blocks per (sequence, head) -> TTT_FLAG_ROWS1/2/4
 
 
@@ -59,6 +66,9 @@ EXPORTS = (
     "ttt_mlp_decode", "ttt_mlp_decode_validate", "ttt_mlp_ln_decode", "ttt_mlp_ln_decode_validate",
     "ttt_mlp_ln_kernel_name", "ttt_mlp_bwd", "ttt_mlp_bwd_validate", "ttt_mlp_bwd_workspace_bytes",
     "ttt_mlp_bwd_kernel_name", "ttt_mlp_ln_bwd", "ttt_mlp_ln_bwd_validate", "ttt_mlp_ln_bwd_kernel_name",
+    "ttt_linear_attn_fwd", "ttt_linear_attn_fwd_validate", "ttt_linear_attn_bwd", "ttt_linear_attn_bwd_validate",
+    "ttt_linear_attn_workspace_bytes", "ttt_linear_attn_decode", "ttt_linear_attn_decode_validate",
+    "ttt_rotary", "ttt_rotary_validate",
     "ttt_status_str", "ttt_abi_version",
 )
 
@@ -81,6 +91,36 @@ class MlpDesc(ctypes.Structure):
         ("flags", ctypes.c_uint32), ("reserved", ctypes.c_int32),
         ("w_batch_stride", ctypes.c_int64),
         ("eta_stride_b", ctypes.c_int64), ("eta_stride_h", ctypes.c_int64), ("eta_stride_t", ctypes.c_int64),
+    ]
+
+
+class Strides(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("t", ctypes.c_int64)]
+
+
+class LinearAttnDesc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("H", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("T", ctypes.c_int32),
+        ("d", ctypes.c_int32), ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32),
+        ("scale", ctypes.c_float), ("reserved", ctypes.c_int32), ("w0_batch_stride", ctypes.c_int64),
+        ("q", Strides), ("k", Strides), ("v", Strides), ("z", Strides),
+        ("dq", Strides), ("dk", Strides), ("dv", Strides),
+    ]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [
+        ("pos", ctypes.c_void_p), ("pos_stride_b", ctypes.c_int64), ("pos_stride_t", ctypes.c_int64),
+        ("pos_offset", ctypes.c_int64), ("freqs", ctypes.c_void_p), ("rot", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+    ]
+
+
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("H", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("T", ctypes.c_int32),
+        ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32), ("reserved", ctypes.c_int32),
+        ("q", Strides), ("k", Strides), ("q_out", Strides), ("k_out", Strides),
     ]
 
 
@@ -201,6 +241,25 @@ def lib() -> ctypes.CDLL:
     L.ttt_mlp_ln_decode_validate.argtypes = [ctypes.POINTER(MlpDesc), vp, vp, vp, fp, fp, fp, ctypes.c_float, vp,
                                              fp, fp, fp, fp, ctypes.c_int64]
     L.ttt_mlp_ln_decode_validate.restype = ctypes.c_int
+    ad, i64 = ctypes.POINTER(LinearAttnDesc), ctypes.c_int64
+    L.ttt_linear_attn_fwd.argtypes = [ad, vp, vp, vp, fp, fp, vp, vp, fp, vp, i64, vp]
+    L.ttt_linear_attn_fwd.restype = ctypes.c_int
+    L.ttt_linear_attn_fwd_validate.argtypes = [ad, vp, vp, vp, fp, fp, vp, vp, fp, vp, i64]
+    L.ttt_linear_attn_fwd_validate.restype = ctypes.c_int
+    L.ttt_linear_attn_bwd.argtypes = [ad, vp, vp, vp, fp, fp, vp, vp, fp, vp, vp, vp, fp, fp, vp, i64, vp]
+    L.ttt_linear_attn_bwd.restype = ctypes.c_int
+    L.ttt_linear_attn_bwd_validate.argtypes = [ad, vp, vp, vp, fp, fp, vp, vp, fp, vp, vp, vp, fp, fp, vp, i64]
+    L.ttt_linear_attn_bwd_validate.restype = ctypes.c_int
+    L.ttt_linear_attn_workspace_bytes.argtypes = [ad, ctypes.c_int32]
+    L.ttt_linear_attn_workspace_bytes.restype = i64
+    L.ttt_linear_attn_decode.argtypes = [ad, vp, vp, vp, fp, vp, ctypes.POINTER(Rope), vp, fp, vp]
+    L.ttt_linear_attn_decode.restype = ctypes.c_int
+    L.ttt_linear_attn_decode_validate.argtypes = [ad, vp, vp, vp, fp, vp, ctypes.POINTER(Rope), vp, fp]
+    L.ttt_linear_attn_decode_validate.restype = ctypes.c_int
+    L.ttt_rotary.argtypes = [ctypes.POINTER(RotaryDesc), ctypes.POINTER(Rope), vp, vp, vp, vp, vp]
+    L.ttt_rotary.restype = ctypes.c_int
+    L.ttt_rotary_validate.argtypes = [ctypes.POINTER(RotaryDesc), ctypes.POINTER(Rope), vp, vp, vp, vp]
+    L.ttt_rotary_validate.restype = ctypes.c_int
     L.ttt_status_str.argtypes = [ctypes.c_int]
     L.ttt_status_str.restype = ctypes.c_char_p
     L.ttt_abi_version.argtypes = []
@@ -907,3 +966,316 @@ def mlp_decode(q, k, v, eta, w1, w2, w1b, w2b, pos: int, b: int, out_dtype=None,
                               _ptr(w2), _ptr(w1b), _ptr(w2b), int(pos), _stream_handle(stream))
     _done(st, "ttt_mlp_decode")
     return z
+
+
+# --------------------------------- linear attention with a decay per head --
+
+def _on(x, stream):
+    """Context in which a call's tensors are made and its kernels launched: the given
+    stream, else the current stream of the device that ``x`` is on."""
+    torch = _torch()
+    if stream is not None:
+        if stream.device != x.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {x.device}")
+        return torch.cuda.stream(stream)
+    if x.is_cuda and x.device.index != torch.cuda.current_device():
+        return torch.cuda.device(x.device)
+    return contextlib.nullcontext()
+
+
+def _check_same_dev(x, *ts):
+    if not x.is_cuda:
+        raise ValueError("every tensor must be on the GPU")
+    for t in ts:
+        if t is not None and t.device != x.device:
+            raise ValueError(f"every tensor must be on one GPU ({t.device} and {x.device})")
+
+
+def _strides(t) -> Strides:
+    """(b, h, t) element strides of a [B, H, T, d] tensor whose rows are contiguous."""
+    b, h, s, e = t.stride()
+    if e != 1 and t.shape[3] > 1:
+        raise ValueError("the last dimension must be contiguous")
+    return Strides(b, h, s)
+
+
+def _like(x, dtype):
+    """An empty tensor of x's shape and, where x is dense, its layout."""
+    return _torch().empty_like(x, dtype=dtype)
+
+
+def _attn_args(q, k, v, log_decay, w0, lens):
+    """Checks what every linear-attention call takes; returns (B, H, Hkv, T, d, w0 batch stride)."""
+    torch = _torch()
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q, k, v must be [B, H, T, d]")
+    B, H, T, d = q.shape
+    Hkv = k.shape[1]
+    if tuple(k.shape) != (B, Hkv, T, d) or v.shape != k.shape:
+        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}: expected [B, H, T, d] and "
+                         "twice [B, Hkv, T, d]")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k, v must have the same dtype")
+    if H and (Hkv == 0 or H % Hkv):
+        raise ValueError(f"{H} query heads do not share {Hkv} key / value heads evenly")
+    if tuple(log_decay.shape) != (H,):
+        raise ValueError(f"log_decay shape {tuple(log_decay.shape)}: expected [H]")
+    if log_decay.dtype != torch.float32:
+        raise TypeError("log_decay must be float32")
+    if lens is not None:
+        if tuple(lens.shape) != (B,):
+            raise ValueError(f"lens shape {tuple(lens.shape)}: expected [B]")
+        if lens.dtype != torch.int32:
+            raise TypeError("lens must be int32")
+    wstride = 0
+    if w0 is not None:
+        if w0.dtype != torch.float32:
+            raise TypeError("w0 must be float32")
+        wstride = _w0_stride(w0, B, H, d)
+    for x in (log_decay, lens, w0):
+        if x is not None and not x.is_contiguous():
+            raise ValueError("log_decay, lens and w0 must be contiguous")
+    _check_same_dev(q, k, v, log_decay, w0, lens)
+    return B, H, Hkv, T, d, wstride
+
+
+def _want(x, shape, dtype, what):
+    if tuple(x.shape) != tuple(shape) or x.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype} {tuple(shape)}, not {x.dtype} {tuple(x.shape)}")
+
+
+def _attn_workspace(desc, backward, workspace, like):
+    need = int(lib().ttt_linear_attn_workspace_bytes(ctypes.byref(desc), int(backward)))
+    if workspace is None:
+        return (_torch().empty(need, dtype=_torch().uint8, device=like.device), need) if need > 0 else (None, 0)
+    if not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def linear_attn_workspace_bytes(q, k, out_dtype=None, backward: bool = False) -> int:
+    """Bytes of workspace that a call on inputs like q [B, H, T, d] and k [B, Hkv, T, d] takes."""
+    B, H, T, d = q.shape
+    desc = LinearAttnDesc(B, H, k.shape[1], T, d, _dtype_code(q.dtype), _dtype_code(out_dtype or q.dtype))
+    return int(lib().ttt_linear_attn_workspace_bytes(ctypes.byref(desc), int(backward)))
+
+
+def linear_attn_fwd(q, k, v, log_decay, w0=None, scale: float = 1.0, lens=None, out_dtype=None, w_final=None, z=None,
+                    workspace=None, stream=None):
+    """Linear attention with a decay per head, forward: W_t = exp(log_decay) W_{t-1} + v_t k_t^T, z_t = scale W_t q_t.
+
+    q         : [B, H, T, d] bfloat16 or float32; k, v : [B, Hkv, T, d] of the same dtype, H a multiple of Hkv
+                (query head h reads head h // (H // Hkv)).  d in {16, 32, 64, 128}.  Rows contiguous, 16-byte aligned;
+                any strides between them (transposed or sliced projections need no copy)
+    log_decay : [H] float32, the logarithm of each head's decay (0 keeps everything)
+    w0        : initial state [H, d, d] or [B, H, d, d] float32 (z = W q), or None (zero)
+    lens      : [B] int32, the tokens of each sequence, or None (T each).  Rows behind them are not read and give
+                zero rows of Z; W_final is the state after the last token
+    returns (Z [B, H, T, d] of out_dtype (default float32), W_final [B, H, d, d] float32).
+    ``w_final`` may be ``w0`` itself when w0 is [B, H, d, d].  ``workspace``: uint8 tensor of
+    :func:`linear_attn_workspace_bytes` (allocated when omitted); calls that may overlap need one each.
+    """
+    torch = _torch()
+    B, H, Hkv, T, d, wstride = _attn_args(q, k, v, log_decay, w0, lens)
+    with _on(q, stream):
+        if z is None:
+            z = _like(q, torch.float32 if out_dtype is None else out_dtype)
+        elif tuple(z.shape) != (B, H, T, d):
+            raise ValueError(f"z shape {tuple(z.shape)}: expected {(B, H, T, d)}")
+        if w_final is None:
+            w_final = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
+        _want(w_final, (B, H, d, d), torch.float32, "w_final")
+        if not w_final.is_contiguous():
+            raise ValueError("w_final must be contiguous")
+        _check_same_dev(q, z, w_final, workspace)
+        desc = LinearAttnDesc(B, H, Hkv, T, d, _dtype_code(q.dtype), _dtype_code(z.dtype), 0, scale, 0, wstride,
+                              _strides(q), _strides(k), _strides(v), _strides(z))
+        workspace, wbytes = _attn_workspace(desc, False, workspace, q)
+        st = lib().ttt_linear_attn_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(w0),
+                                       _ptr(lens), _ptr(z), _ptr(w_final), _ptr(workspace), wbytes,
+                                       _stream_handle(stream))
+        _done(st, "ttt_linear_attn_fwd")
+    return z, w_final
+
+
+def linear_attn_bwd(q, k, v, log_decay, dz, w0=None, dw_final=None, scale: float = 1.0, lens=None, workspace=None,
+                    out=None, stream=None):
+    """Backward of :func:`linear_attn_fwd`, from its inputs alone.
+
+    q, k, v, log_decay, w0, scale, lens : as given to the forward
+    dz        : [B, H, T, d] gradient of the loss with respect to Z (its dtype is that of dq, dk, dv)
+    dw_final  : [B, H, d, d] float32 gradient with respect to W_final, or None (zero)
+    workspace : uint8 tensor of linear_attn_workspace_bytes(..., out_dtype=dz.dtype, backward=True), or None
+    out       : optional (dq, dk, dv, dlog_decay, dw0) preallocated outputs
+    returns (dq [B, H, T, d], dk, dv [B, Hkv, T, d] (summed over the query heads that share them),
+    dlog_decay [B, H] float32 and dw0 [B, H, d, d] float32, both per sequence: sum them over B for shared parameters).
+    """
+    torch = _torch()
+    B, H, Hkv, T, d, wstride = _attn_args(q, k, v, log_decay, w0, lens)
+    if tuple(dz.shape) != (B, H, T, d):
+        raise ValueError(f"dz shape {tuple(dz.shape)}: expected {(B, H, T, d)}")
+    if dw_final is not None:
+        _want(dw_final, (B, H, d, d), torch.float32, "dw_final")
+        if not dw_final.is_contiguous():
+            raise ValueError("dw_final must be contiguous")
+    with _on(q, stream):
+        if out is None:
+            out = (_like(q, dz.dtype), _like(k, dz.dtype), _like(v, dz.dtype),
+                   torch.empty((B, H), dtype=torch.float32, device=q.device),
+                   torch.empty((B, H, d, d), dtype=torch.float32, device=q.device))
+        dq, dk, dv, dg, dw0 = out
+        for x, like, what in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
+            _want(x, like.shape, dz.dtype, what)
+        _want(dg, (B, H), torch.float32, "dlog_decay")
+        _want(dw0, (B, H, d, d), torch.float32, "dw0")
+        if not dg.is_contiguous() or not dw0.is_contiguous():
+            raise ValueError("dlog_decay and dw0 must be contiguous")
+        _check_same_dev(q, dz, dw_final, workspace, *out)
+        desc = LinearAttnDesc(B, H, Hkv, T, d, _dtype_code(q.dtype), _dtype_code(dz.dtype), 0, scale, 0, wstride,
+                              _strides(q), _strides(k), _strides(v), _strides(dz), _strides(dq), _strides(dk),
+                              _strides(dv))
+        workspace, wbytes = _attn_workspace(desc, True, workspace, q)
+        st = lib().ttt_linear_attn_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(w0),
+                                       _ptr(lens), _ptr(dz), _ptr(dw_final), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg),
+                                       _ptr(dw0), _ptr(workspace), wbytes, _stream_handle(stream))
+        _done(st, "ttt_linear_attn_bwd")
+    return dq, dk, dv, dg, dw0
+
+
+def linear_attn_decode(q, k, v, log_decay, w, scale: float = 1.0, lens=None, rope=None, out_dtype=None, z=None,
+                       stream=None):
+    """Continue B*H sequences of :func:`linear_attn_fwd` by T new tokens (often 1), the state carried in place.
+
+    q, k, v : [B, H or Hkv, T, d] as for the forward (any alignment);  w : [B, H, d, d] float32, updated in place
+    lens    : [B] int32, the new tokens of each sequence (0: its state stays), or None (T each)
+    rope    : (pos, freqs[, layout[, scale]]) to turn q and k as :func:`rotary` would, in the same launch, or None
+    returns Z [B, H, T, d].
+    """
+    torch = _torch()
+    B, H, Hkv, T, d, _ = _attn_args(q, k, v, log_decay, None, lens)
+    _want(w, (B, H, d, d), torch.float32, "w")
+    if not w.is_contiguous():
+        raise ValueError("w must be contiguous")
+    with _on(q, stream):
+        if z is None:
+            z = _like(q, torch.float32 if out_dtype is None else out_dtype)
+        elif tuple(z.shape) != (B, H, T, d):
+            raise ValueError(f"z shape {tuple(z.shape)}: expected {(B, H, T, d)}")
+        _check_same_dev(q, w, z)
+        desc = LinearAttnDesc(B, H, Hkv, T, d, _dtype_code(q.dtype), _dtype_code(z.dtype), 0, scale, 0, 0,
+                              _strides(q), _strides(k), _strides(v), _strides(z))
+        turn = None if rope is None else _rope(q, *rope)
+        st = lib().ttt_linear_attn_decode(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(lens),
+                                          None if turn is None else ctypes.byref(turn), _ptr(z), _ptr(w),
+                                          _stream_handle(stream))
+        _done(st, "ttt_linear_attn_decode")
+    return z
+
+
+# ------------------------------------------------------- rotary positions --
+
+def rotary_freqs(rot: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+                 original: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
+    """Frequencies for :func:`rotary`: (freqs [rot / 2] float64, scale).
+
+    Plain: base^(-2i / rot) radians per position, scale 1.  For contexts ``factor`` times longer than the ``original``
+    one: "linear" divides the positions by factor; "ntk" raises the base, so that the slowest pair is slowed by factor
+    and the fastest not at all; "yarn" (Peng et al., arXiv 2309.00071) divides the frequencies of pairs that turn less
+    than beta_slow times within the original context, keeps those that turn more than beta_fast times, blends between
+    them by the number of turns, and scales q and k by 0.1 ln(factor) + 1.
+    """
+    torch = _torch()
+    if rot < 0 or rot % 2:
+        raise ValueError(f"rot must be even and >= 0, not {rot}")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"scaling must be None, 'linear', 'ntk' or 'yarn', not {scaling!r}")
+    if factor < 1.0 or (scaling is None and factor != 1.0):
+        raise ValueError("factor must be >= 1, and 1 without scaling")
+    if scaling == "yarn" and not beta_fast > beta_slow:
+        raise ValueError("beta_fast must be greater than beta_slow")
+    i = torch.arange(0, rot, 2, dtype=torch.float64, device=device)
+    if scaling == "ntk" and rot > 2:
+        base = base * factor ** (rot / (rot - 2))
+    f = base ** (-i / rot) if rot else i
+    if scaling == "linear":
+        return f / factor, 1.0
+    if scaling == "yarn":
+        turns = original * f / (2 * math.pi)
+        keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0, 1)
+        return f / factor * (1 - keep) + f * keep, 0.1 * math.log(factor) + 1.0
+    return f, 1.0
+
+
+def _rope(x, pos, freqs, layout: str = "half", scale: float = 1.0) -> Rope:
+    """The ttt_rope of positions ``pos`` for rows like x [B, H, T, d]."""
+    torch = _torch()
+    B, _, T, _ = x.shape
+    if layout not in ("half", "interleaved"):
+        raise ValueError(f"layout must be 'half' or 'interleaved', not {layout!r}")
+    if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise ValueError("freqs must be a contiguous float64 vector")
+    r = Rope(None, 0, 0, 0, freqs.data_ptr(), 2 * freqs.shape[0], layout == "interleaved", scale, 0)
+    if torch.is_tensor(pos):
+        if pos.dtype != torch.int64:
+            raise TypeError("positions must be int64")
+        if tuple(pos.shape) == (B, T):
+            r.pos_stride_b, r.pos_stride_t = pos.stride()
+            if T > 1 and r.pos_stride_t == 0:
+                raise ValueError("positions of one sequence must not be expanded along T")
+        elif tuple(pos.shape) == (B,):
+            r.pos_stride_b = pos.stride(0)
+        else:
+            raise ValueError(f"positions {tuple(pos.shape)}: expected an int, [B] (of the first token) or [B, T]")
+        _check_same_dev(x, pos, freqs)
+        r.pos = pos.data_ptr()
+    else:
+        r.pos_offset = int(pos)
+        _check_same_dev(x, freqs)
+    return r
+
+
+def _rotary_call(q, k, pos, freqs, layout, scale, out, stream, flags, what):
+    torch = _torch()
+    if q.dim() != 4:
+        raise ValueError("q must be [B, H, T, d]")
+    B, H, T, d = q.shape
+    if k is not None:
+        if k.dim() != 4 or (k.shape[0], k.shape[2], k.shape[3]) != (B, T, d):
+            raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}: expected [B, H, T, d] and [B, Hkv, T, d]")
+        if k.dtype != q.dtype:
+            raise ValueError("q and k must have the same dtype")
+    with _on(q, stream):
+        qo, ko = out if out is not None else (_like(q, q.dtype), None if k is None else _like(k, k.dtype))
+        if (ko is None) != (k is None):
+            raise ValueError("out must hold an output for k exactly where k is given")
+        _want(qo, q.shape, q.dtype, "out[0]")
+        if k is not None:
+            _want(ko, k.shape, k.dtype, "out[1]")
+        _check_same_dev(q, k, qo, ko)
+        none = Strides()
+        desc = RotaryDesc(B, H, 0 if k is None else k.shape[1], T, d, _dtype_code(q.dtype), flags, 0, _strides(q),
+                          none if k is None else _strides(k), _strides(qo), none if k is None else _strides(ko))
+        rope = _rope(q, pos, freqs, layout, scale)
+        st = lib().ttt_rotary(ctypes.byref(desc), ctypes.byref(rope), _ptr(q), _ptr(k), _ptr(qo), _ptr(ko),
+                              _stream_handle(stream))
+        _done(st, what)
+    return qo, ko
+
+
+def rotary(q, k, pos, freqs, layout: str = "half", scale: float = 1.0, out=None, stream=None):
+    """Rotary positions: each pair of the first 2 len(freqs) elements of q's and k's rows turned by position * freqs[i].
+
+    q      : [B, H, T, d], k : [B, Hkv, T, d] or None; bfloat16 or float32, any strides between contiguous rows
+    pos    : int (position of every sequence's first token), int64 [B] (of each one's) or int64 [B, T] (of each token)
+    freqs  : float64 vector on the GPU, from :func:`rotary_freqs` (angles are computed in 64 bits)
+    layout : "half" pairs (i, i + len(freqs)), "interleaved" pairs (2i, 2i + 1)
+    scale  : factor on the turned elements (the second result of :func:`rotary_freqs`); the others are passed on
+    out    : optional (q_out, k_out), which may be q and k themselves
+    returns (q_out, k_out).
+    """
+    return _rotary_call(q, k, pos, freqs, layout, scale, out, stream, 0, "ttt_rotary")
+
+
+def rotary_bwd(dq, dk, pos, freqs, layout: str = "half", scale: float = 1.0, out=None, stream=None):
+    """Backward of :func:`rotary`: the gradients with respect to its q and k, given those with respect to its outputs."""
+    return _rotary_call(dq, dk, pos, freqs, layout, scale, out, stream, TTT_FLAG_INVERSE, "ttt_rotary")

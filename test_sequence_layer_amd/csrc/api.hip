@@ -1267,3 +1267,528 @@ const char* ttt_mlp_ln_bwd_kernel_name(const ttt_mlp_desc* d) {
 }
 
 }  // extern "C"
+
+// ------------------------------------- linear attention, rotary positions --
+
+namespace {
+
+// A strided [B, H, T, d] tensor.
+struct View {
+  const void* p;
+  int64_t B, H, T, d;
+  ttt_strides s;
+  int64_t size;  // bytes of an element
+};
+
+View view(const void* p, int64_t B, int64_t H, int64_t T, int64_t d, ttt_strides s, int32_t dtype) {
+  // strides of dimensions of size 1 (or 0) carry nothing
+  if (B <= 1) s.b = 0;
+  if (H <= 1) s.h = 0;
+  if (T <= 1) s.t = 0;
+  return View{p, B, H, T, d, s, dtype_size(dtype)};
+}
+
+ttt::Strides3 strides(const View& v) { return ttt::Strides3{v.s.b, v.s.h, v.s.t}; }
+
+bool empty(const View& v) { return v.B == 0 || v.H == 0 || v.T == 0; }
+
+// elements from the first to behind the last, with the heads, tokens and sequences named
+int64_t extent(const View& v, bool tokens = true, bool batch = true) {
+  return (v.H - 1) * v.s.h + (tokens ? (v.T - 1) * v.s.t : 0) + (batch ? (v.B - 1) * v.s.b : 0) + v.d;
+}
+
+Range range(const View& v) { return Range{v.p, empty(v) ? 0 : extent(v) * v.size}; }
+
+// strides >= 0, no extent beyond 2^46 elements; an output's elements apart
+bool strides_ok(const View& v, bool output) {
+  if (v.s.b < 0 || v.s.h < 0 || v.s.t < 0) return false;
+  if (empty(v)) return true;
+  int64_t st[3] = {v.s.b, v.s.h, v.s.t}, n[3] = {v.B, v.H, v.T};
+  int64_t span = v.d;
+  for (int i = 0; i < 3; ++i) {
+    int64_t e = 1;
+    if (n[i] > 1 && (!mul_ok(e, n[i] - 1) || !mul_ok(e, st[i]))) return false;
+  }
+  if (!output) return true;
+  for (int done = 0; done < 3; ++done) {  // smallest stride first
+    int m = -1;
+    for (int i = 0; i < 3; ++i)
+      if (n[i] > 1 && (m < 0 || st[i] < st[m])) m = i;
+    if (m < 0) break;
+    if (st[m] < span) return false;
+    span += (n[m] - 1) * st[m];
+    n[m] = 1;
+  }
+  return true;
+}
+
+bool view_aligned(const View& v, int64_t bytes) {
+  if (empty(v)) return true;
+  return aligned(v.p, static_cast<uintptr_t>(bytes)) && v.s.b * v.size % bytes == 0 && v.s.h * v.size % bytes == 0 &&
+         v.s.t * v.size % bytes == 0;
+}
+
+// Whether two tensors of the same B and T share memory.  Tensors whose ranges
+// interleave are apart if they are slices of the same rows: the same strides
+// between tokens and sequences (or sequences alone), and one's rows end before
+// the other's begin, within a row's pitch.
+bool views_overlap(const View& a, const View& b) {
+  if (!overlaps(range(a), range(b))) return false;
+  const View &lo = reinterpret_cast<uintptr_t>(a.p) <= reinterpret_cast<uintptr_t>(b.p) ? a : b;
+  const View& hi = &lo == &a ? b : a;
+  const int64_t bytes = static_cast<int64_t>(reinterpret_cast<uintptr_t>(hi.p) - reinterpret_cast<uintptr_t>(lo.p));
+  if (lo.size != hi.size || bytes % lo.size != 0 || lo.s.b != hi.s.b) return true;
+  const int64_t off = bytes / lo.size;
+  for (bool tokens : {false, true}) {  // slices of a token's row; of a sequence's
+    if (!tokens && lo.s.t != hi.s.t) continue;
+    if (off < extent(lo, tokens, false)) continue;
+    const int64_t end = off + extent(hi, tokens, false);
+    const int64_t row = !tokens && lo.T > 1 ? lo.s.t : INT64_MAX;
+    if (end > row) continue;
+    const int64_t seq = end + (tokens ? 0 : (lo.T - 1) * lo.s.t);
+    if (lo.B > 1 && seq > lo.s.b) continue;
+    return false;
+  }
+  return true;
+}
+
+bool same_view(const View& a, const View& b) {
+  return a.p == b.p && a.s.b == b.s.b && a.s.h == b.s.h && a.s.t == b.s.t && a.size == b.size && a.H == b.H;
+}
+
+constexpr int64_t kMaxTokens = int64_t(1) << 30;
+bool finite(float x) { return x - x == 0.f; }
+
+// sizes, types, flags; chains = B * H
+ttt_status check_attn_desc(const ttt_linear_attn_desc* d, int64_t* chains) {
+  if (!d) return TTT_ERR_NULL;
+  if (d->B < 0 || d->H < 0 || d->Hkv < 0 || d->T < 0 || d->d < 1 || d->T > kMaxTokens) return TTT_ERR_SHAPE;
+  if (d->H > 0 && (d->Hkv < 1 || d->H % d->Hkv != 0)) return TTT_ERR_SHAPE;
+  if (!finite(d->scale)) return TTT_ERR_SHAPE;
+  if (!dtype_ok(d->in_dtype) || !dtype_ok(d->out_dtype)) return TTT_ERR_DTYPE;
+  if (d->flags != 0 || d->reserved != 0) return TTT_ERR_FLAGS;
+  *chains = 1;
+  if (!mul_ok(*chains, d->B) || !mul_ok(*chains, d->H) || *chains > INT_MAX) return TTT_ERR_SHAPE;
+  int64_t tok = *chains, wel = *chains;
+  if (!mul_ok(tok, d->T) || !mul_ok(tok, d->d) || !mul_ok(wel, d->d) || !mul_ok(wel, d->d)) return TTT_ERR_SHAPE;
+  if (d->w0_batch_stride != 0 && d->w0_batch_stride != static_cast<int64_t>(d->H) * d->d * d->d) return TTT_ERR_STRIDE;
+  if (!ttt::attn_supported(d->d)) return TTT_ERR_UNSUPPORTED;
+  return TTT_OK;
+}
+
+struct AttnPlan {
+  int nseg, seglen;
+  int64_t loc, gloc, dgpart, dk, dv, bytes;  // workspace offsets
+};
+
+AttnPlan attn_plan(const ttt_linear_attn_desc* d, bool backward) {
+  AttnPlan p;
+  const int64_t chains = static_cast<int64_t>(d->B) * d->H, dd = static_cast<int64_t>(d->d) * d->d * 4;
+  const int n = ttt::attn_segments(chains, d->T, d->d);
+  const int c = ttt::kAttnChunk;
+  p.seglen = ((d->T + n - 1) / n + c - 1) / c * c;
+  if (p.seglen < c) p.seglen = c;
+  p.nseg = d->T > 0 ? (d->T + p.seglen - 1) / p.seglen : 1;
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t o = at;
+    at += (bytes + 255) / 256 * 256;
+    return o;
+  };
+  const bool split = p.nseg > 1;
+  p.loc = take(split ? chains * p.nseg * dd : 0);
+  p.gloc = take(split && backward ? chains * p.nseg * 2 * dd : 0);
+  p.dgpart = take(split && backward ? chains * p.nseg * 8 : 0);
+  const int64_t part = backward && d->H > d->Hkv ? chains * d->T * d->d * 4 : 0;
+  p.dk = take(part);
+  p.dv = take(part);
+  p.bytes = at;
+  return p;
+}
+
+ttt_status check_rope(const ttt_rope* r, int32_t d, int64_t B, int64_t T, Range* pos, Range* freqs) {
+  if (r->rot < 0 || r->rot % 2 != 0 || r->rot > d) return TTT_ERR_SHAPE;
+  if (!finite(r->scale)) return TTT_ERR_SHAPE;
+  if ((r->interleaved != 0 && r->interleaved != 1) || r->reserved != 0) return TTT_ERR_FLAGS;
+  if (r->pos_stride_b < 0 || r->pos_stride_t < 0) return TTT_ERR_STRIDE;
+  for (int i = 0; i < 2; ++i) {
+    int64_t e = 1;
+    if (!mul_ok(e, i ? T : B) || !mul_ok(e, i ? r->pos_stride_t : r->pos_stride_b)) return TTT_ERR_STRIDE;
+  }
+  if (r->rot > 0 && !r->freqs) return TTT_ERR_NULL;
+  if (!aligned(r->pos, 8) || !aligned(r->freqs, 8)) return TTT_ERR_ALIGN;
+  const int64_t n = B == 0 || T == 0 ? 0 : (B - 1) * r->pos_stride_b + (T - 1) * r->pos_stride_t + 1;
+  *pos = Range{r->pos, n * 8};
+  *freqs = Range{r->freqs, static_cast<int64_t>(r->rot) * 4};
+  return TTT_OK;
+}
+
+ttt::Rope make_rope(const ttt_rope* r) {
+  ttt::Rope o;
+  o.pos = r ? r->pos : nullptr;
+  o.pos_b = r ? r->pos_stride_b : 0;
+  o.pos_t = r ? r->pos_stride_t : 0;
+  o.pos0 = r ? r->pos_offset : 0;
+  o.freqs = r && r->rot > 0 ? r->freqs : nullptr;
+  o.rot = r ? r->rot : 0;
+  o.interleaved = r && r->interleaved;
+  o.scale = r ? r->scale : 1.f;
+  return o;
+}
+
+// each output against every input and the outputs before it
+ttt_status check_alias(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
+  for (const Range* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Range& in : ins)
+      if (overlaps(*o, in)) return TTT_ERR_ALIAS;
+    for (const Range* p = outs.begin(); p != o; ++p)
+      if (overlaps(*o, *p)) return TTT_ERR_ALIAS;
+  }
+  return TTT_OK;
+}
+
+// q, k, v and z (Z or dZ) of the forward and the backward
+ttt_status check_attn_views(const ttt_linear_attn_desc* d, const View& q, const View& k, const View& v, const View& z,
+                            bool z_out, int64_t align) {
+  const bool any = !empty(q);
+  if (any && (!q.p || !k.p || !v.p || !z.p)) return TTT_ERR_NULL;
+  for (const View* x : {&q, &k, &v})
+    if (!strides_ok(*x, false)) return TTT_ERR_STRIDE;
+  if (!strides_ok(z, z_out)) return TTT_ERR_STRIDE;
+  for (const View* x : {&q, &k, &v, &z})
+    if (!view_aligned(*x, align ? align : x->size)) return TTT_ERR_ALIGN;
+  (void)d;
+  return TTT_OK;
+}
+
+ttt_status check_workspace(const void* ws, int64_t bytes, int64_t need) {
+  if (need == 0) return TTT_OK;
+  if (!ws || !aligned(ws, 16) || bytes < need) return TTT_ERR_WORKSPACE;
+  return TTT_OK;
+}
+
+struct AttnViews {
+  View q, k, v, z;
+  Range g, w0, lens;
+  int64_t state_bytes;
+};
+
+AttnViews attn_views(const ttt_linear_attn_desc* d, const void* Q, const void* K, const void* V, const void* Z,
+                     const float* g, const float* W0, const int32_t* lens) {
+  AttnViews v;
+  v.q = view(Q, d->B, d->H, d->T, d->d, d->q, d->in_dtype);
+  v.k = view(K, d->B, d->Hkv, d->T, d->d, d->k, d->in_dtype);
+  v.v = view(V, d->B, d->Hkv, d->T, d->d, d->v, d->in_dtype);
+  v.z = view(Z, d->B, d->H, d->T, d->d, d->z, d->out_dtype);
+  const int64_t hdd = static_cast<int64_t>(d->H) * d->d * d->d * 4;
+  v.state_bytes = hdd * d->B;
+  v.g = Range{g, static_cast<int64_t>(d->H) * 4};
+  v.w0 = Range{W0, W0 ? (d->w0_batch_stride ? v.state_bytes : hdd) : 0};
+  v.lens = Range{lens, lens ? static_cast<int64_t>(d->B) * 4 : 0};
+  return v;
+}
+
+ttt_status validate_attn_fwd(const ttt_linear_attn_desc* d, const void* Q, const void* K, const void* V, const float* g,
+                             const float* W0, const int32_t* lens, const void* Z, const float* Wf, const void* ws,
+                             int64_t ws_bytes) {
+  int64_t chains;
+  ttt_status st = check_attn_desc(d, &chains);
+  if (st != TTT_OK) return st;
+  const AttnViews v = attn_views(d, Q, K, V, Z, g, W0, lens);
+  const AttnPlan plan = attn_plan(d, false);
+  if (chains * plan.nseg > INT_MAX) return TTT_ERR_SHAPE;
+  if (chains == 0) return TTT_OK;
+  if (!g || !Wf) return TTT_ERR_NULL;
+  if ((st = check_attn_views(d, v.q, v.k, v.v, v.z, true, 16)) != TTT_OK) return st;
+  if (!aligned(g, 4) || !aligned(lens, 4) || !aligned(W0, 16) || !aligned(Wf, 16)) return TTT_ERR_ALIGN;
+  if ((st = check_workspace(ws, ws_bytes, plan.bytes)) != TTT_OK) return st;
+  const Range wf{Wf, v.state_bytes}, wsr{ws, plan.bytes}, z = range(v.z);
+  if ((st = check_alias({wf, wsr}, {range(v.q), range(v.k), range(v.v), v.g, v.lens, z})) != TTT_OK) return st;
+  if ((st = check_alias({z}, {v.g, v.lens})) != TTT_OK) return st;
+  if (views_overlap(v.z, v.q) || views_overlap(v.z, v.k) || views_overlap(v.z, v.v)) return TTT_ERR_ALIAS;
+  if (overlaps(z, v.w0) || overlaps(wsr, v.w0)) return TTT_ERR_ALIAS;
+  if (overlaps(wf, v.w0) && !(Wf == W0 && d->w0_batch_stride != 0)) return TTT_ERR_ALIAS;
+  return TTT_OK;
+}
+
+ttt_status validate_attn_bwd(const ttt_linear_attn_desc* d, const void* Q, const void* K, const void* V, const float* g,
+                             const float* W0, const int32_t* lens, const void* dZ, const float* dWf, const void* dQ,
+                             const void* dK, const void* dV, const float* dg, const float* dW0, const void* ws,
+                             int64_t ws_bytes) {
+  int64_t chains;
+  ttt_status st = check_attn_desc(d, &chains);
+  if (st != TTT_OK) return st;
+  const AttnViews v = attn_views(d, Q, K, V, dZ, g, W0, lens);
+  const View dq = view(dQ, d->B, d->H, d->T, d->d, d->dq, d->out_dtype);
+  const View dk = view(dK, d->B, d->Hkv, d->T, d->d, d->dk, d->out_dtype);
+  const View dv = view(dV, d->B, d->Hkv, d->T, d->d, d->dv, d->out_dtype);
+  const AttnPlan plan = attn_plan(d, true);
+  if (chains * plan.nseg > INT_MAX) return TTT_ERR_SHAPE;
+  if (chains * d->T * (d->d / 4) / 256 > INT_MAX - 1) return TTT_ERR_SHAPE;
+  if (chains == 0) return TTT_OK;
+  if (!g || !dg || !dW0) return TTT_ERR_NULL;
+  if (!empty(dq) && (!dQ || !dK || !dV)) return TTT_ERR_NULL;
+  if ((st = check_attn_views(d, v.q, v.k, v.v, v.z, false, 16)) != TTT_OK) return st;
+  for (const View* x : {&dq, &dk, &dv}) {
+    if (!strides_ok(*x, true)) return TTT_ERR_STRIDE;
+    if (!view_aligned(*x, 16)) return TTT_ERR_ALIGN;
+  }
+  if (!aligned(g, 4) || !aligned(lens, 4) || !aligned(W0, 16) || !aligned(dWf, 16) || !aligned(dg, 4) ||
+      !aligned(dW0, 16))
+    return TTT_ERR_ALIGN;
+  if ((st = check_workspace(ws, ws_bytes, plan.bytes)) != TTT_OK) return st;
+  const Range wsr{ws, plan.bytes}, dgr{dg, chains * 4}, dw0r{dW0, v.state_bytes};
+  const Range dwf{dWf, dWf ? v.state_bytes : 0};
+  const Range dqr = range(dq), dkr = range(dk), dvr = range(dv);
+  for (const Range& o : {dqr, dkr, dvr, dgr, dw0r, wsr})
+    for (const Range& in : {v.g, v.w0, v.lens, dwf})
+      if (overlaps(o, in)) return TTT_ERR_ALIAS;
+  for (const View* in : {&v.q, &v.k, &v.v, &v.z}) {
+    for (const View* o : {&dq, &dk, &dv})
+      if (views_overlap(*o, *in)) return TTT_ERR_ALIAS;
+    for (const Range& o : {dgr, dw0r, wsr})
+      if (overlaps(o, range(*in))) return TTT_ERR_ALIAS;
+  }
+  if ((st = check_alias({dgr, dw0r, wsr}, {dqr, dkr, dvr})) != TTT_OK) return st;
+  if (views_overlap(dq, dk) || views_overlap(dq, dv) || views_overlap(dk, dv)) return TTT_ERR_ALIAS;
+  return TTT_OK;
+}
+
+ttt_status validate_attn_decode(const ttt_linear_attn_desc* d, const void* Q, const void* K, const void* V,
+                                const float* g, const int32_t* lens, const ttt_rope* rope, const void* Z,
+                                const float* W) {
+  int64_t chains;
+  ttt_status st = check_attn_desc(d, &chains);
+  if (st != TTT_OK) return st;
+  if (d->w0_batch_stride != 0) return TTT_ERR_STRIDE;
+  Range pos{nullptr, 0}, freqs{nullptr, 0};
+  if (rope && (st = check_rope(rope, d->d, d->B, d->T, &pos, &freqs)) != TTT_OK) return st;
+  if (chains == 0) return TTT_OK;
+  if (!g || !W) return TTT_ERR_NULL;
+  const AttnViews v = attn_views(d, Q, K, V, Z, g, nullptr, lens);
+  if ((st = check_attn_views(d, v.q, v.k, v.v, v.z, true, 0)) != TTT_OK) return st;
+  if (!aligned(g, 4) || !aligned(lens, 4) || !aligned(W, 16)) return TTT_ERR_ALIGN;
+  if (views_overlap(v.z, v.q) || views_overlap(v.z, v.k) || views_overlap(v.z, v.v)) return TTT_ERR_ALIAS;
+  if ((st = check_alias({range(v.z)}, {v.g, v.lens, pos, freqs})) != TTT_OK) return st;
+  return check_alias({Range{W, v.state_bytes}},
+                     {range(v.q), range(v.k), range(v.v), range(v.z), v.g, v.lens, pos, freqs});
+}
+
+struct RotaryViews {
+  View q, k, qo, ko;
+};
+
+RotaryViews rotary_views(const ttt_rotary_desc* d, const void* q, const void* k, const void* qo, const void* ko) {
+  return RotaryViews{view(q, d->B, d->H, d->T, d->d, d->q, d->dtype), view(k, d->B, d->Hkv, d->T, d->d, d->k, d->dtype),
+                     view(qo, d->B, d->H, d->T, d->d, d->q_out, d->dtype),
+                     view(ko, d->B, d->Hkv, d->T, d->d, d->k_out, d->dtype)};
+}
+
+ttt_status validate_rotary(const ttt_rotary_desc* d, const ttt_rope* rope, const void* q, const void* k, const void* qo,
+                           const void* ko) {
+  if (!d || !rope) return TTT_ERR_NULL;
+  if (d->B < 0 || d->H < 0 || d->Hkv < 0 || d->T < 0 || d->d < 1 || d->T > kMaxTokens) return TTT_ERR_SHAPE;
+  if (!dtype_ok(d->dtype)) return TTT_ERR_DTYPE;
+  if ((d->flags & ~TTT_FLAG_INVERSE) || d->reserved != 0) return TTT_ERR_FLAGS;
+  const int64_t heads = static_cast<int64_t>(d->H) + d->Hkv;
+  int64_t n = 1;
+  if (heads > INT_MAX || !mul_ok(n, d->B) || !mul_ok(n, d->T) || !mul_ok(n, d->d)) return TTT_ERR_SHAPE;
+  if (n / 256 >= INT_MAX || !mul_ok(n, heads)) return TTT_ERR_SHAPE;
+  Range pos, freqs;
+  ttt_status st = check_rope(rope, d->d, d->B, d->T, &pos, &freqs);
+  if (st != TTT_OK) return st;
+  const RotaryViews v = rotary_views(d, q, k, qo, ko);
+  if (empty(v.q) && empty(v.k)) return TTT_OK;
+  if ((!empty(v.q) && (!q || !qo)) || (!empty(v.k) && (!k || !ko))) return TTT_ERR_NULL;
+  for (const View* x : {&v.q, &v.k})
+    if (!strides_ok(*x, false)) return TTT_ERR_STRIDE;
+  for (const View* x : {&v.qo, &v.ko})
+    if (!strides_ok(*x, true)) return TTT_ERR_STRIDE;
+  for (const View* x : {&v.q, &v.k, &v.qo, &v.ko})
+    if (!view_aligned(*x, x->size)) return TTT_ERR_ALIGN;
+  if ((!same_view(v.q, v.qo) && views_overlap(v.q, v.qo)) || (!same_view(v.k, v.ko) && views_overlap(v.k, v.ko)))
+    return TTT_ERR_ALIAS;
+  if (views_overlap(v.qo, v.ko) || views_overlap(v.qo, v.k) || views_overlap(v.ko, v.q)) return TTT_ERR_ALIAS;
+  for (const Range& o : {range(v.qo), range(v.ko)})
+    if (overlaps(o, pos) || overlaps(o, freqs)) return TTT_ERR_ALIAS;
+  return TTT_OK;
+}
+
+ttt_status hip_status(hipError_t e) { return e == hipSuccess ? TTT_OK : TTT_ERR_HIP; }
+
+}  // namespace
+
+extern "C" {
+
+int64_t ttt_linear_attn_workspace_bytes(const ttt_linear_attn_desc* desc, int32_t backward) {
+  int64_t chains;
+  if (check_attn_desc(desc, &chains) != TTT_OK) return -1;
+  return chains == 0 ? 0 : attn_plan(desc, backward != 0).bytes;
+}
+
+ttt_status ttt_linear_attn_fwd_validate(const ttt_linear_attn_desc* desc, const void* Q, const void* K, const void* V,
+                                        const float* log_decay, const float* W0, const int32_t* lens, const void* Z,
+                                        const float* W_final, const void* workspace, int64_t workspace_bytes) {
+  return validate_attn_fwd(desc, Q, K, V, log_decay, W0, lens, Z, W_final, workspace, workspace_bytes);
+}
+
+ttt_status ttt_linear_attn_fwd(const ttt_linear_attn_desc* desc, const void* Q, const void* K, const void* V,
+                               const float* log_decay, const float* W0, const int32_t* lens, void* Z, float* W_final,
+                               void* workspace, int64_t workspace_bytes, void* stream) {
+  const ttt_status st =
+      validate_attn_fwd(desc, Q, K, V, log_decay, W0, lens, Z, W_final, workspace, workspace_bytes);
+  if (st != TTT_OK) return st;
+  if (static_cast<int64_t>(desc->B) * desc->H == 0) return TTT_OK;
+  const AttnViews v = attn_views(desc, Q, K, V, Z, log_decay, W0, lens);
+  const AttnPlan plan = attn_plan(desc, false);
+  ttt::AttnArgs a;
+  a.B = desc->B; a.H = desc->H; a.T = desc->T; a.d = desc->d;
+  a.group = desc->H / desc->Hkv;
+  a.nseg = plan.nseg; a.seglen = plan.seglen;
+  a.x_dtype = desc->in_dtype; a.in_dtype = desc->in_dtype; a.out_dtype = desc->out_dtype;
+  a.X = Q; a.Y = K; a.V = V;
+  a.xs = strides(v.q); a.ys = strides(v.k); a.vs = strides(v.v); a.os = strides(v.z);
+  a.log_decay = log_decay; a.scale = desc->scale;
+  a.S0 = W0; a.s0_bstride = desc->w0_batch_stride; a.transposed = false;
+  a.lens = lens;
+  a.loc = static_cast<float*>(workspace);
+  a.O = Z; a.S_final = W_final;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (plan.nseg > 1) {
+    const hipError_t e = ttt::launch_attn_states(a, s);
+    if (e != hipSuccess) return TTT_ERR_HIP;
+  }
+  return hip_status(ttt::launch_attn_fwd(a, s));
+}
+
+ttt_status ttt_linear_attn_bwd_validate(const ttt_linear_attn_desc* desc, const void* Q, const void* K, const void* V,
+                                        const float* log_decay, const float* W0, const int32_t* lens, const void* dZ,
+                                        const float* dW_final, const void* dQ, const void* dK, const void* dV,
+                                        const float* dlog_decay, const float* dW0, const void* workspace,
+                                        int64_t workspace_bytes) {
+  return validate_attn_bwd(desc, Q, K, V, log_decay, W0, lens, dZ, dW_final, dQ, dK, dV, dlog_decay, dW0, workspace,
+                           workspace_bytes);
+}
+
+ttt_status ttt_linear_attn_bwd(const ttt_linear_attn_desc* desc, const void* Q, const void* K, const void* V,
+                               const float* log_decay, const float* W0, const int32_t* lens, const void* dZ,
+                               const float* dW_final, void* dQ, void* dK, void* dV, float* dlog_decay, float* dW0,
+                               void* workspace, int64_t workspace_bytes, void* stream) {
+  const ttt_status st = validate_attn_bwd(desc, Q, K, V, log_decay, W0, lens, dZ, dW_final, dQ, dK, dV, dlog_decay, dW0,
+                                          workspace, workspace_bytes);
+  if (st != TTT_OK) return st;
+  if (static_cast<int64_t>(desc->B) * desc->H == 0) return TTT_OK;
+  const AttnViews v = attn_views(desc, Q, K, V, dZ, log_decay, W0, lens);
+  const AttnPlan plan = attn_plan(desc, true);
+  char* ws = static_cast<char*>(workspace);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const int group = desc->H / desc->Hkv;
+
+  ttt::AttnArgs a;  // dQ: the forward walk of dZ over V, K
+  a.B = desc->B; a.H = desc->H; a.T = desc->T; a.d = desc->d;
+  a.group = group;
+  a.nseg = plan.nseg; a.seglen = plan.seglen;
+  a.x_dtype = desc->out_dtype; a.in_dtype = desc->in_dtype; a.out_dtype = desc->out_dtype;
+  a.X = dZ; a.Y = V; a.V = K;
+  a.xs = strides(v.z); a.ys = strides(v.v); a.vs = strides(v.k);
+  a.os = strides(view(dQ, desc->B, desc->H, desc->T, desc->d, desc->dq, desc->out_dtype));
+  a.log_decay = log_decay; a.scale = desc->scale;
+  a.S0 = W0; a.s0_bstride = desc->w0_batch_stride; a.transposed = true;
+  a.lens = lens;
+  a.loc = reinterpret_cast<float*>(ws + plan.loc);
+  a.O = dQ; a.S_final = nullptr;
+
+  ttt::AttnBwdArgs r;
+  r.B = desc->B; r.H = desc->H; r.T = desc->T; r.d = desc->d;
+  r.group = group;
+  r.nseg = plan.nseg; r.seglen = plan.seglen;
+  r.in_dtype = desc->in_dtype; r.out_dtype = desc->out_dtype;
+  r.Q = Q; r.K = K; r.V = V; r.dZ = dZ;
+  r.qs = strides(v.q); r.ks = strides(v.k); r.vs = strides(v.v); r.zs = strides(v.z);
+  r.log_decay = log_decay; r.scale = desc->scale;
+  r.W0 = W0; r.w0_bstride = desc->w0_batch_stride;
+  r.lens = lens; r.dWf = dW_final;
+  r.gloc = reinterpret_cast<float*>(ws + plan.gloc);
+  r.dgpart = reinterpret_cast<double*>(ws + plan.dgpart);
+  r.parts = group > 1;
+  const ttt::Strides3 dks = strides(view(dK, desc->B, desc->Hkv, desc->T, desc->d, desc->dk, desc->out_dtype));
+  const ttt::Strides3 dvs = strides(view(dV, desc->B, desc->Hkv, desc->T, desc->d, desc->dv, desc->out_dtype));
+  const int64_t hs = static_cast<int64_t>(desc->T) * desc->d;
+  const ttt::Strides3 packed{hs * desc->H, hs, desc->d};
+  r.dK = r.parts ? ws + plan.dk : dK;
+  r.dV = r.parts ? ws + plan.dv : dV;
+  r.dks = r.parts ? packed : dks;
+  r.dvs = r.parts ? packed : dvs;
+  r.dg = dlog_decay; r.dW0 = dW0;
+
+  if (plan.nseg > 1) {
+    ttt::AttnArgs p = a;  // the states themselves: V K^T
+    p.Y = K; p.V = V;
+    p.ys = strides(v.k); p.vs = strides(v.v);
+    if (ttt::launch_attn_states(p, s) != hipSuccess) return TTT_ERR_HIP;
+    if (ttt::launch_attn_bwd_states(r, s) != hipSuccess) return TTT_ERR_HIP;
+  }
+  if (ttt::launch_attn_fwd(a, s) != hipSuccess) return TTT_ERR_HIP;
+  if (ttt::launch_attn_bwd(r, s) != hipSuccess) return TTT_ERR_HIP;
+  if (plan.nseg > 1 && ttt::launch_attn_bwd_dg(r, s) != hipSuccess) return TTT_ERR_HIP;
+  if (r.parts && desc->T > 0) {
+    ttt::AttnSumArgs m{desc->B, desc->Hkv, desc->T, desc->d, group, desc->out_dtype,
+                       reinterpret_cast<const float*>(ws + plan.dk), dK, dks};
+    if (ttt::launch_attn_sum(m, s) != hipSuccess) return TTT_ERR_HIP;
+    m.parts = reinterpret_cast<const float*>(ws + plan.dv);
+    m.out = dV;
+    m.os = dvs;
+    if (ttt::launch_attn_sum(m, s) != hipSuccess) return TTT_ERR_HIP;
+  }
+  return TTT_OK;
+}
+
+ttt_status ttt_linear_attn_decode_validate(const ttt_linear_attn_desc* desc, const void* Q, const void* K,
+                                           const void* V, const float* log_decay, const int32_t* lens,
+                                           const ttt_rope* rope, const void* Z, const float* W) {
+  return validate_attn_decode(desc, Q, K, V, log_decay, lens, rope, Z, W);
+}
+
+ttt_status ttt_linear_attn_decode(const ttt_linear_attn_desc* desc, const void* Q, const void* K, const void* V,
+                                  const float* log_decay, const int32_t* lens, const ttt_rope* rope, void* Z, float* W,
+                                  void* stream) {
+  const ttt_status st = validate_attn_decode(desc, Q, K, V, log_decay, lens, rope, Z, W);
+  if (st != TTT_OK) return st;
+  if (static_cast<int64_t>(desc->B) * desc->H == 0 || desc->T == 0) return TTT_OK;
+  const AttnViews v = attn_views(desc, Q, K, V, Z, log_decay, nullptr, lens);
+  ttt::AttnDecodeArgs a;
+  a.B = desc->B; a.H = desc->H; a.T = desc->T; a.d = desc->d;
+  a.group = desc->H / desc->Hkv;
+  a.in_dtype = desc->in_dtype; a.out_dtype = desc->out_dtype;
+  a.Q = Q; a.K = K; a.V = V;
+  a.qs = strides(v.q); a.ks = strides(v.k); a.vs = strides(v.v); a.os = strides(v.z);
+  a.log_decay = log_decay; a.scale = desc->scale;
+  a.lens = lens; a.W = W; a.Z = Z;
+  a.rope = make_rope(rope);
+  return hip_status(ttt::launch_attn_decode(a, static_cast<hipStream_t>(stream)));
+}
+
+ttt_status ttt_rotary_validate(const ttt_rotary_desc* desc, const ttt_rope* rope, const void* q, const void* k,
+                               const void* q_out, const void* k_out) {
+  return validate_rotary(desc, rope, q, k, q_out, k_out);
+}
+
+ttt_status ttt_rotary(const ttt_rotary_desc* desc, const ttt_rope* rope, const void* q, const void* k, void* q_out,
+                      void* k_out, void* stream) {
+  const ttt_status st = validate_rotary(desc, rope, q, k, q_out, k_out);
+  if (st != TTT_OK) return st;
+  const RotaryViews v = rotary_views(desc, q, k, q_out, k_out);
+  if (empty(v.q) && empty(v.k)) return TTT_OK;
+  ttt::RotaryArgs a;
+  a.B = desc->B; a.H = desc->H; a.Hkv = desc->Hkv; a.T = desc->T; a.d = desc->d;
+  a.dtype = desc->dtype;
+  a.q = q; a.k = k; a.qo = q_out; a.ko = k_out;
+  a.qs = strides(v.q); a.ks = strides(v.k); a.qos = strides(v.qo); a.kos = strides(v.ko);
+  a.rope = make_rope(rope);
+  a.inverse = (desc->flags & TTT_FLAG_INVERSE) != 0;
+  a.in_place = (desc->H == 0 || same_view(v.q, v.qo)) && (desc->Hkv == 0 || same_view(v.k, v.ko));
+  if (a.in_place && a.rope.rot == 0) return TTT_OK;
+  return hip_status(ttt::launch_rotary(a, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

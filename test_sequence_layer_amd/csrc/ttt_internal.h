@@ -1,6 +1,7 @@
 // Internal declarations of libttt.so (not part of the C ABI): every kernel
 // family's launch arguments and entry points, for the host-side dispatch.
 #pragma once
+#include "args_attn.h"
 #include "args_bwd.h"
 #include "args_linear.h"
 #include "args_mlp.h"

@@ -1,0 +1,282 @@
+"""Host-side checks of the linear-attention and rotary entry points, without a GPU:
+the C ABI through ttt_*_validate with fake (never dereferenced) addresses, and what
+the Python binding refuses."""
+import ctypes
+
+import pytest
+
+import test_sequence_layer_amd as ttt
+
+OK, NULL, SHAPE, DTYPE, UNSUP, ALIAS, ALIGN, HIP, STRIDE, FLAGS, POS, WORKSPACE, SCRATCH = range(13)
+GB = 1 << 30
+S = ttt.Strides
+L = ttt.lib()
+
+
+def desc(B=2, H=4, Hkv=2, T=64, d=64, ind=1, outd=1, flags=0, scale=1.0, reserved=0, wstride=0, **strides):
+    q, k = S(H * T * d, T * d, d), S(Hkv * T * d, T * d, d)
+    s = dict(q=q, k=k, v=k, z=q, dq=q, dk=k, dv=k)
+    s.update(strides)
+    return ttt.LinearAttnDesc(B, H, Hkv, T, d, ind, outd, flags, scale, reserved, wstride,
+                              *(s[x] for x in ("q", "k", "v", "z", "dq", "dk", "dv")))
+
+
+FWD = dict(q=GB, k=2 * GB, v=3 * GB, g=4 * GB, w0=5 * GB, lens=6 * GB, z=7 * GB, wf=8 * GB, ws=9 * GB, wsb=GB)
+BWD = dict(q=GB, k=2 * GB, v=3 * GB, g=4 * GB, w0=5 * GB, lens=6 * GB, dz=7 * GB, dwf=8 * GB, dq=10 * GB, dk=11 * GB,
+           dv=12 * GB, dg=13 * GB, dw0=14 * GB, ws=15 * GB, wsb=GB)
+DEC = dict(q=GB, k=2 * GB, v=3 * GB, g=4 * GB, lens=6 * GB, rope=None, z=7 * GB, w=8 * GB)
+
+
+def fwd(d, **over):
+    a = {**FWD, **over}
+    return L.ttt_linear_attn_fwd_validate(None if d is None else ctypes.byref(d), *a.values())
+
+
+def bwd(d, **over):
+    a = {**BWD, **over}
+    return L.ttt_linear_attn_bwd_validate(None if d is None else ctypes.byref(d), *a.values())
+
+
+def dec(d, **over):
+    a = {**DEC, **over}
+    r = a["rope"]
+    a["rope"] = None if r is None else ctypes.byref(r)
+    return L.ttt_linear_attn_decode_validate(None if d is None else ctypes.byref(d), *a.values())
+
+
+def rope(pos=20 * GB, sb=1, st=0, off=0, freqs=21 * GB, rot=64, inter=0, scale=1.0, reserved=0):
+    return ttt.Rope(pos, sb, st, off, freqs, rot, inter, scale, reserved)
+
+
+def rdesc(B=2, H=4, Hkv=2, T=64, d=64, dtype=1, flags=0, reserved=0, **strides):
+    q, k = S(H * T * d, T * d, d), S(Hkv * T * d, T * d, d)
+    s = dict(q=q, k=k, qo=q, ko=k)
+    s.update(strides)
+    return ttt.RotaryDesc(B, H, Hkv, T, d, dtype, flags, reserved, s["q"], s["k"], s["qo"], s["ko"])
+
+
+def rot(d, r, q=GB, k=2 * GB, qo=3 * GB, ko=4 * GB):
+    return L.ttt_rotary_validate(None if d is None else ctypes.byref(d), None if r is None else ctypes.byref(r), q, k, qo,
+                                 ko)
+
+
+@pytest.mark.parametrize("call", [fwd, bwd, dec])
+def test_valid_calls(call):
+    for ind in (0, 1):
+        for outd in (0, 1):
+            for d in (16, 32, 64, 128):
+                assert call(desc(d=d, ind=ind, outd=outd)) == OK
+    assert call(desc(), lens=None) == OK
+    assert call(desc(T=1)) == OK and call(desc(T=61)) == OK
+    assert call(desc(H=6, Hkv=1)) == OK
+
+
+@pytest.mark.parametrize("call", [fwd, bwd, dec])
+def test_desc_refusals(call):
+    assert call(None) == NULL
+    for kw in (dict(B=-1), dict(T=-1), dict(d=0), dict(H=4, Hkv=3), dict(H=4, Hkv=0), dict(H=2, Hkv=4),
+               dict(scale=float("nan")), dict(scale=float("inf")), dict(B=1 << 20, H=1 << 20, Hkv=1 << 20)):
+        assert call(desc(**kw)) == SHAPE, kw
+    big = S(1 << 36, 1 << 36, 64)
+    assert call(desc(T=(1 << 30) + 1, q=big, k=big, v=big, z=big, dq=big, dk=big, dv=big)) == SHAPE
+    assert call(desc(ind=2)) == DTYPE and call(desc(outd=-1)) == DTYPE
+    assert call(desc(flags=1)) == FLAGS and call(desc(reserved=1)) == FLAGS
+    assert call(desc(wstride=64)) == STRIDE
+    assert call(desc(d=48)) == UNSUP and call(desc(d=256)) == UNSUP
+
+
+@pytest.mark.parametrize("call,names", [(fwd, ("q", "k", "v", "g", "z", "wf")),
+                                        (bwd, ("q", "k", "v", "g", "dz", "dq", "dk", "dv", "dg", "dw0")),
+                                        (dec, ("q", "k", "v", "g", "z", "w"))])
+def test_null_and_empty(call, names):
+    for n in names:
+        assert call(desc(), **{n: None}) == NULL, n
+    none = {n: None for n in names}
+    assert call(desc(B=0), **none) == OK
+    assert call(desc(H=0, Hkv=0), **none) == OK
+    # no tokens: only the state and the decay are looked at
+    keep = {"g", "wf", "w", "dg", "dw0"}
+    assert call(desc(T=0), **{n: None for n in names if n not in keep}) == OK
+    assert call(desc(T=0), g=None) == NULL
+
+
+def test_strides():
+    d = 64
+    ok = S(64 * 4 * d, d, 4 * d)  # [B, T, H, d]
+    okk = S(64 * 2 * d, d, 2 * d)
+    for call in (fwd, bwd, dec):
+        assert call(desc(q=ok, k=okk, v=okk, z=ok, dq=ok, dk=okk, dv=okk)) == OK
+        assert call(desc(q=S(-64, 0, 0))) == STRIDE
+        assert call(desc(k=S(0, 0, 0))) == OK              # inputs may repeat
+        assert call(desc(k=S(1 << 60, 0, 0))) == STRIDE    # beyond any memory
+    assert fwd(desc(z=S(0, 64 * d, d))) == STRIDE          # outputs may not
+    assert fwd(desc(z=S(4 * 64 * d, 64 * d, d - 8))) == STRIDE
+    assert dec(desc(z=S(0, 64 * d, d))) == STRIDE
+    assert bwd(desc(dq=S(0, 64 * d, d))) == STRIDE and bwd(desc(dv=S(0, 64 * d, d))) == STRIDE
+    # strides of dimensions of size 1 carry nothing
+    assert fwd(desc(B=1, H=1, Hkv=1, T=1, q=S(-5, -7, -1), k=S(3, 3, 3), v=S(1, 1, 1), z=S(0, 0, 0))) == OK
+
+
+def test_alignment():
+    for call, names in ((fwd, ("q", "k", "v", "z", "w0", "wf")), (bwd, ("q", "k", "v", "dz", "dq", "dk", "dv", "w0", "dwf",
+                                                                        "dw0"))):
+        for n in names:
+            base = (FWD if call is fwd else BWD)[n]
+            assert call(desc(), **{n: base + 8}) == ALIGN, n
+        assert call(desc(), g=4 * GB + 2) == ALIGN and call(desc(), lens=6 * GB + 2) == ALIGN
+    assert fwd(desc(q=S(4 * 64 * 68, 64 * 68, 68))) == ALIGN
+    # single tokens come from anywhere
+    assert dec(desc(q=S(4 * 64 * 67, 64 * 67, 67)), q=GB + 2) == OK
+    assert dec(desc(), q=GB + 1) == ALIGN and dec(desc(), w=8 * GB + 4) == ALIGN
+
+
+def test_workspace():
+    few = desc(B=1, H=1, Hkv=1, T=4096)
+    for backward, call in ((0, fwd), (1, bwd)):
+        need = L.ttt_linear_attn_workspace_bytes(ctypes.byref(few), backward)
+        assert need > 0
+        assert call(few, wsb=need) == OK and call(few, wsb=need - 1) == WORKSPACE
+        assert call(few, ws=None) == WORKSPACE and call(few, ws=9 * GB + 8) == WORKSPACE
+        many = desc(B=64, H=16, Hkv=16, T=64)
+        assert L.ttt_linear_attn_workspace_bytes(ctypes.byref(many), backward) == 0
+        assert call(many, ws=None, wsb=0) == OK
+    shared = desc(B=64, H=16, Hkv=8, T=64)  # the parts of shared heads
+    assert L.ttt_linear_attn_workspace_bytes(ctypes.byref(shared), 1) >= 2 * 64 * 16 * 64 * 64 * 4
+    assert L.ttt_linear_attn_workspace_bytes(ctypes.byref(desc(d=20)), 0) == -1
+    assert L.ttt_linear_attn_workspace_bytes(None, 0) == -1
+
+
+def test_alias():
+    for n in ("q", "k", "v", "g", "lens", "w0"):
+        assert fwd(desc(), z=FWD[n]) == ALIAS, n
+    for n in ("q", "k", "v", "g", "lens"):
+        assert fwd(desc(), wf=FWD[n]) == ALIAS, n
+    assert fwd(desc(), wf=FWD["z"]) == ALIAS
+    assert fwd(desc(), wf=FWD["w0"]) == ALIAS                                   # a shared W0
+    each = desc(wstride=4 * 64 * 64)
+    assert fwd(each, wf=FWD["w0"]) == OK                                        # in place
+    assert fwd(each, wf=FWD["w0"] + 64) == ALIAS
+    few = dict(B=1, H=1, Hkv=1, T=4096)
+    for n in ("q", "k", "v", "g", "lens", "w0", "z", "wf"):
+        assert fwd(desc(**few), ws=FWD[n]) == ALIAS, n
+    for o in ("dq", "dk", "dv", "dg", "dw0"):
+        for n in ("q", "k", "v", "g", "w0", "lens", "dz", "dwf"):
+            assert bwd(desc(), **{o: BWD[n]}) == ALIAS, (o, n)
+    for o, p in (("dq", "dk"), ("dk", "dv"), ("dq", "dg"), ("dg", "dw0"), ("dv", "dw0")):
+        assert bwd(desc(), **{o: BWD[p]}) == ALIAS, (o, p)
+    for n in ("q", "k", "v", "g", "lens", "z"):
+        assert dec(desc(), w=DEC[n]) == ALIAS, n
+    assert dec(desc(), z=DEC["q"]) == ALIAS
+
+
+def test_gradients_as_slices_of_one_buffer():
+    """dq, dk, dv as [B, T, 3, H, d] slices: ranges that interleave without sharing an element."""
+    H, T, d = 4, 64, 64
+    s = S(T * 3 * H * d, d, 3 * H * d)
+    args = dict(Hkv=H, dq=s, dk=s, dv=s)
+    base = 40 * GB
+    assert bwd(desc(**args), dq=base, dk=base + 2 * H * d, dv=base + 4 * H * d) == OK
+    assert bwd(desc(**args), dq=base, dk=base + 2 * H * d - 16, dv=base + 4 * H * d) == ALIAS
+    assert bwd(desc(**args), dq=base, dk=base + 2 * H * d, dv=base + 4 * H * d + 16) == ALIAS  # into the next row
+    # [B, 3, H, T, d]
+    s = S(3 * H * T * d, T * d, d)
+    n = 2 * H * T * d
+    args = dict(Hkv=H, dq=s, dk=s, dv=s)
+    assert bwd(desc(**args), dq=base, dk=base + n, dv=base + 2 * n) == OK
+    assert bwd(desc(**args), dq=base, dk=base + n - 128, dv=base + 2 * n) == ALIAS
+
+
+def test_rope_refusals():
+    ok = desc()
+    assert dec(ok, rope=rope()) == OK
+    for kw in (dict(rot=63), dict(rot=-2), dict(rot=66), dict(scale=float("nan"))):
+        assert dec(ok, rope=rope(**kw)) == SHAPE and rot(rdesc(), rope(**kw)) == SHAPE, kw
+    for kw in (dict(sb=-1), dict(st=-1)):
+        assert dec(ok, rope=rope(**kw)) == STRIDE and rot(rdesc(), rope(**kw)) == STRIDE, kw
+    for kw in (dict(inter=2), dict(reserved=1)):
+        assert dec(ok, rope=rope(**kw)) == FLAGS and rot(rdesc(), rope(**kw)) == FLAGS, kw
+    assert dec(ok, rope=rope(freqs=None)) == NULL
+    assert dec(ok, rope=rope(freqs=None, rot=0)) == OK
+    assert dec(ok, rope=rope(pos=None, off=7)) == OK
+    assert dec(ok, rope=rope(pos=20 * GB + 4)) == ALIGN and dec(ok, rope=rope(freqs=21 * GB + 4)) == ALIGN
+    assert dec(ok, rope=rope(), w=20 * GB) == ALIAS and dec(ok, rope=rope(), z=21 * GB) == ALIAS
+
+
+def test_rotary_refusals():
+    r = rope()
+    assert rot(rdesc(), r) == OK and rot(None, r) == NULL and rot(rdesc(), None) == NULL
+    assert rot(rdesc(d=100), r) == OK and rot(rdesc(flags=1), r) == OK
+    for kw in (dict(B=-1), dict(d=0), dict(T=-3), dict(Hkv=-1)):
+        assert rot(rdesc(**kw), r) == SHAPE, kw
+    assert rot(rdesc(dtype=2), r) == DTYPE and rot(rdesc(flags=2), r) == FLAGS and rot(rdesc(reserved=1), r) == FLAGS
+    for n in ("q", "k", "qo", "ko"):
+        assert rot(rdesc(), r, **{n: None}) == NULL
+        assert rot(rdesc(), r, **{n: 9 * GB + 1}) == ALIGN
+    assert rot(rdesc(Hkv=0), r, k=None, ko=None) == OK
+    assert rot(rdesc(B=0), r, q=None, k=None, qo=None, ko=None) == OK
+    assert rot(rdesc(qo=S(0, 64, 64 * 4)), r) == STRIDE and rot(rdesc(q=S(0, 0, 0)), r) == OK
+    # in place, and not quite
+    assert rot(rdesc(), r, qo=GB, ko=2 * GB) == OK
+    assert rot(rdesc(), r, qo=GB) == OK
+    assert rot(rdesc(), r, qo=GB + 128) == ALIAS
+    assert rot(rdesc(qo=S(64, 2 * 64 * 64, 2 * 64)), r, qo=GB) == ALIAS    # another layout over q
+    assert rot(rdesc(), r, qo=2 * GB) == ALIAS and rot(rdesc(), r, ko=GB) == ALIAS and rot(rdesc(), r, ko=3 * GB) == ALIAS
+    assert rot(rdesc(Hkv=4), r, k=GB, qo=GB, ko=GB) == ALIAS               # q and k the same tensor, both in place
+    # q and k in place within one [B, T, 3, H, d] buffer
+    s = S(64 * 3 * 4 * 64, 64, 3 * 4 * 64)
+    packed = rdesc(Hkv=4, q=s, k=s, qo=s, ko=s)
+    assert rot(packed, r, q=GB, k=GB + 2 * 4 * 64, qo=GB, ko=GB + 2 * 4 * 64) == OK
+    assert rot(packed, r, q=GB, k=GB + 4 * 64, qo=GB, ko=GB + 4 * 64) == ALIAS
+
+
+# ---- the Python binding ----------------------------------------------------------
+
+torch = pytest.importorskip("torch")
+
+
+def test_python_refusals():
+    q, k, g = torch.zeros(2, 4, 8, 16), torch.zeros(2, 2, 8, 16), torch.zeros(4)
+    f = ttt.rotary_freqs(16)[0]
+    with pytest.raises(ValueError, match="on the GPU"):
+        ttt.linear_attn_fwd(q, k, k, g)
+    with pytest.raises(ValueError, match="on the GPU"):
+        ttt.rotary(q, k, 0, f)
+    with pytest.raises(ValueError, match="dtype"):
+        ttt.linear_attn_fwd(q, k.bfloat16(), k, g)
+    with pytest.raises(ValueError, match="share"):
+        ttt.linear_attn_fwd(q, k[:, :1].expand(2, 3, 8, 16), k[:, :1].expand(2, 3, 8, 16), g)
+    with pytest.raises(ValueError, match="expected"):
+        ttt.linear_attn_fwd(q, k[:, :, :7], k, g)
+    with pytest.raises(ValueError, match="log_decay"):
+        ttt.linear_attn_fwd(q, k, k, g[:3])
+    with pytest.raises(TypeError, match="log_decay"):
+        ttt.linear_attn_fwd(q, k, k, g.double())
+    with pytest.raises(ValueError, match="lens"):
+        ttt.linear_attn_fwd(q, k, k, g, lens=torch.zeros(3, dtype=torch.int32))
+    with pytest.raises(TypeError, match="lens"):
+        ttt.linear_attn_fwd(q, k, k, g, lens=torch.zeros(2, dtype=torch.int64))
+    with pytest.raises(ValueError, match="w0"):
+        ttt.linear_attn_fwd(q, k, k, g, w0=torch.zeros(2, 16, 16))
+    with pytest.raises(ValueError, match=r"\[B, H, T, d\]"):
+        ttt.linear_attn_fwd(q[0], k, k, g)
+    with pytest.raises(ValueError, match="expected"):
+        ttt.rotary(q, k[:, :, :7], 0, f)
+
+
+def test_rotary_freqs():
+    f, s = ttt.rotary_freqs(8)
+    assert f.dtype == torch.float64 and s == 1.0 and torch.allclose(f, 10000.0 ** -(torch.arange(4).double() / 4))
+    f2, s = ttt.rotary_freqs(8, scaling="linear", factor=4.0)
+    assert s == 1.0 and torch.allclose(f2, f / 4)
+    # the base raised: the fastest pair as it was, the slowest slowed by the factor
+    f3, s = ttt.rotary_freqs(8, scaling="ntk", factor=4.0)
+    assert s == 1.0 and f3[0] == 1.0 and torch.allclose(f3[-1], f[-1] / 4)
+    f4, s = ttt.rotary_freqs(64, scaling="yarn", factor=4.0, original=2048)
+    g4 = ttt.rotary_freqs(64)[0]
+    assert abs(s - (0.1 * torch.log(torch.tensor(4.0)).item() + 1)) < 1e-6
+    assert f4[0] == g4[0] and f4[-1] == g4[-1] / 4 and ((f4 <= g4) & (f4 >= g4 / 4)).all()
+    assert ttt.rotary_freqs(0)[0].numel() == 0 and ttt.rotary_freqs(2, scaling="ntk", factor=2.0)[0].tolist() == [1.0]
+    for bad in (dict(rot=7), dict(rot=-2), dict(rot=8, scaling="cubic"), dict(rot=8, factor=2.0),
+                dict(rot=8, scaling="linear", factor=0.5), dict(rot=8, scaling="yarn", factor=2.0, beta_fast=1.0)):
+        with pytest.raises(ValueError):
+            ttt.rotary_freqs(**bad)
