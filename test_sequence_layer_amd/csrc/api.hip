@@ -1378,13 +1378,13 @@ ttt_status check_attn_desc(const ttt_linear_attn_desc* d, int64_t* chains) {
 
 struct AttnPlan {
   int nseg, seglen;
-  int64_t loc, gloc, dgpart, dk, dv, bytes;  // workspace offsets
+  int64_t loc, dgpart, dk, dv, bytes;  // workspace offsets
 };
 
 AttnPlan attn_plan(const ttt_linear_attn_desc* d, bool backward) {
   AttnPlan p;
   const int64_t chains = static_cast<int64_t>(d->B) * d->H, dd = static_cast<int64_t>(d->d) * d->d * 4;
-  const int n = ttt::attn_segments(chains, d->T, d->d);
+  const int n = ttt::attn_segments(chains, d->T, d->d, backward);
   const int c = ttt::kAttnChunk;
   p.seglen = ((d->T + n - 1) / n + c - 1) / c * c;
   if (p.seglen < c) p.seglen = c;
@@ -1396,8 +1396,7 @@ AttnPlan attn_plan(const ttt_linear_attn_desc* d, bool backward) {
     return o;
   };
   const bool split = p.nseg > 1;
-  p.loc = take(split ? chains * p.nseg * dd : 0);
-  p.gloc = take(split && backward ? chains * p.nseg * 2 * dd : 0);
+  p.loc = take(split ? chains * p.nseg * dd * (backward ? 3 : 1) : 0);
   p.dgpart = take(split && backward ? chains * p.nseg * 8 : 0);
   const int64_t part = backward && d->H > d->Hkv ? chains * d->T * d->d * 4 : 0;
   p.dk = take(part);
@@ -1523,8 +1522,8 @@ ttt_status validate_attn_bwd(const ttt_linear_attn_desc* d, const void* Q, const
   const View dk = view(dK, d->B, d->Hkv, d->T, d->d, d->dk, d->out_dtype);
   const View dv = view(dV, d->B, d->Hkv, d->T, d->d, d->dv, d->out_dtype);
   const AttnPlan plan = attn_plan(d, true);
-  if (chains * plan.nseg > INT_MAX) return TTT_ERR_SHAPE;
-  if (chains * d->T * (d->d / 4) / 256 > INT_MAX - 1) return TTT_ERR_SHAPE;
+  if (3 * chains * plan.nseg > INT_MAX) return TTT_ERR_SHAPE;                    // workgroups of the walks
+  if (2 * chains * d->T * (d->d / 4) / 256 > INT_MAX - 1) return TTT_ERR_SHAPE;  // and of the sums
   if (chains == 0) return TTT_OK;
   if (!g || !dg || !dW0) return TTT_ERR_NULL;
   if (!empty(dq) && (!dQ || !dK || !dV)) return TTT_ERR_NULL;
@@ -1645,14 +1644,14 @@ ttt_status ttt_linear_attn_fwd(const ttt_linear_attn_desc* desc, const void* Q, 
   a.B = desc->B; a.H = desc->H; a.T = desc->T; a.d = desc->d;
   a.group = desc->H / desc->Hkv;
   a.nseg = plan.nseg; a.seglen = plan.seglen;
-  a.x_dtype = desc->in_dtype; a.in_dtype = desc->in_dtype; a.out_dtype = desc->out_dtype;
-  a.X = Q; a.Y = K; a.V = V;
-  a.xs = strides(v.q); a.ys = strides(v.k); a.vs = strides(v.v); a.os = strides(v.z);
+  a.in_dtype = desc->in_dtype; a.out_dtype = desc->out_dtype;
+  a.Q = Q; a.K = K; a.V = V;
+  a.qs = strides(v.q); a.ks = strides(v.k); a.vs = strides(v.v); a.zs = strides(v.z);
   a.log_decay = log_decay; a.scale = desc->scale;
-  a.S0 = W0; a.s0_bstride = desc->w0_batch_stride; a.transposed = false;
+  a.W0 = W0; a.w0_bstride = desc->w0_batch_stride;
   a.lens = lens;
   a.loc = static_cast<float*>(workspace);
-  a.O = Z; a.S_final = W_final;
+  a.Z = Z; a.W_final = W_final;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if (plan.nseg > 1) {
     const hipError_t e = ttt::launch_attn_states(a, s);
@@ -1684,20 +1683,6 @@ ttt_status ttt_linear_attn_bwd(const ttt_linear_attn_desc* desc, const void* Q, 
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int group = desc->H / desc->Hkv;
 
-  ttt::AttnArgs a;  // dQ: the forward walk of dZ over V, K
-  a.B = desc->B; a.H = desc->H; a.T = desc->T; a.d = desc->d;
-  a.group = group;
-  a.nseg = plan.nseg; a.seglen = plan.seglen;
-  a.x_dtype = desc->out_dtype; a.in_dtype = desc->in_dtype; a.out_dtype = desc->out_dtype;
-  a.X = dZ; a.Y = V; a.V = K;
-  a.xs = strides(v.z); a.ys = strides(v.v); a.vs = strides(v.k);
-  a.os = strides(view(dQ, desc->B, desc->H, desc->T, desc->d, desc->dq, desc->out_dtype));
-  a.log_decay = log_decay; a.scale = desc->scale;
-  a.S0 = W0; a.s0_bstride = desc->w0_batch_stride; a.transposed = true;
-  a.lens = lens;
-  a.loc = reinterpret_cast<float*>(ws + plan.loc);
-  a.O = dQ; a.S_final = nullptr;
-
   ttt::AttnBwdArgs r;
   r.B = desc->B; r.H = desc->H; r.T = desc->T; r.d = desc->d;
   r.group = group;
@@ -1708,39 +1693,33 @@ ttt_status ttt_linear_attn_bwd(const ttt_linear_attn_desc* desc, const void* Q, 
   r.log_decay = log_decay; r.scale = desc->scale;
   r.W0 = W0; r.w0_bstride = desc->w0_batch_stride;
   r.lens = lens; r.dWf = dW_final;
-  r.gloc = reinterpret_cast<float*>(ws + plan.gloc);
+  r.loc = reinterpret_cast<float*>(ws + plan.loc);
   r.dgpart = reinterpret_cast<double*>(ws + plan.dgpart);
   r.parts = group > 1;
   const ttt::Strides3 dks = strides(view(dK, desc->B, desc->Hkv, desc->T, desc->d, desc->dk, desc->out_dtype));
   const ttt::Strides3 dvs = strides(view(dV, desc->B, desc->Hkv, desc->T, desc->d, desc->dv, desc->out_dtype));
   const int64_t hs = static_cast<int64_t>(desc->T) * desc->d;
   const ttt::Strides3 packed{hs * desc->H, hs, desc->d};
+  r.dQ = dQ;
   r.dK = r.parts ? ws + plan.dk : dK;
   r.dV = r.parts ? ws + plan.dv : dV;
+  r.dqs = strides(view(dQ, desc->B, desc->H, desc->T, desc->d, desc->dq, desc->out_dtype));
   r.dks = r.parts ? packed : dks;
   r.dvs = r.parts ? packed : dvs;
   r.dg = dlog_decay; r.dW0 = dW0;
-
-  if (plan.nseg > 1) {
-    ttt::AttnArgs p = a;  // the states themselves: V K^T
-    p.Y = K; p.V = V;
-    p.ys = strides(v.k); p.vs = strides(v.v);
-    if (ttt::launch_attn_states(p, s) != hipSuccess) return TTT_ERR_HIP;
-    if (ttt::launch_attn_bwd_states(r, s) != hipSuccess) return TTT_ERR_HIP;
-  }
-  if (ttt::launch_attn_fwd(a, s) != hipSuccess) return TTT_ERR_HIP;
+  if (plan.nseg > 1 && ttt::launch_attn_bwd_states(r, s) != hipSuccess) return TTT_ERR_HIP;
   if (ttt::launch_attn_bwd(r, s) != hipSuccess) return TTT_ERR_HIP;
-  if (plan.nseg > 1 && ttt::launch_attn_bwd_dg(r, s) != hipSuccess) return TTT_ERR_HIP;
-  if (r.parts && desc->T > 0) {
-    ttt::AttnSumArgs m{desc->B, desc->Hkv, desc->T, desc->d, group, desc->out_dtype,
-                       reinterpret_cast<const float*>(ws + plan.dk), dK, dks};
-    if (ttt::launch_attn_sum(m, s) != hipSuccess) return TTT_ERR_HIP;
-    m.parts = reinterpret_cast<const float*>(ws + plan.dv);
-    m.out = dV;
-    m.os = dvs;
-    if (ttt::launch_attn_sum(m, s) != hipSuccess) return TTT_ERR_HIP;
-  }
-  return TTT_OK;
+
+  ttt::AttnSumArgs m;
+  m.B = desc->B; m.Hkv = desc->Hkv; m.T = desc->T; m.d = desc->d;
+  m.group = group; m.nseg = plan.nseg; m.out_dtype = desc->out_dtype;
+  m.dk_parts = r.parts ? static_cast<const float*>(r.dK) : nullptr;
+  m.dv_parts = r.parts ? static_cast<const float*>(r.dV) : nullptr;
+  m.dK = dK; m.dV = dV;
+  m.dks = dks; m.dvs = dvs;
+  m.dgpart = plan.nseg > 1 ? r.dgpart : nullptr;
+  m.dg = dlog_decay;
+  return hip_status(ttt::launch_attn_sum(m, s));
 }
 
 ttt_status ttt_linear_attn_decode_validate(const ttt_linear_attn_desc* desc, const void* Q, const void* K,

@@ -20,31 +20,28 @@ struct Rope {
   float scale;
 };
 
-// One recurrence over the tokens of every (sequence, head):
-//   S_t = lambda S_{t-1} + V_t Y_t^T,   O_t = scale S_t X_t      (S: d x d, row = element of V)
-// The forward has X, Y, V = Q, K, V; dQ has X, Y, V = dZ, V, K (S is then W^T).
+// Forward: Z and the last state.
 struct AttnArgs {
   int B, H, T, d;
   int group;             // query heads per key / value head
   int nseg, seglen;      // segments per sequence, tokens per segment (a multiple of the chunk)
-  int x_dtype, in_dtype, out_dtype;
-  const void* X;         // by query head
-  const void* Y;         // by key / value head
-  const void* V;         // by key / value head
-  Strides3 xs, ys, vs, os;
+  int in_dtype, out_dtype;
+  const void* Q;         // by query head
+  const void* K;         // by key / value head
+  const void* V;
+  Strides3 qs, ks, vs, zs;
   const float* log_decay;  // [H]
   float scale;
-  const float* S0;       // initial state or nullptr (zero)
-  int64_t s0_bstride;
-  bool transposed;       // the walk reads S0 and loc as S^T
+  const float* W0;       // initial state or nullptr (zero)
+  int64_t w0_bstride;
   const int32_t* lens;   // [B] or nullptr (every sequence has T tokens)
-  float* loc;            // [B * H, nseg, d, d] (nseg > 1): end states of segments 0 .. nseg-2, then S0
-  void* O;
-  float* S_final;        // [B, H, d, d] or nullptr
+  float* loc;            // [B * H, nseg, d, d] (nseg > 1): end states of segments 0 .. nseg-2, then W0
+  void* Z;
+  float* W_final;        // [B, H, d, d]
 };
 
-// The reverse recurrence of the backward: with G_t the gradient of the state after token t,
-//   G_{t-1} = lambda (G_t + scale dZ_t Q_t^T) ...,  dV_t = G_t K_t,  dK_t = G_t^T V_t
+// Backward: three walks for each (sequence, head) segment, dQ from the first token to
+// the last, dK and dV from the last to the first (their segments are counted from there).
 struct AttnBwdArgs {
   int B, H, T, d;
   int group;
@@ -61,22 +58,29 @@ struct AttnBwdArgs {
   int64_t w0_bstride;
   const int32_t* lens;
   const float* dWf;      // [B, H, d, d] or nullptr
-  float* gloc;           // [B * H, nseg, 2, d, d]: each segment's G and dG/dlog_decay from zero (nseg > 1)
+  float* loc;            // [B * H, nseg, 3, d, d] (nseg > 1): end values of segments 0 .. nseg-2 of W^T and
+                         // dW^T/dlog_decay, and of G^T
   double* dgpart;        // [B * H, nseg] (nseg > 1)
+  void* dQ;
   void* dK;              // by key / value head, or fp32 [B, H, T, d] in the workspace where group > 1
   void* dV;
-  Strides3 dks, dvs;
+  Strides3 dqs, dks, dvs;
   bool parts;            // dK, dV go to the workspace, one fp32 part per query head
   float* dg;             // [B, H]
   float* dW0;            // [B, H, d, d]
 };
 
-// dK, dV of a shared head: the sum of its query heads' parts.
+// What the walks leave in parts: dK, dV of shared heads (the sum over their query heads) and the decay's
+// gradient (the sum over segments).
 struct AttnSumArgs {
-  int B, Hkv, T, d, group, out_dtype;
-  const float* parts;    // [B, Hkv * group, T, d]
-  void* out;
-  Strides3 os;
+  int B, Hkv, T, d, group, nseg, out_dtype;
+  const float* dk_parts;  // [B, Hkv * group, T, d], or nullptr
+  const float* dv_parts;
+  void* dK;
+  void* dV;
+  Strides3 dks, dvs;
+  const double* dgpart;   // [B * Hkv * group, nseg], or nullptr
+  float* dg;
 };
 
 // One or a few tokens, the state carried in place.
@@ -113,12 +117,11 @@ struct RotaryArgs {
 constexpr int kAttnChunk = 32;  // tokens per chunk of the chunked form
 
 bool attn_supported(int d);
-int attn_segments(int64_t chains, int T, int d);
+int attn_segments(int64_t chains, int T, int d, bool backward);
 hipError_t launch_attn_states(const AttnArgs& a, hipStream_t s);
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t s);
 hipError_t launch_attn_bwd_states(const AttnBwdArgs& a, hipStream_t s);
 hipError_t launch_attn_bwd(const AttnBwdArgs& a, hipStream_t s);
-hipError_t launch_attn_bwd_dg(const AttnBwdArgs& a, hipStream_t s);
 hipError_t launch_attn_sum(const AttnSumArgs& a, hipStream_t s);
 hipError_t launch_attn_decode(const AttnDecodeArgs& a, hipStream_t s);
 hipError_t launch_rotary(const RotaryArgs& a, hipStream_t s);

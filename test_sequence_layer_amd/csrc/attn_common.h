@@ -1,23 +1,22 @@
-// Device pieces shared by the linear-attention kernels (forward and backward):
-// matrix products on 16 x 16 blocks in bf16 or fp32, the split of fp32 values
-// into bf16 parts, chunk loads, and decays.
+// Device pieces shared by the linear-attention kernels: matrix products on 16 x 16
+// blocks, operands in bf16 parts, chunk loads, and decays.
 //
 // Blocks.  Every product is a sum of 16 x 16 x 16 block products.  A wave holds
 // a block operand as a Frag: lane l (li = l % 16, g = l / 16) holds the four
 // values of contraction indices 4g .. 4g + 3 at row (A) or column (B) li.  An
 // accumulator block X (lane holds X[4g + r][li]) is therefore directly the
 // A operand of X^T or the B operand of X: states and scores go back into the
-// matrix cores from registers.
-//   bf16: v_mfma_f32_16x16x32_bf16 takes two Frags at once (blocks p and p + 1 of
-//         the contraction); products of bf16 values are exact, sums are fp32.
-//   fp32: four v_mfma_f32_16x16x4_f32, the r-th on contraction indices 4g + r.
+// matrix cores from registers.  v_mfma_f32_16x16x32_bf16 takes two Frags of either
+// operand at once; products of bf16 values are exact and sums are fp32.
 //
-// Splits.  An fp32 operand (state, score, decayed value) of a bf16 product is
-// the sum of NP bf16 parts, each the rounding of what the parts before it leave:
-// the error is 2^-8 (half a step of bf16 relative to the value) to the power NP,
-// so 2^-24 with three parts, an fp32 rounding, and 2^-16 with two, which is
-// 1/256 of what rounding an output to bf16 costs.  Kernels with bf16 outputs use
-// two parts where only an output depends on them; states always get three.
+// Parts.  An fp32 operand (an fp32 input, the state, a score, a decayed value) is
+// the sum of bf16 parts, each the rounding of what the parts before it leave, so
+// that n parts are off by at most 2^-8n: half a bf16 step, n times.  A product of
+// level LV takes the part pairs (p, q) with p + q < LV: level 3 is an fp32 product
+// (2^-24), level 2 is off by 2^-16, 1/256 of what rounding the output to bf16
+// costs.  States and fp32 outputs are level 3, products that only a bf16 output
+// depends on are level 2.  The fp32 matrix instruction (v_mfma_f32_16x16x4_f32)
+// does the same at 1/16 of the bf16 rate: six part pairs take 3/8 of its time.
 #pragma once
 
 #include "args_attn.h"
@@ -28,161 +27,174 @@ namespace ttt {
 namespace attn {
 
 using mfma::bf16x4;
-using mfma::bf16x8;
 using mfma::float2v;
 using mfma::float4v;
 using mfma::u32x2;
 using mfma::u32x4;
 
 constexpr int C = kAttnChunk;
+typedef bf16x4 Frag;
 
-template <typename CT>
-struct Ops;
+// parts of an input of type T, and the level of products that only an output of type T depends on
+template <typename T>
+__host__ __device__ constexpr int parts_of() { return sizeof(T) == 2 ? 1 : 3; }
+template <typename T>
+__host__ __device__ constexpr int level_of() { return sizeof(T) == 2 ? 2 : 3; }
 
-template <>
-struct Ops<uint16_t> {
-  typedef bf16x4 Frag;
-  static constexpr bool kSplit = true;
-  template <int D>
-  static constexpr int row_stride() { return D + 8; }
+__device__ __forceinline__ float4v widen(Frag x) {
+  const u32x2 w = __builtin_bit_cast(u32x2, x);
+  return float4v{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xffff0000u), __uint_as_float(w[1] << 16),
+                 __uint_as_float(w[1] & 0xffff0000u)};
+}
+
+// x = p[0] + ... + p[N-1]
+template <int N>
+__device__ __forceinline__ void split(float4v x, Frag p[N]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const mfma::bf16x2 h0 = __builtin_convertvector(float2v{x[0], x[1]}, mfma::bf16x2);
+    const mfma::bf16x2 h1 = __builtin_convertvector(float2v{x[2], x[3]}, mfma::bf16x2);
+    const u32x2 w = {__builtin_bit_cast(uint32_t, h0), __builtin_bit_cast(uint32_t, h1)};
+    p[n] = __builtin_bit_cast(bf16x4, w);
+    if (n + 1 < N) x = x - widen(p[n]);
+  }
+}
+
+__device__ __forceinline__ Frag zero_frag() { return __builtin_bit_cast(bf16x4, u32x2{0u, 0u}); }
+__device__ __forceinline__ float4v mm2(Frag a0, Frag a1, Frag b0, Frag b1, float4v c) {
+  return mfma::mfma32(mfma::cat(a0, a1), mfma::cat(b0, b1), c);
+}
+
+// c += a . x over one contraction block: two part pairs per instruction
+template <int NA, int NX, int LV>
+__device__ __forceinline__ float4v dot1(const Frag a[NA], const Frag x[NX], float4v c) {
+  Frag l[8], r[8];
+  int n = 0;
+#pragma unroll
+  for (int p = 0; p < NA; ++p)
+#pragma unroll
+    for (int q = 0; q < NX; ++q)
+      if (p + q < LV) {
+        l[n] = a[p];
+        r[n] = x[q];
+        ++n;
+      }
+  if (n % 2) {
+    l[n] = r[n] = zero_frag();
+    ++n;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    if (i < n) c = mm2(l[i], l[i + 1], r[i], r[i + 1], c);
+  return c;
+}
+
+// c += a0 . x0 + a1 . x1, two contraction blocks
+template <int NA, int NX, int LV>
+__device__ __forceinline__ float4v dot2(const Frag a0[NA], const Frag a1[NA], const Frag x0[NX], const Frag x1[NX],
+                                        float4v c) {
+#pragma unroll
+  for (int p = 0; p < NA; ++p)
+#pragma unroll
+    for (int q = 0; q < NX; ++q)
+      if (p + q < LV) c = mm2(a0[p], a1[p], x0[q], x1[q], c);
+  return c;
+}
+
+// One tensor's chunk in LDS: C rows of D elements, a plane for each part.
+template <int D, int N>
+struct Tile {
+  static constexpr int RS = D + 8;  // row stride: the rows of a Frag in different banks
+  static constexpr int kPlane = C * RS;
+  static constexpr int kSize = N * kPlane;
   // X[row0 + li][16 blk + 4g ..]
-  template <int RS>
-  __device__ static __forceinline__ Frag rows(const uint16_t* tile, int row0, int blk, int li, int g) {
-    return *reinterpret_cast<const bf16x4*>(tile + (row0 + li) * RS + 16 * blk + 4 * g);
+  __device__ static __forceinline__ void rows(const uint16_t* t, int row0, int blk, int li, int g, Frag f[N]) {
+#pragma unroll
+    for (int p = 0; p < N; ++p)
+      f[p] = *reinterpret_cast<const bf16x4*>(t + p * kPlane + (row0 + li) * RS + 16 * blk + 4 * g);
   }
   // X[row0 + 4g ..][col0 + li]
-  template <int RS>
-  __device__ static __forceinline__ Frag cols(const uint16_t* tile, int row0, int col0, int li, int g) {
-    return mfma::read_cols<RS>(tile, row0, col0, li, g);
-  }
-  __device__ static __forceinline__ Frag zero() { return __builtin_bit_cast(bf16x4, u32x2{0u, 0u}); }
-  __device__ static __forceinline__ float4v widen(Frag x) {
-    const u32x2 w = __builtin_bit_cast(u32x2, x);
-    return float4v{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xffff0000u), __uint_as_float(w[1] << 16),
-                   __uint_as_float(w[1] & 0xffff0000u)};
-  }
-  __device__ static __forceinline__ float4v mm2(Frag a0, Frag a1, Frag b0, Frag b1, float4v c) {
-    return mfma::mfma32(mfma::cat(a0, a1), mfma::cat(b0, b1), c);
-  }
-  // x = p[0] + p[1] (+ p[2])
-  template <int NP>
-  __device__ static __forceinline__ void split(float4v x, Frag p[NP]) {
+  __device__ static __forceinline__ void cols(const uint16_t* t, int row0, int col0, int li, int g, Frag f[N]) {
 #pragma unroll
-    for (int n = 0; n < NP; ++n) {
-      const mfma::bf16x2 h0 = __builtin_convertvector(float2v{x[0], x[1]}, mfma::bf16x2);
-      const mfma::bf16x2 h1 = __builtin_convertvector(float2v{x[2], x[3]}, mfma::bf16x2);
-      const u32x2 w = {__builtin_bit_cast(uint32_t, h0), __builtin_bit_cast(uint32_t, h1)};
-      p[n] = __builtin_bit_cast(bf16x4, w);
-      if (n + 1 < NP) x = x - widen(p[n]);
-    }
+    for (int p = 0; p < N; ++p) f[p] = mfma::read_cols<RS>(t + p * kPlane, row0, col0, li, g);
+  }
+  __device__ static __forceinline__ float4v sum(const Frag f[N]) {
+    float4v x = widen(f[N - 1]);
+#pragma unroll
+    for (int p = N - 2; p >= 0; --p) x = widen(f[p]) + x;
+    return x;
   }
 };
 
-template <>
-struct Ops<float> {
-  typedef float4v Frag;
-  static constexpr bool kSplit = false;
-  template <int D>
-  static constexpr int row_stride() { return D + 4; }
-  template <int RS>
-  __device__ static __forceinline__ Frag rows(const float* tile, int row0, int blk, int li, int g) {
-    return *reinterpret_cast<const float4v*>(tile + (row0 + li) * RS + 16 * blk + 4 * g);
-  }
-  template <int RS>
-  __device__ static __forceinline__ Frag cols(const float* tile, int row0, int col0, int li, int g) {
-    const float* p = tile + (row0 + 4 * g) * RS + col0 + li;
-    return float4v{p[0], p[RS], p[2 * RS], p[3 * RS]};
-  }
-  __device__ static __forceinline__ Frag zero() { return mfma::zero4v(); }
-  __device__ static __forceinline__ float4v widen(Frag x) { return x; }
-  __device__ static __forceinline__ float4v mm1(Frag a, Frag b, float4v c) {
+// A 16 x 16 block of A B^T: lane holds [4g + r of A's rows][li of B's rows].
+template <int D, int NA, int NX, int LV>
+__device__ __forceinline__ float4v rows_dot(const uint16_t* a, int ra, const uint16_t* x, int rx, int li, int g) {
+  constexpr int NB = D / 16;
+  float4v c = mfma::zero4v();
+  if constexpr (NB == 1) {
+    Frag f[NA], h[NX];
+    Tile<D, NA>::rows(a, ra, 0, li, g, f);
+    Tile<D, NX>::rows(x, rx, 0, li, g, h);
+    c = dot1<NA, NX, LV>(f, h, c);
+  } else {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], b[r], c, 0, 0, 0);
-    return c;
-  }
-  __device__ static __forceinline__ float4v mm2(Frag a0, Frag a1, Frag b0, Frag b1, float4v c) {
-    return mm1(a1, b1, mm1(a0, b0, c));
-  }
-  template <int NP>
-  __device__ static __forceinline__ void split(float4v x, Frag p[NP]) {
-    static_assert(NP == 1, "fp32 products take fp32 operands whole");
-    p[0] = x;
-  }
-};
-
-// Parts of an fp32 operand: where only an output of type OT depends on it, and of state updates.
-template <typename CT, typename OT>
-__host__ __device__ constexpr int out_parts() { return Ops<CT>::kSplit ? (sizeof(OT) == 2 ? 2 : 3) : 1; }
-template <typename CT>
-__host__ __device__ constexpr int state_parts() { return Ops<CT>::kSplit ? 3 : 1; }
-
-// c += sum over NB contraction blocks of a[b] . x[b]
-template <typename CT, int NB>
-__device__ __forceinline__ float4v dot(const typename Ops<CT>::Frag a[NB], const typename Ops<CT>::Frag x[NB],
-                                       float4v c) {
-  typedef Ops<CT> O;
-#pragma unroll
-  for (int b = 0; b + 1 < NB; b += 2) c = O::mm2(a[b], a[b + 1], x[b], x[b + 1], c);
-  if constexpr (NB % 2 == 1) {
-    if constexpr (O::kSplit) {
-      c = O::mm2(a[NB - 1], O::zero(), x[NB - 1], O::zero(), c);
-    } else {
-      c = O::mm1(a[NB - 1], x[NB - 1], c);
+    for (int k = 0; k < NB; k += 2) {
+      Frag f0[NA], f1[NA], h0[NX], h1[NX];
+      Tile<D, NA>::rows(a, ra, k, li, g, f0);
+      Tile<D, NA>::rows(a, ra, k + 1, li, g, f1);
+      Tile<D, NX>::rows(x, rx, k, li, g, h0);
+      Tile<D, NX>::rows(x, rx, k + 1, li, g, h1);
+      c = dot2<NA, NX, LV>(f0, f1, h0, h1, c);
     }
   }
   return c;
 }
 
-// c += a . (x[0] + ... + x[NP-1]) over one contraction block: two parts per instruction
-template <typename CT, int NP>
-__device__ __forceinline__ float4v dot_parts(typename Ops<CT>::Frag a, const typename Ops<CT>::Frag x[NP], float4v c) {
-  typedef Ops<CT> O;
-  if constexpr (NP == 1) {
-    const typename O::Frag av[1] = {a};
-    return dot<CT, 1>(av, x, c);
-  } else {
-#pragma unroll
-    for (int n = 0; n < NP; n += 2) c = O::mm2(a, a, x[n], n + 1 < NP ? x[n + 1] : O::zero(), c);
-    return c;
-  }
-}
-
 // Eight elements of one row of a chunk, from global memory to LDS.
 template <typename T>
 struct Slab {
-  u32x4 r[sizeof(T) / 2];
+  static constexpr int kWords = sizeof(T) / 2;
+  u32x4 r[kWords];
   __device__ __forceinline__ void load(const T* p, bool ok) {
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) {
+    for (int i = 0; i < kWords; ++i) {
       r[i] = u32x4{0u, 0u, 0u, 0u};
-      if (ok) r[i] = mfma::ld_stream(reinterpret_cast<const u32x4*>(p) + i);
+      if (ok) r[i] = reinterpret_cast<const u32x4*>(p)[i];
     }
   }
-  __device__ __forceinline__ void put(T* p) const {
+  // to the planes of a Tile<D, parts_of<T>()>
+  template <int PLANE>
+  __device__ __forceinline__ void put(uint16_t* t) const {
+    if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<u32x4*>(t) = r[0];
+    } else {
+      Frag f[2][3];
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) reinterpret_cast<u32x4*>(p)[i] = r[i];
+      for (int i = 0; i < 2; ++i) split<3>(__builtin_bit_cast(float4v, r[i]), f[i]);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        const u32x2 lo = __builtin_bit_cast(u32x2, f[0][p]), hi = __builtin_bit_cast(u32x2, f[1][p]);
+        *reinterpret_cast<u32x4*>(t + p * PLANE) = u32x4{lo[0], lo[1], hi[0], hi[1]};
+      }
+    }
   }
 };
-__device__ __forceinline__ void put_slab(const Slab<uint16_t>& s, uint16_t* p) { s.put(p); }
-__device__ __forceinline__ void put_slab(const Slab<float>& s, float* p) { s.put(p); }
-__device__ __forceinline__ void put_slab(const Slab<uint16_t>& s, float* p) {  // widened on the way
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t w0 = s.r[0][2 * i], w1 = s.r[0][2 * i + 1];
-    *reinterpret_cast<float4v*>(p + 4 * i) =
-        float4v{__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u), __uint_as_float(w1 << 16),
-                __uint_as_float(w1 & 0xffff0000u)};
-  }
-}
 
-// lambda^n for n >= 0 (lambda^0 = 1 also where lambda = 0), and x lambda^n with
-// lambda^n taken as 1 + expm1(n log lambda): for a decay close to 1 the product
-// of thousands of chunks then keeps the accuracy that a rounded lambda^n loses.
+// lambda^n for n >= 0 (lambda^0 = 1 also where lambda = 0)
 __device__ __forceinline__ float powl(float g, int n) { return n == 0 ? 1.f : expf(g * static_cast<float>(n)); }
-__device__ __forceinline__ float powm1(float g, int n) { return n == 0 ? 0.f : expm1f(g * static_cast<float>(n)); }
-__device__ __forceinline__ float4v decayed(float4v x, float em1) {
+
+// x lambda^n as m x + a x.  Near 1 lambda^n is taken as 1 + expm1(n log lambda): a rounded lambda^n is off by
+// up to 2^-25 the same way in every chunk, which thousands of chunks add up.  Below 1/2 it is lambda^n itself.
+struct Decay {
+  float m, a;
+};
+__device__ __forceinline__ Decay decay(float g, int n) {
+  const float p = powl(g, n);
+  return p > 0.5f ? Decay{1.f, n == 0 ? 0.f : expm1f(g * static_cast<float>(n))} : Decay{0.f, p};
+}
+__device__ __forceinline__ float4v decayed(float4v x, Decay d) {
 #pragma unroll
-  for (int r = 0; r < 4; ++r) x[r] = fmaf(x[r], em1, x[r]);
+  for (int r = 0; r < 4; ++r) x[r] = fmaf(x[r], d.a, x[r] * d.m);
   return x;
 }
 

@@ -57,7 +57,10 @@ __global__ __launch_bounds__(4 * D) void ttt_attn_decode(AttnDecodeArgs a) {
   const int tid = threadIdx.x, i = tid >> 2, n = tid & 3;
   const int chain = blockIdx.x;
   const int b = chain / a.H, h = chain % a.H, hk = h / a.group;
-  const float em = expm1f(a.log_decay[h]);
+  // lambda x as m x + a x: near 1 as 1 + expm1(log lambda), so that thousands of tokens do not add up the
+  // rounding of lambda
+  const float lam = expf(a.log_decay[h]);
+  const float m = lam > 0.5f ? 1.f : 0.f, em = lam > 0.5f ? expm1f(a.log_decay[h]) : lam;
   int len = a.T;
   if (a.lens) len = max(0, min(a.lens[b], a.T));
   const InT* q = static_cast<const InT*>(a.Q) + b * a.qs.b + h * a.qs.h;
@@ -89,10 +92,10 @@ __global__ __launch_bounds__(4 * D) void ttt_attn_decode(AttnDecodeArgs a) {
         for (int c = 0; c < NB; ++c) {
           const float4 kc = *reinterpret_cast<const float4*>(&ks[t][16 * c + 4 * n]);
           const float4 qc = *reinterpret_cast<const float4*>(&qs[t][16 * c + 4 * n]);
-          w[c].x = fmaf(vi, kc.x, fmaf(w[c].x, em, w[c].x));
-          w[c].y = fmaf(vi, kc.y, fmaf(w[c].y, em, w[c].y));
-          w[c].z = fmaf(vi, kc.z, fmaf(w[c].z, em, w[c].z));
-          w[c].w = fmaf(vi, kc.w, fmaf(w[c].w, em, w[c].w));
+          w[c].x = fmaf(vi, kc.x, fmaf(w[c].x, em, w[c].x * m));
+          w[c].y = fmaf(vi, kc.y, fmaf(w[c].y, em, w[c].y * m));
+          w[c].z = fmaf(vi, kc.z, fmaf(w[c].z, em, w[c].z * m));
+          w[c].w = fmaf(vi, kc.w, fmaf(w[c].w, em, w[c].w * m));
           sum = fmaf(w[c].x, qc.x, sum);
           sum = fmaf(w[c].y, qc.y, sum);
           sum = fmaf(w[c].z, qc.z, sum);
