@@ -3,8 +3,11 @@ from __future__ import annotations
 
 import glob
 import os
+import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -30,9 +33,7 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.hip")))
 
 
-def build(verbose: bool = False, extra=()) -> str:
-    tmp = LIB + ".tmp"
-    cmd = [HIPCC, *FLAGS, *extra, "-o", tmp, *sources()]
+def _run(cmd, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -41,6 +42,22 @@ def build(verbose: bool = False, extra=()) -> str:
         raise RuntimeError(f"hipcc failed ({res.returncode}):\n{msg}")
     if verbose and msg.strip():
         print(msg, file=sys.stderr)
+
+
+def build(verbose: bool = False, extra=()) -> str:
+    """Compile every source to an object of its own (as many at a time as there
+    are CPUs, at most 8) and link them; the library is replaced at the end."""
+    tmp = LIB + ".tmp"
+    objects = tempfile.mkdtemp(prefix="libttt_")
+    try:
+        flags = [f for f in FLAGS if f != "-shared"]
+        outs = [os.path.join(objects, os.path.basename(src)[:-4] + ".o") for src in sources()]
+        with ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            list(pool.map(lambda p: _run([HIPCC, *flags, *extra, "-c", "-o", p[1], p[0]], verbose),
+                          zip(sources(), outs)))
+        _run([HIPCC, *FLAGS, *extra, "-o", tmp, *outs], verbose)
+    finally:
+        shutil.rmtree(objects, ignore_errors=True)
     os.replace(tmp, LIB)
     return LIB
 

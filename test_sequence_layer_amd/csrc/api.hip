@@ -1376,6 +1376,10 @@ ttt_status check_attn_desc(const ttt_linear_attn_desc* d, int64_t* chains) {
   return TTT_OK;
 }
 
+// From this many segments on a launch of its own carries their states on; below, each workgroup carries those
+// before its own (64 segments: 77 us against 99 for B1 H8 T32768, 6 segments: 52 us against 48 for B8 H12 T2048).
+constexpr int kCarry = 8;
+
 struct AttnPlan {
   int nseg, seglen;
   int64_t loc, dgpart, dk, dv, bytes;  // workspace offsets
@@ -1403,6 +1407,17 @@ AttnPlan attn_plan(const ttt_linear_attn_desc* d, bool backward) {
   p.dv = take(part);
   p.bytes = at;
   return p;
+}
+
+ttt::AttnCarryArgs make_carry_args(const ttt_linear_attn_desc* d, const AttnPlan& p, const float* g, float* loc,
+                                   bool backward) {
+  ttt::AttnCarryArgs a;
+  a.chains = static_cast<int64_t>(d->B) * d->H;
+  a.H = d->H; a.d = d->d;
+  a.nseg = p.nseg; a.seglen = p.seglen;
+  a.backward = backward;
+  a.log_decay = g; a.loc = loc;
+  return a;
 }
 
 ttt_status check_rope(const ttt_rope* r, int32_t d, int64_t B, int64_t T, Range* pos, Range* freqs) {
@@ -1653,10 +1668,10 @@ ttt_status ttt_linear_attn_fwd(const ttt_linear_attn_desc* desc, const void* Q, 
   a.loc = static_cast<float*>(workspace);
   a.Z = Z; a.W_final = W_final;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (plan.nseg > 1) {
-    const hipError_t e = ttt::launch_attn_states(a, s);
-    if (e != hipSuccess) return TTT_ERR_HIP;
-  }
+  a.carried = plan.nseg >= kCarry;
+  if (plan.nseg > 1 && ttt::launch_attn_states(a, s) != hipSuccess) return TTT_ERR_HIP;
+  if (a.carried && ttt::launch_attn_carry(make_carry_args(desc, plan, log_decay, a.loc, false), s) != hipSuccess)
+    return TTT_ERR_HIP;
   return hip_status(ttt::launch_attn_fwd(a, s));
 }
 
@@ -1707,7 +1722,10 @@ ttt_status ttt_linear_attn_bwd(const ttt_linear_attn_desc* desc, const void* Q, 
   r.dks = r.parts ? packed : dks;
   r.dvs = r.parts ? packed : dvs;
   r.dg = dlog_decay; r.dW0 = dW0;
+  r.carried = plan.nseg >= kCarry;
   if (plan.nseg > 1 && ttt::launch_attn_bwd_states(r, s) != hipSuccess) return TTT_ERR_HIP;
+  if (r.carried && ttt::launch_attn_carry(make_carry_args(desc, plan, log_decay, r.loc, true), s) != hipSuccess)
+    return TTT_ERR_HIP;
   if (ttt::launch_attn_bwd(r, s) != hipSuccess) return TTT_ERR_HIP;
 
   ttt::AttnSumArgs m;

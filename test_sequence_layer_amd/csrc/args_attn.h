@@ -25,6 +25,7 @@ struct AttnArgs {
   int B, H, T, d;
   int group;             // query heads per key / value head
   int nseg, seglen;      // segments per sequence, tokens per segment (a multiple of the chunk)
+  bool carried;          // loc holds the states themselves, else what each segment adds to them
   int in_dtype, out_dtype;
   const void* Q;         // by query head
   const void* K;         // by key / value head
@@ -46,6 +47,7 @@ struct AttnBwdArgs {
   int B, H, T, d;
   int group;
   int nseg, seglen;
+  bool carried;
   int in_dtype, out_dtype;
   const void* Q;
   const void* K;
@@ -68,6 +70,15 @@ struct AttnBwdArgs {
   bool parts;            // dK, dV go to the workspace, one fp32 part per query head
   float* dg;             // [B, H]
   float* dW0;            // [B, H, d, d]
+};
+
+// Segments' own states -> the states at their ends, in place: s_c <- lambda^seglen s_{c-1} + s_c.
+struct AttnCarryArgs {
+  int64_t chains;
+  int H, d, nseg, seglen;
+  bool backward;           // three matrices a segment: W^T, dW^T/dlog_decay, G^T; else one
+  const float* log_decay;
+  float* loc;
 };
 
 // What the walks leave in parts: dK, dV of shared heads (the sum over their query heads) and the decay's
@@ -119,6 +130,7 @@ constexpr int kAttnChunk = 32;  // tokens per chunk of the chunked form
 bool attn_supported(int d);
 int attn_segments(int64_t chains, int T, int d, bool backward);
 hipError_t launch_attn_states(const AttnArgs& a, hipStream_t s);
+hipError_t launch_attn_carry(const AttnCarryArgs& a, hipStream_t s);
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t s);
 hipError_t launch_attn_bwd_states(const AttnBwdArgs& a, hipStream_t s);
 hipError_t launch_attn_bwd(const AttnBwdArgs& a, hipStream_t s);

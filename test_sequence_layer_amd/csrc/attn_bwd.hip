@@ -5,14 +5,14 @@
 //   dQ_t = scale W_t^T dZ_t,   dK_t = G_t^T V_t,   dV_t = G_t K_t,   dW0 = lambda G_0
 // each of dQ, dK, dV is the forward's walk (attn_walk.h) over other tensors, dK and dV
 // from the last token to the first.  One launch holds the three walks of every
-// (sequence, head) or segment as workgroups of their own: three times the workgroups
-// of one fused reverse walk, each with one state (dQ's walk, with the decay's gradient,
-// two) instead of three, and no state kept in two layouts.  Measured on MI355X against
-// a fused dK, dV walk after a dQ launch: see the constants below.
+// (sequence, head) or segment as workgroups of their own: three times the workgroups of
+// one fused reverse walk, each with one state (dQ's walk, with the decay's gradient, two)
+// instead of three, and no state kept in two layouts.  Measured on MI355X: a dQ launch and
+// a fused dK, dV, decay walk with its states in two layouts 173 us for B8 H12 T2048 d64 in
+// bf16, this 120 us; 410 us both at B16 H32 T2048; two launches, dK and dV first, 437 us.
 //
-// The walks of dK and dV read the same rows at the same time; eight (sequence, head)s'
-// workgroups of one kind follow each other, so that the walks of one land on the same
-// XCD (workgroups go round the eight XCDs) and find each other's rows in its L2.
+// The walks of dK and dV read the same rows at the same time, on the same XCD (unit_of):
+// the second finds them in its L2 (measured: 8.3 tensors fetched instead of 10).
 #include "attn_walk.h"
 
 namespace ttt {
@@ -31,53 +31,35 @@ __device__ __forceinline__ const T* at(const void* p, const Strides3& s, int b, 
   return static_cast<const T*>(p) + b * s.b + h * s.h + t * s.t;
 }
 
-struct Place {
-  int kind, chain, seg;  // kind 0: dQ, 1: dK, 2: dV
-};
-
-// workgroup -> walk: kinds change every 8 (sequence, head, segment)s
-__device__ __forceinline__ Place place(int64_t id, int kinds, int nseg, int64_t total) {
-  const int64_t whole = total / 8 * 8;  // in full groups of 8
-  Place p;
-  int64_t unit;
-  if (id < whole * kinds) {
-    unit = id / (8 * kinds) * 8 + id % 8;
-    p.kind = static_cast<int>(id / 8 % kinds);
-  } else {
-    const int64_t r = id - whole * kinds, left = total - whole;
-    unit = whole + r % left;
-    p.kind = static_cast<int>(r / left);
-  }
-  p.chain = static_cast<int>(unit / nseg);
-  p.seg = static_cast<int>(unit % nseg);
-  return p;
-}
-
 constexpr int max2(int a, int b) { return a > b ? a : b; }
 
-#ifndef ATTN_BWD_WAVES
-#define ATTN_BWD_WAVES 1
-#endif
 template <int D, typename QT, typename ZT, typename OT>
-__global__ __launch_bounds__(4 * D, ATTN_BWD_WAVES) void ttt_attn_bwd(AttnBwdArgs a) {
+__global__ __launch_bounds__(4 * D, 2) void ttt_attn_bwd(AttnBwdArgs a) {
   constexpr int NB = D / 16;
-  constexpr int kLds = max2(WalkLds<D, true, true, ZT, QT, QT, QT>::kSize,
-                            max2(WalkLds<D, true, false, QT, ZT, QT, QT>::kSize,
-                                 WalkLds<D, true, false, QT, QT, ZT, QT>::kSize));
+  constexpr int kLds = max2(WalkLds<D, true, true, ZT, QT, QT, QT, ZT>::kSize,
+                            max2(WalkLds<D, true, false, QT, ZT, QT, QT, OT>::kSize,
+                                 WalkLds<D, true, false, QT, QT, ZT, QT, OT>::kSize));
   __shared__ __align__(16) uint16_t lds[kLds];
-  __shared__ float pw[C + 1];
+  __shared__ float powers[15 + C + 1];
+  const float* pw = powers + 15;
   __shared__ double part[NB];
   const int tid = threadIdx.x, w = tid / 64, lane = tid % 64, li = lane % 16, g4 = lane / 16;
-  const Place pl = place(blockIdx.x, 3, a.nseg, static_cast<int64_t>(a.B) * a.H * a.nseg);
-  const int chain = pl.chain, seg = pl.seg;
+  // kind 0: dQ, 1: dK, 2: dV.  The dQ walks, which take twice the others' time, begin first.
+  const int64_t units = static_cast<int64_t>(a.B) * a.H * a.nseg, id = blockIdx.x;
+  Unit pl{id, 0};
+  if (id >= units) {
+    pl = unit_of(id - units, 2, units);
+    ++pl.kind;
+  }
+  const int chain = static_cast<int>(pl.unit / a.nseg), seg = static_cast<int>(pl.unit % a.nseg);
   const int b = chain / a.H, h = chain % a.H, hk = h / a.group;
   const float lg = a.log_decay[h];
-  if (tid <= C) pw[tid] = powl(lg, tid);
+  if (tid < 15 + C + 1) powers[tid] = tid < 15 ? 0.f : powl(lg, tid - 15);
   const int len = seq_len(a.lens, b, a.T);
   const int sb = seg * a.seglen, se = min(sb + a.seglen, a.T);
   const int n = max(0, min(len, se) - sb);
   const int64_t dd = static_cast<int64_t>(D) * D;
-  const Decay em = decay(lg, a.seglen);
+  const float em = powl(lg, a.seglen);
   const float* loc = a.loc + static_cast<int64_t>(chain) * a.nseg * 3 * dd;
   const int pad0 = max(len, sb);  // padding rows among this segment's
 
@@ -89,14 +71,18 @@ __global__ __launch_bounds__(4 * D, ATTN_BWD_WAVES) void ttt_attn_bwd(AttnBwdArg
 #pragma unroll
     for (int i = 0; i < NB; ++i) u[i] = mfma::zero4v();
     if (seg == 0 && a.W0) load_state<D>(a.W0 + b * a.w0_bstride + h * dd, true, w, li, g4, s);
-    for (int c = 0; c < seg && n > 0; ++c) {
+    if (n > 0 && a.carried && seg > 0) {
+      load_state<D>(loc + (seg - 1) * 3 * dd, false, w, li, g4, s);
+      load_state<D>(loc + (seg - 1) * 3 * dd + dd, false, w, li, g4, u);
+    }
+    for (int c = 0; c < seg && n > 0 && !a.carried; ++c) {
       float4v x[NB], y[NB];
       load_state<D>(loc + c * 3 * dd, false, w, li, g4, x);
       load_state<D>(loc + c * 3 * dd + dd, false, w, li, g4, y);
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
-        u[i] = decayed(u[i] + s[i] * static_cast<float>(a.seglen), em) + y[i];
-        s[i] = decayed(s[i], em) + x[i];
+        u[i] = (u[i] + s[i] * static_cast<float>(a.seglen)) * em + y[i];
+        s[i] = s[i] * em + x[i];
       }
     }
     __syncthreads();
@@ -145,12 +131,8 @@ __global__ __launch_bounds__(4 * D, ATTN_BWD_WAVES) void ttt_attn_bwd(AttnBwdArg
     load_state<D>(a.dWf + chain * dd, pl.kind == 1, w, li, g4, s);
     fresh = true;
   }
-  for (int c = 0; c < seg && n > 0; ++c) {
-    float4v x[NB];
-    load_state<D>(loc + c * 3 * dd + 2 * dd, pl.kind == 2, w, li, g4, x);
-#pragma unroll
-    for (int i = 0; i < NB; ++i) s[i] = decayed(s[i], em) + x[i];
-  }
+  if (n > 0 && a.carried && seg > 0) load_state<D>(loc + (seg - 1) * 3 * dd + 2 * dd, pl.kind == 2, w, li, g4, s);
+  if (n > 0 && !a.carried) carry_states<D>(loc + 2 * dd, 3 * dd, seg, em, pl.kind == 2, w, li, g4, s);
   __syncthreads();
   const int64_t t0 = len - 1 - sb;  // (only for a walk of at least one token)
   const int ho = a.parts ? h : hk;
@@ -195,9 +177,9 @@ __global__ __launch_bounds__(4 * D, ATTN_BWD_WAVES) void ttt_attn_bwd(AttnBwdArg
   }
   if (pad0 < se) zero_rows<D>(out, ot, pad0, se);
   if (pl.kind == 2 && seg == (len > 0 ? (len - 1) / a.seglen : 0)) {
-    const Decay e1 = len > 0 ? decay(lg, 1) : Decay{1.f, 0.f};  // from the first token's state to the one before it
+    const float e1 = len > 0 ? pw[1] : 1.f;  // from the first token's state to the one before it
 #pragma unroll
-    for (int i = 0; i < NB; ++i) s[i] = decayed(s[i], e1);
+    for (int i = 0; i < NB; ++i) s[i] = s[i] * e1;
     store_state<D>(a.dW0 + chain * dd, w, li, g4, s);
   }
 }
@@ -208,15 +190,16 @@ template <int D, typename QT, typename ZT>
 __global__ __launch_bounds__(4 * D) void ttt_attn_bwd_states(AttnBwdArgs a) {
   constexpr int NB = D / 16;
   constexpr int kLds =
-      max2(WalkLds<D, false, true, QT, QT, QT, QT>::kSize, WalkLds<D, false, false, QT, ZT, QT, QT>::kSize);
+      max2(WalkLds<D, false, true, QT, QT, QT, QT, QT>::kSize, WalkLds<D, false, false, QT, ZT, QT, QT, QT>::kSize);
   __shared__ __align__(16) uint16_t lds[kLds];
-  __shared__ float pw[C + 1];
+  __shared__ float powers[15 + C + 1];
+  const float* pw = powers + 15;
   const int tid = threadIdx.x, w = tid / 64, lane = tid % 64, li = lane % 16, g4 = lane / 16;
-  const Place pl = place(blockIdx.x, 2, a.nseg - 1, static_cast<int64_t>(a.B) * a.H * (a.nseg - 1));
-  const int chain = pl.chain, seg = pl.seg;
+  const Unit pl = unit_of(blockIdx.x, 2, static_cast<int64_t>(a.B) * a.H * (a.nseg - 1));
+  const int chain = static_cast<int>(pl.unit / (a.nseg - 1)), seg = static_cast<int>(pl.unit % (a.nseg - 1));
   const int b = chain / a.H, h = chain % a.H, hk = h / a.group;
   const float lg = a.log_decay[h];
-  if (tid <= C) pw[tid] = powl(lg, tid);
+  if (tid < 15 + C + 1) powers[tid] = tid < 15 ? 0.f : powl(lg, tid - 15);
   const int len = seq_len(a.lens, b, a.T);
   const int sb = seg * a.seglen;
   if (len <= sb + a.seglen) return;  // no segment behind this one has a token
@@ -306,7 +289,7 @@ hipError_t go(const AttnBwdArgs& a, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(a.B) * a.H * a.nseg * 3), block(4 * D);
   const bool qf = a.in_dtype == 0, zf = a.out_dtype == 0;
   if (qf && zf) ttt_attn_bwd<D, float, float, float><<<grid, block, 0, s>>>(a);
-  else if (!qf && zf) ttt_attn_bwd<D, uint16_t, float, float><<<grid, block, 0, s>>>(a);
+  else if (zf) ttt_attn_bwd<D, uint16_t, float, float><<<grid, block, 0, s>>>(a);
   else if (qf && a.parts) ttt_attn_bwd<D, float, uint16_t, float><<<grid, block, 0, s>>>(a);
   else if (qf) ttt_attn_bwd<D, float, uint16_t, uint16_t><<<grid, block, 0, s>>>(a);
   else if (a.parts) ttt_attn_bwd<D, uint16_t, uint16_t, float><<<grid, block, 0, s>>>(a);

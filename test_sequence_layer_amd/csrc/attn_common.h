@@ -101,22 +101,50 @@ __device__ __forceinline__ float4v dot2(const Frag a0[NA], const Frag a1[NA], co
   return c;
 }
 
-// One tensor's chunk in LDS: C rows of D elements, a plane for each part.
+// One tensor's chunk in LDS: C rows of D elements, a plane for each part.  Within a row the 8-byte units are
+// exchanged by an exclusive or with a function of the row, chosen so that both ways of reading a Frag touch
+// all 32 banks once: by rows (16 lanes: one unit of 16 rows) and by columns (16 lanes: four units of four
+// rows).  A padded row (D + 8 elements) leaves two-way conflicts in both: 43% of the LDS cycles.
+template <int D>
+__host__ __device__ constexpr int swizzle(int row) {
+  return D >= 64 ? ((row & 3) << 2) | ((row >> 2) & 3) : D == 32 ? (((row >> 1) & 1) << 2) | ((row >> 2) & 3) : (row >> 2) & 3;
+}
+// Elements from row 0 to row 16.  Eight bytes over: reads of a unit in both halves then have no common
+// ds_read2 form, which the compiler would take and then need two moves each to pair up units of one half.
+template <int D>
+__host__ __device__ constexpr int half_at() { return 16 * D + 4; }
+template <int D>
+__device__ __forceinline__ int unit_at(int row, int unit) {
+  return row * D + (row >= 16 ? half_at<D>() - 16 * D : 0) + 4 * (unit ^ swizzle<D>(row));
+}
+
+// Where a lane finds its Frags X[li][16k + 4g ..] and X[4g ..][16k + li]; half_at further: 16 rows on.
+template <int D>
+struct Places {
+  int row[D / 16], col[D / 16];
+  __device__ __forceinline__ Places(int li, int g) {
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      row[k] = unit_at<D>(li, 4 * k + g);
+      col[k] = unit_at<D>(4 * g + (li >> 2), 4 * k + (li & 3));
+    }
+  }
+};
+
 template <int D, int N>
 struct Tile {
-  static constexpr int RS = D + 8;  // row stride: the rows of a Frag in different banks
-  static constexpr int kPlane = C * RS;
+  static constexpr int kPlane = half_at<D>() + 16 * D + 4;  // (16-byte steps)
   static constexpr int kSize = N * kPlane;
-  // X[row0 + li][16 blk + 4g ..]
-  __device__ static __forceinline__ void rows(const uint16_t* t, int row0, int blk, int li, int g, Frag f[N]) {
+  __device__ static __forceinline__ void rows(const uint16_t* t, Frag f[N]) {
+#pragma unroll
+    for (int p = 0; p < N; ++p) f[p] = *reinterpret_cast<const bf16x4*>(t + p * kPlane);
+  }
+  // ds_read_b64_tr_b16: lane l of 16 gets element r of the 8 bytes that lane 4r + l / 4 addresses, position l % 4
+  __device__ static __forceinline__ void cols(const uint16_t* t, Frag f[N]) {
+    typedef mfma::short4v __attribute__((address_space(3))) * ptr;
 #pragma unroll
     for (int p = 0; p < N; ++p)
-      f[p] = *reinterpret_cast<const bf16x4*>(t + p * kPlane + (row0 + li) * RS + 16 * blk + 4 * g);
-  }
-  // X[row0 + 4g ..][col0 + li]
-  __device__ static __forceinline__ void cols(const uint16_t* t, int row0, int col0, int li, int g, Frag f[N]) {
-#pragma unroll
-    for (int p = 0; p < N; ++p) f[p] = mfma::read_cols<RS>(t + p * kPlane, row0, col0, li, g);
+      f[p] = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(t + p * kPlane)));
   }
   __device__ static __forceinline__ float4v sum(const Frag f[N]) {
     float4v x = widen(f[N - 1]);
@@ -126,24 +154,24 @@ struct Tile {
   }
 };
 
-// A 16 x 16 block of A B^T: lane holds [4g + r of A's rows][li of B's rows].
+// A 16 x 16 block of A B^T: lane holds [4g + r of A's rows][li of B's rows].  a, x: the first of the 16 rows.
 template <int D, int NA, int NX, int LV>
-__device__ __forceinline__ float4v rows_dot(const uint16_t* a, int ra, const uint16_t* x, int rx, int li, int g) {
+__device__ __forceinline__ float4v rows_dot(const uint16_t* a, const uint16_t* x, const Places<D>& at) {
   constexpr int NB = D / 16;
   float4v c = mfma::zero4v();
   if constexpr (NB == 1) {
     Frag f[NA], h[NX];
-    Tile<D, NA>::rows(a, ra, 0, li, g, f);
-    Tile<D, NX>::rows(x, rx, 0, li, g, h);
+    Tile<D, NA>::rows(a + at.row[0], f);
+    Tile<D, NX>::rows(x + at.row[0], h);
     c = dot1<NA, NX, LV>(f, h, c);
   } else {
 #pragma unroll
     for (int k = 0; k < NB; k += 2) {
       Frag f0[NA], f1[NA], h0[NX], h1[NX];
-      Tile<D, NA>::rows(a, ra, k, li, g, f0);
-      Tile<D, NA>::rows(a, ra, k + 1, li, g, f1);
-      Tile<D, NX>::rows(x, rx, k, li, g, h0);
-      Tile<D, NX>::rows(x, rx, k + 1, li, g, h1);
+      Tile<D, NA>::rows(a + at.row[k], f0);
+      Tile<D, NA>::rows(a + at.row[k + 1], f1);
+      Tile<D, NX>::rows(x + at.row[k], h0);
+      Tile<D, NX>::rows(x + at.row[k + 1], h1);
       c = dot2<NA, NX, LV>(f0, f1, h0, h1, c);
     }
   }
@@ -155,26 +183,24 @@ template <typename T>
 struct Slab {
   static constexpr int kWords = sizeof(T) / 2;
   u32x4 r[kWords];
-  __device__ __forceinline__ void load(const T* p, bool ok) {
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      r[i] = u32x4{0u, 0u, 0u, 0u};
-      if (ok) r[i] = reinterpret_cast<const u32x4*>(p)[i];
-    }
+    for (int i = 0; i < kWords; ++i) r[i] = reinterpret_cast<const u32x4*>(p)[i];
   }
-  // to the planes of a Tile<D, parts_of<T>()>
+  // the two units to the planes of a Tile<D, parts_of<T>()>
   template <int PLANE>
-  __device__ __forceinline__ void put(uint16_t* t) const {
+  __device__ __forceinline__ void put(uint16_t* t, int u0, int u1) const {
     if constexpr (sizeof(T) == 2) {
-      *reinterpret_cast<u32x4*>(t) = r[0];
+      *reinterpret_cast<u32x2*>(t + u0) = u32x2{r[0][0], r[0][1]};
+      *reinterpret_cast<u32x2*>(t + u1) = u32x2{r[0][2], r[0][3]};
     } else {
       Frag f[2][3];
 #pragma unroll
       for (int i = 0; i < 2; ++i) split<3>(__builtin_bit_cast(float4v, r[i]), f[i]);
 #pragma unroll
       for (int p = 0; p < 3; ++p) {
-        const u32x2 lo = __builtin_bit_cast(u32x2, f[0][p]), hi = __builtin_bit_cast(u32x2, f[1][p]);
-        *reinterpret_cast<u32x4*>(t + p * PLANE) = u32x4{lo[0], lo[1], hi[0], hi[1]};
+        *reinterpret_cast<bf16x4*>(t + p * PLANE + u0) = f[0][p];
+        *reinterpret_cast<bf16x4*>(t + p * PLANE + u1) = f[1][p];
       }
     }
   }
@@ -183,19 +209,39 @@ struct Slab {
 // lambda^n for n >= 0 (lambda^0 = 1 also where lambda = 0)
 __device__ __forceinline__ float powl(float g, int n) { return n == 0 ? 1.f : expf(g * static_cast<float>(n)); }
 
-// x lambda^n as m x + a x.  Near 1 lambda^n is taken as 1 + expm1(n log lambda): a rounded lambda^n is off by
-// up to 2^-25 the same way in every chunk, which thousands of chunks add up.  Below 1/2 it is lambda^n itself.
-struct Decay {
-  float m, a;
+// lambda^C, chunk after chunk.  A rounded power near 1 is off by up to 2^-25 the same way every time, which
+// thousands of chunks add up: the two fp32 values around it are taken in turn, by a running sum of where it
+// lies between them, so that the product of any number of chunks' factors is off by one such step at most.
+struct Decays {
+  float lo, step, frac, sum;
+  __device__ __forceinline__ explicit Decays(float g) {
+    const double p = exp(static_cast<double>(g) * C);
+    lo = __double2float_rd(p);
+    // the next value up (p = 0 and p = inf have none to share with)
+    const float hi = lo > 0.f && lo < 3.0e38f ? __uint_as_float(__float_as_uint(lo) + 1u) : lo;
+    step = hi - lo;
+    frac = step > 0.f ? static_cast<float>((p - lo) / step) : 0.f;
+    sum = 0.5f;
+  }
+  __device__ __forceinline__ float next() {
+    sum += frac;
+    const bool up = sum >= 1.f;
+    sum -= up ? 1.f : 0.f;
+    return up ? lo + step : lo;
+  }
 };
-__device__ __forceinline__ Decay decay(float g, int n) {
-  const float p = powl(g, n);
-  return p > 0.5f ? Decay{1.f, n == 0 ? 0.f : expm1f(g * static_cast<float>(n))} : Decay{0.f, p};
-}
-__device__ __forceinline__ float4v decayed(float4v x, Decay d) {
-#pragma unroll
-  for (int r = 0; r < 4; ++r) x[r] = fmaf(x[r], d.a, x[r] * d.m);
-  return x;
+
+// Workgroup -> unit and kind of work: kinds change every 8 units.  Workgroups go round the eight XCDs, so the
+// kinds of one unit run on the same XCD, at about the same time.
+struct Unit {
+  int64_t unit;
+  int kind;
+};
+__device__ __forceinline__ Unit unit_of(int64_t id, int kinds, int64_t units) {
+  const int64_t whole = units / 8 * 8;  // in full groups of 8
+  if (id < whole * kinds) return Unit{id / (8 * kinds) * 8 + id % 8, static_cast<int>(id / 8 % kinds)};
+  const int64_t r = id - whole * kinds, left = units - whole;
+  return Unit{whole + r % left, static_cast<int>(r / left)};
 }
 
 // Rows 16w .. 16w+15 of a d x d state as accumulator blocks: lane holds
@@ -210,6 +256,28 @@ __device__ __forceinline__ void load_state(const float* p, bool transposed, int 
       const float* c = p + (16 * a + 4 * g) * D + 16 * w + li;
       s[a] = float4v{c[0], c[D], c[2 * D], c[3 * D]};
     }
+  }
+}
+// s carried over n segments: s <- e s + (the c-th state at p + c step), four loads at a time on their way.
+template <int D>
+__device__ __forceinline__ void carry_states(const float* p, int64_t step, int n, float e, bool transposed, int w, int li,
+                                             int g, float4v s[D / 16]) {
+  constexpr int U = D <= 64 ? 4 : 2;
+  int c = 0;
+  for (; c + U <= n; c += U) {
+    float4v x[U][D / 16];
+#pragma unroll
+    for (int i = 0; i < U; ++i) load_state<D>(p + (c + i) * step, transposed, w, li, g, x[i]);
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) s[k] = s[k] * e + x[i][k];
+  }
+  for (; c < n; ++c) {
+    float4v x[D / 16];
+    load_state<D>(p + c * step, transposed, w, li, g, x);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) s[k] = s[k] * e + x[k];
   }
 }
 template <int D>

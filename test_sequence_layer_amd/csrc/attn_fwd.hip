@@ -21,15 +21,16 @@ __device__ __forceinline__ const T* at(const void* p, const Strides3& s, int b, 
 }
 
 template <int D, typename IT, typename OT>
-__global__ __launch_bounds__(4 * D) void ttt_attn_fwd(AttnArgs a) {
+__global__ __launch_bounds__(4 * D, 2) void ttt_attn_fwd(AttnArgs a) {
   constexpr int NB = D / 16;
-  __shared__ __align__(16) uint16_t lds[WalkLds<D, true, false, IT, IT, IT, IT>::kSize];
-  __shared__ float pw[C + 1];  // lambda^n
+  __shared__ __align__(16) uint16_t lds[WalkLds<D, true, false, IT, IT, IT, IT, OT>::kSize];
+  __shared__ float powers[15 + C + 1];
+  const float* pw = powers + 15;
   const int tid = threadIdx.x, w = tid / 64, lane = tid % 64, li = lane % 16, g4 = lane / 16;
   const int chain = blockIdx.x / a.nseg, seg = blockIdx.x % a.nseg;
   const int b = chain / a.H, h = chain % a.H, hk = h / a.group;
   const float lg = a.log_decay[h];
-  if (tid <= C) pw[tid] = powl(lg, tid);
+  if (tid < 15 + C + 1) powers[tid] = tid < 15 ? 0.f : powl(lg, tid - 15);
   const int len = seq_len(a.lens, b, a.T);
   const int sb = seg * a.seglen, se = min(sb + a.seglen, a.T);  // this segment's rows
   const int n = max(0, min(len, se) - sb);                      // and tokens
@@ -41,14 +42,10 @@ __global__ __launch_bounds__(4 * D) void ttt_attn_fwd(AttnArgs a) {
     if (a.W0) load_state<D>(a.W0 + b * a.w0_bstride + static_cast<int64_t>(h) * D * D, false, w, li, g4, s);
   } else {
     const float* loc = a.loc + static_cast<int64_t>(chain) * a.nseg * D * D;
-    const Decay em = decay(lg, a.seglen);
+    const float em = powl(lg, a.seglen);
     if (seg == 0) load_state<D>(loc + static_cast<int64_t>(a.nseg - 1) * D * D, false, w, li, g4, s);
-    for (int c = 0; c < seg && n > 0; ++c) {
-      float4v x[NB];
-      load_state<D>(loc + static_cast<int64_t>(c) * D * D, false, w, li, g4, x);
-#pragma unroll
-      for (int i = 0; i < NB; ++i) s[i] = decayed(s[i], em) + x[i];
-    }
+    if (n > 0 && a.carried && seg > 0) load_state<D>(loc + static_cast<int64_t>(seg - 1) * D * D, false, w, li, g4, s);
+    if (n > 0 && !a.carried) carry_states<D>(loc, static_cast<int64_t>(D) * D, seg, em, false, w, li, g4, s);
   }
   __syncthreads();
 
@@ -82,13 +79,14 @@ __global__ __launch_bounds__(4 * D) void ttt_attn_fwd(AttnArgs a) {
 template <int D, typename IT>
 __global__ __launch_bounds__(4 * D) void ttt_attn_states(AttnArgs a) {
   constexpr int NB = D / 16;
-  __shared__ __align__(16) uint16_t lds[WalkLds<D, false, false, IT, IT, IT, IT>::kSize];
-  __shared__ float pw[C + 1];
+  __shared__ __align__(16) uint16_t lds[WalkLds<D, false, false, IT, IT, IT, IT, IT>::kSize];
+  __shared__ float powers[15 + C + 1];
+  const float* pw = powers + 15;
   const int tid = threadIdx.x, w = tid / 64, lane = tid % 64, li = lane % 16, g4 = lane / 16;
   const int chain = blockIdx.x / (a.nseg - 1), seg = blockIdx.x % (a.nseg - 1);
   const int b = chain / a.H, h = chain % a.H, hk = h / a.group;
   const float lg = a.log_decay[h];
-  if (tid <= C) pw[tid] = powl(lg, tid);
+  if (tid < 15 + C + 1) powers[tid] = tid < 15 ? 0.f : powl(lg, tid - 15);
   const int len = seq_len(a.lens, b, a.T);
   const int sb = seg * a.seglen;
   float4v s[NB];
@@ -117,6 +115,39 @@ __global__ __launch_bounds__(4 * D) void ttt_attn_states(AttnArgs a) {
   store_state<D>(loc + static_cast<int64_t>(seg) * D * D, w, li, g4, s);
 }
 
+// Four elements of one chain's states a thread, from segment to segment.
+__global__ __launch_bounds__(256) void ttt_attn_carry(AttnCarryArgs a) {
+  constexpr int U = 8;  // segments on their way
+  const int quads = a.d * a.d / 4;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (id >= a.chains * quads * (a.backward ? 2 : 1)) return;
+  const bool grad = id >= a.chains * quads;  // of G^T
+  const int64_t at = grad ? id - a.chains * quads : id, chain = at / quads;
+  const int64_t dd = static_cast<int64_t>(a.d) * a.d, step = a.backward ? 3 * dd : dd;
+  float* p = a.loc + chain * a.nseg * step + 4 * (at % quads) + (grad ? 2 * dd : 0);
+  const float e = powl(a.log_decay[chain % a.H], a.seglen), len = static_cast<float>(a.seglen);
+  float4v s = mfma::zero4v(), u = s;
+  const bool with_u = a.backward && !grad;
+  for (int c = 0; c < a.nseg - 1; c += U) {
+    float4v x[U], y[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int64_t k = min(c + i, a.nseg - 2) * step;
+      x[i] = *reinterpret_cast<const float4v*>(p + k);
+      y[i] = with_u ? *reinterpret_cast<const float4v*>(p + k + dd) : x[i];
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (c + i >= a.nseg - 1) break;
+      const int64_t k = (c + i) * step;
+      u = (u + s * len) * e + y[i];
+      s = s * e + x[i];
+      *reinterpret_cast<float4v*>(p + k) = s;
+      if (with_u) *reinterpret_cast<float4v*>(p + k + dd) = u;
+    }
+  }
+}
+
 template <int D>
 hipError_t go(const AttnArgs& a, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(a.B) * a.H * a.nseg), block(4 * D);
@@ -141,21 +172,17 @@ hipError_t go_states(const AttnArgs& a, hipStream_t s) {
 
 bool attn_supported(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 
-#ifndef ATTN_SEG_WG
-#define ATTN_SEG_WG 768
-#endif
-#ifndef ATTN_SEG_MIN
-#define ATTN_SEG_MIN 128
-#endif
-// Segments per sequence: as many as it takes for about three workgroups per CU
-// (256 CUs), none shorter than 128 tokens.
+// Segments per sequence.  One workgroup walks 32 tokens in about 1.3 us, so a few chains leave most of the 256
+// CUs idle for long; segments fill them, at the price of a first pass over K and V (Q and dZ too in the
+// backward) and of carrying the states.  Forward: two workgroups a CU (512): B8 H12 T2048 48 us (768: 57, 256:
+// 59, none: 102).  Backward, three walks a segment: 320 segments in all: B2 H32 T4096 142 us (256: 159, 512: 172).
+// None where the chains alone come near that; none shorter than 128 tokens (B1 H12 T200 gradients 25 us, 33 with
+// 96), at most 64 a sequence (B1 H1 T32768: 104 us with 256).
 int attn_segments(int64_t chains, int T, int d, bool backward) {
   (void)d;
-  if (chains <= 0 || T <= 0) return 1;
-  const int64_t wgs = backward ? 3 * chains : chains;
-  if (wgs >= 384) return 1;
-  int64_t n = (ATTN_SEG_WG + wgs - 1) / wgs;
-  const int64_t most = T / ATTN_SEG_MIN;
+  if (chains <= 0 || T <= 0 || chains >= (backward ? 256 : 384)) return 1;
+  int64_t n = ((backward ? 320 : 512) + chains - 1) / chains;
+  const int64_t most = T / 128 < 64 ? T / 128 : 64;
   if (n > most) n = most;
   return n < 1 ? 1 : static_cast<int>(n);
 }
@@ -168,6 +195,12 @@ hipError_t launch_attn_states(const AttnArgs& a, hipStream_t s) {
     case 128: return attn::go_states<128>(a, s);
     default: return hipErrorInvalidValue;
   }
+}
+
+hipError_t launch_attn_carry(const AttnCarryArgs& a, hipStream_t s) {
+  const int64_t n = a.chains * (a.d * a.d / 4) * (a.backward ? 2 : 1);
+  attn::ttt_attn_carry<<<dim3(static_cast<unsigned>((n + 255) / 256)), 256, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t s) {
