@@ -21,7 +21,6 @@ form, TTT-Linear and TTT-MLP).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -972,22 +971,23 @@ def mlp_decode(q, k, v, eta, w1, w2, w1b, w2b, pos: int, b: int, out_dtype=None,
 
 def _on(x, stream):
     """Context in which a call's tensors are made and its kernels launched: the given
-    stream, else the current stream of the device that ``x`` is on."""
+    stream, else the current stream of the device that ``x`` is on (None: it is current)."""
     torch = _torch()
     if stream is not None:
         if stream.device != x.device:
             raise ValueError(f"stream is on {stream.device}, the tensors are on {x.device}")
         return torch.cuda.stream(stream)
-    if x.is_cuda and x.device.index != torch.cuda.current_device():
+    if x.get_device() != torch._C._cuda_getDevice():
         return torch.cuda.device(x.device)
-    return contextlib.nullcontext()
+    return None
 
 
 def _check_same_dev(x, *ts):
-    if not x.is_cuda:
+    dev = x.get_device()
+    if dev < 0:
         raise ValueError("every tensor must be on the GPU")
     for t in ts:
-        if t is not None and t.device != x.device:
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"every tensor must be on one GPU ({t.device} and {x.device})")
 
 
@@ -1002,6 +1002,35 @@ def _strides(t) -> Strides:
 def _like(x, dtype):
     """An empty tensor of x's shape and, where x is dense, its layout."""
     return _torch().empty_like(x, dtype=dtype)
+
+
+# Checked descriptors by what they were checked from (shapes, strides, types): a call's checks and its
+# descriptor take as long as its launch.  Nothing in them belongs to a tensor's memory.
+_attn_descs = {}
+
+
+def _layout(x):
+    return None if x is None else (x.shape, x.stride(), x.dtype)
+
+
+def _attn_desc(q, k, v, log_decay, w0, lens, scale, z, grads=()):
+    """(descriptor, forward workspace bytes, backward workspace bytes) of a linear-attention call; z: Z or dZ,
+    grads: dq, dk, dv."""
+    key = (q.shape, q.stride(), q.dtype, k.shape, k.stride(), k.dtype, v.shape, v.stride(), v.dtype, log_decay.shape,
+           log_decay.stride(), log_decay.dtype, _layout(w0), _layout(lens), scale, z.shape, z.stride(), z.dtype,
+           *map(_layout, grads))
+    got = _attn_descs.get(key)
+    if got is None:
+        B, H, Hkv, T, d, wstride = _attn_args(q, k, v, log_decay, w0, lens)
+        if z.shape != q.shape:
+            raise ValueError(f"z or dz {tuple(z.shape)}: expected {tuple(q.shape)}")
+        desc = LinearAttnDesc(B, H, Hkv, T, d, _dtype_code(q.dtype), _dtype_code(z.dtype), 0, scale, 0, wstride,
+                              _strides(q), _strides(k), _strides(v), _strides(z), *map(_strides, grads))
+        got = (desc, *(int(lib().ttt_linear_attn_workspace_bytes(ctypes.byref(desc), b)) for b in (0, 1)))
+        if len(_attn_descs) >= 1024:
+            _attn_descs.clear()
+        _attn_descs[key] = got
+    return got
 
 
 def _attn_args(q, k, v, log_decay, w0, lens):
@@ -1035,19 +1064,19 @@ def _attn_args(q, k, v, log_decay, w0, lens):
     for x in (log_decay, lens, w0):
         if x is not None and not x.is_contiguous():
             raise ValueError("log_decay, lens and w0 must be contiguous")
-    _check_same_dev(q, k, v, log_decay, w0, lens)
     return B, H, Hkv, T, d, wstride
 
 
 def _want(x, shape, dtype, what):
     if tuple(x.shape) != tuple(shape) or x.dtype != dtype:
         raise ValueError(f"{what} must be {dtype} {tuple(shape)}, not {x.dtype} {tuple(x.shape)}")
+    if not x.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
 
 
-def _attn_workspace(desc, backward, workspace, like):
-    need = int(lib().ttt_linear_attn_workspace_bytes(ctypes.byref(desc), int(backward)))
+def _attn_workspace(need, workspace, dev):
     if workspace is None:
-        return (_torch().empty(need, dtype=_torch().uint8, device=like.device), need) if need > 0 else (None, 0)
+        return (_torch().empty(need, dtype=_torch().uint8, device=dev), need) if need > 0 else (None, 0)
     if not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous")
     return workspace, workspace.numel() * workspace.element_size()
@@ -1075,26 +1104,33 @@ def linear_attn_fwd(q, k, v, log_decay, w0=None, scale: float = 1.0, lens=None, 
     ``w_final`` may be ``w0`` itself when w0 is [B, H, d, d].  ``workspace``: uint8 tensor of
     :func:`linear_attn_workspace_bytes` (allocated when omitted); calls that may overlap need one each.
     """
+    if not q.is_cuda:
+        _attn_args(q, k, v, log_decay, w0, lens)
+    _check_same_dev(q, k, v, log_decay, w0, lens, z, w_final, workspace)
+    on = _on(q, stream)
+    if on is not None:
+        with on:
+            return _attn_fwd(q, k, v, log_decay, w0, scale, lens, out_dtype, w_final, z, workspace, stream)
+    return _attn_fwd(q, k, v, log_decay, w0, scale, lens, out_dtype, w_final, z, workspace, None)
+
+
+def _attn_fwd(q, k, v, log_decay, w0, scale, lens, out_dtype, w_final, z, workspace, stream):
     torch = _torch()
-    B, H, Hkv, T, d, wstride = _attn_args(q, k, v, log_decay, w0, lens)
-    with _on(q, stream):
-        if z is None:
-            z = _like(q, torch.float32 if out_dtype is None else out_dtype)
-        elif tuple(z.shape) != (B, H, T, d):
-            raise ValueError(f"z shape {tuple(z.shape)}: expected {(B, H, T, d)}")
-        if w_final is None:
-            w_final = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
-        _want(w_final, (B, H, d, d), torch.float32, "w_final")
-        if not w_final.is_contiguous():
-            raise ValueError("w_final must be contiguous")
-        _check_same_dev(q, z, w_final, workspace)
-        desc = LinearAttnDesc(B, H, Hkv, T, d, _dtype_code(q.dtype), _dtype_code(z.dtype), 0, scale, 0, wstride,
-                              _strides(q), _strides(k), _strides(v), _strides(z))
-        workspace, wbytes = _attn_workspace(desc, False, workspace, q)
-        st = lib().ttt_linear_attn_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(w0),
-                                       _ptr(lens), _ptr(z), _ptr(w_final), _ptr(workspace), wbytes,
-                                       _stream_handle(stream))
-        _done(st, "ttt_linear_attn_fwd")
+    dev = q.device
+    if z is None:
+        z = _like(q, torch.float32 if out_dtype is None else out_dtype)
+    desc, need, _ = _attn_desc(q, k, v, log_decay, w0, lens, scale, z)
+    shape = (desc.B, desc.H, desc.d, desc.d)
+    if w_final is None:
+        w_final = torch.empty(shape, dtype=torch.float32, device=dev)
+    else:
+        _want(w_final, shape, torch.float32, "w_final")
+    if need or workspace is not None:
+        workspace, need = _attn_workspace(need, workspace, dev)
+    st = lib().ttt_linear_attn_fwd(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                                   _ptr(w0), _ptr(lens), z.data_ptr(), w_final.data_ptr(), _ptr(workspace), need,
+                                   _stream_handle(stream, dev.index))
+    _done(st, "ttt_linear_attn_fwd")
     return z, w_final
 
 
@@ -1110,35 +1146,43 @@ def linear_attn_bwd(q, k, v, log_decay, dz, w0=None, dw_final=None, scale: float
     returns (dq [B, H, T, d], dk, dv [B, Hkv, T, d] (summed over the query heads that share them),
     dlog_decay [B, H] float32 and dw0 [B, H, d, d] float32, both per sequence: sum them over B for shared parameters).
     """
+    if not q.is_cuda:
+        _attn_args(q, k, v, log_decay, w0, lens)
+    _check_same_dev(q, k, v, log_decay, dz, w0, dw_final, lens, workspace, *(out or ()))
+    on = _on(q, stream)
+    if on is not None:
+        with on:
+            return _attn_bwd(q, k, v, log_decay, dz, w0, dw_final, scale, lens, workspace, out, stream)
+    return _attn_bwd(q, k, v, log_decay, dz, w0, dw_final, scale, lens, workspace, out, None)
+
+
+def _attn_bwd(q, k, v, log_decay, dz, w0, dw_final, scale, lens, workspace, out, stream):
     torch = _torch()
-    B, H, Hkv, T, d, wstride = _attn_args(q, k, v, log_decay, w0, lens)
-    if tuple(dz.shape) != (B, H, T, d):
-        raise ValueError(f"dz shape {tuple(dz.shape)}: expected {(B, H, T, d)}")
-    if dw_final is not None:
-        _want(dw_final, (B, H, d, d), torch.float32, "dw_final")
-        if not dw_final.is_contiguous():
-            raise ValueError("dw_final must be contiguous")
-    with _on(q, stream):
-        if out is None:
-            out = (_like(q, dz.dtype), _like(k, dz.dtype), _like(v, dz.dtype),
-                   torch.empty((B, H), dtype=torch.float32, device=q.device),
-                   torch.empty((B, H, d, d), dtype=torch.float32, device=q.device))
+    dev = q.device
+    if out is None:
+        dq, dk, dv = _like(q, dz.dtype), _like(k, dz.dtype), _like(v, dz.dtype)
+    else:
         dq, dk, dv, dg, dw0 = out
         for x, like, what in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
-            _want(x, like.shape, dz.dtype, what)
-        _want(dg, (B, H), torch.float32, "dlog_decay")
-        _want(dw0, (B, H, d, d), torch.float32, "dw0")
-        if not dg.is_contiguous() or not dw0.is_contiguous():
-            raise ValueError("dlog_decay and dw0 must be contiguous")
-        _check_same_dev(q, dz, dw_final, workspace, *out)
-        desc = LinearAttnDesc(B, H, Hkv, T, d, _dtype_code(q.dtype), _dtype_code(dz.dtype), 0, scale, 0, wstride,
-                              _strides(q), _strides(k), _strides(v), _strides(dz), _strides(dq), _strides(dk),
-                              _strides(dv))
-        workspace, wbytes = _attn_workspace(desc, True, workspace, q)
-        st = lib().ttt_linear_attn_bwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(w0),
-                                       _ptr(lens), _ptr(dz), _ptr(dw_final), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg),
-                                       _ptr(dw0), _ptr(workspace), wbytes, _stream_handle(stream))
-        _done(st, "ttt_linear_attn_bwd")
+            if x.shape != like.shape or x.dtype != dz.dtype:
+                raise ValueError(f"{what} must be {dz.dtype} {tuple(like.shape)}, not {x.dtype} {tuple(x.shape)}")
+    desc, _, need = _attn_desc(q, k, v, log_decay, w0, lens, scale, dz, (dq, dk, dv))
+    shape = (desc.B, desc.H, desc.d, desc.d)
+    if dw_final is not None:
+        _want(dw_final, shape, torch.float32, "dw_final")
+    if out is None:
+        dg = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+        dw0 = torch.empty(shape, dtype=torch.float32, device=dev)
+    else:
+        _want(dg, shape[:2], torch.float32, "dlog_decay")
+        _want(dw0, shape, torch.float32, "dw0")
+    if need or workspace is not None:
+        workspace, need = _attn_workspace(need, workspace, dev)
+    st = lib().ttt_linear_attn_bwd(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                                   _ptr(w0), _ptr(lens), dz.data_ptr(), _ptr(dw_final), dq.data_ptr(), dk.data_ptr(),
+                                   dv.data_ptr(), dg.data_ptr(), dw0.data_ptr(), _ptr(workspace), need,
+                                   _stream_handle(stream, dev.index))
+    _done(st, "ttt_linear_attn_bwd")
     return dq, dk, dv, dg, dw0
 
 
@@ -1151,24 +1195,26 @@ def linear_attn_decode(q, k, v, log_decay, w, scale: float = 1.0, lens=None, rop
     rope    : (pos, freqs[, layout[, scale]]) to turn q and k as :func:`rotary` would, in the same launch, or None
     returns Z [B, H, T, d].
     """
+    if not q.is_cuda:
+        _attn_args(q, k, v, log_decay, None, lens)
+    _check_same_dev(q, k, v, log_decay, w, lens, z)
+    on = _on(q, stream)
+    if on is not None:
+        with on:
+            return _attn_decode(q, k, v, log_decay, w, scale, lens, rope, out_dtype, z, stream)
+    return _attn_decode(q, k, v, log_decay, w, scale, lens, rope, out_dtype, z, None)
+
+
+def _attn_decode(q, k, v, log_decay, w, scale, lens, rope, out_dtype, z, stream):
     torch = _torch()
-    B, H, Hkv, T, d, _ = _attn_args(q, k, v, log_decay, None, lens)
-    _want(w, (B, H, d, d), torch.float32, "w")
-    if not w.is_contiguous():
-        raise ValueError("w must be contiguous")
-    with _on(q, stream):
-        if z is None:
-            z = _like(q, torch.float32 if out_dtype is None else out_dtype)
-        elif tuple(z.shape) != (B, H, T, d):
-            raise ValueError(f"z shape {tuple(z.shape)}: expected {(B, H, T, d)}")
-        _check_same_dev(q, w, z)
-        desc = LinearAttnDesc(B, H, Hkv, T, d, _dtype_code(q.dtype), _dtype_code(z.dtype), 0, scale, 0, 0,
-                              _strides(q), _strides(k), _strides(v), _strides(z))
-        turn = None if rope is None else _rope(q, *rope)
-        st = lib().ttt_linear_attn_decode(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(lens),
-                                          None if turn is None else ctypes.byref(turn), _ptr(z), _ptr(w),
-                                          _stream_handle(stream))
-        _done(st, "ttt_linear_attn_decode")
+    if z is None:
+        z = _like(q, torch.float32 if out_dtype is None else out_dtype)
+    desc, _, _ = _attn_desc(q, k, v, log_decay, None, lens, scale, z)
+    _want(w, (desc.B, desc.H, desc.d, desc.d), torch.float32, "w")
+    turn = None if rope is None else ctypes.byref(_rope(q, *rope))
+    st = lib().ttt_linear_attn_decode(ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                                      _ptr(lens), turn, z.data_ptr(), w.data_ptr(), _stream_handle(stream, q.device.index))
+    _done(st, "ttt_linear_attn_decode")
     return z
 
 
@@ -1234,31 +1280,51 @@ def _rope(x, pos, freqs, layout: str = "half", scale: float = 1.0) -> Rope:
     return r
 
 
-def _rotary_call(q, k, pos, freqs, layout, scale, out, stream, flags, what):
-    torch = _torch()
-    if q.dim() != 4:
-        raise ValueError("q must be [B, H, T, d]")
-    B, H, T, d = q.shape
-    if k is not None:
-        if k.dim() != 4 or (k.shape[0], k.shape[2], k.shape[3]) != (B, T, d):
-            raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}: expected [B, H, T, d] and [B, Hkv, T, d]")
-        if k.dtype != q.dtype:
-            raise ValueError("q and k must have the same dtype")
-    with _on(q, stream):
-        qo, ko = out if out is not None else (_like(q, q.dtype), None if k is None else _like(k, k.dtype))
+_rotary_descs = {}  # as _attn_descs
+
+
+def _rotary_desc(q, k, qo, ko, flags):
+    key = (q.shape, q.stride(), q.dtype, _layout(k), _layout(qo), _layout(ko), flags)
+    desc = _rotary_descs.get(key)
+    if desc is None:
+        B, H, T, d = q.shape
         if (ko is None) != (k is None):
             raise ValueError("out must hold an output for k exactly where k is given")
-        _want(qo, q.shape, q.dtype, "out[0]")
-        if k is not None:
-            _want(ko, k.shape, k.dtype, "out[1]")
-        _check_same_dev(q, k, qo, ko)
+        for x, like, name in ((qo, q, "out[0]"), (ko, k, "out[1]")):
+            if x is not None and (x.shape != like.shape or x.dtype != like.dtype):
+                raise ValueError(f"{name} must be {like.dtype} {tuple(like.shape)}, not {x.dtype} {tuple(x.shape)}")
         none = Strides()
         desc = RotaryDesc(B, H, 0 if k is None else k.shape[1], T, d, _dtype_code(q.dtype), flags, 0, _strides(q),
                           none if k is None else _strides(k), _strides(qo), none if k is None else _strides(ko))
-        rope = _rope(q, pos, freqs, layout, scale)
-        st = lib().ttt_rotary(ctypes.byref(desc), ctypes.byref(rope), _ptr(q), _ptr(k), _ptr(qo), _ptr(ko),
-                              _stream_handle(stream))
-        _done(st, what)
+        if len(_rotary_descs) >= 1024:
+            _rotary_descs.clear()
+        _rotary_descs[key] = desc
+    return desc
+
+
+def _rotary_call(q, k, pos, freqs, layout, scale, out, stream, flags, what):
+    if q.dim() != 4:
+        raise ValueError("q must be [B, H, T, d]")
+    if k is not None:
+        if k.dim() != 4 or k.shape[0] != q.shape[0] or k.shape[2:] != q.shape[2:]:
+            raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}: expected [B, H, T, d] and [B, Hkv, T, d]")
+        if k.dtype != q.dtype:
+            raise ValueError("q and k must have the same dtype")
+    _check_same_dev(q, k, *(out or ()))
+    on = _on(q, stream)
+    if on is not None:
+        with on:
+            return _rotary_launch(q, k, pos, freqs, layout, scale, out, stream, flags, what)
+    return _rotary_launch(q, k, pos, freqs, layout, scale, out, None, flags, what)
+
+
+def _rotary_launch(q, k, pos, freqs, layout, scale, out, stream, flags, what):
+    qo, ko = out if out is not None else (_like(q, q.dtype), None if k is None else _like(k, k.dtype))
+    desc = _rotary_desc(q, k, qo, ko, flags)
+    rope = _rope(q, pos, freqs, layout, scale)
+    st = lib().ttt_rotary(ctypes.byref(desc), ctypes.byref(rope), q.data_ptr(), _ptr(k), qo.data_ptr(), _ptr(ko),
+                          _stream_handle(stream, q.device.index))
+    _done(st, what)
     return qo, ko
 
 

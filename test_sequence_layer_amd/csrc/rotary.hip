@@ -1,12 +1,20 @@
 // Rotary positions of q and k: the pairs of each row turned by position * frequency.
 //
-//   (y1, y2) = scale ((x1, x2) cos t - (x2, -x1) sin t),   t = position * freqs[i]
+//   (y1, y2) = scale (x1 cos t - x2 sin t, x1 sin t + x2 cos t),   t = position * freqs[i]
 // The gradient turns back by the same angle with the same scale.  Every value is
 // read and written once and costs three flops, so the kernel is a copy: what it
 // must not do is compute an angle (64-bit product, sine and cosine) per value.
-// A thread owns V pairs of one (sequence, token), computes their V angles once and
-// walks the heads of q and of k with them; where there are too few tokens to
-// fill the chip, the heads are dealt out over blockIdx.y.
+// A thread owns a piece of a row at one (sequence, token), computes its angles once
+// and walks the heads of q and of k with them, the next four heads' loads on their
+// way while it turns four; where there are too few tokens to fill the chip, the
+// heads are dealt out over blockIdx.y.  Three ways of cutting rows into pieces:
+//   interleaved pairs, rows of whole 16-byte pieces: a piece, its pairs within it;
+//   halves of whole pieces: a piece, its partner from the lane that has it;
+//   other halves: a piece, the elements of the other half through LDS;
+//   rows at any address: one pair, element by element.
+// Measured on MI355X for B2 H32+32 T32768 d64 bf16, 1.07 GB (a copy of that size: 204 us): interleaved 214 us,
+// halves 212 us (through LDS 240, eight elements of both halves a thread 243, four 241), halves of 31 pairs 241 us
+// (pair by pair 638), half of the head 215 us.
 #include <type_traits>
 
 #include "mfma_common.h"
@@ -15,159 +23,250 @@
 namespace ttt {
 namespace {
 
-using mfma::u32x2;
 using mfma::u32x4;
 
-// N consecutive elements as fp32, aligned to their own size (at most 16 bytes at a time)
-template <int N, typename T>
-__device__ __forceinline__ void ld(const T* p, float x[N]) {
-  if constexpr (N == 1) {
-    if constexpr (sizeof(T) == 4) x[0] = p[0];
-    else x[0] = bf16_bits_to_f32(p[0]);
-  } else if constexpr (sizeof(T) == 4) {
+// a 16-byte piece of T as fp32 and back
+template <typename T>
+__device__ __forceinline__ void unpack(u32x4 w, float x[16 / sizeof(T)]) {
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const u32x4 w = mfma::ld_stream(reinterpret_cast<const u32x4*>(p) + i);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[4 * i + j] = __uint_as_float(w[j]);
-    }
-  } else {
-    static_assert(N == 8, "16 bytes of bf16");
-    const u32x4 w = mfma::ld_stream(reinterpret_cast<const u32x4*>(p));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[2 * j] = __uint_as_float(w[j] << 16), x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (sizeof(T) == 4) x[j] = __uint_as_float(w[j]);
+    else x[2 * j] = __uint_as_float(w[j] << 16), x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
   }
 }
-template <int N, typename T>
-__device__ __forceinline__ void st(T* p, const float x[N]) {
-  if constexpr (N == 1) {
-    if constexpr (sizeof(T) == 4) p[0] = x[0];
-    else p[0] = f32_to_bf16_bits(x[0]);
-  } else if constexpr (sizeof(T) == 4) {
+template <typename T>
+__device__ __forceinline__ u32x4 pack(const float x[16 / sizeof(T)]) {
+  u32x4 w;
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      u32x4 w;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(x[4 * i + j]);
-      mfma::st_stream(reinterpret_cast<u32x4*>(p) + i, w);
-    }
-  } else {
-    u32x4 w;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(mfma::float2v{x[2 * j], x[2 * j + 1]}, mfma::bf16x2));
-    mfma::st_stream(reinterpret_cast<u32x4*>(p), w);
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (sizeof(T) == 4) w[j] = __float_as_uint(x[j]);
+    else w[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(mfma::float2v{x[2 * j], x[2 * j + 1]}, mfma::bf16x2));
   }
+  return w;
+}
+template <typename T>
+__device__ __forceinline__ u32x4 ld(const T* p) {
+  return mfma::ld_stream(reinterpret_cast<const u32x4*>(p));
+}
+template <typename T>
+__device__ __forceinline__ void st(T* p, u32x4 w) {
+  mfma::st_stream(reinterpret_cast<u32x4*>(p), w);
 }
 
-// E elements a thread: 16 bytes twice (half layout), or E elements in a row (interleaved); E = 1: one
-// pair, element by element, where alignment or an odd rot allows no more.
-template <typename T, bool INTER, int E>
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(uint16_t x) { return bf16_bits_to_f32(x); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(uint16_t* p, float x) { *p = f32_to_bf16_bits(x); }
+
+enum { kInterleaved, kHalves, kOddHalves, kPairs };
+
+// Threads a row takes.
+template <typename T, int WAY>
+__host__ __device__ __forceinline__ int row_threads(int d, int rot, bool in_place) {
+  constexpr int E = 16 / sizeof(T);
+  if (WAY == kInterleaved) return in_place ? (rot + E - 1) / E : d / E;
+  if (WAY == kHalves || WAY == kOddHalves) return d / E;
+  return rot / 2 + (in_place ? 0 : d - rot);
+}
+
+// The rows of one (sequence, token) that a thread walks: heads h0 .. h1 - 1 of q, then k.
+template <typename T>
+struct Heads {
+  const T *qi, *ki;
+  T *qo, *ko;
+  int64_t qih, kih, qoh, koh;
+  int H, h0, h1;
+  __device__ __forceinline__ Heads(const RotaryArgs& a, int b, int t) {
+    qi = static_cast<const T*>(a.q) + b * a.qs.b + t * a.qs.t;
+    ki = static_cast<const T*>(a.k) + b * a.ks.b + t * a.ks.t;
+    qo = static_cast<T*>(a.qo) + b * a.qos.b + t * a.qos.t;
+    ko = static_cast<T*>(a.ko) + b * a.kos.b + t * a.kos.t;
+    qih = a.qs.h, kih = a.ks.h, qoh = a.qos.h, koh = a.kos.h;
+    H = a.H;
+    const int64_t heads = a.H + static_cast<int64_t>(a.Hkv);
+    h0 = static_cast<int>(heads * blockIdx.y / gridDim.y);
+    h1 = static_cast<int>(heads * (blockIdx.y + 1) / gridDim.y);
+  }
+  __device__ __forceinline__ const T* in(int h) const { return h < H ? qi + h * qih : ki + (h - H) * kih; }
+  __device__ __forceinline__ T* out(int h) const { return h < H ? qo + h * qoh : ko + (h - H) * koh; }
+};
+
+template <typename T, int WAY>
 __global__ __launch_bounds__(256) void ttt_rotary(RotaryArgs a) {
-  constexpr int V = E == 1 ? 1 : (INTER ? E / 2 : E);  // pairs per thread
-  const int half = a.rope.rot / 2;
-  const int turned = half / V;                            // threads per row with pairs
-  const int rest = a.in_place ? 0 : (a.d - a.rope.rot) / E;  // and with elements to pass on
-  const int per = turned + rest;
+  constexpr int E = 16 / sizeof(T);
+    constexpr int HU = 4;  // heads a step: 212 us [B, H, T, d] and 222 [B, T, H, d]; 2: 208 and 234, 8: 232 and 218
+  const int rot = a.rope.rot, half = rot / 2;
+  const int per = row_threads<T, WAY>(a.d, rot, a.in_place);
   const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (id >= static_cast<int64_t>(a.B) * a.T * per) return;
+  const int64_t rows = static_cast<int64_t>(a.B) * a.T;
+  // (kOddHalves: all threads of a workgroup keep step; the ones left over walk the last row and store nothing)
+  const bool live = id < rows * per;
+  if (WAY != kOddHalves && !live) return;
   const int unit = static_cast<int>(id % per);
-  const int64_t bt = id / per;
+  const int64_t bt = live ? id / per : rows - 1;
   const int b = static_cast<int>(bt / a.T), t = static_cast<int>(bt % a.T);
-  const int heads = a.H + a.Hkv;
-  const int h0 = static_cast<int>(static_cast<int64_t>(heads) * blockIdx.y / gridDim.y);
-  const int h1 = static_cast<int>(static_cast<int64_t>(heads) * (blockIdx.y + 1) / gridDim.y);
-  const T* qi = static_cast<const T*>(a.q) + b * a.qs.b + t * a.qs.t;
-  const T* ki = static_cast<const T*>(a.k) + b * a.ks.b + t * a.ks.t;
-  T* qo = static_cast<T*>(a.qo) + b * a.qos.b + t * a.qos.t;
-  T* ko = static_cast<T*>(a.ko) + b * a.kos.b + t * a.kos.t;
-  auto in = [&](int h) { return h < a.H ? qi + h * a.qs.h : ki + (h - a.H) * a.ks.h; };
-  auto out = [&](int h) { return h < a.H ? qo + h * a.qos.h : ko + (h - a.H) * a.kos.h; };
-
-  if (unit >= turned) {
-    const int c = a.rope.rot + (unit - turned) * E;
-    for (int h = h0; h < h1; ++h) {
-      float x[E];
-      ld<E>(in(h) + c, x);
-      st<E>(out(h) + c, x);
-    }
-    return;
-  }
-  float cs[V], sn[V];
+  const Heads<T> hd(a, b, t);
   const int64_t pos = rope_pos(a.rope, b, t);
-#pragma unroll
-  for (int p = 0; p < V; ++p) {
-    rope_angle(pos, a.rope.freqs[unit * V + p], cs[p], sn[p]);
-    cs[p] *= a.rope.scale;
-    sn[p] *= a.inverse ? -a.rope.scale : a.rope.scale;
-  }
-  auto turn = [&](float& x, float& y, int p) {
-    const float u = fmaf(-y, sn[p], x * cs[p]);
-    y = fmaf(x, sn[p], y * cs[p]);
+  auto angle = [&](int i, float& c, float& s) {
+    rope_angle(pos, a.rope.freqs[i], c, s);
+    c *= a.rope.scale;
+    s *= a.inverse ? -a.rope.scale : a.rope.scale;
+  };
+  auto turn = [](float& x, float& y, float c, float s) {
+    const float u = fmaf(-y, s, x * c);
+    y = fmaf(x, s, y * c);
     x = u;
   };
-  constexpr int HU = 4;  // heads in flight
-  constexpr int N = INTER ? 2 * V : V;
-  for (int h = h0; h < h1; h += HU) {
-    float x[HU][N], y[HU][INTER ? 1 : N];
+
+  if constexpr (WAY == kInterleaved || WAY == kHalves) {
+    constexpr int V = WAY == kHalves ? E : E / 2;  // angles
+    typedef u32x4 W;
+    const int o = unit * E, pieces = half / E;
+    const bool turned = o < rot, first = o < half;
+    const int partner = static_cast<int>(threadIdx.x % 64) + (!turned ? 0 : first ? pieces : -pieces);  // lane
+    auto load = [&](W r[HU], int h) __attribute__((always_inline)) {
 #pragma unroll
-    for (int u = 0; u < HU; ++u) {
-      if (h + u >= h1) break;
-      const T* p = in(h + u);
-      if constexpr (INTER && E == 1) {
-        ld<1>(p + 2 * unit, &x[u][0]);
-        ld<1>(p + 2 * unit + 1, &x[u][1]);
-      } else if constexpr (INTER) {
-        ld<N>(p + unit * N, x[u]);
-      } else {
-        ld<N>(p + unit * N, x[u]);
-        ld<N>(p + half + unit * N, y[u]);
+      for (int u = 0; u < HU; ++u) r[u] = ld(hd.in(min(h + u, hd.h1 - 1)) + o);
+    };
+    W now[HU], next[HU];
+    load(now, hd.h0);
+    float cs[V], sn[V];
+#pragma unroll
+    for (int p = 0; p < V; ++p) {
+      const int i = WAY == kHalves ? (first ? o : o - half) + p : o / 2 + p;
+      cs[p] = 1.f;
+      sn[p] = 0.f;
+      if (turned && i < half) angle(i, cs[p], sn[p]);
+      if (WAY == kHalves && first) sn[p] = -sn[p];
+    }
+    for (int h = hd.h0; h < hd.h1; h += HU) {
+      if (h + HU < hd.h1) load(next, h + HU);
+#pragma unroll
+      for (int u = 0; u < HU; ++u) {
+        float x[E];
+        unpack<T>(now[u], x);
+        if constexpr (WAY == kHalves) {
+          W other;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) other[j] = __shfl(now[u][j], partner);
+          float y[E];
+          unpack<T>(other, y);
+#pragma unroll
+          for (int i = 0; i < V; ++i) x[i] = fmaf(y[i], sn[i], x[i] * cs[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (o / 2 + i < half) turn(x[2 * i], x[2 * i + 1], cs[i], sn[i]);
+        }
+        if (turned) now[u] = pack<T>(x);
+        if (h + u < hd.h1) st(hd.out(h + u) + o, now[u]);
+        now[u] = next[u];
       }
     }
+  } else if constexpr (WAY == kOddHalves) {
+    // Each thread's piece goes to LDS, where the threads of its row find the elements that their own are paired with.
+    constexpr int kStep = 20 / sizeof(T);  // elements between pieces: 20 bytes, so that pieces begin in other banks
+    __shared__ __align__(16) T buf[2][2][256 * kStep];
+    const int o = unit * E;
+    const int mine = static_cast<int>(threadIdx.x);
+    constexpr int HL = 2;  // heads a barrier
+    typedef u32x4 W;
+    W now[HL], next[HL];
+    auto load = [&](W* r, int h) __attribute__((always_inline)) {
 #pragma unroll
-    for (int u = 0; u < HU; ++u) {
-      if (h + u >= h1) break;
-      T* p = out(h + u);
+      for (int u = 0; u < HL; ++u) r[u] = ld(hd.in(min(h + u, hd.h1 - 1)) + o);
+    };
+    load(now, hd.h0);
+    float cs[E], sn[E];
+    int from[E];  // of the partner, in this thread's row
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if constexpr (INTER) turn(x[u][2 * v], x[u][2 * v + 1], v);
-        else turn(x[u][v], y[u][v], v);
+    for (int j = 0; j < E; ++j) {
+      const int c = o + j;
+      cs[j] = 1.f;
+      sn[j] = 0.f;
+      from[j] = c;
+      if (c < rot) {
+        angle(c < half ? c : c - half, cs[j], sn[j]);
+        if (c < half) sn[j] = -sn[j];
+        from[j] = c < half ? c + half : c - half;
       }
-      if constexpr (INTER && E == 1) {
-        st<1>(p + 2 * unit, &x[u][0]);
-        st<1>(p + 2 * unit + 1, &x[u][1]);
-      } else if constexpr (INTER) {
-        st<N>(p + unit * N, x[u]);
-      } else {
-        st<N>(p + unit * N, x[u]);
-        st<N>(p + half + unit * N, y[u]);
+    }
+    int n = 0;
+    for (int h = hd.h0; h < hd.h1; h += HL, n ^= 1) {
+#pragma unroll
+      for (int u = 0; u < HL; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) reinterpret_cast<uint32_t*>(buf[n][u] + mine * kStep)[j] = now[u][j];
+      if (h + HL < hd.h1) load(next, h + HL);
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < HL; ++u) {
+        if (h + u >= hd.h1) break;
+        float x[E];
+        unpack<T>(now[u], x);
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          if (o + j < rot) {
+            const int piece = mine - unit + from[j] / E;
+            const float y =
+                piece < 256 && piece >= 0 ? widen(buf[n][u][piece * kStep + from[j] % E]) : widen(hd.in(h + u)[from[j]]);
+            x[j] = fmaf(y, sn[j], x[j] * cs[j]);
+          }
+        }
+        if (live) st(hd.out(h + u) + o, pack<T>(x));
+        now[u] = next[u];
       }
+    }
+  } else {
+    if (unit >= half) {
+      const int c = rot + unit - half;
+      for (int h = hd.h0; h < hd.h1; ++h) hd.out(h)[c] = hd.in(h)[c];
+      return;
+    }
+    const int o1 = a.rope.interleaved ? 2 * unit : unit, o2 = a.rope.interleaved ? o1 + 1 : o1 + half;
+    float c, s;
+    angle(unit, c, s);
+    for (int h = hd.h0; h < hd.h1; ++h) {
+      float x = widen(hd.in(h)[o1]), y = widen(hd.in(h)[o2]);
+      turn(x, y, c, s);
+      put(hd.out(h) + o1, x);
+      put(hd.out(h) + o2, y);
     }
   }
 }
 
-template <typename T, bool INTER, int E>
+template <typename T, int WAY>
 hipError_t go(const RotaryArgs& a, hipStream_t s) {
-  constexpr int V = E == 1 ? 1 : (INTER ? E / 2 : E);
-  const int64_t per = a.rope.rot / 2 / V + (a.in_place ? 0 : (a.d - a.rope.rot) / E);
+  const int64_t per = row_threads<T, WAY>(a.d, a.rope.rot, a.in_place);
   const int64_t blocks = (static_cast<int64_t>(a.B) * a.T * per + 255) / 256;
-  const int heads = a.H + a.Hkv;
+  const int64_t heads = static_cast<int64_t>(a.H) + a.Hkv;
   int64_t y = (1024 + blocks - 1) / blocks;  // four workgroups per CU
   if (y > heads) y = heads;
-  ttt_rotary<T, INTER, E><<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(y)), 256, 0, s>>>(a);
+  ttt_rotary<T, WAY><<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(y)), 256, 0, s>>>(a);
   return hipGetLastError();
+}
+
+// every row begins on a multiple of `bytes`
+bool aligned_to(const RotaryArgs& a, int bytes, int size) {
+  for (const void* p : {a.q, a.k, static_cast<const void*>(a.qo), static_cast<const void*>(a.ko)})
+    if (reinterpret_cast<uintptr_t>(p) % bytes != 0) return false;
+  for (const Strides3& x : {a.qs, a.ks, a.qos, a.kos})
+    if (x.b * size % bytes != 0 || x.h * size % bytes != 0 || x.t * size % bytes != 0) return false;
+  return true;
 }
 
 template <typename T>
 hipError_t pick(const RotaryArgs& a, hipStream_t s) {
-  constexpr int E = 16 / sizeof(T);
-  // whole 16-byte pieces: every row and both halves of its pairs begin on one
-  bool wide = a.rope.rot % (a.rope.interleaved ? E : 2 * E) == 0 && a.d % E == 0;
-  for (const void* p : {a.q, a.k, static_cast<const void*>(a.qo), static_cast<const void*>(a.ko)})
-    wide = wide && reinterpret_cast<uintptr_t>(p) % 16 == 0;
-  for (const Strides3& x : {a.qs, a.ks, a.qos, a.kos}) wide = wide && x.b % E == 0 && x.h % E == 0 && x.t % E == 0;
-  if (a.rope.interleaved) return wide ? go<T, true, E>(a, s) : go<T, true, 1>(a, s);
-  return wide ? go<T, false, E>(a, s) : go<T, false, 1>(a, s);
+  constexpr int E = 16 / sizeof(T), kSize = sizeof(T);
+  if (a.rope.interleaved && a.d % E == 0 && aligned_to(a, 16, kSize)) return go<T, kInterleaved>(a, s);
+  // (whole rows in a wave)
+  if (!a.rope.interleaved && a.rope.rot % (2 * E) == 0 && a.d % E == 0 && 64 % (a.d / E) == 0 && aligned_to(a, 16, kSize))
+    return go<T, kHalves>(a, s);
+  // (a partner in another workgroup's piece is read from the row itself, which must not be written yet)
+  if (!a.rope.interleaved && a.d % E == 0 && aligned_to(a, 16, kSize) &&
+      (256 % (a.d / E) == 0 || (a.q != a.qo && a.k != a.ko)))
+    return go<T, kOddHalves>(a, s);
+  return go<T, kPairs>(a, s);
 }
 
 }  // namespace

@@ -38,7 +38,8 @@ def make(B, H, Hkv, T, d, dtype, seed=0):
 
 
 # d, rot: whole head, half of it, an odd number of pairs, one pair, none; rows that are no multiple of 16 bytes
-SIZES = [(64, 64), (64, 32), (64, 62), (128, 128), (16, 16), (32, 16), (64, 2), (64, 0), (30, 12), (7, 6), (256, 64)]
+SIZES = [(64, 64), (64, 32), (64, 62), (128, 128), (16, 16), (32, 16), (64, 2), (64, 0), (30, 12), (7, 6), (256, 64),
+         (24, 22), (40, 34), (12, 10), (20, 8), (64, 48), (36, 24)]
 
 
 @pytest.mark.parametrize("layout,dtype", list(itertools.product(["half", "interleaved"], [BF16, F32])))
@@ -100,6 +101,31 @@ def test_layouts_and_in_place(ttt, layout):
     with pytest.raises(ttt.TTTError) as e:
         ttt.rotary(q, q, 11, freqs, layout, out=(q, q))
     assert e.value.status == 5
+
+
+@pytest.mark.parametrize("d,rot", [(64, 62), (24, 22), (16, 10)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_odd_halves_in_place(ttt, d, rot, dtype):
+    """both, and only one, of q and k in place, with rows that end inside a workgroup's last piece"""
+    freqs = ttt.rotary_freqs(rot, device=DEV)[0]
+    q, k = (x.to(DEV) for x in make(3, 5, 2, 211, d, dtype))
+    ref = ttt.rotary(q, k, 7, freqs)
+    qc, kc = q.clone(), k.clone()
+    ttt.rotary(qc, kc, 7, freqs, out=(qc, kc))
+    assert torch.equal(qc, ref[0]) and torch.equal(kc, ref[1])
+    qc = q.clone()
+    got = ttt.rotary(qc, k, 7, freqs, out=(qc, torch.empty_like(k)))
+    assert torch.equal(qc, ref[0]) and torch.equal(got[1], ref[1])
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rest_of_the_head_is_passed_on(ttt, layout):
+    """infinities and NaN beside and behind the turned elements stay where they are"""
+    for d, rot in ((64, 16), (64, 30), (64, 32), (9, 4)):
+        q = torch.randn(1, 2, 5, d, device=DEV)
+        q[..., rot:] = torch.tensor([float("inf"), float("nan"), -float("inf")], device=DEV).repeat(d)[:d - rot]
+        y = ttt.rotary(q, None, 3, ttt.rotary_freqs(rot, device=DEV)[0], layout)[0]
+        assert torch.isfinite(y[..., :rot]).all() and torch.equal(y[..., rot:].nan_to_num(7.0), q[..., rot:].nan_to_num(7.0))
 
 
 def test_many_heads_and_few(ttt):
