@@ -1388,7 +1388,7 @@ struct AttnPlan {
 AttnPlan attn_plan(const ttt_linear_attn_desc* d, bool backward) {
   AttnPlan p;
   const int64_t chains = static_cast<int64_t>(d->B) * d->H, dd = static_cast<int64_t>(d->d) * d->d * 4;
-  const int n = ttt::attn_segments(chains, d->T, d->d, backward);
+  const int n = ttt::attn_segments(chains, d->T, backward);
   const int c = ttt::kAttnChunk;
   p.seglen = ((d->T + n - 1) / n + c - 1) / c * c;
   if (p.seglen < c) p.seglen = c;

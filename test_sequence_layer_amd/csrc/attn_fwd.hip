@@ -172,16 +172,18 @@ hipError_t go_states(const AttnArgs& a, hipStream_t s) {
 
 bool attn_supported(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 
-// Segments per sequence.  One workgroup walks 32 tokens in about 1.3 us, so a few chains leave most of the 256
+// Segments per sequence.  One workgroup walks a chain 32 tokens at a time, so a few chains leave most of the 256
 // CUs idle for long; segments fill them, at the price of a first pass over K and V (Q and dZ too in the
-// backward) and of carrying the states.  Forward: two workgroups a CU (512): B8 H12 T2048 48 us (768: 57, 256:
-// 59, none: 102).  Backward, three walks a segment: 320 segments in all: B2 H32 T4096 142 us (256: 159, 512: 172).
-// None where the chains alone come near that; none shorter than 128 tokens (B1 H12 T200 gradients 25 us, 33 with
-// 96), at most 64 a sequence (B1 H1 T32768: 104 us with 256).
-int attn_segments(int64_t chains, int T, int d, bool backward) {
-  (void)d;
-  if (chains <= 0 || T <= 0 || chains >= (backward ? 256 : 384)) return 1;
-  int64_t n = ((backward ? 320 : 512) + chains - 1) / chains;
+// backward) and of carrying the states.  d = 64, bf16, [B, H, T, d]:
+//   forward, at most two workgroups a CU (512): B8 H12 T2048 46.6 us (at most 256: 58, 768: 51, none: 83); two
+//     segments for 300 chains would cost 100 us, none 85; 512 rounded up instead of down: 49.7
+//   backward, three walks a segment, at most 320 segments: B2 H32 T4096 144 us (256: 166, 512: 162, none: 232);
+//     two segments for 192 chains would cost 196 us, none 162
+// None shorter than 128 tokens (B1 H12 T200 gradients 20 us, 28 with 96; B1 H12 T512 17 us, 22 with 192), at most
+// 64 a sequence (B1 H1 T32768: 60 us, 105 with 256).
+int attn_segments(int64_t chains, int T, bool backward) {
+  if (chains <= 0 || T <= 0) return 1;
+  int64_t n = (backward ? 320 : 512) / chains;
   const int64_t most = T / 128 < 64 ? T / 128 : 64;
   if (n > most) n = most;
   return n < 1 ? 1 : static_cast<int>(n);

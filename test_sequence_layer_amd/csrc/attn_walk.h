@@ -16,14 +16,22 @@
 // One workgroup of d / 16 waves.  Wave w owns rows 16w .. 16w+15 of S (as
 // accumulator blocks, for the whole walk) and the same 16 output columns.  The three
 // causal 16 x 16 blocks of X Y^T come out of the matrix cores, transposed, in the
-// layout that the product with V reads: one wave computes, decays and splits a block
-// one chunk ahead and leaves it in LDS for the others (computed by every wave they
-// were a fifth of all instructions, and issue slots are what this kernel runs out of:
-// 75% busy before, with HBM at 4.2 TB/s).  A chunk's rows are loaded three chunks
-// ahead into registers (16 bytes a thread and tensor for bf16), stored to one of
-// three LDS buffers two chunks ahead, and one barrier a chunk separates its readers
-// and writers.  fp32 inputs go to LDS as three planes, in one buffer, with a barrier
-// for each of these steps.
+// layout that the product with V reads: one wave computes, decays and splits a block and
+// leaves it in LDS for the others (computed by every wave they were a fifth of all
+// instructions, and issue slots are what this kernel runs out of: 75% busy in the
+// forward, 85% in the backward at B16 H32 d64 bf16).
+//
+// Chunks on their way.  bf16: two chunks in registers (16 bytes a thread and tensor)
+// and two LDS buffers, so a chunk is loaded three chunks before it is used and stored
+// one before; two barriers a chunk, behind the scores and behind the chunk.  Otherwise
+// (three planes a tensor, or the four tiles of the decay's gradient at d = 128) one of
+// each, and a third barrier behind the stores.  The barrier behind the scores
+// comes after the products with the start state, which do not need them (gradients of
+// B16 H16 T2048 d128 bf16: 654 us, 712 with it before; fp32 inputs -1 to -3%), but before
+// them for bf16 at d = 64, where the other workgroups of the CU fill the wait (B16 H32
+// T8192: 429 us, 439 with it after).  At d = 64 a wave also issues a chunk's products
+// before the other waves' loads and scores (the same case 440 us without, gradients of
+// B16 H32 T2048 400 us, 393 with; at d = 128 it costs 1 to 9%, below 64 nothing changes).
 //
 // The decay's gradient (with dQ): a second state U = dS/dlog_decay counts each pair
 // j <= i by its distance,
@@ -65,6 +73,7 @@ struct WalkLds {
   static constexpr int kChunk = kX + kY + kV + kQ;
   static constexpr bool kRing = sizeof(XT) + sizeof(YT) + sizeof(VT) == 6 && !(DG && OUT && D == 128);
   static constexpr int kBufs = kRing ? 2 : 1;
+  static constexpr bool kScoresFirst = kRing && D == 64;  // where the barrier behind the scores stands
   static constexpr int kLevel = DG ? 3 : level_of<OT>();  // of outputs: parts of scores and of the state for them
   static constexpr int kScoreHalf = 3 * kLevel * 64 * 4;  // a chunk's score blocks
   static constexpr int kScores = OUT ? kScoreHalf : 0;
@@ -196,6 +205,7 @@ __device__ __forceinline__ void walk(const Walk<XT, YT, VT, QT, OT>& a, bool fre
         f1[r] = j + 16 < L ? a.su * pw[j + 16 < L ? L - 17 - j : 0] : 0.f;
       }
     }
+    if constexpr (D == 64) prio_mfma();
     Frag v0[NV], v1[NV];
     TV::cols(V + own_col, v0);
     TV::cols(V + kHalf + own_col, v1);
@@ -241,6 +251,7 @@ __device__ __forceinline__ void walk(const Walk<XT, YT, VT, QT, OT>& a, bool fre
       }
       z0 = z0 * far0;
       z1 = z1 * far1;
+      if constexpr (!Lds::kScoresFirst) __syncthreads();
       Frag p0[NP], p1[NP];
       const uint16_t* P = scores;
 #pragma unroll
@@ -282,6 +293,7 @@ __device__ __forceinline__ void walk(const Walk<XT, YT, VT, QT, OT>& a, bool fre
         s[k] = dot2<NY, 3, 3>(y0, y1, q0, q1, s[k] * e);
       }
     }
+    if constexpr (D == 64) prio_valu();
     far0 = near0;
     far1 = near1;
     un = 0;
@@ -299,7 +311,7 @@ __device__ __forceinline__ void walk(const Walk<XT, YT, VT, QT, OT>& a, bool fre
     auto step = [&](Ring& r, int buf, int n) __attribute__((always_inline)) {
       if constexpr (OUT) {
         score(buf, n);
-        __syncthreads();
+        if constexpr (Lds::kScoresFirst) __syncthreads();
       }
       stage(r, 1 - buf);
       fetch(r, n + 3);
@@ -314,7 +326,7 @@ __device__ __forceinline__ void walk(const Walk<XT, YT, VT, QT, OT>& a, bool fre
     if (nfull < nch) {
       if constexpr (OUT) {
         score(nfull % 2, nfull);
-        __syncthreads();
+        if constexpr (Lds::kScoresFirst) __syncthreads();
       }
       chunk(F{}, nfull % 2, nfull);
     }
@@ -325,10 +337,7 @@ __device__ __forceinline__ void walk(const Walk<XT, YT, VT, QT, OT>& a, bool fre
       stage(r, 0);
       fetch(r, n + 1);
       __syncthreads();
-      if constexpr (OUT) {
-        score(0, n);
-        __syncthreads();
-      }
+      if constexpr (OUT) score(0, n);
       if (n < nfull) chunk(T{}, 0, n);
       else chunk(F{}, 0, n);
       if (n + 1 < nch) __syncthreads();
