@@ -571,7 +571,10 @@ ttt_status ttt_mlp_ln_decode_validate(const ttt_mlp_desc* desc, const void* Q, c
  *    outputs and gradients are written as zero; the state is that after the last
  *    token.
  *  - log_decay: [H] fp32 on the device; 0 keeps everything, -inf nothing.
- *  - 0 <= T <= 2^30.
+ *  - 0 <= T <= 2^30, and a launch has fewer than 2^32 threads (TTT_ERR_SHAPE):
+ *    4 B H d per segment in the forward and in decode, three times that in the
+ *    backward, which also sums B Hkv T d / 2 where heads are shared; B T d for
+ *    ttt_rotary.
  *  - Finite values: a NaN or infinity reaches only tokens at or after its own, but
  *    for V (and dZ in the backward) also the others of its 16-token block.
  */
@@ -599,8 +602,8 @@ typedef struct {
  *       (TTT_ERR_WORKSPACE), overlapping nothing else; unspecified on return.
  * Chunks of 32 tokens as matrix products; where there are few (sequence, head)
  * chains a sequence is walked in segments at the same time, whose start states a
- * first launch computes.  d in {16, 32, 64, 128}; bf16 inputs on the bf16 matrix
- * cores (fp32 operands split into bf16 parts), fp32 inputs on the fp32 ones.
+ * first launch computes.  d in {16, 32, 64, 128}.  All products run on the bf16
+ * matrix cores, fp32 operands (fp32 inputs, states, scores) as two or three bf16 parts.
  */
 ttt_status ttt_linear_attn_fwd(const ttt_linear_attn_desc* desc, const void* Q, const void* K, const void* V,
                                const float* log_decay, const float* W0, const int32_t* lens, void* Z, float* W_final,

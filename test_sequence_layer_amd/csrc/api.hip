@@ -1357,6 +1357,7 @@ bool same_view(const View& a, const View& b) {
 }
 
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 256;  // of a launch
 bool finite(float x) { return x - x == 0.f; }
 
 // sizes, types, flags; chains = B * H
@@ -1510,7 +1511,7 @@ ttt_status validate_attn_fwd(const ttt_linear_attn_desc* d, const void* Q, const
   if (st != TTT_OK) return st;
   const AttnViews v = attn_views(d, Q, K, V, Z, g, W0, lens);
   const AttnPlan plan = attn_plan(d, false);
-  if (chains * plan.nseg > INT_MAX) return TTT_ERR_SHAPE;
+  if (chains * plan.nseg * 4 * d->d > kMaxThreads) return TTT_ERR_SHAPE;
   if (chains == 0) return TTT_OK;
   if (!g || !Wf) return TTT_ERR_NULL;
   if ((st = check_attn_views(d, v.q, v.k, v.v, v.z, true, 16)) != TTT_OK) return st;
@@ -1537,8 +1538,8 @@ ttt_status validate_attn_bwd(const ttt_linear_attn_desc* d, const void* Q, const
   const View dk = view(dK, d->B, d->Hkv, d->T, d->d, d->dk, d->out_dtype);
   const View dv = view(dV, d->B, d->Hkv, d->T, d->d, d->dv, d->out_dtype);
   const AttnPlan plan = attn_plan(d, true);
-  if (3 * chains * plan.nseg > INT_MAX) return TTT_ERR_SHAPE;                    // workgroups of the walks
-  if (2 * chains * d->T * (d->d / 4) / 256 > INT_MAX - 1) return TTT_ERR_SHAPE;  // and of the sums
+  if (3 * chains * plan.nseg * 4 * d->d > kMaxThreads) return TTT_ERR_SHAPE;  // the walks
+  if (d->H > d->Hkv && 2 * chains / (d->H / d->Hkv) * d->T * (d->d / 4) + chains > kMaxThreads) return TTT_ERR_SHAPE;  // the sums
   if (chains == 0) return TTT_OK;
   if (!g || !dg || !dW0) return TTT_ERR_NULL;
   if (!empty(dq) && (!dQ || !dK || !dV)) return TTT_ERR_NULL;
@@ -1575,6 +1576,7 @@ ttt_status validate_attn_decode(const ttt_linear_attn_desc* d, const void* Q, co
   ttt_status st = check_attn_desc(d, &chains);
   if (st != TTT_OK) return st;
   if (d->w0_batch_stride != 0) return TTT_ERR_STRIDE;
+  if (chains * 4 * d->d > kMaxThreads) return TTT_ERR_SHAPE;
   Range pos{nullptr, 0}, freqs{nullptr, 0};
   if (rope && (st = check_rope(rope, d->d, d->B, d->T, &pos, &freqs)) != TTT_OK) return st;
   if (chains == 0) return TTT_OK;
@@ -1607,7 +1609,7 @@ ttt_status validate_rotary(const ttt_rotary_desc* d, const ttt_rope* rope, const
   const int64_t heads = static_cast<int64_t>(d->H) + d->Hkv;
   int64_t n = 1;
   if (heads > INT_MAX || !mul_ok(n, d->B) || !mul_ok(n, d->T) || !mul_ok(n, d->d)) return TTT_ERR_SHAPE;
-  if (n / 256 >= INT_MAX || !mul_ok(n, heads)) return TTT_ERR_SHAPE;
+  if (n > kMaxThreads || !mul_ok(n, heads)) return TTT_ERR_SHAPE;
   Range pos, freqs;
   ttt_status st = check_rope(rope, d->d, d->B, d->T, &pos, &freqs);
   if (st != TTT_OK) return st;

@@ -12,7 +12,8 @@
 // 4n .. 16a + 4n + 3], so that each load of a wave covers 16 rows x 64 bytes, and the
 // row's product with q is finished by a quad sum.  q, k and v go through LDS as
 // fp32; with rotary positions q and k are turned there, so that a generated token
-// is one launch.
+// is one launch.  Measured on MI355X for B512 H32 d64 bf16 with rotary positions: 106 us, 5.07 TB/s of 537 MB
+// (a copy of 512 MiB reaches 5.3 TB/s); B16 H32: 5.6 us, most of it the launch and three dependent loads.
 #include <type_traits>
 
 #include "args_attn.h"
@@ -108,7 +109,8 @@ __global__ __launch_bounds__(4 * D) void ttt_attn_decode(AttnDecodeArgs a) {
 #pragma unroll
     for (int c = 0; c < NB; ++c) wp[4 * c] = w[c];
   }
-  for (int e = tid; e < (a.T - len) * D; e += 4 * D) put(z + (len + e / D) * a.os.t + e % D, 0.f);
+  for (int t = len + tid / D; t < a.T; t += 4)  // four rows of D a step
+    put(z + t * a.os.t + tid % D, 0.f);
 }
 
 template <int D>

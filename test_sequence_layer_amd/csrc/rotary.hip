@@ -7,7 +7,7 @@
 // A thread owns a piece of a row at one (sequence, token), computes its angles once
 // and walks the heads of q and of k with them, the next four heads' loads on their
 // way while it turns four; where there are too few tokens to fill the chip, the
-// heads are dealt out over blockIdx.y.  Three ways of cutting rows into pieces:
+// heads are dealt out over blockIdx.y.  Four ways of cutting rows into pieces:
 //   interleaved pairs, rows of whole 16-byte pieces: a piece, its pairs within it;
 //   halves of whole pieces: a piece, its partner from the lane that has it;
 //   other halves: a piece, the elements of the other half through LDS;
@@ -94,7 +94,7 @@ struct Heads {
 template <typename T, int WAY>
 __global__ __launch_bounds__(256) void ttt_rotary(RotaryArgs a) {
   constexpr int E = 16 / sizeof(T);
-    constexpr int HU = 4;  // heads a step: 212 us [B, H, T, d] and 222 [B, T, H, d]; 2: 208 and 234, 8: 232 and 218
+  constexpr int HU = 4;  // heads a step: 212 us [B, H, T, d] and 222 [B, T, H, d]; 2: 208 and 234, 8: 232 and 218
   const int rot = a.rope.rot, half = rot / 2;
   const int per = row_threads<T, WAY>(a.d, rot, a.in_place);
   const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;

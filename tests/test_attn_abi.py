@@ -280,3 +280,26 @@ def test_rotary_freqs():
                 dict(rot=8, scaling="linear", factor=0.5), dict(rot=8, scaling="yarn", factor=2.0, beta_fast=1.0)):
         with pytest.raises(ValueError):
             ttt.rotary_freqs(**bad)
+
+
+def test_threads_of_a_launch():
+    # 2^32 threads are refused, one workgroup less than that many is not
+    far = {n: (i + 1) << 44 for i, n in enumerate(["q", "k", "v", "g", "w0", "lens", "z", "wf", "ws", "dz", "dwf", "dq",
+                                                   "dk", "dv", "dg", "dw0", "w", "qo", "ko"])}
+    take = lambda names: {n: far[n] for n in names.split()}
+    f = {**take("q k v g w0 lens z wf ws"), "wsb": 1 << 43}
+    b = {**take("q k v g w0 lens dz dwf dq dk dv dg dw0 ws"), "wsb": 1 << 43}
+    n = 1 << 20
+    assert fwd(desc(B=n, H=16, Hkv=16, T=1), **f) == SHAPE
+    assert fwd(desc(B=n - 1, H=16, Hkv=16, T=1), **f) == OK
+    assert dec(desc(B=n, H=16, Hkv=16, T=1), **take("q k v g lens z w")) == SHAPE
+    assert dec(desc(B=n - 1, H=16, Hkv=16, T=1), **take("q k v g lens z w")) == OK
+    assert bwd(desc(B=n // 3 + 1, H=16, Hkv=16, T=1), **b) == SHAPE
+    assert bwd(desc(B=n // 3, H=16, Hkv=16, T=1), **b) == OK
+    # the sums over shared heads: B Hkv T d / 2 threads, and one for each decay's gradient
+    assert bwd(desc(B=1, H=4, Hkv=2, T=1 << 26), **b) == SHAPE
+    assert bwd(desc(B=1, H=4, Hkv=2, T=(1 << 26) - 16), **b) == OK
+    assert bwd(desc(B=1, H=4, Hkv=4, T=1 << 26), **b) == OK
+    r = rope(pos=None, sb=0, freqs=50 << 44)
+    assert rot(rdesc(B=1, H=1, Hkv=1, T=1 << 26), r, **take("q k qo ko")) == SHAPE
+    assert rot(rdesc(B=1, H=1, Hkv=1, T=(1 << 26) - 4), r, **take("q k qo ko")) == OK

@@ -473,3 +473,18 @@ def test_refusals_on_the_gpu(ttt):
     assert e.value.status == 11
     with pytest.raises(ValueError, match="one GPU"):
         ttt.linear_attn_fwd(**{**c, "log_decay": c["log_decay"].cpu()})
+
+
+def test_decode_zero_rows_past_32_bits(ttt):
+    # 2^24 + 8 rows of 128 elements, of which one sequence has a token: the rows behind it are zero to the last
+    T, d = (1 << 24) + 8, 128
+    gen = torch.Generator().manual_seed(5)
+    row = torch.randn(3, 1, 1, 1, d, generator=gen).to(BF16).cuda()
+    q, k, v = (x.expand(1, 1, T, d) for x in row)
+    w = torch.zeros(1, 1, d, d, device="cuda")
+    z = torch.full((1, 1, T, d), 7.0, dtype=BF16, device="cuda")
+    ttt.linear_attn_decode(q, k, v, torch.zeros(1, device="cuda"), w, lens=torch.tensor([1], dtype=torch.int32).cuda(), z=z)
+    assert torch.equal(w[0, 0], row[2].float().reshape(d, 1) * row[1].float().reshape(1, d))
+    assert z[0, 0, 0].abs().max() > 0
+    for part in z[0, 0, 1:].split(1 << 20):
+        assert int(torch.count_nonzero(part)) == 0
