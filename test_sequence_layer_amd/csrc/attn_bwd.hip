@@ -9,7 +9,9 @@
 // one fused reverse walk, each with one state (dQ's walk, with the decay's gradient, two)
 // instead of three, and no state kept in two layouts.  Measured on MI355X: a dQ launch and
 // a fused dK, dV, decay walk with its states in two layouts 173 us for B8 H12 T2048 d64 in
-// bf16, this 120 us; 410 us both at B16 H32 T2048; two launches, dK and dV first, 437 us.
+// bf16, this 120 us (108 us by now); 410 us both at B16 H32 T2048; two launches, dK and dV
+// first, 437 us.  Bound by issue slots there (88% busy, 68% vector instructions: parts of
+// states, scores and decayed values), with 1.48 GB moved in 406 us.
 //
 // The walks of dK and dV read the same rows at the same time, on the same XCD (unit_of):
 // the second finds them in its L2 (measured: 8.3 tensors fetched instead of 10).

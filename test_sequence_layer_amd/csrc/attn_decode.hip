@@ -12,7 +12,7 @@
 // 4n .. 16a + 4n + 3], so that each load of a wave covers 16 rows x 64 bytes, and the
 // row's product with q is finished by a quad sum.  q, k and v go through LDS as
 // fp32; with rotary positions q and k are turned there, so that a generated token
-// is one launch.  Measured on MI355X for B512 H32 d64 bf16 with rotary positions: 106 us, 5.07 TB/s of 537 MB
+// is one launch.  Measured on MI355X for B512 H32 d64 bf16 with rotary positions: 106 us, 5.15 TB/s of 545 MB
 // (a copy of 512 MiB reaches 5.3 TB/s); B16 H32: 5.6 us, most of it the launch and three dependent loads.
 #include <type_traits>
 
