@@ -1377,9 +1377,11 @@ ttt_status check_attn_desc(const ttt_linear_attn_desc* d, int64_t* chains) {
   return TTT_OK;
 }
 
-// From this many segments on a launch of its own carries their states on; below, each workgroup carries those
-// before its own (64 segments: 77 us against 99 for B1 H8 T32768, 6 segments: 52 us against 48 for B8 H12 T2048).
-constexpr int kCarry = 8;
+// From this many segments on a launch of its own carries their states on; below, each workgroup reads those before
+// its own.  T2048, us with that launch and without: d128 10 segments of 24 chains 46.9 and 49.9, gradients 136 and
+// 156; d64 16 segments of 24 chains 29.4 and 32.9, but 10 of 48 chains 33.6 and 30.4, gradients with 13 of 24 chains
+// 56 and 60; 16 segments of 24 chains at d32 22.5 and 19.2, at d16 20.1 and 16.1.
+int carry_from(int d, bool backward) { return d == 128 ? 8 : d == 64 ? (backward ? 8 : 16) : 24; }
 
 struct AttnPlan {
   int nseg, seglen;
@@ -1389,7 +1391,7 @@ struct AttnPlan {
 AttnPlan attn_plan(const ttt_linear_attn_desc* d, bool backward) {
   AttnPlan p;
   const int64_t chains = static_cast<int64_t>(d->B) * d->H, dd = static_cast<int64_t>(d->d) * d->d * 4;
-  const int n = ttt::attn_segments(chains, d->T, backward);
+  const int n = ttt::attn_segments(chains, d->T, d->d, d->in_dtype == TTT_F32 || d->d == 128, backward);
   const int c = ttt::kAttnChunk;
   p.seglen = ((d->T + n - 1) / n + c - 1) / c * c;
   if (p.seglen < c) p.seglen = c;
@@ -1670,7 +1672,7 @@ ttt_status ttt_linear_attn_fwd(const ttt_linear_attn_desc* desc, const void* Q, 
   a.loc = static_cast<float*>(workspace);
   a.Z = Z; a.W_final = W_final;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  a.carried = plan.nseg >= kCarry;
+  a.carried = plan.nseg >= carry_from(a.d, false);
   if (plan.nseg > 1 && ttt::launch_attn_states(a, s) != hipSuccess) return TTT_ERR_HIP;
   if (a.carried && ttt::launch_attn_carry(make_carry_args(desc, plan, log_decay, a.loc, false), s) != hipSuccess)
     return TTT_ERR_HIP;
@@ -1724,7 +1726,7 @@ ttt_status ttt_linear_attn_bwd(const ttt_linear_attn_desc* desc, const void* Q, 
   r.dks = r.parts ? packed : dks;
   r.dvs = r.parts ? packed : dvs;
   r.dg = dlog_decay; r.dW0 = dW0;
-  r.carried = plan.nseg >= kCarry;
+  r.carried = plan.nseg >= carry_from(r.d, true);
   if (plan.nseg > 1 && ttt::launch_attn_bwd_states(r, s) != hipSuccess) return TTT_ERR_HIP;
   if (r.carried && ttt::launch_attn_carry(make_carry_args(desc, plan, log_decay, r.loc, true), s) != hipSuccess)
     return TTT_ERR_HIP;

@@ -128,7 +128,7 @@ struct RotaryArgs {
 constexpr int kAttnChunk = 32;  // tokens per chunk of the chunked form
 
 bool attn_supported(int d);
-int attn_segments(int64_t chains, int T, bool backward);
+int attn_segments(int64_t chains, int T, int d, bool wide, bool backward);
 hipError_t launch_attn_states(const AttnArgs& a, hipStream_t s);
 hipError_t launch_attn_carry(const AttnCarryArgs& a, hipStream_t s);
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t s);

@@ -174,19 +174,25 @@ bool attn_supported(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 
 // Segments per sequence.  One workgroup walks a chain 32 tokens at a time, so a few chains leave most of the 256
 // CUs idle for long; segments fill them, at the price of a first pass over K and V (Q and dZ too in the
-// backward) and of carrying the states.  d = 64, bf16, [B, H, T, d]:
-//   forward, at most two workgroups a CU (512): B8 H12 T2048 46.6 us (at most 256: 58, 768: 51, none: 83); two
-//     segments for 300 chains would cost 100 us, none 85; 512 rounded up instead of down: 49.7
-//   backward, three walks a segment, at most 320 segments: B2 H32 T4096 144 us (256: 166, 512: 162, none: 232);
-//     two segments for 192 chains would cost 196 us, none 162
-// None shorter than 128 tokens (B1 H12 T200 gradients 20 us, 28 with 96; B1 H12 T512 17 us, 22 with 192), at most
-// 64 a sequence (B1 H1 T32768: 60 us, 105 with 256).
-int attn_segments(int64_t chains, int T, bool backward) {
+// backward), of carrying the states and of a launch.  us at T2048 in bf16, [B, H, T, d]:
+//   forward, 8 waves a CU (32768 / d workgroups at most): 96 chains d64 38.6 (half as many: 57.6, twice: 52.0, one
+//     segment a chain: 83), 200 chains d128 124 (twice: 173), d32 34 (half: 53), d16 23 (half: 25, a quarter: 45)
+//   backward, three walks a segment.  d128, 240 segments: 96 chains 320 (320: 350, 160: 371).  d64, 320: 96 chains 113
+//     (160: 125, 640: 131).  d32, 384: 200 chains 95 (640: 107), 96 chains 60 with 640, 70 with 320.  d16, 640: 300
+//     chains 79 (320: 98), 400 chains 99 (960: 105).
+// Shortest segment.  wide (fp32 inputs or d = 128): 3 chunks of 32 tokens, from 6 chunks on (12 chains T1009 d128 fp32:
+// 47, 4 chunks 52, 6 chunks 56; T200 28 to 31 for 33, gradients 63 to 71 for 94).  Otherwise 4 chunks, from 12 on
+// (T330: 15.9 for 15.8, T512: 16.1 for 20.6; T200 would cost 16 for 12, gradients 26 for 19).  At most 64 segments
+// (B1 H1 T32768: 60, 105 with 256).
+int attn_segments(int64_t chains, int T, int d, bool wide, bool backward) {
   if (chains <= 0 || T <= 0) return 1;
-  int64_t n = (backward ? 320 : 512) / chains;
-  const int64_t most = T / 128 < 64 ? T / 128 : 64;
-  if (n > most) n = most;
-  return n < 1 ? 1 : static_cast<int>(n);
+  const int all = !backward ? 32768 / d : d == 128 ? 240 : d == 64 ? 320 : d == 32 ? 384 : 640;
+  const int chunks = (T + kAttnChunk - 1) / kAttnChunk;
+  if (chunks < (wide ? 6 : 12)) return 1;
+  int64_t most = wide ? (chunks + 2) / 3 : chunks / 4;
+  if (most > 64) most = 64;
+  const int64_t n = all / chains;
+  return n < 1 ? 1 : static_cast<int>(n < most ? n : most);
 }
 
 hipError_t launch_attn_states(const AttnArgs& a, hipStream_t s) {

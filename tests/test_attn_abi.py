@@ -303,3 +303,23 @@ def test_threads_of_a_launch():
     r = rope(pos=None, sb=0, freqs=50 << 44)
     assert rot(rdesc(B=1, H=1, Hkv=1, T=1 << 26), r, **take("q k qo ko")) == SHAPE
     assert rot(rdesc(B=1, H=1, Hkv=1, T=(1 << 26) - 4), r, **take("q k qo ko")) == OK
+
+
+def test_few_chains_are_walked_in_segments():
+    """A workspace of one state a segment and chain (three in the backward, and the decay's sums)."""
+    def segments(backward, **kw):
+        d = desc(Hkv=kw["H"], outd=kw.get("ind", 1), **kw)
+        need = L.ttt_linear_attn_workspace_bytes(ctypes.byref(d), backward)
+        state = d.B * d.H * d.d * d.d * 4
+        return need // (3 * state if backward else state)
+    for backward in (0, 1):
+        for T, n in ((1, 0), (352, 0), (353, 3), (384, 3), (512, 4), (1 << 20, 64)):
+            assert segments(backward, B=1, H=2, T=T) == n, (backward, T)
+        for T, n in ((160, 0), (161, 2), (288, 3), (289, 4)):
+            assert segments(backward, B=1, H=2, T=T, ind=0) == n
+            assert segments(backward, B=1, H=2, T=T, d=128) == n
+    for d, n in ((16, 64), (32, 32), (64, 16), (128, 8)):
+        assert segments(0, B=2, H=16, T=1 << 16, d=d) == n
+    for d, n in ((16, 20), (32, 12), (64, 10), (128, 7)):
+        assert segments(1, B=2, H=16, T=1 << 16, d=d) == n
+    assert segments(0, B=32, H=16, T=1 << 16) == 0 == segments(1, B=21, H=16, T=1 << 16)

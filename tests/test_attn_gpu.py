@@ -77,7 +77,7 @@ def check_bwd(ttt, c, out, dw=True, **more):
     return got
 
 
-# lengths around the block (16) and chunk (32), segments (from 256 tokens on with this few chains), odd ones
+# lengths around the block (16) and chunk (32), segments (from 353 tokens on with this few chains), odd ones
 LENGTHS = [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 100, 255, 256, 257, 300, 515]
 
 
@@ -101,6 +101,17 @@ def test_backward_lengths(ttt, T):
 def test_backward_types(ttt, d, dtype, out):
     check_bwd(ttt, case(2, 3, 3, 77, d, dtype, seed=d, w0="shared"), out)
     check_bwd(ttt, case(1, 4, 2, 290, d, dtype, seed=d + 1, w0="none", scale=-0.3), out, dw=False)
+
+
+# segments of 3 or 4 chunks whose states the workgroups carry over themselves, then so many that a launch does
+@pytest.mark.parametrize("d,dtype,T", [(32, F32, 200), (128, BF16, 330), (64, BF16, 384), (16, BF16, 1000),
+                                       (128, BF16, 800), (64, F32, 1500), (64, BF16, 2081), (32, F32, 2300),
+                                       (16, BF16, 3200)])
+def test_segments(ttt, d, dtype, T):
+    for lens in (None, [T * 2 // 3, T - 1]):
+        c = case(2, 2, 1, T, d, dtype, seed=T, lens=lens)
+        check_fwd(ttt, c, dtype)
+        check_bwd(ttt, c, dtype)
 
 
 DECAYS = [0.0, float("-inf"), -1e-7, -1e-3, -0.7, -30.0, -1e4, 1e-3]
