@@ -1119,6 +1119,8 @@ def _attn_fwd(q, k, v, log_decay, w0, scale, lens, out_dtype, w_final, z, worksp
     dev = q.device
     if z is None:
         z = _like(q, torch.float32 if out_dtype is None else out_dtype)
+    elif out_dtype is not None and z.dtype != out_dtype:
+        raise ValueError(f"z is {z.dtype}, out_dtype {out_dtype}")
     desc, need, _ = _attn_desc(q, k, v, log_decay, w0, lens, scale, z)
     shape = (desc.B, desc.H, desc.d, desc.d)
     if w_final is None:
@@ -1209,6 +1211,8 @@ def _attn_decode(q, k, v, log_decay, w, scale, lens, rope, out_dtype, z, stream)
     torch = _torch()
     if z is None:
         z = _like(q, torch.float32 if out_dtype is None else out_dtype)
+    elif out_dtype is not None and z.dtype != out_dtype:
+        raise ValueError(f"z is {z.dtype}, out_dtype {out_dtype}")
     desc, _, _ = _attn_desc(q, k, v, log_decay, None, lens, scale, z)
     _want(w, (desc.B, desc.H, desc.d, desc.d), torch.float32, "w")
     turn = None if rope is None else ctypes.byref(_rope(q, *rope))

@@ -499,3 +499,14 @@ def test_decode_zero_rows_past_32_bits(ttt):
     assert z[0, 0, 0].abs().max() > 0
     for part in z[0, 0, 1:].split(1 << 20):
         assert int(torch.count_nonzero(part)) == 0
+
+
+def test_output_of_another_type_is_refused(ttt):
+    c = on_gpu(case(1, 1, 1, 5, 16, BF16, w0="none"))
+    z = torch.empty_like(c["q"], dtype=F32)
+    with pytest.raises(ValueError, match="out_dtype"):
+        ttt.linear_attn_fwd(**c, z=z, out_dtype=BF16)
+    with pytest.raises(ValueError, match="out_dtype"):
+        ttt.linear_attn_decode(c["q"], c["k"], c["v"], c["log_decay"], torch.zeros(1, 1, 16, 16, device=DEV), z=z,
+                               out_dtype=BF16)
+    assert ttt.linear_attn_fwd(**c, z=z)[0] is z and ttt.linear_attn_fwd(**c, z=z, out_dtype=F32)[0] is z
