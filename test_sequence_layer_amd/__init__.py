@@ -1016,6 +1016,7 @@ def _layout(x):
 def _attn_desc(q, k, v, log_decay, w0, lens, scale, z, grads=()):
     """(descriptor, forward workspace bytes, backward workspace bytes) of a linear-attention call; z: Z or dZ,
     grads: dq, dk, dv."""
+    scale = float(scale)  # (a tensor's value at this call: as a key it would stand for itself)
     key = (q.shape, q.stride(), q.dtype, k.shape, k.stride(), k.dtype, v.shape, v.stride(), v.dtype, log_decay.shape,
            log_decay.stride(), log_decay.dtype, _layout(w0), _layout(lens), scale, z.shape, z.stride(), z.dtype,
            *map(_layout, grads))
