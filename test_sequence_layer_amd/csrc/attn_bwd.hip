@@ -38,9 +38,9 @@ constexpr int max2(int a, int b) { return a > b ? a : b; }
 template <int D, typename QT, typename ZT, typename OT>
 __global__ __launch_bounds__(4 * D, 2) void ttt_attn_bwd(AttnBwdArgs a) {
   constexpr int NB = D / 16;
-  constexpr int kLds = max2(WalkLds<D, true, true, ZT, QT, QT, QT, ZT>::kSize,
-                            max2(WalkLds<D, true, false, QT, ZT, QT, QT, OT>::kSize,
-                                 WalkLds<D, true, false, QT, QT, ZT, QT, OT>::kSize));
+  constexpr int kLds = max2(WalkLds<D, true, true, ZT, QT, QT, QT>::kSize,
+                            max2(WalkLds<D, true, false, QT, ZT, QT, QT>::kSize,
+                                 WalkLds<D, true, false, QT, QT, ZT, QT>::kSize));
   __shared__ __align__(16) uint16_t lds[kLds];
   __shared__ float powers[15 + C + 1];
   const float* pw = powers + 15;
@@ -192,7 +192,7 @@ template <int D, typename QT, typename ZT>
 __global__ __launch_bounds__(4 * D) void ttt_attn_bwd_states(AttnBwdArgs a) {
   constexpr int NB = D / 16;
   constexpr int kLds =
-      max2(WalkLds<D, false, true, QT, QT, QT, QT, QT>::kSize, WalkLds<D, false, false, QT, ZT, QT, QT, QT>::kSize);
+      max2(WalkLds<D, false, true, QT, QT, QT, QT>::kSize, WalkLds<D, false, false, QT, ZT, QT, QT>::kSize);
   __shared__ __align__(16) uint16_t lds[kLds];
   __shared__ float powers[15 + C + 1];
   const float* pw = powers + 15;

@@ -10,13 +10,18 @@
 // operand at once; products of bf16 values are exact and sums are fp32.
 //
 // Parts.  An fp32 operand (an fp32 input, the state, a score, a decayed value) is
-// the sum of bf16 parts, each the rounding of what the parts before it leave, so
-// that n parts are off by at most 2^-8n: half a bf16 step, n times.  A product of
-// level LV takes the part pairs (p, q) with p + q < LV: level 3 is an fp32 product
-// (2^-24), level 2 is off by 2^-16, 1/256 of what rounding the output to bf16
-// costs.  States and fp32 outputs are level 3, products that only a bf16 output
-// depends on are level 2.  The fp32 matrix instruction (v_mfma_f32_16x16x4_f32)
-// does the same at 1/16 of the bf16 rate: six part pairs take 3/8 of its time.
+// the sum of three bf16 parts, each the rounding of what the parts before it leave:
+// half a bf16 step, three times, so that less than 2^-24 is left.  A product takes the
+// part pairs (p, q) with p + q < 3, six of nine; the others are below 2^-24 of it.  With
+// a bf16 operand, which is its own single part, it is three of three.  The fp32 matrix
+// instruction (v_mfma_f32_16x16x4_f32) does the same at 1/16 of the bf16 rate: six part
+// pairs take 3/8 of its time.  Outputs of bf16 take three parts as well: with two (2^-16
+// of the sum of the terms' magnitudes) terms that cancel leave the bits that were cut
+// off, and 0.25% of ordinary bf16 outputs round to the neighbouring value, with three
+// 0.02%.  What that costs, two parts and three: B16 H32 T8192 d64 [B, H, T, d] 431 and
+// 498 us, [B, T, H, d] 501 and 492, gradients at T2048 406 and 434.
+// An fp32 value above bf16's largest (3.39e38) rounds to an infinite first part, and an
+// infinity leaves NaN behind its first part: both come out as NaN.
 #pragma once
 
 #include "args_attn.h"
@@ -35,11 +40,10 @@ using mfma::u32x4;
 constexpr int C = kAttnChunk;
 typedef bf16x4 Frag;
 
-// parts of an input of type T, and the level of products that only an output of type T depends on
+constexpr int kParts = 3;  // of an fp32 value
+// parts of an input of type T
 template <typename T>
-__host__ __device__ constexpr int parts_of() { return sizeof(T) == 2 ? 1 : 3; }
-template <typename T>
-__host__ __device__ constexpr int level_of() { return sizeof(T) == 2 ? 2 : 3; }
+__host__ __device__ constexpr int parts_of() { return sizeof(T) == 2 ? 1 : kParts; }
 
 __device__ __forceinline__ float4v widen(Frag x) {
   const u32x2 w = __builtin_bit_cast(u32x2, x);
@@ -66,7 +70,7 @@ __device__ __forceinline__ float4v mm2(Frag a0, Frag a1, Frag b0, Frag b1, float
 }
 
 // c += a . x over one contraction block: two part pairs per instruction
-template <int NA, int NX, int LV>
+template <int NA, int NX>
 __device__ __forceinline__ float4v dot1(const Frag a[NA], const Frag x[NX], float4v c) {
   Frag l[8], r[8];
   int n = 0;
@@ -74,7 +78,7 @@ __device__ __forceinline__ float4v dot1(const Frag a[NA], const Frag x[NX], floa
   for (int p = 0; p < NA; ++p)
 #pragma unroll
     for (int q = 0; q < NX; ++q)
-      if (p + q < LV) {
+      if (p + q < kParts) {
         l[n] = a[p];
         r[n] = x[q];
         ++n;
@@ -90,14 +94,14 @@ __device__ __forceinline__ float4v dot1(const Frag a[NA], const Frag x[NX], floa
 }
 
 // c += a0 . x0 + a1 . x1, two contraction blocks
-template <int NA, int NX, int LV>
+template <int NA, int NX>
 __device__ __forceinline__ float4v dot2(const Frag a0[NA], const Frag a1[NA], const Frag x0[NX], const Frag x1[NX],
                                         float4v c) {
 #pragma unroll
   for (int p = 0; p < NA; ++p)
 #pragma unroll
     for (int q = 0; q < NX; ++q)
-      if (p + q < LV) c = mm2(a0[p], a1[p], x0[q], x1[q], c);
+      if (p + q < kParts) c = mm2(a0[p], a1[p], x0[q], x1[q], c);
   return c;
 }
 
@@ -155,7 +159,7 @@ struct Tile {
 };
 
 // A 16 x 16 block of A B^T: lane holds [4g + r of A's rows][li of B's rows].  a, x: the first of the 16 rows.
-template <int D, int NA, int NX, int LV>
+template <int D, int NA, int NX>
 __device__ __forceinline__ float4v rows_dot(const uint16_t* a, const uint16_t* x, const Places<D>& at) {
   constexpr int NB = D / 16;
   float4v c = mfma::zero4v();
@@ -163,7 +167,7 @@ __device__ __forceinline__ float4v rows_dot(const uint16_t* a, const uint16_t* x
     Frag f[NA], h[NX];
     Tile<D, NA>::rows(a + at.row[0], f);
     Tile<D, NX>::rows(x + at.row[0], h);
-    c = dot1<NA, NX, LV>(f, h, c);
+    c = dot1<NA, NX>(f, h, c);
   } else {
 #pragma unroll
     for (int k = 0; k < NB; k += 2) {
@@ -172,7 +176,7 @@ __device__ __forceinline__ float4v rows_dot(const uint16_t* a, const uint16_t* x
       Tile<D, NA>::rows(a + at.row[k + 1], f1);
       Tile<D, NX>::rows(x + at.row[k], h0);
       Tile<D, NX>::rows(x + at.row[k + 1], h1);
-      c = dot2<NA, NX, LV>(f0, f1, h0, h1, c);
+      c = dot2<NA, NX>(f0, f1, h0, h1, c);
     }
   }
   return c;
@@ -194,11 +198,11 @@ struct Slab {
       *reinterpret_cast<u32x2*>(t + u0) = u32x2{r[0][0], r[0][1]};
       *reinterpret_cast<u32x2*>(t + u1) = u32x2{r[0][2], r[0][3]};
     } else {
-      Frag f[2][3];
+      Frag f[2][kParts];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) split<3>(__builtin_bit_cast(float4v, r[i]), f[i]);
+      for (int i = 0; i < 2; ++i) split<kParts>(__builtin_bit_cast(float4v, r[i]), f[i]);
 #pragma unroll
-      for (int p = 0; p < 3; ++p) {
+      for (int p = 0; p < kParts; ++p) {
         *reinterpret_cast<bf16x4*>(t + p * PLANE + u0) = f[0][p];
         *reinterpret_cast<bf16x4*>(t + p * PLANE + u1) = f[1][p];
       }

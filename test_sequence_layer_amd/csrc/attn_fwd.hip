@@ -23,7 +23,7 @@ __device__ __forceinline__ const T* at(const void* p, const Strides3& s, int b, 
 template <int D, typename IT, typename OT>
 __global__ __launch_bounds__(4 * D, 2) void ttt_attn_fwd(AttnArgs a) {
   constexpr int NB = D / 16;
-  __shared__ __align__(16) uint16_t lds[WalkLds<D, true, false, IT, IT, IT, IT, OT>::kSize];
+  __shared__ __align__(16) uint16_t lds[WalkLds<D, true, false, IT, IT, IT, IT>::kSize];
   __shared__ float powers[15 + C + 1];
   const float* pw = powers + 15;
   const int tid = threadIdx.x, w = tid / 64, lane = tid % 64, li = lane % 16, g4 = lane / 16;
@@ -79,7 +79,7 @@ __global__ __launch_bounds__(4 * D, 2) void ttt_attn_fwd(AttnArgs a) {
 template <int D, typename IT>
 __global__ __launch_bounds__(4 * D) void ttt_attn_states(AttnArgs a) {
   constexpr int NB = D / 16;
-  __shared__ __align__(16) uint16_t lds[WalkLds<D, false, false, IT, IT, IT, IT, IT>::kSize];
+  __shared__ __align__(16) uint16_t lds[WalkLds<D, false, false, IT, IT, IT, IT>::kSize];
   __shared__ float powers[15 + C + 1];
   const float* pw = powers + 15;
   const int tid = threadIdx.x, w = tid / 64, lane = tid % 64, li = lane % 16, g4 = lane / 16;

@@ -64,7 +64,7 @@ struct Walk {
 };
 
 // LDS of a walk: tiles of X (with outputs), Y, V and Q (with the decay's gradient), and score blocks
-template <int D, bool OUT, bool DG, typename XT, typename YT, typename VT, typename QT, typename OT>
+template <int D, bool OUT, bool DG, typename XT, typename YT, typename VT, typename QT>
 struct WalkLds {
   static constexpr int kX = OUT ? Tile<D, parts_of<XT>()>::kSize : 0;
   static constexpr int kY = Tile<D, parts_of<YT>()>::kSize;
@@ -74,9 +74,7 @@ struct WalkLds {
   static constexpr bool kRing = sizeof(XT) + sizeof(YT) + sizeof(VT) == 6 && !(DG && OUT && D == 128);
   static constexpr int kBufs = kRing ? 2 : 1;
   static constexpr bool kScoresFirst = kRing && D == 64;  // where the barrier behind the scores stands
-  static constexpr int kLevel = DG ? 3 : level_of<OT>();  // of outputs: parts of scores and of the state for them
-  static constexpr int kScoreHalf = 3 * kLevel * 64 * 4;  // a chunk's score blocks
-  static constexpr int kScores = OUT ? kScoreHalf : 0;
+  static constexpr int kScores = OUT ? 3 * kParts * 64 * 4 : 0;  // a chunk's score blocks
   static constexpr int kSize = kBufs * kChunk + kScores;
 };
 
@@ -85,14 +83,14 @@ struct WalkLds {
 template <int D, bool OUT, bool DG, typename XT, typename YT, typename VT, typename QT, typename OT>
 __device__ __forceinline__ void walk(const Walk<XT, YT, VT, QT, OT>& a, bool fresh, uint16_t* lds, const float* pw,
                                      float4v s[D / 16], float4v u[D / 16], double& dg) {
-  typedef WalkLds<D, OUT, DG, XT, YT, VT, QT, OT> Lds;
+  typedef WalkLds<D, OUT, DG, XT, YT, VT, QT> Lds;
   constexpr int NB = D / 16, NX = parts_of<XT>(), NY = parts_of<YT>(), NV = parts_of<VT>(), NQ = parts_of<QT>();
   typedef Tile<D, NX> TX;
   typedef Tile<D, NY> TY;
   typedef Tile<D, NV> TV;
   typedef Tile<D, NQ> TQ;
   constexpr int kPlane = TX::kPlane, kHalf = half_at<D>();
-  constexpr int LO = Lds::kLevel, NP = LO;
+  constexpr int NP = kParts;  // of scores and of the state
 
   const int tid = threadIdx.x, w = tid / 64, lane = tid % 64, li = lane % 16, g4 = lane / 16;
   const int nfull = a.n / C, nch = (a.n + C - 1) / C;
@@ -154,13 +152,13 @@ __device__ __forceinline__ void walk(const Walk<XT, YT, VT, QT, OT>& a, bool fre
     float dgc = 0.f;
     auto block = [&](int t) __attribute__((always_inline)) {
       const int rj = t == 2 ? kHalf : 0, ri = t == 0 ? 0 : kHalf;
-      float4v c = rows_dot<D, NY, NX, LO>(Y + rj, X + ri, at);
+      float4v c = rows_dot<D, NY, NX>(Y + rj, X + ri, at);
       float4v f;  // sp lambda^{i-j}, or what stands before lambda^0 in the table
       const float* pt = pw + (t == 1 ? 16 : 0) + li - 4 * g4;
 #pragma unroll
       for (int r = 0; r < 4; ++r) f[r] = a.sp * pt[-r];
       if constexpr (DG) {  // pairs within the chunk
-        const float4v k = rows_dot<D, NV, NQ, 3>(V + rj, Q + ri, at);
+        const float4v k = rows_dot<D, NV, NQ>(V + rj, Q + ri, at);
         const bool live = n * C + (t == 0 ? 0 : 16) + li < a.n;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -219,16 +217,16 @@ __device__ __forceinline__ void walk(const Walk<XT, YT, VT, QT, OT>& a, bool fre
           split<NP>(st[k], a0);
           TX::rows(X + at.row[k], x0);
           if constexpr (NB == 1) {
-            o0 = dot1<NP, NX, LO>(a0, x0, o0);
+            o0 = dot1<NP, NX>(a0, x0, o0);
             TX::rows(X + kHalf + at.row[k], x0);
-            o1 = dot1<NP, NX, LO>(a0, x0, o1);
+            o1 = dot1<NP, NX>(a0, x0, o1);
           } else {
             split<NP>(st[k + 1], a1);
             TX::rows(X + at.row[k + 1], x1);
-            o0 = dot2<NP, NX, LO>(a0, a1, x0, x1, o0);
+            o0 = dot2<NP, NX>(a0, a1, x0, x1, o0);
             TX::rows(X + kHalf + at.row[k], x0);
             TX::rows(X + kHalf + at.row[k + 1], x1);
-            o1 = dot2<NP, NX, LO>(a0, a1, x0, x1, o1);
+            o1 = dot2<NP, NX>(a0, a1, x0, x1, o1);
           }
         }
       };
@@ -256,23 +254,23 @@ __device__ __forceinline__ void walk(const Walk<XT, YT, VT, QT, OT>& a, bool fre
       const uint16_t* P = scores;
 #pragma unroll
       for (int m = 0; m < NP; ++m) p0[m] = *reinterpret_cast<const bf16x4*>(P + 256 * m);
-      z0 = dot1<NV, NP, LO>(v0, p0, z0);
+      z0 = dot1<NV, NP>(v0, p0, z0);
 #pragma unroll
       for (int m = 0; m < NP; ++m) {
         p0[m] = *reinterpret_cast<const bf16x4*>(P + 256 * (NP + 2 * m));
         p1[m] = *reinterpret_cast<const bf16x4*>(P + 256 * (NP + 2 * m + 1));
       }
-      z1 = dot2<NV, NP, LO>(v0, v1, p0, p1, z1);
+      z1 = dot2<NV, NP>(v0, v1, p0, p1, z1);
       if (full || li < L) store4(op, z0);
       if (full || 16 + li < L) store4(op + 16 * a.ot, z1);
       op += C * a.ot;
     }
     // S = lambda^L S + (decayed V)^T Y
     {
-      Frag q0[3], q1[3], d0[3], d1[3];
+      Frag q0[NP], q1[NP], d0[NP], d1[NP];
       const float4v x0 = TV::sum(v0) * f0, x1 = TV::sum(v1) * f1;
-      split<3>(x0, q0);
-      split<3>(x1, q1);
+      split<NP>(x0, q0);
+      split<NP>(x1, q1);
       if constexpr (DG) {
         float4v m0, m1;
 #pragma unroll
@@ -281,16 +279,16 @@ __device__ __forceinline__ void walk(const Walk<XT, YT, VT, QT, OT>& a, bool fre
           m0[r] = x0[r] * static_cast<float>(left);
           m1[r] = x1[r] * static_cast<float>(left - 16);
         }
-        split<3>(m0, d0);
-        split<3>(m1, d1);
+        split<NP>(m0, d0);
+        split<NP>(m1, d1);
       }
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
         Frag y0[NY], y1[NY];
         TY::cols(Y + at.col[k], y0);
         TY::cols(Y + kHalf + at.col[k], y1);
-        if constexpr (DG) u[k] = dot2<NY, 3, 3>(y0, y1, d0, d1, (u[k] + s[k] * static_cast<float>(L)) * e);
-        s[k] = dot2<NY, 3, 3>(y0, y1, q0, q1, s[k] * e);
+        if constexpr (DG) u[k] = dot2<NY, NP>(y0, y1, d0, d1, (u[k] + s[k] * static_cast<float>(L)) * e);
+        s[k] = dot2<NY, NP>(y0, y1, q0, q1, s[k] * e);
       }
     }
     if constexpr (D == 64) prio_valu();
