@@ -61,7 +61,6 @@ __global__ __launch_bounds__(4 * D, 2) void ttt_attn_bwd(AttnBwdArgs a) {
   const int sb = seg * a.seglen, se = min(sb + a.seglen, a.T);
   const int n = max(0, min(len, se) - sb);
   const int64_t dd = static_cast<int64_t>(D) * D;
-  const float em = powl(lg, a.seglen);
   const float* loc = a.loc + static_cast<int64_t>(chain) * a.nseg * 3 * dd;
   const int pad0 = max(len, sb);  // padding rows among this segment's
 
@@ -77,14 +76,18 @@ __global__ __launch_bounds__(4 * D, 2) void ttt_attn_bwd(AttnBwdArgs a) {
       load_state<D>(loc + (seg - 1) * 3 * dd, false, w, li, g4, s);
       load_state<D>(loc + (seg - 1) * 3 * dd + dd, false, w, li, g4, u);
     }
-    for (int c = 0; c < seg && n > 0 && !a.carried; ++c) {
-      float4v x[NB], y[NB];
-      load_state<D>(loc + c * 3 * dd, false, w, li, g4, x);
-      load_state<D>(loc + c * 3 * dd + dd, false, w, li, g4, y);
+    if (n > 0 && !a.carried && seg > 0) {
+      const SegmentDecay e(lg, a.seglen);
+      const float sl = static_cast<float>(a.seglen);
+      for (int c = 0; c < seg; ++c) {
+        float4v x[NB], y[NB];
+        load_state<D>(loc + c * 3 * dd, false, w, li, g4, x);
+        load_state<D>(loc + c * 3 * dd + dd, false, w, li, g4, y);
 #pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        u[i] = (u[i] + s[i] * static_cast<float>(a.seglen)) * em + y[i];
-        s[i] = s[i] * em + x[i];
+        for (int i = 0; i < NB; ++i) {
+          u[i] = e.carry(u[i] + s[i] * sl, y[i]);
+          s[i] = e.carry(s[i], x[i]);
+        }
       }
     }
     __syncthreads();
@@ -134,7 +137,8 @@ __global__ __launch_bounds__(4 * D, 2) void ttt_attn_bwd(AttnBwdArgs a) {
     fresh = true;
   }
   if (n > 0 && a.carried && seg > 0) load_state<D>(loc + (seg - 1) * 3 * dd + 2 * dd, pl.kind == 2, w, li, g4, s);
-  if (n > 0 && !a.carried) carry_states<D>(loc + 2 * dd, 3 * dd, seg, em, pl.kind == 2, w, li, g4, s);
+  if (n > 0 && !a.carried && seg > 0)
+    carry_states<D>(loc + 2 * dd, 3 * dd, seg, SegmentDecay(lg, a.seglen), pl.kind == 2, w, li, g4, s);
   __syncthreads();
   const int64_t t0 = len - 1 - sb;  // (only for a walk of at least one token)
   const int ho = a.parts ? h : hk;

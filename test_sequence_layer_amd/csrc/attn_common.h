@@ -235,6 +235,25 @@ struct Decays {
   }
 };
 
+// lambda^n of a whole segment, n > 0, in two fp32 parts: one rounded power, taken by up to 63 segments one after the
+// other, would be off the same way in each (64 segments of 512 tokens, log_decay -3e-5: the oldest tokens' share is
+// off by 29 steps of 2^-24, in two parts by 1).
+struct SegmentDecay {
+  float hi, lo;
+  __device__ __forceinline__ SegmentDecay(float g, int n) {
+    const double p = exp(static_cast<double>(g) * n);
+    hi = static_cast<float>(p);
+    lo = hi <= 3.0e38f ? static_cast<float>(p - static_cast<double>(hi)) : 0.f;
+  }
+  // s lambda^n + x, rounded once
+  __device__ __forceinline__ float4v carry(float4v s, float4v x) const {
+    float4v r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = fmaf(s[i], hi, fmaf(s[i], lo, x[i]));
+    return r;
+  }
+};
+
 // Workgroup -> unit and kind of work: kinds change every 8 units.  Workgroups go round the eight XCDs, so the
 // kinds of one unit run on the same XCD, at about the same time.
 struct Unit {
@@ -264,7 +283,7 @@ __device__ __forceinline__ void load_state(const float* p, bool transposed, int 
 }
 // s carried over n segments: s <- e s + (the c-th state at p + c step), four loads at a time on their way.
 template <int D>
-__device__ __forceinline__ void carry_states(const float* p, int64_t step, int n, float e, bool transposed, int w, int li,
+__device__ __forceinline__ void carry_states(const float* p, int64_t step, int n, SegmentDecay e, bool transposed, int w, int li,
                                              int g, float4v s[D / 16]) {
   constexpr int U = D <= 64 ? 4 : 2;
   int c = 0;
@@ -275,13 +294,13 @@ __device__ __forceinline__ void carry_states(const float* p, int64_t step, int n
 #pragma unroll
     for (int i = 0; i < U; ++i)
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) s[k] = s[k] * e + x[i][k];
+      for (int k = 0; k < D / 16; ++k) s[k] = e.carry(s[k], x[i][k]);
   }
   for (; c < n; ++c) {
     float4v x[D / 16];
     load_state<D>(p + c * step, transposed, w, li, g, x);
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) s[k] = s[k] * e + x[k];
+    for (int k = 0; k < D / 16; ++k) s[k] = e.carry(s[k], x[k]);
   }
 }
 template <int D>

@@ -42,10 +42,10 @@ __global__ __launch_bounds__(4 * D, 2) void ttt_attn_fwd(AttnArgs a) {
     if (a.W0) load_state<D>(a.W0 + b * a.w0_bstride + static_cast<int64_t>(h) * D * D, false, w, li, g4, s);
   } else {
     const float* loc = a.loc + static_cast<int64_t>(chain) * a.nseg * D * D;
-    const float em = powl(lg, a.seglen);
     if (seg == 0) load_state<D>(loc + static_cast<int64_t>(a.nseg - 1) * D * D, false, w, li, g4, s);
     if (n > 0 && a.carried && seg > 0) load_state<D>(loc + static_cast<int64_t>(seg - 1) * D * D, false, w, li, g4, s);
-    if (n > 0 && !a.carried) carry_states<D>(loc, static_cast<int64_t>(D) * D, seg, em, false, w, li, g4, s);
+    if (n > 0 && !a.carried && seg > 0)
+      carry_states<D>(loc, static_cast<int64_t>(D) * D, seg, SegmentDecay(lg, a.seglen), false, w, li, g4, s);
   }
   __syncthreads();
 
@@ -125,7 +125,8 @@ __global__ __launch_bounds__(256) void ttt_attn_carry(AttnCarryArgs a) {
   const int64_t at = grad ? id - a.chains * quads : id, chain = at / quads;
   const int64_t dd = static_cast<int64_t>(a.d) * a.d, step = a.backward ? 3 * dd : dd;
   float* p = a.loc + chain * a.nseg * step + 4 * (at % quads) + (grad ? 2 * dd : 0);
-  const float e = powl(a.log_decay[chain % a.H], a.seglen), len = static_cast<float>(a.seglen);
+  const SegmentDecay e(a.log_decay[chain % a.H], a.seglen);
+  const float len = static_cast<float>(a.seglen);
   float4v s = mfma::zero4v(), u = s;
   const bool with_u = a.backward && !grad;
   for (int c = 0; c < a.nseg - 1; c += U) {
@@ -140,8 +141,8 @@ __global__ __launch_bounds__(256) void ttt_attn_carry(AttnCarryArgs a) {
     for (int i = 0; i < U; ++i) {
       if (c + i >= a.nseg - 1) break;
       const int64_t k = (c + i) * step;
-      u = (u + s * len) * e + y[i];
-      s = s * e + x[i];
+      u = e.carry(u + s * len, y[i]);
+      s = e.carry(s, x[i]);
       *reinterpret_cast<float4v*>(p + k) = s;
       if (with_u) *reinterpret_cast<float4v*>(p + k + dd) = u;
     }
