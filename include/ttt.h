@@ -564,8 +564,9 @@ ttt_status ttt_mlp_ln_decode_validate(const ttt_mlp_desc* desc, const void* Q, c
  *    1 are not looked at.  Inputs may repeat (stride 0).  For ttt_linear_attn_fwd
  *    and _bwd every base address and stride is a multiple of 16 bytes
  *    (TTT_ERR_ALIGN), for the others of the element's size.
- *  - Outputs share no element with an input or another output (TTT_ERR_ALIAS);
- *    slices of the same rows ([B, T, 3, H, d]) are apart.
+ *  - Outputs share no element with an input or another output (TTT_ERR_ALIAS).
+ *    Tensors whose ranges interleave pass if they are slices of the same rows:
+ *    of sequences, tokens or heads ([B, 3, H, T, d], [B, T, 3, H, d], [B, T, H, 3, d]).
  *  - lens: [B] int32 on the device, the tokens of each sequence (taken into
  *    [0, T]), or NULL for T each.  Rows behind the last token are not read; their
  *    outputs and gradients are written as zero; the state is that after the last

@@ -1292,10 +1292,8 @@ ttt::Strides3 strides(const View& v) { return ttt::Strides3{v.s.b, v.s.h, v.s.t}
 
 bool empty(const View& v) { return v.B == 0 || v.H == 0 || v.T == 0; }
 
-// elements from the first to behind the last, with the heads, tokens and sequences named
-int64_t extent(const View& v, bool tokens = true, bool batch = true) {
-  return (v.H - 1) * v.s.h + (tokens ? (v.T - 1) * v.s.t : 0) + (batch ? (v.B - 1) * v.s.b : 0) + v.d;
-}
+// elements from the first to behind the last
+int64_t extent(const View& v) { return (v.B - 1) * v.s.b + (v.H - 1) * v.s.h + (v.T - 1) * v.s.t + v.d; }
 
 Range range(const View& v) { return Range{v.p, empty(v) ? 0 : extent(v) * v.size}; }
 
@@ -1328,26 +1326,44 @@ bool view_aligned(const View& v, int64_t bytes) {
          v.s.t * v.size % bytes == 0;
 }
 
-// Whether two tensors of the same B and T share memory.  Tensors whose ranges
-// interleave are apart if they are slices of the same rows: the same strides
-// between tokens and sequences (or sequences alone), and one's rows end before
-// the other's begin, within a row's pitch.
+// Whether two tensors share memory.  Tensors whose ranges interleave are apart if they
+// are slices of the same rows: with some of the dimensions b, h, t (any choice of them)
+// of the same strides in both, what the other dimensions reach in the one ends before it
+// begins in the other, and both together fit the pitch of the chosen ones, each of which
+// holds all of the smaller.
 bool views_overlap(const View& a, const View& b) {
   if (!overlaps(range(a), range(b))) return false;
   const View &lo = reinterpret_cast<uintptr_t>(a.p) <= reinterpret_cast<uintptr_t>(b.p) ? a : b;
   const View& hi = &lo == &a ? b : a;
   const int64_t bytes = static_cast<int64_t>(reinterpret_cast<uintptr_t>(hi.p) - reinterpret_cast<uintptr_t>(lo.p));
-  if (lo.size != hi.size || bytes % lo.size != 0 || lo.s.b != hi.s.b) return true;
+  if (lo.size != hi.size || bytes % lo.size != 0) return true;
   const int64_t off = bytes / lo.size;
-  for (bool tokens : {false, true}) {  // slices of a token's row; of a sequence's
-    if (!tokens && lo.s.t != hi.s.t) continue;
-    if (off < extent(lo, tokens, false)) continue;
-    const int64_t end = off + extent(hi, tokens, false);
-    const int64_t row = !tokens && lo.T > 1 ? lo.s.t : INT64_MAX;
-    if (end > row) continue;
-    const int64_t seq = end + (tokens ? 0 : (lo.T - 1) * lo.s.t);
-    if (lo.B > 1 && seq > lo.s.b) continue;
-    return false;
+  const int64_t ls[3] = {lo.s.b, lo.s.h, lo.s.t}, ln[3] = {lo.B, lo.H, lo.T};
+  const int64_t hs[3] = {hi.s.b, hi.s.h, hi.s.t}, hn[3] = {hi.B, hi.H, hi.T};
+  for (int rows = 1; rows < 8; ++rows) {  // the chosen dimensions
+    int64_t low = lo.d, end = off + hi.d, n[3], s[3] = {0, 0, 0};
+    bool ok = true;
+    for (int i = 0; i < 3; ++i) {
+      n[i] = 0;
+      if (!(rows >> i & 1)) {
+        low += (ln[i] - 1) * ls[i];
+        end += (hn[i] - 1) * hs[i];
+      } else if (ln[i] > 1 || hn[i] > 1) {  // (a dimension of size 1 has no stride)
+        ok = ok && (ln[i] == 1 || hn[i] == 1 || ls[i] == hs[i]);
+        n[i] = ln[i] > hn[i] ? ln[i] : hn[i];
+        s[i] = ln[i] > 1 ? ls[i] : hs[i];
+      }
+    }
+    if (!ok || off < low) continue;
+    for (;;) {  // smallest pitch first
+      int m = -1;
+      for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && (m < 0 || s[i] < s[m])) m = i;
+      if (m < 0) return false;
+      if (s[m] < end) break;
+      end += (n[m] - 1) * s[m];
+      n[m] = 0;
+    }
   }
   return true;
 }

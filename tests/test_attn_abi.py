@@ -323,3 +323,78 @@ def test_few_chains_are_walked_in_segments():
     for d, n in ((16, 20), (32, 12), (64, 10), (128, 7)):
         assert segments(1, B=2, H=16, T=1 << 16, d=d) == n
     assert segments(0, B=32, H=16, T=1 << 16) == 0 == segments(1, B=21, H=16, T=1 << 16)
+
+
+def test_gradients_interleaved_within_heads():
+    """dq, dk, dv as [B, T, H, 3, d] slices, as a projection that keeps each head's three together leaves them."""
+    H, T, d = 4, 64, 64
+    s = S(T * 3 * H * d, 3 * d, 3 * H * d)
+    base, n = 40 * GB, 2 * d
+    for B in (1, 2):
+        args = dict(B=B, Hkv=H, dq=s, dk=s, dv=s)
+        assert bwd(desc(**args), dq=base, dk=base + n, dv=base + 2 * n) == OK
+        assert bwd(desc(**args), dq=base + 2 * n, dk=base, dv=base + n) == OK
+        assert bwd(desc(**args), dq=base, dk=base + n - 16, dv=base + 2 * n) == ALIAS
+        assert bwd(desc(**args), dq=base, dk=base + n, dv=base + 2 * n + 16) == ALIAS      # into the next head's dq
+    # [B, H, T, 3, d]
+    s = S(T * 3 * H * d, T * 3 * d, 3 * d)
+    args = dict(Hkv=H, dq=s, dk=s, dv=s)
+    assert bwd(desc(**args), dq=base, dk=base + n, dv=base + 2 * n) == OK
+    assert bwd(desc(**args), dq=base, dk=base + n, dv=base + 2 * n + 16) == ALIAS
+    # [B, T, Hkv, group + 2, d] with one key / value head: q's four heads, then k, then v
+    s = S(T * 6 * d, d, 6 * d)
+    args = dict(Hkv=1, dq=s, dk=s, dv=s)
+    assert bwd(desc(**args), dq=base, dk=base + 4 * n, dv=base + 5 * n) == OK
+    assert bwd(desc(**args), dq=base, dk=base + 3 * n, dv=base + 5 * n) == ALIAS
+    # one behind the other, of other strides
+    q = S(H * T * d, T * d, d)
+    assert bwd(desc(Hkv=H, dq=q, dk=S(T * H * d, d, H * d), dv=q), dq=base, dk=base + 2 * 2 * H * T * d,
+               dv=base + 4 * 2 * H * T * d) == OK
+    # the same first token, other strides between tokens: row 3 of one is row 1 of the other
+    assert bwd(desc(B=1, H=1, Hkv=1, dq=S(0, 0, d), dk=S(0, 0, 3 * d)), dq=base, dk=base + 2 * 3 * d) == ALIAS
+
+
+def test_rotary_in_place_within_heads():
+    """q and k of a [B, T, H, 3, d] projection turned where they are"""
+    H, T, d = 4, 64, 64
+    s = S(T * 3 * H * d, 3 * d, 3 * H * d)
+    p = rdesc(Hkv=H, q=s, k=s, qo=s, ko=s)
+    r = rope()
+    assert rot(p, r, q=GB, k=GB + 2 * d, qo=GB, ko=GB + 2 * d) == OK
+    assert rot(p, r, q=GB, k=GB + 2 * d, qo=GB + 2 * d, ko=GB) == ALIAS
+    assert rot(p, r, q=GB, k=GB + d, qo=GB, ko=GB + d) == ALIAS
+    # k's output in the third place
+    assert rot(p, r, q=GB, k=GB + 2 * d, qo=GB, ko=GB + 4 * d) == OK
+    assert rot(p, r, q=GB, k=GB + 2 * d, qo=GB, ko=GB + 5 * d) == ALIAS
+
+
+def test_apart_is_apart():
+    """Random slices of one buffer against the elements themselves: never accepted where one is shared, and what is
+    refused without one is not of the kinds that the header names (slices of the same rows)."""
+    import random
+    rng = random.Random(3)
+    seen = {OK: 0, ALIAS: 0}
+    for _ in range(3000):
+        B, H, T, d = rng.choice([1, 2]), rng.choice([1, 2, 3]), rng.choice([1, 2, 3]), 16
+        def strides():
+            order, s, span = rng.sample("bht", 3), {}, d
+            for a in order:
+                s[a] = span + d * rng.choice([0, 0, 1, 2])
+                span = s[a] + {"b": B, "h": H, "t": T}[a] * s[a] - s[a] if {"b": B, "h": H, "t": T}[a] > 1 else span
+            return S(s["b"], s["h"], s["t"])
+        a = strides()
+        b = a if rng.random() < 0.7 else strides()
+        off = rng.randrange(0, 20) * (d // 2)
+        def cells(s, at):
+            return {at + x * s.b + y * s.h + z * s.t + i for x in range(B) for y in range(H) for z in range(T) for i in range(d)}
+        def ok(s):
+            return len(cells(s, 0)) == B * H * T * d
+        if not (ok(a) and ok(b)):
+            continue
+        got = bwd(desc(B=B, H=H, Hkv=H, T=T, d=d, dq=a, dk=b, dv=S(H * T * d, T * d, d)), dq=40 * GB, dk=40 * GB + 2 * off)
+        if got == STRIDE:
+            continue
+        seen[got] += 1
+        if cells(a, 0) & cells(b, off):
+            assert got == ALIAS, (B, H, T, [a.b, a.h, a.t], [b.b, b.h, b.t], off)
+    assert min(seen.values()) > 100, seen
