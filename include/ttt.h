@@ -699,6 +699,11 @@ ttt_status ttt_rotary(const ttt_rotary_desc* desc, const ttt_rope* rope, const v
 ttt_status ttt_rotary_validate(const ttt_rotary_desc* desc, const ttt_rope* rope, const void* q, const void* k,
                                const void* q_out, const void* k_out);
 
+/* Name of the kernel ttt_rotary would launch (rows in 16-byte pieces: ttt_rotary_interleaved, _halves, _odd_halves; element
+ * by element: ttt_rotary_pairs), or NULL for an invalid call or one that launches nothing. */
+const char* ttt_rotary_kernel_name(const ttt_rotary_desc* desc, const ttt_rope* rope, const void* q, const void* k,
+                                   const void* q_out, const void* k_out);
+
 /* Human-readable text of a status code (never NULL). */
 const char* ttt_status_str(int status);
 

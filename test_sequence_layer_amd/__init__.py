@@ -67,7 +67,7 @@ EXPORTS = (
     "ttt_mlp_bwd_kernel_name", "ttt_mlp_ln_bwd", "ttt_mlp_ln_bwd_validate", "ttt_mlp_ln_bwd_kernel_name",
     "ttt_linear_attn_fwd", "ttt_linear_attn_fwd_validate", "ttt_linear_attn_bwd", "ttt_linear_attn_bwd_validate",
     "ttt_linear_attn_workspace_bytes", "ttt_linear_attn_decode", "ttt_linear_attn_decode_validate",
-    "ttt_rotary", "ttt_rotary_validate",
+    "ttt_rotary", "ttt_rotary_validate", "ttt_rotary_kernel_name",
     "ttt_status_str", "ttt_abi_version",
 )
 
@@ -259,6 +259,8 @@ def lib() -> ctypes.CDLL:
     L.ttt_rotary.restype = ctypes.c_int
     L.ttt_rotary_validate.argtypes = [ctypes.POINTER(RotaryDesc), ctypes.POINTER(Rope), vp, vp, vp, vp]
     L.ttt_rotary_validate.restype = ctypes.c_int
+    L.ttt_rotary_kernel_name.argtypes = [ctypes.POINTER(RotaryDesc), ctypes.POINTER(Rope), vp, vp, vp, vp]
+    L.ttt_rotary_kernel_name.restype = ctypes.c_char_p
     L.ttt_status_str.argtypes = [ctypes.c_int]
     L.ttt_status_str.restype = ctypes.c_char_p
     L.ttt_abi_version.argtypes = []

@@ -1648,6 +1648,22 @@ ttt_status validate_rotary(const ttt_rotary_desc* d, const ttt_rope* rope, const
   return TTT_OK;
 }
 
+// a valid call's launch; false: nothing to do
+bool rotary_args(const ttt_rotary_desc* desc, const ttt_rope* rope, const void* q, const void* k, void* q_out, void* k_out,
+                 ttt::RotaryArgs* args) {
+  const RotaryViews v = rotary_views(desc, q, k, q_out, k_out);
+  if (empty(v.q) && empty(v.k)) return false;
+  ttt::RotaryArgs& a = *args;
+  a.B = desc->B; a.H = desc->H; a.Hkv = desc->Hkv; a.T = desc->T; a.d = desc->d;
+  a.dtype = desc->dtype;
+  a.q = q; a.k = k; a.qo = q_out; a.ko = k_out;
+  a.qs = strides(v.q); a.ks = strides(v.k); a.qos = strides(v.qo); a.kos = strides(v.ko);
+  a.rope = make_rope(rope);
+  a.inverse = (desc->flags & TTT_FLAG_INVERSE) != 0;
+  a.in_place = (desc->H == 0 || same_view(v.q, v.qo)) && (desc->Hkv == 0 || same_view(v.k, v.ko));
+  return !(a.in_place && a.rope.rot == 0);
+}
+
 ttt_status hip_status(hipError_t e) { return e == hipSuccess ? TTT_OK : TTT_ERR_HIP; }
 
 }  // namespace
@@ -1790,21 +1806,20 @@ ttt_status ttt_rotary_validate(const ttt_rotary_desc* desc, const ttt_rope* rope
   return validate_rotary(desc, rope, q, k, q_out, k_out);
 }
 
+const char* ttt_rotary_kernel_name(const ttt_rotary_desc* desc, const ttt_rope* rope, const void* q, const void* k,
+                                   const void* q_out, const void* k_out) {
+  ttt::RotaryArgs a;
+  if (validate_rotary(desc, rope, q, k, q_out, k_out) != TTT_OK) return nullptr;
+  if (!rotary_args(desc, rope, q, k, const_cast<void*>(q_out), const_cast<void*>(k_out), &a)) return nullptr;
+  return ttt::rotary_name(a);
+}
+
 ttt_status ttt_rotary(const ttt_rotary_desc* desc, const ttt_rope* rope, const void* q, const void* k, void* q_out,
                       void* k_out, void* stream) {
   const ttt_status st = validate_rotary(desc, rope, q, k, q_out, k_out);
   if (st != TTT_OK) return st;
-  const RotaryViews v = rotary_views(desc, q, k, q_out, k_out);
-  if (empty(v.q) && empty(v.k)) return TTT_OK;
   ttt::RotaryArgs a;
-  a.B = desc->B; a.H = desc->H; a.Hkv = desc->Hkv; a.T = desc->T; a.d = desc->d;
-  a.dtype = desc->dtype;
-  a.q = q; a.k = k; a.qo = q_out; a.ko = k_out;
-  a.qs = strides(v.q); a.ks = strides(v.k); a.qos = strides(v.qo); a.kos = strides(v.ko);
-  a.rope = make_rope(rope);
-  a.inverse = (desc->flags & TTT_FLAG_INVERSE) != 0;
-  a.in_place = (desc->H == 0 || same_view(v.q, v.qo)) && (desc->Hkv == 0 || same_view(v.k, v.ko));
-  if (a.in_place && a.rope.rot == 0) return TTT_OK;
+  if (!rotary_args(desc, rope, q, k, q_out, k_out, &a)) return TTT_OK;
   return hip_status(ttt::launch_rotary(a, static_cast<hipStream_t>(stream)));
 }
 

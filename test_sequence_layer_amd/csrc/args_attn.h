@@ -137,5 +137,6 @@ hipError_t launch_attn_bwd(const AttnBwdArgs& a, hipStream_t s);
 hipError_t launch_attn_sum(const AttnSumArgs& a, hipStream_t s);
 hipError_t launch_attn_decode(const AttnDecodeArgs& a, hipStream_t s);
 hipError_t launch_rotary(const RotaryArgs& a, hipStream_t s);
+const char* rotary_name(const RotaryArgs& a);  // the way launch_rotary takes
 
 }  // namespace ttt

@@ -10,10 +10,10 @@
 // heads are dealt out over blockIdx.y.  Four ways of cutting rows into pieces:
 //   interleaved pairs, rows of whole 16-byte pieces: a piece, its pairs within it;
 //   halves of whole pieces: a piece, its partner from the lane that has it;
-//   other halves: a piece, the elements of the other half through LDS;
-//   rows at any address: one pair, element by element.
+//   other halves: a piece, the elements of the other half through LDS, whole rows in a workgroup;
+//   rows at any address, or of more than 256 pieces: one pair, element by element.
 // Measured on MI355X for B2 H32+32 T32768 d64 bf16, 1.07 GB (a copy of that size: 204 us): interleaved 214 us,
-// halves 212 us (through LDS 240, eight elements of both halves a thread 243, four 241), halves of 31 pairs 241 us
+// halves 212 us (through LDS 240, eight elements of both halves a thread 243, four 241), halves of 31 pairs 214 us
 // (pair by pair 638), half of the head 215 us.
 #include <type_traits>
 
@@ -64,10 +64,15 @@ enum { kInterleaved, kHalves, kOddHalves, kPairs };
 template <typename T, int WAY>
 __host__ __device__ __forceinline__ int row_threads(int d, int rot, bool in_place) {
   constexpr int E = 16 / sizeof(T);
-  if (WAY == kInterleaved) return in_place ? (rot + E - 1) / E : d / E;
-  if (WAY == kHalves || WAY == kOddHalves) return d / E;
+  if (WAY == kInterleaved || WAY == kOddHalves) return in_place ? (rot + E - 1) / E : d / E;
+  if (WAY == kHalves) return d / E;
   return rot / 2 + (in_place ? 0 : d - rot);
 }
+
+// Threads of a workgroup that have rows: of kOddHalves whole rows, whose pieces meet in its LDS (rows that went on in
+// the next workgroup, and took the partners there from memory: d 96 397 us for 215, d 48 491 for 223, q alone).
+template <int WAY>
+__host__ __device__ __forceinline__ int busy_threads(int per) { return WAY == kOddHalves ? 256 / per * per : 256; }
 
 // The rows of one (sequence, token) that a thread walks: heads h0 .. h1 - 1 of q, then k.
 template <typename T>
@@ -97,10 +102,11 @@ __global__ __launch_bounds__(256) void ttt_rotary(RotaryArgs a) {
   constexpr int HU = 4;  // heads a step: 212 us [B, H, T, d] and 222 [B, T, H, d]; 2: 208 and 234, 8: 232 and 218
   const int rot = a.rope.rot, half = rot / 2;
   const int per = row_threads<T, WAY>(a.d, rot, a.in_place);
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int busy = busy_threads<WAY>(per);
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * busy + threadIdx.x;
   const int64_t rows = static_cast<int64_t>(a.B) * a.T;
   // (kOddHalves: all threads of a workgroup keep step; the ones left over walk the last row and store nothing)
-  const bool live = id < rows * per;
+  const bool live = id < rows * per && static_cast<int>(threadIdx.x) < busy;
   if (WAY != kOddHalves && !live) return;
   const int unit = static_cast<int>(id % per);
   const int64_t bt = live ? id / per : rows - 1;
@@ -178,17 +184,18 @@ __global__ __launch_bounds__(256) void ttt_rotary(RotaryArgs a) {
     };
     load(now, hd.h0);
     float cs[E], sn[E];
-    int from[E];  // of the partner, in this thread's row
+    int from[E];  // the partner in LDS
 #pragma unroll
     for (int j = 0; j < E; ++j) {
       const int c = o + j;
       cs[j] = 1.f;
       sn[j] = 0.f;
-      from[j] = c;
-      if (c < rot) {
+      from[j] = mine * kStep + j;
+      if (live && c < rot) {
         angle(c < half ? c : c - half, cs[j], sn[j]);
         if (c < half) sn[j] = -sn[j];
-        from[j] = c < half ? c + half : c - half;
+        const int other = c < half ? c + half : c - half;
+        from[j] = (mine - unit + other / E) * kStep + other % E;
       }
     }
     int n = 0;
@@ -206,12 +213,7 @@ __global__ __launch_bounds__(256) void ttt_rotary(RotaryArgs a) {
         unpack<T>(now[u], x);
 #pragma unroll
         for (int j = 0; j < E; ++j) {
-          if (o + j < rot) {
-            const int piece = mine - unit + from[j] / E;
-            const float y =
-                piece < 256 && piece >= 0 ? widen(buf[n][u][piece * kStep + from[j] % E]) : widen(hd.in(h + u)[from[j]]);
-            x[j] = fmaf(y, sn[j], x[j] * cs[j]);
-          }
+          if (o + j < rot) x[j] = fmaf(widen(buf[n][u][from[j]]), sn[j], x[j] * cs[j]);
         }
         if (live) st(hd.out(h + u) + o, pack<T>(x));
         now[u] = next[u];
@@ -238,7 +240,8 @@ __global__ __launch_bounds__(256) void ttt_rotary(RotaryArgs a) {
 template <typename T, int WAY>
 hipError_t go(const RotaryArgs& a, hipStream_t s) {
   const int64_t per = row_threads<T, WAY>(a.d, a.rope.rot, a.in_place);
-  const int64_t blocks = (static_cast<int64_t>(a.B) * a.T * per + 255) / 256;
+  const int64_t busy = busy_threads<WAY>(static_cast<int>(per));
+  const int64_t blocks = (static_cast<int64_t>(a.B) * a.T * per + busy - 1) / busy;
   const int64_t heads = static_cast<int64_t>(a.H) + a.Hkv;
   int64_t y = (1024 + blocks - 1) / blocks;  // four workgroups per CU
   if (y > heads) y = heads;
@@ -246,33 +249,48 @@ hipError_t go(const RotaryArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// every row begins on a multiple of `bytes`
+// every row of the tensors that there are begins on a multiple of `bytes`
 bool aligned_to(const RotaryArgs& a, int bytes, int size) {
-  for (const void* p : {a.q, a.k, static_cast<const void*>(a.qo), static_cast<const void*>(a.ko)})
-    if (reinterpret_cast<uintptr_t>(p) % bytes != 0) return false;
-  for (const Strides3& x : {a.qs, a.ks, a.qos, a.kos})
-    if (x.b * size % bytes != 0 || x.h * size % bytes != 0 || x.t * size % bytes != 0) return false;
-  return true;
+  auto ok = [&](const void* p, const Strides3& x) {
+    return reinterpret_cast<uintptr_t>(p) % bytes == 0 && x.b * size % bytes == 0 && x.h * size % bytes == 0 &&
+           x.t * size % bytes == 0;
+  };
+  return (a.H == 0 || (ok(a.q, a.qs) && ok(a.qo, a.qos))) && (a.Hkv == 0 || (ok(a.k, a.ks) && ok(a.ko, a.kos)));
+}
+
+int pick(const RotaryArgs& a) {
+  const int size = a.dtype == 0 ? 4 : 2, e = 16 / size;
+  if (a.d % e != 0 || !aligned_to(a, 16, size)) return kPairs;
+  if (a.rope.interleaved) return kInterleaved;
+  // (whole rows in a wave)
+  if (a.rope.rot % (2 * e) == 0 && 64 % (a.d / e) == 0) return kHalves;
+  // (a row's pieces in a workgroup)
+  return a.d / e <= 256 ? kOddHalves : kPairs;
 }
 
 template <typename T>
-hipError_t pick(const RotaryArgs& a, hipStream_t s) {
-  constexpr int E = 16 / sizeof(T), kSize = sizeof(T);
-  if (a.rope.interleaved && a.d % E == 0 && aligned_to(a, 16, kSize)) return go<T, kInterleaved>(a, s);
-  // (whole rows in a wave)
-  if (!a.rope.interleaved && a.rope.rot % (2 * E) == 0 && a.d % E == 0 && 64 % (a.d / E) == 0 && aligned_to(a, 16, kSize))
-    return go<T, kHalves>(a, s);
-  // (a partner in another workgroup's piece is read from the row itself, which must not be written yet)
-  if (!a.rope.interleaved && a.d % E == 0 && aligned_to(a, 16, kSize) &&
-      (256 % (a.d / E) == 0 || (a.q != a.qo && a.k != a.ko)))
-    return go<T, kOddHalves>(a, s);
-  return go<T, kPairs>(a, s);
+hipError_t launch(const RotaryArgs& a, hipStream_t s) {
+  switch (pick(a)) {
+    case kInterleaved: return go<T, kInterleaved>(a, s);
+    case kHalves: return go<T, kHalves>(a, s);
+    case kOddHalves: return go<T, kOddHalves>(a, s);
+    default: return go<T, kPairs>(a, s);
+  }
 }
 
 }  // namespace
 
 hipError_t launch_rotary(const RotaryArgs& a, hipStream_t s) {
-  return a.dtype == 0 ? pick<float>(a, s) : pick<uint16_t>(a, s);
+  return a.dtype == 0 ? launch<float>(a, s) : launch<uint16_t>(a, s);
+}
+
+const char* rotary_name(const RotaryArgs& a) {
+  switch (pick(a)) {
+    case kInterleaved: return "ttt_rotary_interleaved";
+    case kHalves: return "ttt_rotary_halves";
+    case kOddHalves: return "ttt_rotary_odd_halves";
+    default: return "ttt_rotary_pairs";
+  }
 }
 
 }  // namespace ttt

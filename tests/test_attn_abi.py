@@ -398,3 +398,27 @@ def test_apart_is_apart():
         if cells(a, 0) & cells(b, off):
             assert got == ALIAS, (B, H, T, [a.b, a.h, a.t], [b.b, b.h, b.t], off)
     assert min(seen.values()) > 100, seen
+
+
+def way(d, r, q=GB, k=2 * GB, qo=3 * GB, ko=4 * GB):
+    return L.ttt_rotary_kernel_name(ctypes.byref(d), ctypes.byref(r), q, k, qo, ko)
+
+
+def test_rotary_kernels():
+    """Only rows at any address, or of more than 256 pieces, go element by element: an absent q or k takes no part in the
+    choice, and turning in place makes no difference."""
+    assert way(rdesc(), rope()) == b"ttt_rotary_halves" and way(rdesc(), rope(inter=1)) == b"ttt_rotary_interleaved"
+    assert way(rdesc(), rope(rot=62)) == b"ttt_rotary_odd_halves"
+    for d in (48, 80, 96, 160):  # 256 is no multiple of d / 8 pieces of bf16
+        r = rope(rot=d)
+        assert way(rdesc(d=d), r) == b"ttt_rotary_odd_halves"
+        assert way(rdesc(d=d, Hkv=0), r, k=None, ko=None) == b"ttt_rotary_odd_halves"
+        assert way(rdesc(d=d, H=0), r, q=None, qo=None) == b"ttt_rotary_odd_halves"
+        assert way(rdesc(d=d, Hkv=0), r, k=None, ko=None, qo=GB) == b"ttt_rotary_odd_halves"
+        assert way(rdesc(d=d), r, ko=2 * GB) == b"ttt_rotary_odd_halves"
+    assert way(rdesc(d=2048), rope(rot=62)) == b"ttt_rotary_odd_halves"
+    assert way(rdesc(d=2056), rope(rot=62)) == b"ttt_rotary_pairs"
+    assert way(rdesc(), rope(), q=GB + 2) == b"ttt_rotary_pairs"
+    assert way(rdesc(Hkv=0, k=S(3, 5, 7), ko=S(1, 1, 1)), rope(), k=6, ko=2) == b"ttt_rotary_halves"
+    assert way(rdesc(), rope(rot=63)) is None and way(rdesc(B=0), rope()) is None
+    assert way(rdesc(), rope(rot=0), qo=GB, ko=2 * GB) is None

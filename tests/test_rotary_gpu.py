@@ -193,3 +193,21 @@ def test_offsets_past_32_bits(ttt):
     out = wide[:, 64:128][None, None]
     ttt.rotary(q, None, 0, freqs, out=(out, None))
     assert torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("d,rot", [(48, 48), (80, 80), (96, 96), (96, 30), (1040, 64), (2056, 40)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_q_alone_and_k_alone(ttt, d, rot, dtype):
+    """rows that fill no workgroup evenly, without a k and without a q, out of place and in place"""
+    freqs = ttt.rotary_freqs(rot)[0]
+    f = freqs.to(DEV)
+    for B, H, T in ((3, 5, 211), (1, 1, 1), (2, 4, 64)):
+        q, _ = make(B, H, 1, T, d, dtype, seed=T)
+        ref = turn(q, 9 + torch.arange(T).expand(B, T), freqs)
+        got = ttt.rotary(q.to(DEV), None, 9, f)[0]
+        check("q", got, ref, tol(q, ref, freqs, "half", 1.0, dtype))
+        none = torch.empty(B, 0, T, d, dtype=dtype, device=DEV)
+        assert torch.equal(ttt.rotary(none, q.to(DEV), 9, f)[1], got)
+        here = q.to(DEV)
+        ttt.rotary(here, None, 9, f, out=(here, None))
+        check("in place", here, ref, tol(q, ref, freqs, "half", 1.0, dtype))
