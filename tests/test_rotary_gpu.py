@@ -211,3 +211,21 @@ def test_q_alone_and_k_alone(ttt, d, rot, dtype):
         here = q.to(DEV)
         ttt.rotary(here, None, 9, f, out=(here, None))
         check("in place", here, ref, tol(q, ref, freqs, "half", 1.0, dtype))
+
+
+@pytest.mark.parametrize("start", [1, 77, 100_003])
+def test_sine_and_cosine_keep_their_relative_accuracy(ttt, start):
+    """The pair (1, 0) becomes (cos, sin).  Near whole and half turns, where the sine is small, and near quarter turns,
+    where the cosine is: each within 6 x 2^-24 of itself (two steps of the fp32 functions, one of the correction), and the
+    64-bit angle's own rounding, 2^-52 of it on either side."""
+    gen = torch.Generator().manual_seed(start)
+    quarter = torch.randint(-4, 5, (4096,), generator=gen).double()
+    off = torch.exp(-14 * torch.rand(4096, generator=gen, dtype=torch.float64)) * torch.where(
+        torch.rand(4096, generator=gen) < 0.5, -1.0, 1.0)
+    freqs = (quarter * torch.pi / 2 + off) / start
+    angle = start * freqs
+    q = torch.zeros(1, 1, 1, 8192)
+    q[..., :4096] = 1
+    y = ttt.rotary(q.to(DEV), None, start, freqs.to(DEV))[0].cpu().double().view(2, 4096)
+    for name, got, ref in (("cos", y[0], torch.cos(angle)), ("sin", y[1], torch.sin(angle))):
+        check(name, got, ref, 6 * 2.0 ** -24 * ref.abs() + 4 * 2.0 ** -52 * (1 + angle.abs()))
