@@ -576,8 +576,14 @@ ttt_status ttt_mlp_ln_decode_validate(const ttt_mlp_desc* desc, const void* Q, c
  *    4 B H d per segment in the forward and in decode, three times that in the
  *    backward, which also sums B Hkv T d / 2 where heads are shared; B T d for
  *    ttt_rotary.
- *  - Finite values: a NaN or infinity reaches only tokens at or after its own, but
- *    for V (and dZ in the backward) also the others of its 16-token block.
+ *  - A NaN or an infinity reaches, as the one or the other, the outputs that depend
+ *    on it: Z_i on Q_i and the K, V up to token i; dQ_i on dZ_i and the K, V up to i;
+ *    dK_i on V_i and the Q, dZ from i on; dV_i on K_i and the Q, dZ from i on; dW0 on
+ *    all Q and dZ; dlog_decay on all of its sequence and head; all of these on W0 or
+ *    dW_final.  It also reaches, of its own block of 16 tokens, all tokens of Z (from
+ *    V), dQ (from K), dK (from Q) and dV (from dZ): blocks are counted from a
+ *    sequence's first token for Z and dQ, from its last one backwards for dK and dV.
+ *    (In decode there are no blocks.)  Rows behind a sequence's end reach nothing.
  */
 typedef struct {
   int64_t b, h, t; /* elements between sequences, heads, tokens */
