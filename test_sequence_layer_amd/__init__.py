@@ -1001,6 +1001,13 @@ def _strides(t) -> Strides:
     return Strides(b, h, s)
 
 
+def _check_sizes(*shapes):
+    """ttt_linear_attn_desc and ttt_rotary_desc hold sizes in 32 bits."""
+    for shape in shapes:
+        if any(n >= 1 << 31 for n in shape):
+            raise ValueError(f"{tuple(shape)}: sizes must be below 2^31")
+
+
 def _like(x, dtype):
     """An empty tensor of x's shape and, where x is dense, its layout."""
     return _torch().empty_like(x, dtype=dtype)
@@ -1024,6 +1031,7 @@ def _attn_desc(q, k, v, log_decay, w0, lens, scale, z, grads=()):
            *map(_layout, grads))
     got = _attn_descs.get(key)
     if got is None:
+        _check_sizes(q.shape, k.shape)
         B, H, Hkv, T, d, wstride = _attn_args(q, k, v, log_decay, w0, lens)
         if z.shape != q.shape:
             raise ValueError(f"z or dz {tuple(z.shape)}: expected {tuple(q.shape)}")
@@ -1087,6 +1095,7 @@ def _attn_workspace(need, workspace, dev):
 
 def linear_attn_workspace_bytes(q, k, out_dtype=None, backward: bool = False) -> int:
     """Bytes of workspace that a call on inputs like q [B, H, T, d] and k [B, Hkv, T, d] takes."""
+    _check_sizes(q.shape, k.shape)
     B, H, T, d = q.shape
     desc = LinearAttnDesc(B, H, k.shape[1], T, d, _dtype_code(q.dtype), _dtype_code(out_dtype or q.dtype))
     return int(lib().ttt_linear_attn_workspace_bytes(ctypes.byref(desc), int(backward)))
@@ -1282,6 +1291,8 @@ def _rope(x, pos, freqs, layout: str = "half", scale: float = 1.0) -> Rope:
         _check_same_dev(x, pos, freqs)
         r.pos = pos.data_ptr()
     else:
+        if pos != int(pos) or not -(1 << 63) <= pos < 1 << 63:
+            raise ValueError(f"position {pos}: expected a whole number of 64 bits")
         r.pos_offset = int(pos)
         _check_same_dev(x, freqs)
     return r
@@ -1294,6 +1305,7 @@ def _rotary_desc(q, k, qo, ko, flags):
     key = (q.shape, q.stride(), q.dtype, _layout(k), _layout(qo), _layout(ko), flags)
     desc = _rotary_descs.get(key)
     if desc is None:
+        _check_sizes(q.shape, *(() if k is None else (k.shape,)))
         B, H, T, d = q.shape
         if (ko is None) != (k is None):
             raise ValueError("out must hold an output for k exactly where k is given")

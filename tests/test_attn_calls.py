@@ -27,3 +27,31 @@ def test_cached_descriptors_keep_no_tensor():
     _desc(torch.tensor(0.25))
     flat = lambda x: [z for y in x for z in flat(y)] if isinstance(x, tuple) else [x]  # noqa: E731
     assert not any(torch.is_tensor(x) for key in ttt._attn_descs for x in flat(tuple(key)))
+
+
+def test_sizes_past_32_bits_are_refused():
+    """Expanded tensors of 2^32 + 5 tokens, heads or sequences: not taken for 5."""
+    n = (1 << 32) + 5
+    x = torch.zeros(1, 1, 1, 16)
+    for shape in ((1, 1, n, 16), (n, 1, 1, 16), (1, n, 1, 16)):
+        q = x.expand(shape)
+        with pytest.raises(ValueError, match="2\\^31"):
+            ttt._attn_desc(q, q, q, torch.zeros(1), None, None, 1.0, q)
+        with pytest.raises(ValueError, match="2\\^31"):
+            ttt._rotary_desc(q, q, q, q, 0)
+        with pytest.raises(ValueError, match="2\\^31"):
+            ttt.linear_attn_workspace_bytes(q, q)
+
+
+def test_positions_are_whole_and_fit():
+    q, f = torch.zeros(1, 1, 3, 16), torch.ones(8, dtype=torch.float64)
+    check, ttt._check_same_dev = ttt._check_same_dev, lambda *a: None
+    try:
+        assert ttt._rope(q, 7, f).pos_offset == 7 and ttt._rope(q, -(1 << 40), f).pos_offset == -(1 << 40)
+        for bad in (1 << 63, -(1 << 63) - 1):
+            with pytest.raises(ValueError, match="position"):
+                ttt._rope(q, bad, f)
+        with pytest.raises(ValueError, match="position"):
+            ttt._rope(q, 1.5, f)
+    finally:
+        ttt._check_same_dev = check
