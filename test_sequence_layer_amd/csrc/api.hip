@@ -1394,9 +1394,9 @@ ttt_status check_attn_desc(const ttt_linear_attn_desc* d, int64_t* chains) {
 }
 
 // From this many segments on a launch of its own carries their states on; below, each workgroup reads those before
-// its own.  T2048, us with that launch and without: d128 10 segments of 24 chains 46.9 and 49.9, gradients 136 and
-// 156; d64 16 segments of 24 chains 29.4 and 32.9, but 10 of 48 chains 33.6 and 30.4, gradients with 13 of 24 chains
-// 56 and 60; 16 segments of 24 chains at d32 22.5 and 19.2, at d16 20.1 and 16.1.
+// its own.  T2048, us with that launch and without: d128 10 segments of 24 chains 48.6 and 51.8, gradients 137 and
+// 160; d64 16 segments of 24 chains 29.4 and 32.5, but 10 of 48 chains 34.3 and 31.8, gradients with 13 of 24 chains
+// 57 and 60; 16 segments of 24 chains at d32 22.5 and 20.5, at d16 19.8 and 16.6.
 int carry_from(int d, bool backward) { return d == 128 ? 8 : d == 64 ? (backward ? 8 : 16) : 24; }
 
 struct AttnPlan {

@@ -7,11 +7,13 @@
 // from the last token to the first.  One launch holds the three walks of every
 // (sequence, head) or segment as workgroups of their own: three times the workgroups of
 // one fused reverse walk, each with one state (dQ's walk, with the decay's gradient, two)
-// instead of three, and no state kept in two layouts.  Measured on MI355X: a dQ launch and
-// a fused dK, dV, decay walk with its states in two layouts 173 us for B8 H12 T2048 d64 in
-// bf16, this 120 us (108 us by now); 410 us both at B16 H32 T2048; two launches, dK and dV
-// first, 437 us.  Bound by issue slots there (88% busy, 68% vector instructions: parts of
-// states, scores and decayed values), with 1.48 GB moved in 406 us.
+// instead of three, and no state kept in two layouts.  Measured on MI355X for B8 H12 T2048
+// d64 in bf16, with two parts for bf16 outputs: a dQ launch and a fused dK, dV, decay walk
+// with its states in two layouts 173 us, this 120 us; 410 us both at B16 H32 T2048; two
+// launches, dK and dV first, 437 us.  Now, with three parts, 115 and 430 us.  Bound by issue
+// slots in the latter (93% busy, 74% vector instructions: parts of states, scores and decayed
+// values), with 1.48 GB moved.  At d = 128 the walks spill 18 to 127 registers: 672 us for
+// B16 H16 T2048 in bf16.
 //
 // The walks of dK and dV read the same rows at the same time, on the same XCD (unit_of):
 // the second finds them in its L2 (measured: 8.3 tensors fetched instead of 10).

@@ -18,8 +18,8 @@
 // pairs take 3/8 of its time.  Outputs of bf16 take three parts as well: with two (2^-16
 // of the sum of the terms' magnitudes) terms that cancel leave the bits that were cut
 // off, and 0.25% of ordinary bf16 outputs round to the neighbouring value, with three
-// 0.02%.  What that costs, two parts and three: B16 H32 T8192 d64 [B, H, T, d] 431 and
-// 498 us, [B, T, H, d] 501 and 492, gradients at T2048 406 and 434.
+// 0.02%.  What that costs, us with two parts and with three: B16 H32 T8192 d64 [B, H, T, d]
+// 431 and 498, [B, T, H, d] 501 and 492, d128 571 and 667, gradients at T2048 406 and 434.
 // An fp32 value above bf16's largest (3.39e38) rounds to an infinite first part, and an
 // infinity leaves NaN behind its first part: both come out as NaN.
 #pragma once

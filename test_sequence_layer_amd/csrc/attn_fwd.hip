@@ -176,15 +176,16 @@ bool attn_supported(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 // Segments per sequence.  One workgroup walks a chain 32 tokens at a time, so a few chains leave most of the 256
 // CUs idle for long; segments fill them, at the price of a first pass over K and V (Q and dZ too in the
 // backward), of carrying the states and of a launch.  us at T2048 in bf16, [B, H, T, d]:
-//   forward, 8 waves a CU (32768 / d workgroups at most): 96 chains d64 38.6 (half as many: 57.6, twice: 52.0, one
-//     segment a chain: 83), 200 chains d128 124 (twice: 173), d32 34 (half: 53), d16 23 (half: 25, a quarter: 45)
-//   backward, three walks a segment.  d128, 240 segments: 96 chains 320 (320: 350, 160: 371).  d64, 320: 96 chains 113
-//     (160: 125, 640: 131).  d32, 384: 200 chains 95 (640: 107), 96 chains 60 with 640, 70 with 320.  d16, 640: 300
-//     chains 79 (320: 98), 400 chains 99 (960: 105).
+//   forward, 8 waves a CU (32768 / d workgroups at most): 96 chains d64 43 (half as many: 65, twice: 56, one
+//     segment a chain: 80), 200 chains d128 153 (twice: 200), d32 37 (half: 59, twice: 45), d16 24 (half: 26, a
+//     quarter: 50, twice: 29)
+//   backward, three walks a segment.  d128, 240 segments: 96 chains 312 (320: 355, 160: 319).  d64, 320: 96 chains 123
+//     (160: 134, 640: 140).  d32, 384: 200 chains 101 (640: 112, 200: 101), 96 chains 68 (640: 63, 320: 71).  d16, 640:
+//     300 chains 79 (320: 94, 960: 88), 400 chains 102 (960: 117).
 // Shortest segment.  wide (fp32 inputs or d = 128): 3 chunks of 32 tokens, from 6 chunks on (12 chains T1009 d128 fp32:
-// 47, 4 chunks 52, 6 chunks 56; T200 28 to 31 for 33, gradients 63 to 71 for 94).  Otherwise 4 chunks, from 12 on
-// (T330: 15.9 for 15.8, T512: 16.1 for 20.6; T200 would cost 16 for 12, gradients 26 for 19).  At most 64 segments
-// (B1 H1 T32768: 60, 105 with 256).
+// 40, 4 chunks 45, 6 chunks 55; T200 31 for 33 in one, gradients 70 for 91).  Otherwise 4 chunks, from 12 on
+// (T330: in one 17.3, in two 17.5, T512: 16.4 for 23.1 in one; T200 would cost 16 for 12, gradients 26 for 19).  At most
+// 64 segments (B1 H1 T32768: 63, 109 with 256).
 int attn_segments(int64_t chains, int T, int d, bool wide, bool backward) {
   if (chains <= 0 || T <= 0) return 1;
   const int all = !backward ? 32768 / d : d == 128 ? 240 : d == 64 ? 320 : d == 32 ? 384 : 640;

@@ -18,20 +18,21 @@
 // causal 16 x 16 blocks of X Y^T come out of the matrix cores, transposed, in the
 // layout that the product with V reads: one wave computes, decays and splits a block and
 // leaves it in LDS for the others (computed by every wave they were a fifth of all
-// instructions, and issue slots are what this kernel runs out of: 75% busy in the
-// forward, 85% in the backward at B16 H32 d64 bf16).
+// instructions, and issue slots are what this kernel runs out of: 90% busy in the
+// forward, 93% in the backward at B16 H32 d64 bf16).
 //
 // Chunks on their way.  bf16: two chunks in registers (16 bytes a thread and tensor)
 // and two LDS buffers, so a chunk is loaded three chunks before it is used and stored
 // one before; two barriers a chunk, behind the scores and behind the chunk.  Otherwise
 // (three planes a tensor, or the four tiles of the decay's gradient at d = 128) one of
 // each, and a third barrier behind the stores.  The barrier behind the scores
-// comes after the products with the start state, which do not need them (gradients of
-// B16 H16 T2048 d128 bf16: 654 us, 712 with it before; fp32 inputs -1 to -3%), but before
-// them for bf16 at d = 64, where the other workgroups of the CU fill the wait (B16 H32
-// T8192: 429 us, 439 with it after).  At d = 64 a wave also issues a chunk's products
-// before the other waves' loads and scores (the same case 440 us without, gradients of
-// B16 H32 T2048 400 us, 393 with; at d = 128 it costs 1 to 9%, below 64 nothing changes).
+// comes after the products with the start state, which do not need them (d128 bf16: B16 H16
+// T8192 664 us, 708 with it before, gradients at T2048 665 and 685; fp32 inputs -1 to -3%),
+// but before them for bf16 at d = 64, where the other workgroups of the CU fill the wait
+// ([B, T, H, d], B16 H32 T8192: 494 us, 512 with it after, gradients at T2048 431 and 447;
+// [B, H, T, d] the same either way).  At d = 64 a wave also issues a chunk's products
+// before the other waves' loads and scores ([B, H, T, d]: 490 us, 509 without, gradients
+// 433 and 449; at d = 128 it costs 1 to 3%, below 64 it changes 1 to 3% either way).
 //
 // The decay's gradient (with dQ): a second state U = dS/dlog_decay counts each pair
 // j <= i by its distance,

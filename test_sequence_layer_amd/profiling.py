@@ -54,6 +54,14 @@ KERNEL_SOURCES = {
     "ttt_linear_primal_kernel": ["linear_primal.hip", "args_primal.h", "ttt_common.h"],
     "ttt_linear_ln_primal_kernel": ["linear_primal.hip", "args_primal.h", "ttt_common.h"],
     "ttt_linear_chunk_scan": ["linear_chunked.hip", "args_linear.h", "ttt_common.h"],
+    "ttt_attn_fwd": ["attn_fwd.hip", "attn_walk.h", "attn_common.h", "mfma_common.h", "wave_prio.h", "args_attn.h", "ttt_common.h"],
+    "ttt_attn_states": ["attn_fwd.hip", "attn_walk.h", "attn_common.h", "mfma_common.h", "wave_prio.h", "args_attn.h", "ttt_common.h"],
+    "ttt_attn_carry": ["attn_fwd.hip", "attn_common.h", "mfma_common.h", "args_attn.h", "ttt_common.h"],
+    "ttt_attn_bwd": ["attn_bwd.hip", "attn_walk.h", "attn_common.h", "mfma_common.h", "wave_prio.h", "args_attn.h", "ttt_common.h"],
+    "ttt_attn_bwd_states": ["attn_bwd.hip", "attn_walk.h", "attn_common.h", "mfma_common.h", "wave_prio.h", "args_attn.h", "ttt_common.h"],
+    "ttt_attn_sum": ["attn_bwd.hip", "attn_common.h", "mfma_common.h", "args_attn.h", "ttt_common.h"],
+    "ttt_attn_decode": ["attn_decode.hip", "rope.h", "mfma_common.h", "args_attn.h", "ttt_common.h"],
+    "ttt_rotary": ["rotary.hip", "rope.h", "mfma_common.h", "args_attn.h", "ttt_common.h"],
 }
 
 
