@@ -611,7 +611,8 @@ typedef struct {
  * chains a sequence is walked in segments at the same time, whose start states a
  * first launch computes.  d in {16, 32, 64, 128}.  All products run on the bf16
  * matrix cores, fp32 operands (fp32 inputs, states, scores) as three bf16 parts.  An
- * fp32 value that is infinite or above bf16's largest (3.39e38) comes out as NaN.
+ * infinite fp32 input, and a state or sum above bf16's largest value (3.39e38), may come
+ * out as NaN.
  */
 ttt_status ttt_linear_attn_fwd(const ttt_linear_attn_desc* desc, const void* Q, const void* K, const void* V,
                                const float* log_decay, const float* W0, const int32_t* lens, void* Z, float* W_final,

@@ -12,7 +12,7 @@
 // with its states in two layouts 173 us, this 120 us; 410 us both at B16 H32 T2048; two
 // launches, dK and dV first, 437 us.  Now, with three parts, 115 and 430 us.  Bound by issue
 // slots in the latter (93% busy, 74% vector instructions: parts of states, scores and decayed
-// values), with 1.48 GB moved.  At d = 128 the walks spill 18 to 127 registers: 672 us for
+// values), with 1.48 GB moved.  At d = 128 the walks spill 18 to 128 registers: 672 us for
 // B16 H16 T2048 in bf16.
 //
 // The walks of dK and dV read the same rows at the same time, on the same XCD (unit_of):

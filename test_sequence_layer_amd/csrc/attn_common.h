@@ -20,8 +20,8 @@
 // off, and 0.25% of ordinary bf16 outputs round to the neighbouring value, with three
 // 0.02%.  What that costs, us with two parts and with three: B16 H32 T8192 d64 [B, H, T, d]
 // 431 and 498, [B, T, H, d] 501 and 492, d128 571 and 667, gradients at T2048 406 and 434.
-// An fp32 value above bf16's largest (3.39e38) rounds to an infinite first part, and an
-// infinity leaves NaN behind its first part: both come out as NaN.
+// A state or a sum above bf16's largest value (3.39e38) rounds to an infinite first part,
+// and an infinity leaves NaN behind its first part: both come out as NaN.
 #pragma once
 
 #include "args_attn.h"
@@ -62,6 +62,18 @@ __device__ __forceinline__ void split(float4v x, Frag p[N]) {
     p[n] = __builtin_bit_cast(bf16x4, w);
     if (n + 1 < N) x = x - widen(p[n]);
   }
+}
+
+// The same of an fp32 input, or of one that has only decayed: its first part stays finite where x does, so that the
+// type's largest and lowest values have three parts as all others, and come to nothing where their score is zero.  (0 to
+// 2% of the time of fp32 calls; states and sums, which are as large only next to overflow, do without.)
+__device__ __forceinline__ void split_input(float4v x, Frag p[kParts]) {
+  constexpr float kMost = 3.3895313892515355e38f;  // bf16's largest
+  float4v near;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) near[i] = __builtin_amdgcn_fmed3f(x[i], -kMost, kMost);
+  split<1>(near, p);
+  split<kParts - 1>(x - widen(p[0]), p + 1);
 }
 
 __device__ __forceinline__ Frag zero_frag() { return __builtin_bit_cast(bf16x4, u32x2{0u, 0u}); }
@@ -200,7 +212,7 @@ struct Slab {
     } else {
       Frag f[2][kParts];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) split<kParts>(__builtin_bit_cast(float4v, r[i]), f[i]);
+      for (int i = 0; i < 2; ++i) split_input(__builtin_bit_cast(float4v, r[i]), f[i]);
 #pragma unroll
       for (int p = 0; p < kParts; ++p) {
         *reinterpret_cast<bf16x4*>(t + p * PLANE + u0) = f[0][p];

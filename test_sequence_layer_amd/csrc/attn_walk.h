@@ -270,8 +270,13 @@ __device__ __forceinline__ void walk(const Walk<XT, YT, VT, QT, OT>& a, bool fre
     {
       Frag q0[NP], q1[NP], d0[NP], d1[NP];
       const float4v x0 = TV::sum(v0) * f0, x1 = TV::sum(v1) * f1;
-      split<NP>(x0, q0);
-      split<NP>(x1, q1);
+      if constexpr (NV == 1) {
+        split<NP>(x0, q0);
+        split<NP>(x1, q1);
+      } else {
+        split_input(x0, q0);
+        split_input(x1, q1);
+      }
       if constexpr (DG) {
         float4v m0, m1;
 #pragma unroll

@@ -113,3 +113,31 @@ def test_padding_reaches_nothing(ttt):
             x[b, :, m:] = float("nan")
     got = _run(ttt, dirty, more, None)
     assert all(torch.equal(got[n], clean[n]) for n in clean)
+
+
+@pytest.mark.parametrize("T", [70, 450])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_lowest_values_without_a_score(ttt, dtype, T):
+    """Tokens whose k is zero and whose v holds the type's lowest and largest values, as a mask may leave them: nothing of
+    them in Z and W_final.  The same of dK, dV and dW0 with zeros in dz or q and such values in the other.  (Not of dQ:
+    there such a v is in the score, dz.v, which overflows.)"""
+    c, more = _case(T, dtype, None)
+    more["log_decay"] = torch.tensor([-0.01, 0.0, -1.0, -0.1], device=DEV)
+    gone = torch.zeros(T, dtype=torch.bool)
+    gone[[0, 3, 17, 18, 40, T - 1]] = True
+    most = torch.finfo(dtype).max
+    edge = torch.where(torch.arange(D) % 2 == 0, -most, most).to(dtype).to(DEV)
+
+    def put(n, x):
+        y = c[n].clone()
+        y[:, :, gone] = x
+        return y
+
+    clean, held = ({**c, "k": put("k", 0), "v": put("v", x)} for x in (0, edge))
+    a, b = (_run(ttt, x, more, None) for x in (clean, held))
+    for n in ("z", "w"):
+        assert torch.equal(a[n], b[n]), n
+    for zero, full, names in (("dz", "q", ("dk", "dw0")), ("q", "dz", ("dv", "dw0"))):
+        a, b = (_run(ttt, {**c, zero: put(zero, 0), full: put(full, x)}, more, None) for x in (0, edge))
+        for n in names:
+            assert torch.equal(a[n], b[n]), (zero, n)
