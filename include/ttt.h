@@ -1,8 +1,9 @@
 /*
  * ttt.h -- C ABI of libttt.so, the MI355X (gfx950) TTT (test-time training)
  * sequence layer: the forward of TTT-Linear and TTT-MLP and the backward of
- * TTT-Linear, mini-batch dual form; linear attention with a decay per head; and
- * rotary positions.
+ * TTT-Linear, mini-batch dual form; linear attention with a decay per head; rotary
+ * positions; and what stands around a layer's state: the selective scan, its short
+ * causal convolution, and the norms, gate and residual sum between two blocks.
  *
  * Pages: [TTT] = news article "大模型最强架构TTT问世！斯坦福UCSD等5年磨一剑，
  * 一夜推翻Transformer" (aharts.cn / itmax.cn).
@@ -710,6 +711,233 @@ ttt_status ttt_rotary_validate(const ttt_rotary_desc* desc, const ttt_rope* rope
  * by element: ttt_rotary_pairs), or NULL for an invalid call or one that launches nothing. */
 const char* ttt_rotary_kernel_name(const ttt_rotary_desc* desc, const ttt_rope* rope, const void* q, const void* k,
                                    const void* q_out, const void* k_out);
+
+/*
+ * What stands around a layer's state: a short causal convolution, the selective scan
+ * and the join of two blocks ([TTT] 04: the backbones the layer is measured in).
+ *
+ * Conventions of these entry points, where they differ from those above
+ *  - X, Y and their like are [B, T, D], D channels of a token contiguous: element
+ *    (bi, t, c) is at bi*b + t*t' + c of its ttt_strides {b, h, t'} (h is not looked
+ *    at).  Strides as for linear attention (>= 0, outputs' elements apart).  Any
+ *    address and stride of whole elements will do; where all are multiples of 16
+ *    bytes and the channels (of a group) of 8 elements, rows go in 16-byte pieces.
+ *  - Outputs share no element with an input or another output (TTT_ERR_ALIAS) except
+ *    where said; slices of the same rows ([B, T, 2 D] halves, [B, T, N + N]) pass.
+ *  - lens: [B] int32 on the device, the tokens of each sequence (taken into [0, T]),
+ *    or NULL for T each.  Rows behind the last token are not read and reach nothing;
+ *    their outputs and gradients are written as zero; states are those after it.
+ *  - Parameters are fp32.  Their gradients are sums over all sequences and tokens,
+ *    added in a fixed order: the same inputs give the same bits.
+ *  - Sums and states are held in fp32, products are rounded once, at the end.
+ *  - 0 <= T <= 2^30, and a launch has fewer than 2^32 threads (TTT_ERR_SHAPE).
+ */
+
+#define TTT_FLAG_SILU 1u /* ttt_short_conv: silu(x) = x / (1 + exp(-x)) of the sum */
+
+typedef struct {
+  int32_t B, T, D, K;       /* K taps: 2, 3 or 4 (else TTT_ERR_UNSUPPORTED)                */
+  int32_t in_dtype;         /* ttt_dtype of X and of the states                            */
+  int32_t out_dtype;        /* ttt_dtype of Y; in the backward of dY, dX, dstate, dstate_final */
+  uint32_t flags;           /* 0 or TTT_FLAG_SILU                                          */
+  int32_t reserved;         /* must be 0                                                   */
+  ttt_strides x, y, dx;     /* y: Y, or dY; dx: the backward's output                      */
+} ttt_short_conv_desc;
+
+/*
+ * Short causal convolution, each channel by itself, forward (prompts):
+ *     y_t = act(bias + sum_{j < K} w[:, j] x_{t-K+1+j})
+ *   w    : [D, K], the last tap is the token's own;  bias : [D] or NULL
+ *   state: [B, K-1, D], the inputs before the first token, or NULL (zeros)
+ *   state_final : [B, K-1, D], the last K-1 inputs (reaching into state where a sequence
+ *       has fewer tokens), or NULL (not wanted).  Overlaps nothing.
+ * Each state is contiguous.
+ */
+ttt_status ttt_short_conv_fwd(const ttt_short_conv_desc* desc, const void* X, const float* w, const float* bias,
+                              const void* state, const int32_t* lens, void* Y, void* state_final, void* stream);
+
+/* Runs every host-side check of ttt_short_conv_fwd and launches nothing. */
+ttt_status ttt_short_conv_fwd_validate(const ttt_short_conv_desc* desc, const void* X, const float* w,
+                                       const float* bias, const void* state, const int32_t* lens, const void* Y,
+                                       const void* state_final);
+
+/*
+ * Backward, from the inputs alone: with dY and dstate_final (or NULL for zero) the
+ * gradients of a scalar with respect to Y and state_final, those with respect to
+ *   X : dX [B, T, D];  w : dw [D, K];  bias : dbias [D] or NULL (not wanted);
+ *   state : dstate [B, K-1, D] or NULL (not wanted)
+ * workspace: ttt_short_conv_workspace_bytes(desc) bytes, 16-byte aligned
+ * (TTT_ERR_WORKSPACE), overlapping nothing else; unspecified on return.
+ */
+ttt_status ttt_short_conv_bwd(const ttt_short_conv_desc* desc, const void* X, const float* w, const float* bias,
+                              const void* state, const int32_t* lens, const void* dY, const void* dstate_final,
+                              void* dX, float* dw, float* dbias, void* dstate, void* workspace,
+                              int64_t workspace_bytes, void* stream);
+
+/* Runs every host-side check of ttt_short_conv_bwd and launches nothing. */
+ttt_status ttt_short_conv_bwd_validate(const ttt_short_conv_desc* desc, const void* X, const float* w,
+                                       const float* bias, const void* state, const int32_t* lens, const void* dY,
+                                       const void* dstate_final, const void* dX, const float* dw, const float* dbias,
+                                       const void* dstate, const void* workspace, int64_t workspace_bytes);
+
+/* Workspace bytes of the backward, -1 for an invalid desc. */
+int64_t ttt_short_conv_workspace_bytes(const ttt_short_conv_desc* desc);
+
+/*
+ * Decode: continues B sequences by desc->T new tokens (often 1), state [B, K-1, D]
+ * read and written in place; with lens, sequences of length 0 keep theirs.  Decoding T
+ * tokens gives the Y and state_final of ttt_short_conv_fwd, bit for bit.  One launch.
+ */
+ttt_status ttt_short_conv_decode(const ttt_short_conv_desc* desc, const void* X, const float* w, const float* bias,
+                                 const int32_t* lens, void* Y, void* state, void* stream);
+
+/* Runs every host-side check of ttt_short_conv_decode and launches nothing. */
+ttt_status ttt_short_conv_decode_validate(const ttt_short_conv_desc* desc, const void* X, const float* w,
+                                          const float* bias, const int32_t* lens, const void* Y, const void* state);
+
+#define TTT_FLAG_SOFTPLUS 1u /* ttt_selective_scan: the step is log(1 + exp(dt + dt_bias)) */
+
+typedef struct {
+  int32_t B, T, D, N, G;    /* D channels in G groups, N states a channel: 1 <= N <= 32 (else TTT_ERR_UNSUPPORTED) */
+  int32_t in_dtype;         /* ttt_dtype of u, dt, z, Bm, Cm                               */
+  int32_t out_dtype;        /* ttt_dtype of y; in the backward of dy, du, ddt, dz, dBm, dCm */
+  uint32_t flags;           /* 0 or TTT_FLAG_SOFTPLUS                                      */
+  ttt_strides u, dt, z, y;  /* [B, T, D]; y: y, or dy                                      */
+  ttt_strides Bm, Cm;       /* [B, G, T, N], the N of a token contiguous; h is the group's stride */
+  ttt_strides du, ddt, dz, dBm, dCm; /* the backward's outputs (the others do not look)    */
+} ttt_selective_scan_desc;
+
+/*
+ * Selective scan, forward (prompts): a state of N numbers per channel whose decay and
+ * input depend on the token.  With step_t = dt_t + dt_bias (its softplus with the flag),
+ *     h_t = exp(step_t A) h_{t-1} + step_t Bm_t u_t
+ *     y_t = (sum_n Cm_t h_t + D u_t) silu(z_t)
+ * channel c reading Bm and Cm of group c / (D / G).
+ *   A : [D, N]; -inf keeps nothing;  D, dt_bias : [D], each or NULL (zero)
+ *   z : [B, T, D] or NULL (no gate);  h0 : [B, D, N] fp32 or NULL (zero)
+ *   h_final : [B, D, N] fp32, the state after the last token; may be exactly h0
+ *   workspace : ttt_selective_scan_workspace_bytes(desc, 0) bytes, 16-byte aligned
+ *       (TTT_ERR_WORKSPACE), overlapping nothing else; unspecified on return.
+ * Where there are few channels a sequence is walked in segments at the same time, whose
+ * start states a first launch computes.  exp and 1 / x are the hardware's (1 ulp).
+ */
+ttt_status ttt_selective_scan_fwd(const ttt_selective_scan_desc* desc, const void* u, const void* dt, const float* A,
+                                  const void* Bm, const void* Cm, const float* D, const void* z, const float* dt_bias,
+                                  const float* h0, const int32_t* lens, void* y, float* h_final, void* workspace,
+                                  int64_t workspace_bytes, void* stream);
+
+/* Runs every host-side check of ttt_selective_scan_fwd and launches nothing. */
+ttt_status ttt_selective_scan_fwd_validate(const ttt_selective_scan_desc* desc, const void* u, const void* dt,
+                                           const float* A, const void* Bm, const void* Cm, const float* D,
+                                           const void* z, const float* dt_bias, const float* h0, const int32_t* lens,
+                                           const void* y, const float* h_final, const void* workspace,
+                                           int64_t workspace_bytes);
+
+/*
+ * Backward, from the inputs alone: with dy and dh_final (or NULL for zero) the gradients
+ * of a scalar with respect to y and h_final, those with respect to every input:
+ *   du, ddt, dz [B, T, D] (dz NULL exactly where z is);  dBm, dCm [B, G, T, N]
+ *   dA [D, N];  dD, ddt_bias [D], dh0 [B, D, N] fp32, each or NULL (not wanted)
+ * (the gradient of h0 is there without h0 too).  workspace as for the forward,
+ * ttt_selective_scan_workspace_bytes(desc, 1) bytes.
+ */
+ttt_status ttt_selective_scan_bwd(const ttt_selective_scan_desc* desc, const void* u, const void* dt, const float* A,
+                                  const void* Bm, const void* Cm, const float* D, const void* z, const float* dt_bias,
+                                  const float* h0, const int32_t* lens, const void* dy, const float* dh_final,
+                                  void* du, void* ddt, float* dA, void* dBm, void* dCm, float* dD, void* dz,
+                                  float* ddt_bias, float* dh0, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Runs every host-side check of ttt_selective_scan_bwd and launches nothing. */
+ttt_status ttt_selective_scan_bwd_validate(const ttt_selective_scan_desc* desc, const void* u, const void* dt,
+                                           const float* A, const void* Bm, const void* Cm, const float* D,
+                                           const void* z, const float* dt_bias, const float* h0, const int32_t* lens,
+                                           const void* dy, const float* dh_final, const void* du, const void* ddt,
+                                           const float* dA, const void* dBm, const void* dCm, const float* dD,
+                                           const void* dz, const float* ddt_bias, const float* dh0,
+                                           const void* workspace, int64_t workspace_bytes);
+
+/* Workspace bytes of the forward (backward = 0) or the backward (1); 0 where none is needed, -1 for an invalid desc. */
+int64_t ttt_selective_scan_workspace_bytes(const ttt_selective_scan_desc* desc, int32_t backward);
+
+/*
+ * Decode: continues B sequences by desc->T new tokens (often 1), the state h [B, D, N]
+ * fp32 read and written in place; with lens, sequences of length 0 keep theirs.  Decoding
+ * T tokens from h = h0 gives the y and h_final of ttt_selective_scan_fwd (to rounding).
+ * One launch.
+ */
+ttt_status ttt_selective_scan_decode(const ttt_selective_scan_desc* desc, const void* u, const void* dt,
+                                     const float* A, const void* Bm, const void* Cm, const float* D, const void* z,
+                                     const float* dt_bias, const int32_t* lens, void* y, float* h, void* stream);
+
+/* Runs every host-side check of ttt_selective_scan_decode and launches nothing. */
+ttt_status ttt_selective_scan_decode_validate(const ttt_selective_scan_desc* desc, const void* u, const void* dt,
+                                              const float* A, const void* Bm, const void* Cm, const float* D,
+                                              const void* z, const float* dt_bias, const int32_t* lens, const void* y,
+                                              const float* h);
+
+#define TTT_FLAG_RMS 1u        /* ttt_block_norm: no mean is taken off (else: layer norm)          */
+#define TTT_FLAG_GATE_FIRST 2u /* ttt_block_norm: the gate before the norm behind the block        */
+
+typedef struct {
+  int32_t B, T, D;          /* 1 <= D <= 8192 (else TTT_ERR_UNSUPPORTED)                       */
+  int32_t in_dtype;         /* ttt_dtype of X, Z, Y and their gradients                        */
+  int32_t res_dtype;        /* ttt_dtype of res, S and their gradients                         */
+  uint32_t flags;           /* TTT_FLAG_RMS, TTT_FLAG_GATE_FIRST                               */
+  float eps;                /* finite, >= 0 (TTT_ERR_SHAPE)                                    */
+  int32_t reserved;         /* must be 0                                                       */
+  ttt_strides x, z, res, s, y; /* s, y: S, Y, or dS, dY                                        */
+  ttt_strides dx, dz, dres; /* the backward's outputs                                          */
+} ttt_block_norm_desc;
+
+/*
+ * The join of two blocks: the norm behind one, its gate, the scaled sum with the residual
+ * stream, and the norm before the next.  With NORM(x) = (x - mean) / sqrt(var + eps) over
+ * the D channels of a token (TTT_FLAG_RMS: mean = 0, var the mean square),
+ *     n = NORM(X) gamma_post + beta_post,   v = n silu(Z)
+ *         (TTT_FLAG_GATE_FIRST: v = n = NORM(X silu(Z)) gamma_post + beta_post)
+ *     S = res + alpha v,                    Y = NORM(S) gamma_pre + beta_pre
+ * with Y from S before its rounding.  Z (no gate), res (zero), gamma_post (no norm behind
+ * the block; then no beta_post either, TTT_ERR_NULL), beta_post, alpha (1), beta_pre may be
+ * NULL; so may S or Y, which is then not written (gamma_pre exactly where Y is: TTT_ERR_NULL).
+ * S may be exactly res (same address, strides and type).
+ */
+ttt_status ttt_block_norm_fwd(const ttt_block_norm_desc* desc, const void* X, const void* Z, const void* res,
+                              const float* alpha, const float* gamma_post, const float* beta_post,
+                              const float* gamma_pre, const float* beta_pre, const int32_t* lens, void* S, void* Y,
+                              void* stream);
+
+/* Runs every host-side check of ttt_block_norm_fwd and launches nothing. */
+ttt_status ttt_block_norm_fwd_validate(const ttt_block_norm_desc* desc, const void* X, const void* Z, const void* res,
+                                       const float* alpha, const float* gamma_post, const float* beta_post,
+                                       const float* gamma_pre, const float* beta_pre, const int32_t* lens,
+                                       const void* S, const void* Y);
+
+/*
+ * Backward, from the inputs alone: with dS and dY (each or NULL for zero; gamma_pre where
+ * dY is) the gradients of a scalar with respect to S and Y, those with respect to
+ *   X : dX;  Z : dZ (NULL exactly where Z is);  res : dres or NULL (not wanted);
+ *   dalpha, dgamma_post, dbeta_post, dgamma_pre, dbeta_pre [D], each or NULL (not wanted;
+ *   what they belong to need not have been given: that of a missing alpha is that of 1)
+ * workspace: ttt_block_norm_workspace_bytes(desc) bytes, 16-byte aligned
+ * (TTT_ERR_WORKSPACE), overlapping nothing else; unspecified on return.
+ */
+ttt_status ttt_block_norm_bwd(const ttt_block_norm_desc* desc, const void* X, const void* Z, const void* res,
+                              const float* alpha, const float* gamma_post, const float* beta_post,
+                              const float* gamma_pre, const int32_t* lens, const void* dS, const void* dY, void* dX,
+                              void* dZ, void* dres, float* dalpha, float* dgamma_post, float* dbeta_post,
+                              float* dgamma_pre, float* dbeta_pre, void* workspace, int64_t workspace_bytes,
+                              void* stream);
+
+/* Runs every host-side check of ttt_block_norm_bwd and launches nothing. */
+ttt_status ttt_block_norm_bwd_validate(const ttt_block_norm_desc* desc, const void* X, const void* Z, const void* res,
+                                       const float* alpha, const float* gamma_post, const float* beta_post,
+                                       const float* gamma_pre, const int32_t* lens, const void* dS, const void* dY,
+                                       const void* dX, const void* dZ, const void* dres, const float* dalpha,
+                                       const float* dgamma_post, const float* dbeta_post, const float* dgamma_pre,
+                                       const float* dbeta_pre, const void* workspace, int64_t workspace_bytes);
+
+/* Workspace bytes of the backward, -1 for an invalid desc. */
+int64_t ttt_block_norm_workspace_bytes(const ttt_block_norm_desc* desc);
 
 /* Human-readable text of a status code (never NULL). */
 const char* ttt_status_str(int status);

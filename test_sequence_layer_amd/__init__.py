@@ -1,5 +1,6 @@
 """MI355X (gfx950) TTT sequence layer (forward, and the TTT-Linear backward), linear
-attention with a decay per head, and rotary positions -- Python binding.
+attention with a decay per head, rotary positions, and what stands around a layer's
+state (short convolution, selective scan, block norm) -- Python binding.
 
 Thin ctypes layer over libttt.so (C ABI in include/ttt.h).  It only checks and
 marshals arguments: torch supplies device memory and the current HIP stream,
@@ -14,6 +15,9 @@ no CPU or PyTorch fallback: if libttt.so is missing, importing the ops raises.
     q, k = ttt.rotary(q, k, pos=0, freqs=freqs)
     z, w_final = ttt.linear_attn_fwd(q, k, v, log_decay)
     z = ttt.linear_attn_decode(q1, k1, v1, log_decay, w_final, rope=(pos, freqs))
+    x, conv_state = ttt.short_conv_fwd(x, w, bias, silu=True)
+    y, h_final = ttt.selective_scan_fwd(x, dt, A, Bm, Cm, D=D, z=z, dt_bias=dt_bias, softplus=True)
+    residual, x = ttt.block_norm_fwd(y, res=residual, alpha=alpha, gamma_pre=gamma)
 
 Pages: [TTT] = news article "大模型最强架构TTT问世！斯坦福UCSD等5年磨一剑，一夜推翻Transformer"
 (aharts.cn / itmax.cn), part 03 §1-§9 (the TTT layer, mini-batch GD, the dual
@@ -34,6 +38,9 @@ TTT_F32, TTT_BF16 = 0, 1
 TTT_FLAG_GENERIC = 1
 TTT_FLAG_PRIMAL = 2
 TTT_FLAG_INVERSE = 1  # ttt_rotary
+TTT_FLAG_SILU = 1  # ttt_short_conv
+TTT_FLAG_SOFTPLUS = 1  # ttt_selective_scan
+TTT_FLAG_RMS, TTT_FLAG_GATE_FIRST = 1, 2  # ttt_block_norm
 TTT_FLAG_ROWS = {1: 4, 2: 8, 4: 16}  # row blocks per (sequence, head) -> TTT_FLAG_ROWS1/2/4
 
 
@@ -68,6 +75,13 @@ EXPORTS = (
     "ttt_linear_attn_fwd", "ttt_linear_attn_fwd_validate", "ttt_linear_attn_bwd", "ttt_linear_attn_bwd_validate",
     "ttt_linear_attn_workspace_bytes", "ttt_linear_attn_decode", "ttt_linear_attn_decode_validate",
     "ttt_rotary", "ttt_rotary_validate", "ttt_rotary_kernel_name",
+    "ttt_short_conv_fwd", "ttt_short_conv_fwd_validate", "ttt_short_conv_bwd", "ttt_short_conv_bwd_validate",
+    "ttt_short_conv_workspace_bytes", "ttt_short_conv_decode", "ttt_short_conv_decode_validate",
+    "ttt_selective_scan_fwd", "ttt_selective_scan_fwd_validate", "ttt_selective_scan_bwd",
+    "ttt_selective_scan_bwd_validate", "ttt_selective_scan_workspace_bytes", "ttt_selective_scan_decode",
+    "ttt_selective_scan_decode_validate",
+    "ttt_block_norm_fwd", "ttt_block_norm_fwd_validate", "ttt_block_norm_bwd", "ttt_block_norm_bwd_validate",
+    "ttt_block_norm_workspace_bytes",
     "ttt_status_str", "ttt_abi_version",
 )
 
@@ -120,6 +134,33 @@ class RotaryDesc(ctypes.Structure):
         ("B", ctypes.c_int32), ("H", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("T", ctypes.c_int32),
         ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32), ("reserved", ctypes.c_int32),
         ("q", Strides), ("k", Strides), ("q_out", Strides), ("k_out", Strides),
+    ]
+
+
+class ShortConvDesc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("D", ctypes.c_int32), ("K", ctypes.c_int32),
+        ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32), ("reserved", ctypes.c_int32),
+        ("x", Strides), ("y", Strides), ("dx", Strides),
+    ]
+
+
+class SelectiveScanDesc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("D", ctypes.c_int32), ("N", ctypes.c_int32), ("G", ctypes.c_int32),
+        ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32),
+        ("u", Strides), ("dt", Strides), ("z", Strides), ("y", Strides), ("Bm", Strides), ("Cm", Strides),
+        ("du", Strides), ("ddt", Strides), ("dz", Strides), ("dBm", Strides), ("dCm", Strides),
+    ]
+
+
+class BlockNormDesc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("D", ctypes.c_int32),
+        ("in_dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32), ("eps", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+        ("x", Strides), ("z", Strides), ("res", Strides), ("s", Strides), ("y", Strides),
+        ("dx", Strides), ("dz", Strides), ("dres", Strides),
     ]
 
 
@@ -255,6 +296,19 @@ def lib() -> ctypes.CDLL:
     L.ttt_linear_attn_decode.restype = ctypes.c_int
     L.ttt_linear_attn_decode_validate.argtypes = [ad, vp, vp, vp, fp, vp, ctypes.POINTER(Rope), vp, fp]
     L.ttt_linear_attn_decode_validate.restype = ctypes.c_int
+    cd, sd, nd = ctypes.POINTER(ShortConvDesc), ctypes.POINTER(SelectiveScanDesc), ctypes.POINTER(BlockNormDesc)
+    conv, scan, norm = [cd] + [vp] * 5, [sd] + [vp] * 10, [nd] + [vp] * 8
+    for name, args in (
+            ("ttt_short_conv_fwd", conv + [vp] * 2), ("ttt_short_conv_bwd", conv + [vp] * 7 + [i64]),
+            ("ttt_short_conv_decode", [cd] + [vp] * 6),
+            ("ttt_selective_scan_fwd", scan + [vp] * 3 + [i64]), ("ttt_selective_scan_bwd", scan + [vp] * 12 + [i64]),
+            ("ttt_selective_scan_decode", [sd] + [vp] * 11),
+            ("ttt_block_norm_fwd", norm + [vp] * 3), ("ttt_block_norm_bwd", norm + [vp] * 11 + [i64])):
+        for f, a in ((getattr(L, name), args + [vp]), (getattr(L, name + "_validate"), args)):
+            f.argtypes, f.restype = a, ctypes.c_int
+    for name, args in (("ttt_short_conv_workspace_bytes", [cd]), ("ttt_selective_scan_workspace_bytes", [sd, ctypes.c_int32]),
+                       ("ttt_block_norm_workspace_bytes", [nd])):
+        getattr(L, name).argtypes, getattr(L, name).restype = args, i64
     L.ttt_rotary.argtypes = [ctypes.POINTER(RotaryDesc), ctypes.POINTER(Rope), vp, vp, vp, vp, vp]
     L.ttt_rotary.restype = ctypes.c_int
     L.ttt_rotary_validate.argtypes = [ctypes.POINTER(RotaryDesc), ctypes.POINTER(Rope), vp, vp, vp, vp]
@@ -1364,3 +1418,441 @@ def rotary(q, k, pos, freqs, layout: str = "half", scale: float = 1.0, out=None,
 def rotary_bwd(dq, dk, pos, freqs, layout: str = "half", scale: float = 1.0, out=None, stream=None):
     """Backward of :func:`rotary`: the gradients with respect to its q and k, given those with respect to its outputs."""
     return _rotary_call(dq, dk, pos, freqs, layout, scale, out, stream, TTT_FLAG_INVERSE, "ttt_rotary")
+
+
+# --------------------------- short convolution, selective scan, block norm --
+
+_block_descs = {}  # as _attn_descs, for the three
+
+
+def _row_strides(t) -> Strides:
+    """(b, -, t) element strides of a [B, T, D] tensor whose rows are contiguous; zeros for None."""
+    if t is None:
+        return Strides()
+    b, s, e = t.stride()
+    if e != 1 and t.shape[2] > 1:
+        raise ValueError("the last dimension must be contiguous")
+    return Strides(b, 0, s)
+
+
+def _kept(key, make):
+    got = _block_descs.get(key)
+    if got is None:
+        got = make()
+        if len(_block_descs) >= 1024:
+            _block_descs.clear()
+        _block_descs[key] = got
+    return got
+
+
+def _want_rows(x, shape, dtype, what):
+    if x is not None and (tuple(x.shape) != tuple(shape) or x.dtype != dtype):
+        raise ValueError(f"{what} must be {dtype} {tuple(shape)}, not {x.dtype} {tuple(x.shape)}")
+
+
+def _want_params(shape, **ps):
+    for what, x in ps.items():
+        if x is not None:
+            _want(x, shape, _torch().float32, what)
+
+
+def _want_lens(lens, B):
+    if lens is not None:
+        if lens.dtype != _torch().int32:
+            raise TypeError("lens must be int32")
+        _want(lens, (B,), _torch().int32, "lens")
+
+
+def _call_on(x, stream, call):
+    """call() with the tensors' device and the given stream current, as every entry point here runs."""
+    on = _on(x, stream)
+    if on is None:
+        return call()
+    with on:
+        return call()
+
+
+def _conv_call(x, w, bias, state, lens, out_dtype, silu, y, dx=None):
+    """Checked (descriptor, workspace bytes) of a short convolution; y: Y, or dY."""
+    def make():
+        if x.dim() != 3:
+            raise ValueError(f"x {tuple(x.shape)}: expected [B, T, D]")
+        _check_sizes(x.shape)
+        B, T, D = x.shape
+        if w.dim() != 2 or w.shape[0] != D:
+            raise ValueError(f"w {tuple(w.shape)}: expected [D, K] with D = {D}")
+        K = w.shape[1]
+        _want_params((D, K), w=w)
+        _want_params((D,), bias=bias)
+        _want_lens(lens, B)
+        if state is not None:
+            _want(state, (B, K - 1, D), x.dtype, "state")
+        _want_rows(y, x.shape, out_dtype, "y or dy")
+        _want_rows(dx, x.shape, out_dtype, "dx")
+        desc = ShortConvDesc(B, T, D, K, _dtype_code(x.dtype), _dtype_code(out_dtype), TTT_FLAG_SILU if silu else 0, 0,
+                             _row_strides(x), _row_strides(y), _row_strides(dx))
+        return desc, int(lib().ttt_short_conv_workspace_bytes(ctypes.byref(desc)))
+
+    return _kept(("conv", *map(_layout, (x, w, bias, state, lens, y, dx)), out_dtype, bool(silu)), make)
+
+
+def short_conv_fwd(x, w, bias=None, state=None, silu: bool = False, lens=None, out_dtype=None, y=None, state_final=None,
+                   stream=None):
+    """Short causal convolution of each channel: y_t = act(bias + sum_j w[:, j] x_{t-K+1+j}).
+
+    x      : [B, T, D] bfloat16 or float32, channels contiguous, any strides between sequences and tokens
+    w      : [D, K] float32, K in {2, 3, 4}, the last tap the token's own;  bias : [D] float32 or None
+    state  : [B, K-1, D] of x's dtype, the inputs before the first token, or None (zeros)
+    silu   : act(x) = x / (1 + exp(-x)), else the sum itself
+    lens   : [B] int32, the tokens of each sequence, or None (T each).  Rows behind them are not read and give zeros
+    returns (y [B, T, D] of out_dtype (default x's), state_final [B, K-1, D], the last K-1 inputs).
+    """
+    torch = _torch()
+    _check_same_dev(x, w, bias, state, lens, y, state_final)
+
+    def call():
+        nonlocal y, state_final
+        if y is None:
+            y = _like(x, out_dtype or x.dtype)
+        elif out_dtype is not None and y.dtype != out_dtype:
+            raise ValueError(f"y is {y.dtype}, out_dtype {out_dtype}")
+        desc, _ = _conv_call(x, w, bias, state, lens, y.dtype, silu, y)
+        shape = (desc.B, desc.K - 1, desc.D)
+        if state_final is None:
+            state_final = torch.empty(shape, dtype=x.dtype, device=x.device)
+        else:
+            _want(state_final, shape, x.dtype, "state_final")
+        st = lib().ttt_short_conv_fwd(ctypes.byref(desc), x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(state), _ptr(lens),
+                                      y.data_ptr(), state_final.data_ptr(), _stream_handle(stream, x.device.index))
+        _done(st, "ttt_short_conv_fwd")
+        return y, state_final
+
+    return _call_on(x, stream, call)
+
+
+def short_conv_bwd(x, w, dy, bias=None, state=None, silu: bool = False, lens=None, dstate_final=None, workspace=None,
+                   out=None, stream=None):
+    """Backward of :func:`short_conv_fwd`, from its inputs alone.
+
+    dy           : [B, T, D] gradient with respect to y (its dtype is that of dx, dstate and dstate_final)
+    dstate_final : [B, K-1, D] gradient with respect to state_final, or None (zero)
+    workspace    : uint8 tensor of short_conv_workspace_bytes(...), or None (allocated)
+    out          : optional (dx, dw, dbias, dstate) preallocated outputs
+    returns (dx [B, T, D], dw [D, K], dbias [D] float32, summed over sequences and tokens, dstate [B, K-1, D]).
+    """
+    torch = _torch()
+    _check_same_dev(x, w, dy, bias, state, lens, dstate_final, workspace, *(out or ()))
+
+    def call():
+        nonlocal workspace
+        f32 = torch.float32
+        dx = out[0] if out is not None else _like(x, dy.dtype)
+        desc, need = _conv_call(x, w, bias, state, lens, dy.dtype, silu, dy, dx)
+        B, D, K = desc.B, desc.D, desc.K
+        if dstate_final is not None:
+            _want(dstate_final, (B, K - 1, D), dy.dtype, "dstate_final")
+        if out is None:
+            e = lambda shape, dt: torch.empty(shape, dtype=dt, device=x.device)  # noqa: E731
+            dw, dbias, dstate = e((D, K), f32), e((D,), f32), e((B, K - 1, D), dy.dtype)
+        else:
+            _, dw, dbias, dstate = out
+            _want(dw, (D, K), f32, "dw")
+            _want(dbias, (D,), f32, "dbias")
+            _want(dstate, (B, K - 1, D), dy.dtype, "dstate")
+        ws, need = _attn_workspace(need, workspace, x.device)
+        st = lib().ttt_short_conv_bwd(ctypes.byref(desc), x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(state), _ptr(lens),
+                                      dy.data_ptr(), _ptr(dstate_final), dx.data_ptr(), dw.data_ptr(), dbias.data_ptr(),
+                                      dstate.data_ptr(), _ptr(ws), need, _stream_handle(stream, x.device.index))
+        _done(st, "ttt_short_conv_bwd")
+        return dx, dw, dbias, dstate
+
+    return _call_on(x, stream, call)
+
+
+def short_conv_workspace_bytes(x, w) -> int:
+    """Bytes of workspace that :func:`short_conv_bwd` takes on inputs like x [B, T, D] and w [D, K]."""
+    _check_sizes(x.shape)
+    B, T, D = x.shape
+    code = _dtype_code(x.dtype)
+    return int(lib().ttt_short_conv_workspace_bytes(ctypes.byref(ShortConvDesc(B, T, D, w.shape[1], code, code))))
+
+
+def short_conv_decode(x, w, state, bias=None, silu: bool = False, lens=None, out_dtype=None, y=None, stream=None):
+    """Continue B sequences of :func:`short_conv_fwd` by T new tokens (often 1), the state carried in place.
+
+    x : [B, T, D];  state : [B, K-1, D] of x's dtype, updated in place;  lens : [B] int32, the new tokens of each
+    sequence (0: its state stays), or None (T each).  returns y [B, T, D].
+    """
+    _check_same_dev(x, w, state, bias, lens, y)
+
+    def call():
+        nonlocal y
+        if y is None:
+            y = _like(x, out_dtype or x.dtype)
+        elif out_dtype is not None and y.dtype != out_dtype:
+            raise ValueError(f"y is {y.dtype}, out_dtype {out_dtype}")
+        desc, _ = _conv_call(x, w, bias, state, lens, y.dtype, silu, y)
+        st = lib().ttt_short_conv_decode(ctypes.byref(desc), x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(lens),
+                                         y.data_ptr(), state.data_ptr(), _stream_handle(stream, x.device.index))
+        _done(st, "ttt_short_conv_decode")
+        return y
+
+    return _call_on(x, stream, call)
+
+
+def _scan_call(u, dt, A, Bm, Cm, D, z, dt_bias, h0, softplus, lens, y, grads=(None,) * 5):
+    """Checked (descriptor, forward and backward workspace bytes) of a selective scan; y: y, or dy; grads: du, ddt, dz,
+    dBm, dCm."""
+    def make():
+        if u.dim() != 3 or Bm.dim() != 4:
+            raise ValueError(f"u {tuple(u.shape)}, Bm {tuple(Bm.shape)}: expected [B, T, D] and [B, G, T, N]")
+        _check_sizes(u.shape, Bm.shape)
+        B, T, Dn = u.shape
+        G, N = Bm.shape[1], Bm.shape[3]
+        if G < 1 or Dn % G:
+            raise ValueError(f"{Dn} channels are not {G} groups of one size")
+        for what, x in (("dt", dt), ("z", z)):
+            _want_rows(x, u.shape, u.dtype, what)
+        for what, x in (("Bm", Bm), ("Cm", Cm)):
+            _want_rows(x, (B, G, T, N), u.dtype, what)
+        _want_params((Dn, N), A=A)
+        _want_params((Dn,), D=D, dt_bias=dt_bias)
+        _want_params((B, Dn, N), h0=h0)
+        _want_lens(lens, B)
+        _want_rows(y, u.shape, y.dtype, "y or dy")
+        du, ddt, dz, dB, dC = grads
+        for what, x in (("du", du), ("ddt", ddt), ("dz", dz)):
+            _want_rows(x, u.shape, y.dtype, what)
+        for what, x in (("dBm", dB), ("dCm", dC)):
+            _want_rows(x, Bm.shape, y.dtype, what)
+        bc = lambda x: Strides() if x is None else _strides(x)  # noqa: E731
+        desc = SelectiveScanDesc(B, T, Dn, N, G, _dtype_code(u.dtype), _dtype_code(y.dtype),
+                                 TTT_FLAG_SOFTPLUS if softplus else 0, *map(_row_strides, (u, dt, z, y)), bc(Bm), bc(Cm),
+                                 *map(_row_strides, (du, ddt, dz)), bc(dB), bc(dC))
+        return (desc, *(int(lib().ttt_selective_scan_workspace_bytes(ctypes.byref(desc), b)) for b in (0, 1)))
+
+    return _kept(("scan", *map(_layout, (u, dt, A, Bm, Cm, D, z, dt_bias, h0, lens, y, *grads)), bool(softplus)), make)
+
+
+def selective_scan_fwd(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, softplus: bool = False, lens=None,
+                       out_dtype=None, y=None, h_final=None, workspace=None, stream=None):
+    """Selective scan: h_t = exp(step_t A) h_{t-1} + step_t Bm_t u_t, y_t = (sum_n Cm_t h_t + D u_t) silu(z_t).
+
+    u, dt, z : [B, T, D] bfloat16 or float32, channels contiguous, any strides between sequences and tokens; z may be None
+               (no gate).  step = dt + dt_bias, with ``softplus`` its log(1 + exp(.))
+    Bm, Cm   : [B, G, T, N] of the same dtype, 1 <= N <= 32, the N of a token contiguous; channel c reads group c // (D // G)
+    A        : [D, N] float32 (-inf keeps nothing);  D, dt_bias : [D] float32 or None (zero)
+    h0       : initial state [B, D, N] float32, or None (zero)
+    lens     : [B] int32, the tokens of each sequence, or None (T each).  Rows behind them are not read and give zeros
+    returns (y [B, T, D] of out_dtype (default u's), h_final [B, D, N] float32, the state after the last token).
+    ``h_final`` may be ``h0`` itself.  ``workspace``: uint8 tensor of :func:`selective_scan_workspace_bytes` (allocated when
+    omitted); calls that may overlap need one each.
+    """
+    torch = _torch()
+    _check_same_dev(u, dt, A, Bm, Cm, D, z, dt_bias, h0, lens, y, h_final, workspace)
+
+    def call():
+        nonlocal y, h_final
+        if y is None:
+            y = _like(u, out_dtype or u.dtype)
+        elif out_dtype is not None and y.dtype != out_dtype:
+            raise ValueError(f"y is {y.dtype}, out_dtype {out_dtype}")
+        desc, need, _ = _scan_call(u, dt, A, Bm, Cm, D, z, dt_bias, h0, softplus, lens, y)
+        shape = (desc.B, desc.D, desc.N)
+        if h_final is None:
+            h_final = torch.empty(shape, dtype=torch.float32, device=u.device)
+        else:
+            _want(h_final, shape, torch.float32, "h_final")
+        ws = workspace
+        if need or ws is not None:
+            ws, need = _attn_workspace(need, ws, u.device)
+        st = lib().ttt_selective_scan_fwd(ctypes.byref(desc), u.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(),
+                                          Cm.data_ptr(), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(h0), _ptr(lens), y.data_ptr(),
+                                          h_final.data_ptr(), _ptr(ws), need, _stream_handle(stream, u.device.index))
+        _done(st, "ttt_selective_scan_fwd")
+        return y, h_final
+
+    return _call_on(u, stream, call)
+
+
+def selective_scan_bwd(u, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, h0=None, dh_final=None, softplus: bool = False,
+                       lens=None, workspace=None, out=None, stream=None):
+    """Backward of :func:`selective_scan_fwd`, from its inputs alone.
+
+    dy        : [B, T, D] gradient with respect to y (its dtype is that of du, ddt, dBm, dCm, dz)
+    dh_final  : [B, D, N] float32 gradient with respect to h_final, or None (zero)
+    workspace : uint8 tensor of selective_scan_workspace_bytes(..., backward=True), or None (allocated)
+    out       : optional (du, ddt, dA, dBm, dCm, dD, dz, ddt_bias, dh0) preallocated outputs
+    returns (du, ddt [B, T, D], dA [D, N], dBm, dCm [B, G, T, N], dD [D], dz [B, T, D] or None without z, ddt_bias [D],
+    dh0 [B, D, N]); those of parameters and states are float32, the parameters' summed over sequences and tokens.
+    """
+    torch = _torch()
+    _check_same_dev(u, dt, A, Bm, Cm, dy, D, z, dt_bias, h0, dh_final, lens, workspace, *(out or ()))
+
+    def call():
+        f32 = torch.float32
+        if out is None:
+            du, ddt, dB, dC = _like(u, dy.dtype), _like(dt, dy.dtype), _like(Bm, dy.dtype), _like(Cm, dy.dtype)
+            dz = None if z is None else _like(z, dy.dtype)
+        else:
+            du, ddt, dA, dB, dC, dD, dz, db, dh0 = out
+            if (dz is None) != (z is None):
+                raise ValueError("out must hold an output for z exactly where z is given")
+        desc, _, need = _scan_call(u, dt, A, Bm, Cm, D, z, dt_bias, h0, softplus, lens, dy, (du, ddt, dz, dB, dC))
+        B, Dn, N = desc.B, desc.D, desc.N
+        _want_params((B, Dn, N), dh_final=dh_final)
+        if out is None:
+            dA, dD, db, dh0 = (torch.empty(s, dtype=f32, device=u.device) for s in ((Dn, N), (Dn,), (Dn,), (B, Dn, N)))
+        else:
+            _want_params((Dn, N), dA=dA)
+            _want_params((Dn,), dD=dD, ddt_bias=db)
+            _want_params((B, Dn, N), dh0=dh0)
+        ws, need = _attn_workspace(need, workspace, u.device)
+        st = lib().ttt_selective_scan_bwd(ctypes.byref(desc), u.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(),
+                                          Cm.data_ptr(), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(h0), _ptr(lens),
+                                          dy.data_ptr(), _ptr(dh_final), du.data_ptr(), ddt.data_ptr(), dA.data_ptr(),
+                                          dB.data_ptr(), dC.data_ptr(), _ptr(dD), _ptr(dz), _ptr(db), _ptr(dh0), _ptr(ws),
+                                          need, _stream_handle(stream, u.device.index))
+        _done(st, "ttt_selective_scan_bwd")
+        return du, ddt, dA, dB, dC, dD, dz, db, dh0
+
+    return _call_on(u, stream, call)
+
+
+def selective_scan_workspace_bytes(u, Bm, backward: bool = False) -> int:
+    """Bytes of workspace that a call on inputs like u [B, T, D] and Bm [B, G, T, N] takes."""
+    _check_sizes(u.shape, Bm.shape)
+    B, T, D = u.shape
+    code = _dtype_code(u.dtype)
+    desc = SelectiveScanDesc(B, T, D, Bm.shape[3], Bm.shape[1], code, code)
+    return int(lib().ttt_selective_scan_workspace_bytes(ctypes.byref(desc), int(backward)))
+
+
+def selective_scan_decode(u, dt, A, Bm, Cm, h, D=None, z=None, dt_bias=None, softplus: bool = False, lens=None,
+                          out_dtype=None, y=None, stream=None):
+    """Continue B sequences of :func:`selective_scan_fwd` by T new tokens (often 1), the state carried in place.
+
+    Arguments as there;  h : [B, D, N] float32, updated in place;  lens : [B] int32, the new tokens of each sequence (0:
+    its state stays), or None (T each).  returns y [B, T, D].
+    """
+    _check_same_dev(u, dt, A, Bm, Cm, h, D, z, dt_bias, lens, y)
+
+    def call():
+        nonlocal y
+        if y is None:
+            y = _like(u, out_dtype or u.dtype)
+        elif out_dtype is not None and y.dtype != out_dtype:
+            raise ValueError(f"y is {y.dtype}, out_dtype {out_dtype}")
+        desc, _, _ = _scan_call(u, dt, A, Bm, Cm, D, z, dt_bias, h, softplus, lens, y)
+        st = lib().ttt_selective_scan_decode(ctypes.byref(desc), u.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(),
+                                             Cm.data_ptr(), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(lens), y.data_ptr(),
+                                             h.data_ptr(), _stream_handle(stream, u.device.index))
+        _done(st, "ttt_selective_scan_decode")
+        return y
+
+    return _call_on(u, stream, call)
+
+
+def _norm_call(x, z, res, alpha, gamma_post, beta_post, gamma_pre, beta_pre, kind, eps, gate_first, lens, s, y, res_dtype,
+               grads=(None,) * 3):
+    """Checked (descriptor, workspace bytes) of a block norm; s, y: S, Y, or dS, dY; grads: dx, dz, dres."""
+    eps = float(eps)
+
+    def make():
+        if x.dim() != 3:
+            raise ValueError(f"x {tuple(x.shape)}: expected [B, T, D]")
+        if kind not in ("rms", "layer"):
+            raise ValueError(f"kind must be 'rms' or 'layer', not {kind!r}")
+        _check_sizes(x.shape)
+        B, T, D = x.shape
+        dx, dz, dres = grads
+        for what, t, dt in (("z", z, x.dtype), ("res", res, res_dtype), ("s or ds", s, res_dtype), ("y or dy", y, x.dtype),
+                            ("dx", dx, x.dtype), ("dz", dz, x.dtype), ("dres", dres, res_dtype)):
+            _want_rows(t, x.shape, dt, what)
+        _want_params((D,), alpha=alpha, gamma_post=gamma_post, beta_post=beta_post, gamma_pre=gamma_pre, beta_pre=beta_pre)
+        _want_lens(lens, B)
+        flags = (TTT_FLAG_RMS if kind == "rms" else 0) | (TTT_FLAG_GATE_FIRST if gate_first else 0)
+        desc = BlockNormDesc(B, T, D, _dtype_code(x.dtype), _dtype_code(res_dtype), flags, eps, 0,
+                             *map(_row_strides, (x, z, res, s, y, dx, dz, dres)))
+        return desc, int(lib().ttt_block_norm_workspace_bytes(ctypes.byref(desc)))
+
+    key = ("norm", *map(_layout, (x, z, res, alpha, gamma_post, beta_post, gamma_pre, beta_pre, lens, s, y, *grads)), kind,
+           eps, bool(gate_first), res_dtype)
+    return _kept(key, make)
+
+
+def block_norm_fwd(x, res=None, z=None, alpha=None, gamma_post=None, beta_post=None, gamma_pre=None, beta_pre=None,
+                   kind: str = "rms", eps: float = 1e-6, gate_first: bool = False, lens=None, res_dtype=None, s=None, y=None,
+                   keep: bool = True, stream=None):
+    """The join of two blocks: v = NORM(x) gamma_post + beta_post, gated by silu(z); s = res + alpha v; y = NORM(s) gamma_pre
+    + beta_pre (from s before its rounding).
+
+    x     : [B, T, D] bfloat16 or float32, what a block gave, channels contiguous;  z : its gate, like x, or None
+    res   : [B, T, D] residual stream (its own dtype, e.g. float32), or None (zero);  alpha : [D] float32, or None (1)
+    gamma_post, beta_post : [D] float32, the norm behind the block, or None (none)
+    gamma_pre, beta_pre   : [D] float32, the norm before the next block; without gamma_pre there is no y
+    kind  : "rms" (mean square) or "layer" (mean and variance);  gate_first : NORM(x silu(z)) instead of NORM(x) silu(z)
+    lens  : [B] int32, the tokens of each sequence, or None (T each).  Rows behind them are not read and give zeros
+    keep  : whether s is wanted;  ``s`` may be ``res`` itself
+    returns (s [B, T, D] of res's dtype (without res: res_dtype, default x's) or None, y [B, T, D] of x's dtype or None).
+    """
+    _check_same_dev(x, res, z, alpha, gamma_post, beta_post, gamma_pre, beta_pre, lens, s, y)
+
+    def call():
+        nonlocal s, y
+        rt = s.dtype if s is not None else res.dtype if res is not None else (res_dtype or x.dtype)
+        if res_dtype is not None and res_dtype != rt:
+            raise ValueError(f"res_dtype {res_dtype}, but res or s is {rt}")
+        if s is None and keep:
+            s = _like(x if res is None else res, rt)
+        if y is None and gamma_pre is not None:
+            y = _like(x, x.dtype)
+        if s is None and y is None:
+            raise ValueError("nothing is wanted: neither s (keep) nor y (gamma_pre)")
+        desc, _ = _norm_call(x, z, res, alpha, gamma_post, beta_post, gamma_pre, beta_pre, kind, eps, gate_first, lens, s, y,
+                             rt)
+        st = lib().ttt_block_norm_fwd(ctypes.byref(desc), x.data_ptr(), _ptr(z), _ptr(res), _ptr(alpha), _ptr(gamma_post),
+                                      _ptr(beta_post), _ptr(gamma_pre), _ptr(beta_pre), _ptr(lens), _ptr(s), _ptr(y),
+                                      _stream_handle(stream, x.device.index))
+        _done(st, "ttt_block_norm_fwd")
+        return s, y
+
+    return _call_on(x, stream, call)
+
+
+def block_norm_bwd(x, ds, dy, res=None, z=None, alpha=None, gamma_post=None, beta_post=None, gamma_pre=None, beta_pre=None,
+                   kind: str = "rms", eps: float = 1e-6, gate_first: bool = False, lens=None, workspace=None, stream=None):
+    """Backward of :func:`block_norm_fwd`, from its inputs alone (arguments as there).
+
+    ds : [B, T, D] of res's dtype, the gradient with respect to s, dy : [B, T, D] of x's, that with respect to y; one may
+    be None (zero).  workspace : uint8 tensor of block_norm_workspace_bytes(...), or None (allocated)
+    returns (dx, dz, dres, dalpha, dgamma_post, dbeta_post, dgamma_pre, dbeta_pre), None for what was not given; those of
+    parameters are [D] float32, summed over sequences and tokens.
+    """
+    torch = _torch()
+    _check_same_dev(x, ds, dy, res, z, alpha, gamma_post, beta_post, gamma_pre, beta_pre, lens, workspace)
+
+    def call():
+        rt = res.dtype if res is not None else ds.dtype if ds is not None else x.dtype
+        dx, dz = _like(x, x.dtype), None if z is None else _like(z, x.dtype)
+        dres = None if res is None else _like(res, rt)
+        desc, need = _norm_call(x, z, res, alpha, gamma_post, beta_post, gamma_pre, beta_pre, kind, eps, gate_first, lens, ds,
+                                dy, rt, (dx, dz, dres))
+        ps = [None if p is None else torch.empty_like(p) for p in (alpha, gamma_post, beta_post, gamma_pre, beta_pre)]
+        ws, need = _attn_workspace(need, workspace, x.device)
+        st = lib().ttt_block_norm_bwd(ctypes.byref(desc), x.data_ptr(), _ptr(z), _ptr(res), _ptr(alpha), _ptr(gamma_post),
+                                      _ptr(beta_post), _ptr(gamma_pre), _ptr(lens), _ptr(ds), _ptr(dy), dx.data_ptr(),
+                                      _ptr(dz), _ptr(dres), *map(_ptr, ps), _ptr(ws), need,
+                                      _stream_handle(stream, x.device.index))
+        _done(st, "ttt_block_norm_bwd")
+        return dx, dz, dres, *ps
+
+    return _call_on(x, stream, call)
+
+
+def block_norm_workspace_bytes(x) -> int:
+    """Bytes of workspace that :func:`block_norm_bwd` takes on an input like x [B, T, D]."""
+    _check_sizes(x.shape)
+    B, T, D = x.shape
+    code = _dtype_code(x.dtype)
+    return int(lib().ttt_block_norm_workspace_bytes(ctypes.byref(BlockNormDesc(B, T, D, code, code))))

@@ -1824,3 +1824,672 @@ ttt_status ttt_rotary(const ttt_rotary_desc* desc, const ttt_rope* rope, const v
 }
 
 }  // extern "C"
+
+// ------------------------- short convolution, selective scan, block norm --
+
+namespace {
+
+// Strides, alignment to whole elements and overlap of a call's tensors (a null one is not there).  own: an output that may
+// be exactly that input.
+ttt_status check_tensors(std::initializer_list<View> ins, std::initializer_list<View> outs,
+                         std::initializer_list<Range> flat_ins, std::initializer_list<Range> flat_outs,
+                         const View* own_out = nullptr, const View* own_in = nullptr) {
+  for (const View& v : ins) {
+    if (!v.p) continue;
+    if (!strides_ok(v, false)) return TTT_ERR_STRIDE;
+    if (!view_aligned(v, v.size)) return TTT_ERR_ALIGN;
+  }
+  for (const View& v : outs) {
+    if (!v.p) continue;
+    if (!strides_ok(v, true)) return TTT_ERR_STRIDE;
+    if (!view_aligned(v, v.size)) return TTT_ERR_ALIGN;
+  }
+  for (const View* o = outs.begin(); o != outs.end(); ++o) {
+    if (!o->p) continue;
+    for (const View& in : ins) {
+      if (!in.p) continue;
+      if (own_out && own_in && same_view(*o, *own_out) && same_view(in, *own_in) && same_view(*o, in)) continue;
+      if (views_overlap(*o, in)) return TTT_ERR_ALIAS;
+    }
+    for (const View* p = outs.begin(); p != o; ++p)
+      if (p->p && views_overlap(*o, *p)) return TTT_ERR_ALIAS;
+    for (const Range& in : flat_ins)
+      if (overlaps(range(*o), in)) return TTT_ERR_ALIAS;
+    for (const Range& f : flat_outs)
+      if (overlaps(range(*o), f)) return TTT_ERR_ALIAS;
+  }
+  for (const Range* f = flat_outs.begin(); f != flat_outs.end(); ++f) {
+    for (const View& in : ins)
+      if (in.p && overlaps(*f, range(in))) return TTT_ERR_ALIAS;
+    for (const Range& in : flat_ins)
+      if (overlaps(*f, in)) return TTT_ERR_ALIAS;
+    for (const Range* g = flat_outs.begin(); g != f; ++g)
+      if (overlaps(*f, *g)) return TTT_ERR_ALIAS;
+  }
+  return TTT_OK;
+}
+
+bool all_aligned(std::initializer_list<const void*> ps, uintptr_t n) {
+  for (const void* p : ps)
+    if (!aligned(p, n)) return false;
+  return true;
+}
+
+bool all_wide(std::initializer_list<View> vs) {
+  for (const View& v : vs)
+    if (v.p && !view_aligned(v, 16)) return false;
+  return true;
+}
+
+ttt::Strides2 strides2(const View& v) { return ttt::Strides2{v.s.b, v.s.t}; }
+
+View rows_view(const void* p, int64_t B, int64_t T, int64_t D, ttt_strides s, int32_t dtype) {
+  s.h = 0;
+  return view(p, B, 1, T, D, s, dtype);
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+Range floats(const float* p, int64_t n) { return Range{p, p ? n * 4 : 0}; }
+
+// ---- short convolution
+
+ttt_status check_conv_desc(const ttt_short_conv_desc* d) {
+  if (!d) return TTT_ERR_NULL;
+  if (d->B < 0 || d->T < 0 || d->D < 1 || d->K < 1 || d->T > kMaxTokens) return TTT_ERR_SHAPE;
+  if (!dtype_ok(d->in_dtype) || !dtype_ok(d->out_dtype)) return TTT_ERR_DTYPE;
+  if ((d->flags & ~TTT_FLAG_SILU) || d->reserved != 0) return TTT_ERR_FLAGS;
+  int64_t n = 1;
+  if (!mul_ok(n, d->B) || !mul_ok(n, d->T > 0 ? d->T : 1) || !mul_ok(n, d->D)) return TTT_ERR_SHAPE;
+  if (d->K < 2 || d->K > 4) return TTT_ERR_UNSUPPORTED;
+  return TTT_OK;
+}
+
+struct ConvPlan {
+  int seg, nparts;  // tokens a thread walks, rows of partial sums a sequence
+  int64_t bytes;
+};
+
+// The backward's segments: 8 of them to a workgroup, 16 to 128 tokens each, as long as there are 2^17 walks.
+ConvPlan conv_plan(const ttt_short_conv_desc* d) {
+  ConvPlan p;
+  const int64_t pieces = ceil_div(d->D, d->in_dtype == TTT_BF16 ? 8 : 4);
+  int64_t seg = static_cast<int64_t>(d->T) * d->B * pieces >> 17;
+  p.seg = static_cast<int>(seg < 16 ? 16 : seg > 128 ? 128 : seg);
+  p.nparts = static_cast<int>(d->T > 0 ? ceil_div(ceil_div(d->T, p.seg), 8) : 1);
+  p.bytes = static_cast<int64_t>(d->B) * p.nparts * d->D * (d->K + 1) * 4;
+  return p;
+}
+
+struct ConvViews {
+  View x, y, dx;
+  Range w, bias, lens;
+  int64_t state_in, state_out;  // bytes
+};
+
+ConvViews conv_views(const ttt_short_conv_desc* d, const void* X, const float* w, const float* bias, const int32_t* lens,
+                     const void* Y, const void* dX) {
+  ConvViews v;
+  v.x = rows_view(X, d->B, d->T, d->D, d->x, d->in_dtype);
+  v.y = rows_view(Y, d->B, d->T, d->D, d->y, d->out_dtype);
+  v.dx = rows_view(dX, d->B, d->T, d->D, d->dx, d->out_dtype);
+  v.w = floats(w, static_cast<int64_t>(d->D) * d->K);
+  v.bias = floats(bias, d->D);
+  v.lens = Range{lens, lens ? static_cast<int64_t>(d->B) * 4 : 0};
+  const int64_t n = static_cast<int64_t>(d->B) * (d->K - 1) * d->D;
+  v.state_in = n * dtype_size(d->in_dtype);
+  v.state_out = n * dtype_size(d->out_dtype);
+  return v;
+}
+
+ttt_status validate_conv_fwd(const ttt_short_conv_desc* d, const void* X, const float* w, const float* bias,
+                             const void* state, const int32_t* lens, const void* Y, const void* state_final, bool decode) {
+  ttt_status st = check_conv_desc(d);
+  if (st != TTT_OK) return st;
+  const int64_t pieces = ceil_div(d->D, d->in_dtype == TTT_BF16 ? 8 : 4);
+  if (static_cast<int64_t>(d->B) * (decode ? 1 : ceil_div(d->T, 8) + 1) * pieces > kMaxThreads) return TTT_ERR_SHAPE;
+  if (d->B == 0) return TTT_OK;
+  if (!w || (decode && !state_final)) return TTT_ERR_NULL;
+  if (d->T > 0 && (!X || !Y)) return TTT_ERR_NULL;
+  const ConvViews v = conv_views(d, X, w, bias, lens, Y, nullptr);
+  if (!all_aligned({w, bias, lens}, 4) || !all_aligned({state, state_final}, dtype_size(d->in_dtype))) return TTT_ERR_ALIGN;
+  const Range s{state, state ? v.state_in : 0}, f{state_final, state_final ? v.state_in : 0};
+  return check_tensors({v.x}, {v.y}, {v.w, v.bias, v.lens, s}, {f});
+}
+
+ttt_status validate_conv_bwd(const ttt_short_conv_desc* d, const void* X, const float* w, const float* bias,
+                             const void* state, const int32_t* lens, const void* dY, const void* dstate_final,
+                             const void* dX, const float* dw, const float* dbias, const void* dstate, const void* ws,
+                             int64_t ws_bytes) {
+  ttt_status st = check_conv_desc(d);
+  if (st != TTT_OK) return st;
+  const ConvPlan plan = conv_plan(d);
+  const int64_t pieces = ceil_div(d->D, d->in_dtype == TTT_BF16 ? 8 : 4);
+  if (static_cast<int64_t>(d->B) * plan.nparts * ceil_div(pieces, 32) * 256 > kMaxThreads) return TTT_ERR_SHAPE;
+  if (static_cast<int64_t>(d->D) * (d->K + 1) > kMaxThreads / 16) return TTT_ERR_SHAPE;  // the sums
+  if (!w || !dw) return TTT_ERR_NULL;
+  if (static_cast<int64_t>(d->B) * d->T > 0 && (!X || !dY || !dX)) return TTT_ERR_NULL;
+  const ConvViews v = conv_views(d, X, w, bias, lens, dY, dX);
+  if (!all_aligned({w, bias, lens, dw, dbias}, 4) || !aligned(state, dtype_size(d->in_dtype)) ||
+      !all_aligned({dstate, dstate_final}, dtype_size(d->out_dtype)))
+    return TTT_ERR_ALIGN;
+  if ((st = check_workspace(ws, ws_bytes, plan.bytes)) != TTT_OK) return st;
+  const Range s{state, state ? v.state_in : 0}, df{dstate_final, dstate_final ? v.state_out : 0};
+  return check_tensors({v.x, v.y}, {v.dx}, {v.w, v.bias, v.lens, s, df},
+                       {floats(dw, static_cast<int64_t>(d->D) * d->K), floats(dbias, d->D),
+                        Range{dstate, dstate ? v.state_out : 0}, Range{ws, plan.bytes}});
+}
+
+ttt::ConvArgs make_conv_args(const ttt_short_conv_desc* d, const ConvViews& v, const void* X, const float* w,
+                             const float* bias, const void* state, const int32_t* lens) {
+  ttt::ConvArgs a = {};
+  a.B = d->B; a.T = d->T; a.D = d->D; a.K = d->K;
+  a.in_dtype = d->in_dtype; a.out_dtype = d->out_dtype;
+  a.silu = (d->flags & TTT_FLAG_SILU) != 0;
+  a.X = X; a.w = w; a.bias = bias; a.state = state; a.lens = lens;
+  a.xs = strides2(v.x); a.ys = strides2(v.y); a.dxs = strides2(v.dx);
+  return a;
+}
+
+// ---- selective scan
+
+ttt_status check_scan_desc(const ttt_selective_scan_desc* d) {
+  if (!d) return TTT_ERR_NULL;
+  if (d->B < 0 || d->T < 0 || d->D < 1 || d->N < 1 || d->G < 1 || d->D % d->G != 0 || d->T > kMaxTokens)
+    return TTT_ERR_SHAPE;
+  if (!dtype_ok(d->in_dtype) || !dtype_ok(d->out_dtype)) return TTT_ERR_DTYPE;
+  if (d->flags & ~TTT_FLAG_SOFTPLUS) return TTT_ERR_FLAGS;
+  if (ttt::scan_states(d->N) == 0) return TTT_ERR_UNSUPPORTED;
+  int64_t n = 1;
+  if (!mul_ok(n, d->B) || !mul_ok(n, d->T > 0 ? d->T : 1) || !mul_ok(n, d->D) || !mul_ok(n, d->N)) return TTT_ERR_SHAPE;
+  return TTT_OK;
+}
+
+struct ScanPlan {
+  int nseg, seglen, chunks;
+  int64_t tiles, blocks;  // of channels in a group; workgroups of one segment
+  int64_t hseg, sseg, gseg, ckpt, bcpart, part, bytes;
+};
+
+ScanPlan scan_plan(const ttt_selective_scan_desc* d, bool backward) {
+  ScanPlan p;
+  p.tiles = ceil_div(d->D / d->G, ttt::kScanCh);
+  p.blocks = static_cast<int64_t>(d->B) * d->G * p.tiles;
+  int64_t n = 1;
+  if (p.blocks > 0 && p.blocks < 160) n = ceil_div(512, p.blocks);
+  if (n > ceil_div(d->T, 64)) n = ceil_div(d->T, 64);
+  if (n > 64) n = 64;
+  if (n < 1) n = 1;
+  p.seglen = static_cast<int>(ceil_div(ceil_div(d->T, n), ttt::kScanTile) * ttt::kScanTile);
+  if (p.seglen < ttt::kScanTile) p.seglen = ttt::kScanTile;
+  p.nseg = static_cast<int>(d->T > 0 ? ceil_div(d->T, p.seglen) : 1);
+  p.chunks = static_cast<int>(ceil_div(d->T, ttt::scan_chunk(d->N)));
+  int64_t at = 0;
+  auto take = [&](bool wanted, int64_t elements) {
+    const int64_t o = at;
+    if (wanted) at += ceil_div(elements * 4, 256) * 256;
+    return o;
+  };
+  const int64_t bd = static_cast<int64_t>(d->B) * d->D, bdn = bd * d->N;
+  p.hseg = take(p.nseg > 1, bdn * p.nseg);
+  p.sseg = take(p.nseg > 1, bd * p.nseg);
+  p.gseg = take(backward && p.nseg > 1, bdn * p.nseg);
+  p.ckpt = take(backward, bdn * p.chunks);
+  p.bcpart = take(backward, p.blocks * d->T * 2 * d->N);
+  p.part = take(backward, static_cast<int64_t>(d->B) * p.nseg * d->D * (d->N + 2));
+  p.bytes = at;
+  return p;
+}
+
+struct ScanViews {
+  View u, dt, z, y, Bm, Cm;
+  Range A, D, bias, lens, h0;
+  int64_t state;  // bytes
+};
+
+ScanViews scan_views(const ttt_selective_scan_desc* d, const void* u, const void* dt, const float* A, const void* Bm,
+                     const void* Cm, const float* D, const void* z, const float* bias, const float* h0,
+                     const int32_t* lens, const void* y) {
+  ScanViews v;
+  v.u = rows_view(u, d->B, d->T, d->D, d->u, d->in_dtype);
+  v.dt = rows_view(dt, d->B, d->T, d->D, d->dt, d->in_dtype);
+  v.z = rows_view(z, d->B, d->T, d->D, d->z, d->in_dtype);
+  v.y = rows_view(y, d->B, d->T, d->D, d->y, d->out_dtype);
+  v.Bm = view(Bm, d->B, d->G, d->T, d->N, d->Bm, d->in_dtype);
+  v.Cm = view(Cm, d->B, d->G, d->T, d->N, d->Cm, d->in_dtype);
+  v.A = floats(A, static_cast<int64_t>(d->D) * d->N);
+  v.D = floats(D, d->D);
+  v.bias = floats(bias, d->D);
+  v.lens = Range{lens, lens ? static_cast<int64_t>(d->B) * 4 : 0};
+  v.state = static_cast<int64_t>(d->B) * d->D * d->N * 4;
+  v.h0 = Range{h0, h0 ? v.state : 0};
+  return v;
+}
+
+ttt_status validate_scan_fwd(const ttt_selective_scan_desc* d, const void* u, const void* dt, const float* A,
+                             const void* Bm, const void* Cm, const float* D, const void* z, const float* bias,
+                             const float* h0, const int32_t* lens, const void* y, const float* h, const void* ws,
+                             int64_t ws_bytes, bool decode) {
+  ttt_status st = check_scan_desc(d);
+  if (st != TTT_OK) return st;
+  ScanPlan plan = scan_plan(d, false);
+  if (decode) plan.bytes = 0;
+  if (decode ? static_cast<int64_t>(d->B) * d->D * 4 > kMaxThreads : plan.blocks * plan.nseg * 256 > kMaxThreads)
+    return TTT_ERR_SHAPE;
+  if (d->B == 0) return TTT_OK;
+  if (!A || !h) return TTT_ERR_NULL;
+  if (d->T > 0 && (!u || !dt || !Bm || !Cm || !y)) return TTT_ERR_NULL;
+  const ScanViews v = scan_views(d, u, dt, A, Bm, Cm, D, z, bias, h0, lens, y);
+  if (!all_aligned({A, D, bias, h0, h, lens}, 4)) return TTT_ERR_ALIGN;
+  if ((st = check_workspace(ws, ws_bytes, plan.bytes)) != TTT_OK) return st;
+  const Range hf{h, v.state}, wsr{ws, plan.bytes};
+  const Range other = h == h0 ? Range{nullptr, 0} : v.h0;  // (the state carried in place)
+  if ((st = check_tensors({v.u, v.dt, v.z, v.Bm, v.Cm}, {v.y}, {v.A, v.D, v.bias, v.lens, other}, {hf, wsr})) != TTT_OK)
+    return st;
+  return TTT_OK;
+}
+
+ttt_status validate_scan_bwd(const ttt_selective_scan_desc* d, const void* u, const void* dt, const float* A,
+                             const void* Bm, const void* Cm, const float* D, const void* z, const float* bias,
+                             const float* h0, const int32_t* lens, const void* dy, const float* dhf, const void* du,
+                             const void* ddt, const float* dA, const void* dB, const void* dC, const float* dD,
+                             const void* dz, const float* dbias, const float* dh0, const void* ws, int64_t ws_bytes) {
+  ttt_status st = check_scan_desc(d);
+  if (st != TTT_OK) return st;
+  const ScanPlan plan = scan_plan(d, true);
+  if (plan.blocks * plan.nseg * 256 > kMaxThreads) return TTT_ERR_SHAPE;
+  if (static_cast<int64_t>(d->B) * d->G * d->T * 2 * d->N > kMaxThreads) return TTT_ERR_SHAPE;  // the sums
+  if (static_cast<int64_t>(d->D) * (d->N + 2) > kMaxThreads / 16) return TTT_ERR_SHAPE;
+  if (!A || !dA) return TTT_ERR_NULL;
+  if (static_cast<int64_t>(d->B) * d->T > 0) {
+    if (!u || !dt || !Bm || !Cm || !dy || !du || !ddt || !dB || !dC) return TTT_ERR_NULL;
+    if ((z != nullptr) != (dz != nullptr)) return TTT_ERR_NULL;
+  }
+  const ScanViews v = scan_views(d, u, dt, A, Bm, Cm, D, z, bias, h0, lens, dy);
+  if (!all_aligned({A, D, bias, h0, lens, dhf, dA, dD, dbias, dh0}, 4)) return TTT_ERR_ALIGN;
+  if ((st = check_workspace(ws, ws_bytes, plan.bytes)) != TTT_OK) return st;
+  const View vdu = rows_view(du, d->B, d->T, d->D, d->du, d->out_dtype);
+  const View vddt = rows_view(ddt, d->B, d->T, d->D, d->ddt, d->out_dtype);
+  const View vdz = rows_view(dz, d->B, d->T, d->D, d->dz, d->out_dtype);
+  const View vdB = view(dB, d->B, d->G, d->T, d->N, d->dBm, d->out_dtype);
+  const View vdC = view(dC, d->B, d->G, d->T, d->N, d->dCm, d->out_dtype);
+  return check_tensors({v.u, v.dt, v.z, v.Bm, v.Cm, v.y}, {vdu, vddt, vdz, vdB, vdC},
+                       {v.A, v.D, v.bias, v.lens, v.h0, Range{dhf, dhf ? v.state : 0}},
+                       {floats(dA, static_cast<int64_t>(d->D) * d->N), floats(dD, d->D), floats(dbias, d->D),
+                        Range{dh0, dh0 ? v.state : 0}, Range{ws, plan.bytes}});
+}
+
+ttt::ScanArgs make_scan_args(const ttt_selective_scan_desc* d, const ScanViews& v, const void* u, const void* dt,
+                             const float* A, const void* Bm, const void* Cm, const float* D, const void* z,
+                             const float* bias, const float* h0, const int32_t* lens) {
+  ttt::ScanArgs a = {};
+  a.B = d->B; a.T = d->T; a.D = d->D; a.N = d->N; a.G = d->G;
+  a.in_dtype = d->in_dtype; a.out_dtype = d->out_dtype;
+  a.softplus = (d->flags & TTT_FLAG_SOFTPLUS) != 0;
+  a.u = u; a.dt = dt; a.z = z; a.Bm = Bm; a.Cm = Cm;
+  a.A = A; a.Dskip = D; a.dt_bias = bias; a.h0 = h0; a.lens = lens;
+  a.us = strides2(v.u); a.dts = strides2(v.dt); a.zs = strides2(v.z); a.ys = strides2(v.y);
+  a.bs = strides(v.Bm); a.cs = strides(v.Cm);
+  return a;
+}
+
+// ---- block norm
+
+ttt_status check_norm_desc(const ttt_block_norm_desc* d) {
+  if (!d) return TTT_ERR_NULL;
+  if (d->B < 0 || d->T < 0 || d->D < 1 || d->T > kMaxTokens) return TTT_ERR_SHAPE;
+  if (!finite(d->eps) || d->eps < 0.f) return TTT_ERR_SHAPE;
+  if (!dtype_ok(d->in_dtype) || !dtype_ok(d->res_dtype)) return TTT_ERR_DTYPE;
+  if ((d->flags & ~(TTT_FLAG_RMS | TTT_FLAG_GATE_FIRST)) || d->reserved != 0) return TTT_ERR_FLAGS;
+  if (d->D > ttt::norm_max_d()) return TTT_ERR_UNSUPPORTED;
+  int64_t n = 1;
+  if (!mul_ok(n, d->B) || !mul_ok(n, d->T) || !mul_ok(n, d->D)) return TTT_ERR_SHAPE;
+  return TTT_OK;
+}
+
+// Workgroups of the backward, each with a row of partial sums: as many as stay on the card, with a few rows each.
+int norm_blocks(const ttt_block_norm_desc* d) {
+  const int64_t rows = static_cast<int64_t>(d->B) * d->T, most = d->D <= 4096 ? 512 : 256;
+  const int64_t n = ceil_div(rows, ttt::norm_teams(d->D));
+  return static_cast<int>(n < 1 ? 1 : n < most ? n : most);
+}
+
+int64_t norm_bytes(const ttt_block_norm_desc* d) { return static_cast<int64_t>(norm_blocks(d)) * 5 * d->D * 4; }
+
+struct NormViews {
+  View x, z, res, s, y;
+  Range alpha, gp, bp, gn, bn, lens;
+};
+
+NormViews norm_views(const ttt_block_norm_desc* d, const void* X, const void* Z, const void* res, const float* alpha,
+                     const float* gp, const float* bp, const float* gn, const float* bn, const int32_t* lens,
+                     const void* S, const void* Y) {
+  NormViews v;
+  v.x = rows_view(X, d->B, d->T, d->D, d->x, d->in_dtype);
+  v.z = rows_view(Z, d->B, d->T, d->D, d->z, d->in_dtype);
+  v.res = rows_view(res, d->B, d->T, d->D, d->res, d->res_dtype);
+  v.s = rows_view(S, d->B, d->T, d->D, d->s, d->res_dtype);
+  v.y = rows_view(Y, d->B, d->T, d->D, d->y, d->in_dtype);
+  v.alpha = floats(alpha, d->D);
+  v.gp = floats(gp, d->D);
+  v.bp = floats(bp, d->D);
+  v.gn = floats(gn, d->D);
+  v.bn = floats(bn, d->D);
+  v.lens = Range{lens, lens ? static_cast<int64_t>(d->B) * 4 : 0};
+  return v;
+}
+
+ttt_status validate_norm_fwd(const ttt_block_norm_desc* d, const void* X, const void* Z, const void* res,
+                             const float* alpha, const float* gp, const float* bp, const float* gn, const float* bn,
+                             const int32_t* lens, const void* S, const void* Y) {
+  const ttt_status st = check_norm_desc(d);
+  if (st != TTT_OK) return st;
+  if (static_cast<int64_t>(d->B) * d->T == 0) return TTT_OK;
+  if (!X || (!S && !Y) || (bp && !gp) || (Y && !gn) || (bn && !gn)) return TTT_ERR_NULL;
+  if (!all_aligned({alpha, gp, bp, gn, bn, lens}, 4)) return TTT_ERR_ALIGN;
+  const NormViews v = norm_views(d, X, Z, res, alpha, gp, bp, gn, bn, lens, S, Y);
+  return check_tensors({v.x, v.z, v.res}, {v.s, v.y}, {v.alpha, v.gp, v.bp, v.gn, v.bn, v.lens}, {}, &v.s, &v.res);
+}
+
+ttt_status validate_norm_bwd(const ttt_block_norm_desc* d, const void* X, const void* Z, const void* res,
+                             const float* alpha, const float* gp, const float* bp, const float* gn, const int32_t* lens,
+                             const void* dS, const void* dY, const void* dX, const void* dZ, const void* dres,
+                             const float* dalpha, const float* dgp, const float* dbp, const float* dgn, const float* dbn,
+                             const void* ws, int64_t ws_bytes) {
+  ttt_status st = check_norm_desc(d);
+  if (st != TTT_OK) return st;
+  if (static_cast<int64_t>(d->B) * d->T > 0) {
+    if (!X || !dX || (!dS && !dY) || (Z != nullptr) != (dZ != nullptr)) return TTT_ERR_NULL;
+  }
+  if ((bp && !gp) || (dY && !gn)) return TTT_ERR_NULL;
+  if (!all_aligned({alpha, gp, bp, gn, lens, dalpha, dgp, dbp, dgn, dbn}, 4)) return TTT_ERR_ALIGN;
+  const int64_t need = norm_bytes(d);
+  if ((st = check_workspace(ws, ws_bytes, need)) != TTT_OK) return st;
+  const NormViews v = norm_views(d, X, Z, res, alpha, gp, bp, gn, nullptr, lens, dS, dY);
+  const View dx = rows_view(dX, d->B, d->T, d->D, d->dx, d->in_dtype);
+  const View dz = rows_view(dZ, d->B, d->T, d->D, d->dz, d->in_dtype);
+  const View dr = rows_view(dres, d->B, d->T, d->D, d->dres, d->res_dtype);
+  return check_tensors({v.x, v.z, v.res, v.s, v.y}, {dx, dz, dr}, {v.alpha, v.gp, v.bp, v.gn, v.lens},
+                       {floats(dalpha, d->D), floats(dgp, d->D), floats(dbp, d->D), floats(dgn, d->D), floats(dbn, d->D),
+                        Range{ws, need}});
+}
+
+ttt::NormArgs make_norm_args(const ttt_block_norm_desc* d, const NormViews& v, const void* X, const void* Z,
+                             const void* res, const float* alpha, const float* gp, const float* bp, const float* gn,
+                             const float* bn, const int32_t* lens) {
+  ttt::NormArgs a = {};
+  a.B = d->B; a.T = d->T; a.D = d->D;
+  a.in_dtype = d->in_dtype; a.res_dtype = d->res_dtype;
+  a.layer = !(d->flags & TTT_FLAG_RMS);
+  a.gate_first = Z && (d->flags & TTT_FLAG_GATE_FIRST);
+  a.eps = d->eps;
+  a.X = X; a.Z = Z; a.res = res;
+  a.alpha = alpha; a.gamma_post = gp; a.beta_post = bp; a.gamma_pre = gn; a.beta_pre = bn;
+  a.lens = lens;
+  a.xs = strides2(v.x); a.zs = strides2(v.z); a.rs = strides2(v.res); a.ss = strides2(v.s); a.ys = strides2(v.y);
+  a.wide = d->D % 8 == 0 && all_wide({v.x, v.z, v.res, v.s, v.y}) && all_aligned({alpha, gp, bp, gn, bn}, 16);
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t ttt_short_conv_workspace_bytes(const ttt_short_conv_desc* desc) {
+  if (check_conv_desc(desc) != TTT_OK) return -1;
+  return conv_plan(desc).bytes;
+}
+
+ttt_status ttt_short_conv_fwd_validate(const ttt_short_conv_desc* desc, const void* X, const float* w, const float* bias,
+                                       const void* state, const int32_t* lens, const void* Y, const void* state_final) {
+  return validate_conv_fwd(desc, X, w, bias, state, lens, Y, state_final, false);
+}
+
+ttt_status ttt_short_conv_fwd(const ttt_short_conv_desc* desc, const void* X, const float* w, const float* bias,
+                              const void* state, const int32_t* lens, void* Y, void* state_final, void* stream) {
+  const ttt_status st = validate_conv_fwd(desc, X, w, bias, state, lens, Y, state_final, false);
+  if (st != TTT_OK) return st;
+  if (desc->B == 0 || (desc->T == 0 && !state_final)) return TTT_OK;
+  const ConvViews v = conv_views(desc, X, w, bias, lens, Y, nullptr);
+  ttt::ConvArgs a = make_conv_args(desc, v, X, w, bias, state, lens);
+  a.wide = desc->D % (desc->in_dtype == TTT_BF16 ? 8 : 4) == 0 && all_wide({v.x, v.y}) &&
+           all_aligned({w, bias, state, state_final}, 16);
+  a.Y = Y; a.state_out = state_final;
+  return hip_status(ttt::launch_conv_fwd(a, static_cast<hipStream_t>(stream)));
+}
+
+ttt_status ttt_short_conv_decode_validate(const ttt_short_conv_desc* desc, const void* X, const float* w,
+                                          const float* bias, const int32_t* lens, const void* Y, const void* state) {
+  return validate_conv_fwd(desc, X, w, bias, nullptr, lens, Y, state, true);
+}
+
+ttt_status ttt_short_conv_decode(const ttt_short_conv_desc* desc, const void* X, const float* w, const float* bias,
+                                 const int32_t* lens, void* Y, void* state, void* stream) {
+  const ttt_status st = validate_conv_fwd(desc, X, w, bias, nullptr, lens, Y, state, true);
+  if (st != TTT_OK) return st;
+  if (desc->B == 0 || desc->T == 0) return TTT_OK;
+  const ConvViews v = conv_views(desc, X, w, bias, lens, Y, nullptr);
+  ttt::ConvArgs a = make_conv_args(desc, v, X, w, bias, nullptr, lens);
+  a.wide = desc->D % (desc->in_dtype == TTT_BF16 ? 8 : 4) == 0 && all_wide({v.x, v.y}) && all_aligned({w, bias, state}, 16);
+  a.Y = Y; a.state_out = state;
+  return hip_status(ttt::launch_conv_decode(a, static_cast<hipStream_t>(stream)));
+}
+
+ttt_status ttt_short_conv_bwd_validate(const ttt_short_conv_desc* desc, const void* X, const float* w, const float* bias,
+                                       const void* state, const int32_t* lens, const void* dY, const void* dstate_final,
+                                       const void* dX, const float* dw, const float* dbias, const void* dstate,
+                                       const void* workspace, int64_t workspace_bytes) {
+  return validate_conv_bwd(desc, X, w, bias, state, lens, dY, dstate_final, dX, dw, dbias, dstate, workspace,
+                           workspace_bytes);
+}
+
+ttt_status ttt_short_conv_bwd(const ttt_short_conv_desc* desc, const void* X, const float* w, const float* bias,
+                              const void* state, const int32_t* lens, const void* dY, const void* dstate_final, void* dX,
+                              float* dw, float* dbias, void* dstate, void* workspace, int64_t workspace_bytes,
+                              void* stream) {
+  const ttt_status st = validate_conv_bwd(desc, X, w, bias, state, lens, dY, dstate_final, dX, dw, dbias, dstate, workspace,
+                                          workspace_bytes);
+  if (st != TTT_OK) return st;
+  const ConvPlan plan = conv_plan(desc);
+  const ConvViews v = conv_views(desc, X, w, bias, lens, dY, dX);
+  ttt::ConvArgs a = make_conv_args(desc, v, X, w, bias, state, lens);
+  a.wide = desc->D % (desc->in_dtype == TTT_BF16 ? 8 : 4) == 0 && all_wide({v.x, v.y, v.dx}) &&
+           all_aligned({w, bias, state, dstate, dstate_final}, 16);
+  a.dY = dY; a.dstate_out = dstate_final;
+  a.dX = dX; a.dstate = dstate;
+  a.seg = plan.seg; a.nparts = plan.nparts;
+  a.part = static_cast<float*>(workspace);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (desc->B > 0 && ttt::launch_conv_bwd(a, s) != hipSuccess) return TTT_ERR_HIP;
+  ttt::RowSumArgs r = {};
+  r.part = a.part;
+  r.ld = static_cast<int64_t>(desc->D) * (desc->K + 1);
+  r.rows = desc->B * plan.nparts;
+  r.n[0] = static_cast<int64_t>(desc->D) * desc->K; r.out[0] = dw;
+  r.n[1] = desc->D; r.out[1] = dbias;
+  return hip_status(ttt::launch_row_sum(r, s));
+}
+
+int64_t ttt_selective_scan_workspace_bytes(const ttt_selective_scan_desc* desc, int32_t backward) {
+  if (check_scan_desc(desc) != TTT_OK) return -1;
+  return scan_plan(desc, backward != 0).bytes;
+}
+
+ttt_status ttt_selective_scan_fwd_validate(const ttt_selective_scan_desc* desc, const void* u, const void* dt,
+                                           const float* A, const void* Bm, const void* Cm, const float* D, const void* z,
+                                           const float* dt_bias, const float* h0, const int32_t* lens, const void* y,
+                                           const float* h_final, const void* workspace, int64_t workspace_bytes) {
+  return validate_scan_fwd(desc, u, dt, A, Bm, Cm, D, z, dt_bias, h0, lens, y, h_final, workspace, workspace_bytes, false);
+}
+
+ttt_status ttt_selective_scan_fwd(const ttt_selective_scan_desc* desc, const void* u, const void* dt, const float* A,
+                                  const void* Bm, const void* Cm, const float* D, const void* z, const float* dt_bias,
+                                  const float* h0, const int32_t* lens, void* y, float* h_final, void* workspace,
+                                  int64_t workspace_bytes, void* stream) {
+  const ttt_status st = validate_scan_fwd(desc, u, dt, A, Bm, Cm, D, z, dt_bias, h0, lens, y, h_final, workspace,
+                                          workspace_bytes, false);
+  if (st != TTT_OK) return st;
+  if (desc->B == 0) return TTT_OK;
+  const ScanPlan plan = scan_plan(desc, false);
+  const ScanViews v = scan_views(desc, u, dt, A, Bm, Cm, D, z, dt_bias, h0, lens, y);
+  ttt::ScanArgs a = make_scan_args(desc, v, u, dt, A, Bm, Cm, D, z, dt_bias, h0, lens);
+  a.wide = desc->D / desc->G % 8 == 0 && all_wide({v.u, v.dt, v.z, v.y});
+  a.y = y; a.h_final = h_final;
+  a.nseg = plan.nseg; a.seglen = plan.seglen;
+  char* ws = static_cast<char*>(workspace);
+  a.hseg = reinterpret_cast<float*>(ws + plan.hseg);
+  a.sseg = reinterpret_cast<float*>(ws + plan.sseg);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (plan.nseg > 1 && ttt::launch_scan_states(a, s) != hipSuccess) return TTT_ERR_HIP;
+  return hip_status(ttt::launch_scan_fwd(a, s));
+}
+
+ttt_status ttt_selective_scan_decode_validate(const ttt_selective_scan_desc* desc, const void* u, const void* dt,
+                                              const float* A, const void* Bm, const void* Cm, const float* D,
+                                              const void* z, const float* dt_bias, const int32_t* lens, const void* y,
+                                              const float* h) {
+  return validate_scan_fwd(desc, u, dt, A, Bm, Cm, D, z, dt_bias, nullptr, lens, y, h, nullptr, 0, true);
+}
+
+ttt_status ttt_selective_scan_decode(const ttt_selective_scan_desc* desc, const void* u, const void* dt, const float* A,
+                                     const void* Bm, const void* Cm, const float* D, const void* z, const float* dt_bias,
+                                     const int32_t* lens, void* y, float* h, void* stream) {
+  const ttt_status st =
+      validate_scan_fwd(desc, u, dt, A, Bm, Cm, D, z, dt_bias, nullptr, lens, y, h, nullptr, 0, true);
+  if (st != TTT_OK) return st;
+  if (desc->B == 0 || desc->T == 0) return TTT_OK;
+  const ScanViews v = scan_views(desc, u, dt, A, Bm, Cm, D, z, dt_bias, nullptr, lens, y);
+  ttt::ScanArgs a = make_scan_args(desc, v, u, dt, A, Bm, Cm, D, z, dt_bias, nullptr, lens);
+  a.y = y; a.h_final = h;
+  return hip_status(ttt::launch_scan_decode(a, static_cast<hipStream_t>(stream)));
+}
+
+ttt_status ttt_selective_scan_bwd_validate(const ttt_selective_scan_desc* desc, const void* u, const void* dt,
+                                           const float* A, const void* Bm, const void* Cm, const float* D, const void* z,
+                                           const float* dt_bias, const float* h0, const int32_t* lens, const void* dy,
+                                           const float* dh_final, const void* du, const void* ddt, const float* dA,
+                                           const void* dBm, const void* dCm, const float* dD, const void* dz,
+                                           const float* ddt_bias, const float* dh0, const void* workspace,
+                                           int64_t workspace_bytes) {
+  return validate_scan_bwd(desc, u, dt, A, Bm, Cm, D, z, dt_bias, h0, lens, dy, dh_final, du, ddt, dA, dBm, dCm, dD, dz,
+                           ddt_bias, dh0, workspace, workspace_bytes);
+}
+
+ttt_status ttt_selective_scan_bwd(const ttt_selective_scan_desc* desc, const void* u, const void* dt, const float* A,
+                                  const void* Bm, const void* Cm, const float* D, const void* z, const float* dt_bias,
+                                  const float* h0, const int32_t* lens, const void* dy, const float* dh_final, void* du,
+                                  void* ddt, float* dA, void* dBm, void* dCm, float* dD, void* dz, float* ddt_bias,
+                                  float* dh0, void* workspace, int64_t workspace_bytes, void* stream) {
+  const ttt_status st = validate_scan_bwd(desc, u, dt, A, Bm, Cm, D, z, dt_bias, h0, lens, dy, dh_final, du, ddt, dA, dBm,
+                                          dCm, dD, dz, ddt_bias, dh0, workspace, workspace_bytes);
+  if (st != TTT_OK) return st;
+  const ScanPlan plan = scan_plan(desc, true);
+  const ScanViews v = scan_views(desc, u, dt, A, Bm, Cm, D, z, dt_bias, h0, lens, dy);
+  ttt::ScanArgs a = make_scan_args(desc, v, u, dt, A, Bm, Cm, D, z, dt_bias, h0, lens);
+  const View vdu = rows_view(du, desc->B, desc->T, desc->D, desc->du, desc->out_dtype);
+  const View vddt = rows_view(ddt, desc->B, desc->T, desc->D, desc->ddt, desc->out_dtype);
+  const View vdz = rows_view(dz, desc->B, desc->T, desc->D, desc->dz, desc->out_dtype);
+  a.wide = desc->D / desc->G % 8 == 0 && all_wide({v.u, v.dt, v.z, v.y, vdu, vddt, vdz});
+  a.dy = dy; a.dh_final = dh_final;
+  a.du = du; a.ddt = ddt; a.dz = dz; a.dh0 = dh0;
+  a.dus = strides2(vdu); a.ddts = strides2(vddt); a.dzs = strides2(vdz);
+  a.nseg = plan.nseg; a.seglen = plan.seglen; a.chunks = plan.chunks;
+  char* ws = static_cast<char*>(workspace);
+  auto at = [&](int64_t o) { return reinterpret_cast<float*>(ws + o); };
+  a.hseg = at(plan.hseg); a.sseg = at(plan.sseg); a.gseg = at(plan.gseg); a.ckpt = at(plan.ckpt);
+  a.bcpart = at(plan.bcpart); a.part = at(plan.part);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (desc->B > 0) {
+    if (plan.nseg > 1 && ttt::launch_scan_bwd_states(a, s) != hipSuccess) return TTT_ERR_HIP;
+    if (ttt::launch_scan_bwd(a, s) != hipSuccess) return TTT_ERR_HIP;
+    ttt::ScanBcSumArgs m = {};
+    m.B = desc->B; m.T = desc->T; m.N = desc->N; m.G = desc->G;
+    m.tiles = static_cast<int>(plan.tiles);
+    m.out_dtype = desc->out_dtype;
+    m.lens = lens;
+    m.part = a.bcpart;
+    m.dB = dBm; m.dC = dCm;
+    m.dbs = strides(view(dBm, desc->B, desc->G, desc->T, desc->N, desc->dBm, desc->out_dtype));
+    m.dcs = strides(view(dCm, desc->B, desc->G, desc->T, desc->N, desc->dCm, desc->out_dtype));
+    if (ttt::launch_scan_bc_sum(m, s) != hipSuccess) return TTT_ERR_HIP;
+  }
+  ttt::RowSumArgs r = {};
+  r.part = a.part;
+  r.ld = static_cast<int64_t>(desc->D) * (desc->N + 2);
+  r.rows = desc->B * plan.nseg;
+  r.n[0] = static_cast<int64_t>(desc->D) * desc->N; r.out[0] = dA;
+  r.n[1] = desc->D; r.out[1] = dD;
+  r.n[2] = desc->D; r.out[2] = ddt_bias;
+  return hip_status(ttt::launch_row_sum(r, s));
+}
+
+int64_t ttt_block_norm_workspace_bytes(const ttt_block_norm_desc* desc) {
+  if (check_norm_desc(desc) != TTT_OK) return -1;
+  return norm_bytes(desc);
+}
+
+ttt_status ttt_block_norm_fwd_validate(const ttt_block_norm_desc* desc, const void* X, const void* Z, const void* res,
+                                       const float* alpha, const float* gamma_post, const float* beta_post,
+                                       const float* gamma_pre, const float* beta_pre, const int32_t* lens, const void* S,
+                                       const void* Y) {
+  return validate_norm_fwd(desc, X, Z, res, alpha, gamma_post, beta_post, gamma_pre, beta_pre, lens, S, Y);
+}
+
+ttt_status ttt_block_norm_fwd(const ttt_block_norm_desc* desc, const void* X, const void* Z, const void* res,
+                              const float* alpha, const float* gamma_post, const float* beta_post, const float* gamma_pre,
+                              const float* beta_pre, const int32_t* lens, void* S, void* Y, void* stream) {
+  const ttt_status st =
+      validate_norm_fwd(desc, X, Z, res, alpha, gamma_post, beta_post, gamma_pre, beta_pre, lens, S, Y);
+  if (st != TTT_OK) return st;
+  if (static_cast<int64_t>(desc->B) * desc->T == 0) return TTT_OK;
+  const NormViews v = norm_views(desc, X, Z, res, alpha, gamma_post, beta_post, gamma_pre, beta_pre, lens, S, Y);
+  ttt::NormArgs a = make_norm_args(desc, v, X, Z, res, alpha, gamma_post, beta_post, gamma_pre, beta_pre, lens);
+  a.S = S; a.Y = Y;
+  return hip_status(ttt::launch_norm_fwd(a, static_cast<hipStream_t>(stream)));
+}
+
+ttt_status ttt_block_norm_bwd_validate(const ttt_block_norm_desc* desc, const void* X, const void* Z, const void* res,
+                                       const float* alpha, const float* gamma_post, const float* beta_post,
+                                       const float* gamma_pre, const int32_t* lens, const void* dS, const void* dY,
+                                       const void* dX, const void* dZ, const void* dres, const float* dalpha,
+                                       const float* dgamma_post, const float* dbeta_post, const float* dgamma_pre,
+                                       const float* dbeta_pre, const void* workspace, int64_t workspace_bytes) {
+  return validate_norm_bwd(desc, X, Z, res, alpha, gamma_post, beta_post, gamma_pre, lens, dS, dY, dX, dZ, dres, dalpha,
+                           dgamma_post, dbeta_post, dgamma_pre, dbeta_pre, workspace, workspace_bytes);
+}
+
+ttt_status ttt_block_norm_bwd(const ttt_block_norm_desc* desc, const void* X, const void* Z, const void* res,
+                              const float* alpha, const float* gamma_post, const float* beta_post, const float* gamma_pre,
+                              const int32_t* lens, const void* dS, const void* dY, void* dX, void* dZ, void* dres,
+                              float* dalpha, float* dgamma_post, float* dbeta_post, float* dgamma_pre, float* dbeta_pre,
+                              void* workspace, int64_t workspace_bytes, void* stream) {
+  const ttt_status st =
+      validate_norm_bwd(desc, X, Z, res, alpha, gamma_post, beta_post, gamma_pre, lens, dS, dY, dX, dZ, dres, dalpha,
+                        dgamma_post, dbeta_post, dgamma_pre, dbeta_pre, workspace, workspace_bytes);
+  if (st != TTT_OK) return st;
+  const NormViews v = norm_views(desc, X, Z, res, alpha, gamma_post, beta_post, gamma_pre, nullptr, lens, dS, dY);
+  ttt::NormArgs a = make_norm_args(desc, v, X, Z, res, alpha, gamma_post, beta_post, gamma_pre, nullptr, lens);
+  const View dx = rows_view(dX, desc->B, desc->T, desc->D, desc->dx, desc->in_dtype);
+  const View dz = rows_view(dZ, desc->B, desc->T, desc->D, desc->dz, desc->in_dtype);
+  const View dr = rows_view(dres, desc->B, desc->T, desc->D, desc->dres, desc->res_dtype);
+  a.wide = a.wide && all_wide({dx, dz, dr});
+  a.dS = dS; a.dY = dY;
+  a.dX = dX; a.dZ = dZ; a.dres = dres;
+  a.dxs = strides2(dx); a.dzs = strides2(dz); a.drs = strides2(dr);
+  a.blocks = norm_blocks(desc);
+  a.part = static_cast<float*>(workspace);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (ttt::launch_norm_bwd(a, s) != hipSuccess) return TTT_ERR_HIP;
+  ttt::RowSumArgs r = {};
+  r.part = a.part;
+  r.ld = static_cast<int64_t>(desc->D) * 5;
+  r.rows = a.blocks;
+  float* const out[5] = {dalpha, dgamma_post, dbeta_post, dgamma_pre, dbeta_pre};
+  for (int k = 0; k < 5; ++k) {
+    r.n[k] = desc->D;
+    r.out[k] = out[k];
+  }
+  return hip_status(ttt::launch_row_sum(r, s));
+}
+
+}  // extern "C"

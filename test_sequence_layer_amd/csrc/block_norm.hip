@@ -1,0 +1,424 @@
+// The join of two blocks: a norm behind a block, its gate, the residual scale and sum, and the norm before the next block.
+//
+// Pages: [TTT] = news article "大模型最强架构TTT问世！斯坦福UCSD等5年磨一剑，一夜推翻Transformer"
+// (aharts.cn / itmax.cn), part 03 §9 (layer norm and residual around the layer), part 04 (backbones).
+//
+//   n = NORM(x) gamma_post + beta_post,   v = n silu(z)      (or, gate first, n = NORM(x silu(z)) ..., v = n)
+//   s = res + alpha v,                    y = NORM(s) gamma_pre + beta_pre
+// NORM divides by the root of the mean square plus eps, the layer norm after taking the mean off.  Each row is read once,
+// kept in registers and written once: memory is the bound.
+#include "block_common.h"
+
+namespace ttt {
+namespace {
+
+using namespace block;
+
+__device__ __forceinline__ float wave_sum(float x) { return mfma::sum_rows(mfma::sum16(x)); }
+
+// Sums over the W waves of a row's team.  Each sum has a slot of its own, and two rows in a row two sets of them, so that
+// one barrier a sum is enough.
+template <int W>
+struct Team {
+  float (*slots)[W][2];  // [slot][wave][2] of this team
+  int wave, next;
+  __device__ __forceinline__ float2 sum2(float a, float b) {
+    a = wave_sum(a);
+    b = wave_sum(b);
+    if constexpr (W > 1) {
+      float (*s)[2] = slots[next];
+      next = next + 1 == kSlots ? 0 : next + 1;
+      if ((threadIdx.x & 63) == 0) {
+        s[wave][0] = a;
+        s[wave][1] = b;
+      }
+      __syncthreads();
+      a = s[0][0];
+      b = s[0][1];
+#pragma unroll
+      for (int i = 1; i < W; ++i) {
+        a += s[i][0];
+        b += s[i][1];
+      }
+    }
+    return make_float2(a, b);
+  }
+  static constexpr int kSlots = 8;
+};
+
+// mean (0 for the root-mean-square norm) and 1 / sqrt(var + eps) of a row of D elements, NE of them in a thread (zeros
+// behind the row's end).  The mean comes first, then the squares of what is left: no cancellation.
+template <int W, int NE>
+__device__ __forceinline__ float2 stats(const float (&x)[NE], int valid, int D, bool layer, float eps, Team<W>& team) {
+  float mean = 0.f;
+  if (layer) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) s += x[i];
+    mean = team.sum2(s, 0.f).x / static_cast<float>(D);
+  }
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const float d = i < valid ? x[i] - mean : 0.f;
+    s = fmaf(d, d, s);
+  }
+  const float var = team.sum2(s, 0.f).x / static_cast<float>(D) + eps;
+  return make_float2(mean, 1.f / sqrtf(var));
+}
+
+// A thread's elements of a row: NC pieces of 8, piece i at 8 (i R + r); element by element instead at i R + r.
+template <int R, int NC, bool Wide>
+struct Cols {
+  int r, D;
+  __device__ __forceinline__ int valid() const {  // of the thread's 8 NC elements, in their order
+    if constexpr (Wide) {
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) n += 8 * (i * R + r) < D ? 8 : 0;
+      return n;
+    } else {
+      return r < D ? min(8 * NC, (D - r + R - 1) / R) : 0;
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void load(float (&x)[8 * NC], const T* p) const {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      if constexpr (Wide) {
+        const int c = 8 * (i * R + r);
+        Piece<T, 8> v;
+        if (c < D) v.load(p + c);
+        else v.zero();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[8 * i + j] = v.get(j);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int c = (8 * i + j) * R + r;
+          x[8 * i + j] = c < D ? as_f32(p[c]) : 0.f;
+        }
+      }
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(const float (&x)[8 * NC], T* p) const {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      if constexpr (Wide) {
+        const int c = 8 * (i * R + r);
+        Piece<T, 8> v;
+        v.set_all(&x[8 * i]);
+        if (c < D) v.store(p + c);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int c = (8 * i + j) * R + r;
+          if (c < D) put(p + c, x[8 * i + j]);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void param(float (&x)[8 * NC], const float* p, float none) const {
+    if (p) {
+      load(x, p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8 * NC; ++i) x[i] = none;
+    }
+  }
+};
+
+__device__ __forceinline__ bool dead(const NormArgs& a, int64_t b, int64_t t) {
+  return a.lens && t >= max(0, min(a.lens[b], a.T));
+}
+
+template <typename T, typename RT, int R, int NC, bool Wide>
+__global__ __launch_bounds__(R) void ttt_norm_fwd(NormArgs a) {
+  constexpr int W = R / 64, NE = 8 * NC;
+  __shared__ float slots[Team<W>::kSlots][W][2];
+  Team<W> team{slots, static_cast<int>(threadIdx.x >> 6), 0};
+  const Cols<R, NC, Wide> cols{static_cast<int>(threadIdx.x), a.D};
+  const int valid = cols.valid();
+  const int64_t rows = static_cast<int64_t>(a.B) * a.T;
+  for (int64_t line = blockIdx.x; line < rows; line += gridDim.x) {
+    const int64_t b = line / a.T, t = line - b * a.T;
+    RT* sp = a.S ? static_cast<RT*>(a.S) + b * a.ss.b + t * a.ss.t : nullptr;
+    T* yp = a.Y ? static_cast<T*>(a.Y) + b * a.ys.b + t * a.ys.t : nullptr;
+    float v[NE], w[NE];
+    if (dead(a, b, t)) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) v[i] = 0.f;
+      if (sp) cols.store(v, sp);
+      if (yp) cols.store(v, yp);
+      continue;
+    }
+    float z[NE], res[NE];
+    cols.load(v, static_cast<const T*>(a.X) + b * a.xs.b + t * a.xs.t);
+    if (a.Z) cols.load(z, static_cast<const T*>(a.Z) + b * a.zs.b + t * a.zs.t);
+    if (a.res) cols.load(res, static_cast<const RT*>(a.res) + b * a.rs.b + t * a.rs.t);
+    if (a.Z) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) z[i] *= sigmoid(z[i]);
+      if (a.gate_first) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) v[i] *= z[i];
+      }
+    }
+    if (a.gamma_post) {
+      const float2 st = stats<W>(v, valid, a.D, a.layer, a.eps, team);
+      cols.param(w, a.gamma_post, 1.f);
+#pragma unroll
+      for (int i = 0; i < NE; ++i) v[i] = (v[i] - st.x) * st.y * w[i];
+      if (a.beta_post) {
+        cols.param(w, a.beta_post, 0.f);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) v[i] += w[i];
+      }
+    }
+    if (a.Z && !a.gate_first) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) v[i] *= z[i];
+    }
+    if (a.alpha) {
+      cols.param(w, a.alpha, 1.f);
+#pragma unroll
+      for (int i = 0; i < NE; ++i) v[i] *= w[i];
+    }
+    if (a.res) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) v[i] += res[i];
+    }
+    if (sp) cols.store(v, sp);
+    if (yp) {
+      const float2 st = stats<W>(v, valid, a.D, a.layer, a.eps, team);
+      cols.param(w, a.gamma_pre, 1.f);
+#pragma unroll
+      for (int i = 0; i < NE; ++i) v[i] = (v[i] - st.x) * st.y * w[i];
+      if (a.beta_pre) {
+        cols.param(w, a.beta_pre, 0.f);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) v[i] += w[i];
+      }
+      cols.store(v, yp);
+    }
+  }
+}
+
+// The gradient through unit = (x - mean) rstd, in place: h holds the gradient of unit.
+template <int W, int NE>
+__device__ __forceinline__ void norm_back(float (&h)[NE], const float (&unit)[NE], float rstd, int valid, int D, bool layer,
+                                          Team<W>& team) {
+  float s = 0.f, m = 0.f;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    if (i >= valid) h[i] = 0.f;
+    s = fmaf(h[i], unit[i], s);
+    m += h[i];
+  }
+  const float2 sums = team.sum2(s, layer ? m : 0.f);
+  const float cs = sums.x / static_cast<float>(D), cm = sums.y / static_cast<float>(D);
+#pragma unroll
+  for (int i = 0; i < NE; ++i) h[i] = (h[i] - cm - unit[i] * cs) * rstd;
+}
+
+// Backward: everything of the forward again from the row, then back through it.  A thread keeps its columns' sums of the
+// parameters' gradients over all rows of its workgroup; teams of fewer than 256 threads share a workgroup, which adds theirs up.
+template <typename T, typename RT, int R, int NC, bool Wide>
+__global__ __launch_bounds__(R < 256 ? 256 : R) void ttt_norm_bwd(NormArgs a) {
+  constexpr int W = R / 64, NE = 8 * NC, TEAMS = R < 256 ? 256 / R : 1;
+  __shared__ float slots[TEAMS][Team<W>::kSlots][W][2];
+  __shared__ float sums[TEAMS > 1 ? 256 : 1][TEAMS > 1 ? 9 : 1];
+  const int who = threadIdx.x / R, r = threadIdx.x % R;
+  Team<W> team{slots[who], r >> 6, 0};
+  const Cols<R, NC, Wide> cols{r, a.D};
+  const int valid = cols.valid();
+  const int64_t rows = static_cast<int64_t>(a.B) * a.T;
+  float acc[5][NE];
+#pragma unroll
+  for (int k = 0; k < 5; ++k)
+#pragma unroll
+    for (int i = 0; i < NE; ++i) acc[k][i] = 0.f;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * TEAMS;
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * TEAMS; first < rows; first += step) {
+    const int64_t line = min(first + who, rows - 1);
+    const int64_t b = line / a.T, t = line - b * a.T;
+    const bool off = first + who >= rows, none = off || dead(a, b, t);
+    // (a team without a row goes along on zeros: the others wait for it at the sums)
+    float x[NE], z[NE], u1[NE], v[NE], u2[NE], g[NE], w[NE];
+    float gate[NE], slope[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) x[i] = z[i] = g[i] = u2[i] = v[i] = 0.f;
+    if (!none) {
+      cols.load(x, static_cast<const T*>(a.X) + b * a.xs.b + t * a.xs.t);
+      if (a.Z) cols.load(z, static_cast<const T*>(a.Z) + b * a.zs.b + t * a.zs.t);
+      if (a.res) cols.load(u2, static_cast<const RT*>(a.res) + b * a.rs.b + t * a.rs.t);
+      if (a.dS) cols.load(v, static_cast<const RT*>(a.dS) + b * a.ss.b + t * a.ss.t);
+      if (a.dY) cols.load(g, static_cast<const T*>(a.dY) + b * a.ys.b + t * a.ys.t);
+    }
+    float ds[NE], n1[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) ds[i] = v[i];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      gate[i] = 1.f;
+      slope[i] = 0.f;
+      if (a.Z) {
+        const float s = sigmoid(z[i]);
+        gate[i] = z[i] * s;
+        slope[i] = fmaf(gate[i], 1.f - s, s);
+      }
+      u1[i] = a.gate_first ? x[i] * gate[i] : x[i];
+      n1[i] = u1[i];
+    }
+    float rstd1 = 1.f;
+    if (a.gamma_post) {
+      const float2 st = stats<W>(u1, valid, a.D, a.layer, a.eps, team);
+      rstd1 = st.y;
+      cols.param(w, a.gamma_post, 1.f);
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        u1[i] = i < valid ? (u1[i] - st.x) * st.y : 0.f;
+        n1[i] = u1[i] * w[i];
+      }
+      if (a.beta_post) {
+        cols.param(w, a.beta_post, 0.f);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) n1[i] += w[i];
+      }
+    }
+    cols.param(w, a.alpha, 1.f);
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      v[i] = a.gate_first ? n1[i] : n1[i] * gate[i];
+      u2[i] = fmaf(w[i], v[i], u2[i]);
+    }
+    if (a.dY) {
+      const float2 st = stats<W>(u2, valid, a.D, a.layer, a.eps, team);
+      cols.param(w, a.gamma_pre, 1.f);
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        u2[i] = i < valid ? (u2[i] - st.x) * st.y : 0.f;
+        if (!none) {
+          acc[3][i] = fmaf(g[i], u2[i], acc[3][i]);
+          acc[4][i] += g[i];
+        }
+        g[i] *= w[i];
+      }
+      norm_back<W>(g, u2, st.y, valid, a.D, a.layer, team);
+#pragma unroll
+      for (int i = 0; i < NE; ++i) ds[i] += g[i];
+    }
+    if (none) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) ds[i] = 0.f;
+    }
+    if (a.dres && !off) cols.store(ds, static_cast<RT*>(a.dres) + b * a.drs.b + t * a.drs.t);
+    cols.param(w, a.alpha, 1.f);
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      if (!none) acc[0][i] = fmaf(ds[i], v[i], acc[0][i]);
+      g[i] = ds[i] * w[i];                                   // dv
+      z[i] = a.gate_first ? 0.f : g[i] * n1[i] * slope[i];   // dz
+      if (!a.gate_first) g[i] *= gate[i];                    // dn
+    }
+    if (a.gamma_post) {
+      cols.param(w, a.gamma_post, 1.f);
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        if (!none) {
+          acc[1][i] = fmaf(g[i], u1[i], acc[1][i]);
+          acc[2][i] += g[i];
+        }
+        g[i] *= w[i];
+      }
+      norm_back<W>(g, u1, rstd1, valid, a.D, a.layer, team);
+    }
+    if (a.gate_first) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        z[i] = g[i] * x[i] * slope[i];
+        g[i] *= gate[i];
+      }
+    }
+    if (none) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) g[i] = z[i] = 0.f;
+    }
+    if (!off) {
+      cols.store(g, static_cast<T*>(a.dX) + b * a.dxs.b + t * a.dxs.t);
+      if (a.dZ) cols.store(z, static_cast<T*>(a.dZ) + b * a.dzs.b + t * a.dzs.t);
+    }
+  }
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 5 * a.D;
+#pragma unroll
+  for (int k = 0; k < 5; ++k) {
+    if constexpr (TEAMS > 1) {
+#pragma unroll
+      for (int c0 = 0; c0 < NE; c0 += 8) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sums[threadIdx.x][i] = acc[k][c0 + i];
+        __syncthreads();
+        if (who == 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int m = 1; m < TEAMS; ++m) acc[k][c0 + i] += sums[m * R + r][i];
+        }
+      }
+    }
+    if (who == 0) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        const int c = Wide ? 8 * ((i / 8) * R + r) + i % 8 : i * R + r;
+        if (c < a.D) part[static_cast<int64_t>(k) * a.D + c] = acc[k][i];
+      }
+    }
+  }
+}
+
+template <typename T, typename RT, int R, int NC>
+hipError_t go(bool backward, const NormArgs& a, hipStream_t s) {
+  if (backward) {
+    constexpr int threads = R < 256 ? 256 : R;
+    const unsigned grid = static_cast<unsigned>(a.blocks);
+    if (a.wide) ttt_norm_bwd<T, RT, R, NC, true><<<grid, threads, 0, s>>>(a);
+    else ttt_norm_bwd<T, RT, R, NC, false><<<grid, threads, 0, s>>>(a);
+  } else {
+    const int64_t rows = static_cast<int64_t>(a.B) * a.T, most = 256 * 2048 / R;  // all that run at a time
+    const unsigned grid = static_cast<unsigned>(rows < most ? rows : most);
+    if (a.wide) ttt_norm_fwd<T, RT, R, NC, true><<<grid, R, 0, s>>>(a);
+    else ttt_norm_fwd<T, RT, R, NC, false><<<grid, R, 0, s>>>(a);
+  }
+  return hipGetLastError();
+}
+
+// Threads of a row: the fewest whose 8 elements each hold it.
+template <typename T, typename RT>
+hipError_t go(bool backward, const NormArgs& a, hipStream_t s) {
+  if (a.D <= 512) return go<T, RT, 64, 1>(backward, a, s);
+  if (a.D <= 1024) return go<T, RT, 128, 1>(backward, a, s);
+  if (a.D <= 2048) return go<T, RT, 256, 1>(backward, a, s);
+  if (a.D <= 4096) return go<T, RT, 512, 1>(backward, a, s);
+  if (a.D <= 8192) return go<T, RT, 1024, 1>(backward, a, s);
+  return hipErrorInvalidValue;
+}
+
+hipError_t go(bool backward, const NormArgs& a, hipStream_t s) {
+  const bool f = a.in_dtype == 0, rf = a.res_dtype == 0;
+  if (f && rf) return go<float, float>(backward, a, s);
+  if (f) return go<float, uint16_t>(backward, a, s);
+  if (rf) return go<uint16_t, float>(backward, a, s);
+  return go<uint16_t, uint16_t>(backward, a, s);
+}
+
+}  // namespace
+
+int norm_max_d() { return 8192; }
+int norm_teams(int D) { return D <= 512 ? 4 : D <= 1024 ? 2 : 1; }
+
+hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s) { return go(false, a, s); }
+hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s) { return go(true, a, s); }
+
+}  // namespace ttt

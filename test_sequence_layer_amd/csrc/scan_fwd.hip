@@ -1,0 +1,236 @@
+// Selective scan, forward: prompts.
+//
+// Pages: [TTT] = news article "大模型最强架构TTT问世！斯坦福UCSD等5年磨一剑，一夜推翻Transformer"
+// (aharts.cn / itmax.cn), part 04 (the Mamba layer that TTT is compared with).
+//
+// Per token, channel and state one exp, two products and two multiply-adds: 24 issue cycles a wave of 64 (v_exp_f32 takes 8,
+// measured), against (with N = 16) half a byte: vector issue is the bound.
+#include "scan_common.h"
+
+namespace ttt {
+namespace {
+
+using namespace scan;
+
+// States: only what the segment adds to a zero state and the sum of its dt.
+template <typename InT, typename OutT, int NS, bool Wide, bool States>
+__global__ __launch_bounds__(256) void ttt_scan_fwd(ScanArgs a) {
+  constexpr int NP = 4 * NS;
+  __shared__ __align__(16) float2 sdt[TT][CH];  // dt, dt u
+  __shared__ __align__(16) float sB[TT * NP], sC[States ? 4 : TT * NP];
+  __shared__ __align__(16) float sy[States ? 1 : TT][CH];
+  const int tid = threadIdx.x, lane = tid & 63, q = lane & 3, cw = (tid >> 6) * 16 + (lane >> 2);
+  const int segs = States ? a.nseg - 1 : a.nseg;
+  const int seg = static_cast<int>(blockIdx.x % segs);
+  const Place p = place(a, blockIdx.x / segs);
+  const int c = p.c0 + cw;
+  const bool on = cw < p.nc;
+  const int begin = seg * a.seglen, tokens = min(a.T, begin + a.seglen), end = min(p.len, tokens);
+
+  float a2[NS], h[NS];
+  decays(a2, a, c, q, on);
+  if (States || a.nseg == 1) {
+    load_states(h, States || !a.h0 ? nullptr : a.h0 + (static_cast<int64_t>(p.b) * a.D + c) * a.N, a.N, q, on);
+  } else {
+    start_state(h, a2, a, p, seg, c, q, on);
+  }
+
+  // this thread's piece of a tile: token row, channels oct .. oct + 7
+  const int row = tid >> 3, oct = (tid & 7) * 8;
+  const int n8 = min(8, p.nc - oct);  // (may be negative)
+  const InT* up = static_cast<const InT*>(a.u) + p.b * a.us.b + p.c0 + oct;
+  const InT* dp = static_cast<const InT*>(a.dt) + p.b * a.dts.b + p.c0 + oct;
+  const InT* zp = a.z ? static_cast<const InT*>(a.z) + p.b * a.zs.b + p.c0 + oct : nullptr;
+  const InT* bp = static_cast<const InT*>(a.Bm) + p.b * a.bs.b + p.g * a.bs.h;
+  const InT* cp = static_cast<const InT*>(a.Cm) + p.b * a.cs.b + p.g * a.cs.h;
+  OutT* yp = static_cast<OutT*>(a.y) + p.b * a.ys.b + p.c0 + oct;
+  float bias[8], skip[8];
+  params<8>(bias, a.dt_bias ? a.dt_bias + p.c0 + oct : nullptr, n8, 0.f);
+  if constexpr (!States) params<8>(skip, a.Dskip ? a.Dskip + p.c0 + oct : nullptr, n8, 0.f);
+
+  Piece<InT, 8> u, dt, z;
+  Rows<InT, NS> rb, rc;
+  auto fetch = [&](int t0) {
+    const int64_t t = t0 + row;
+    const int n = t < end ? n8 : 0;
+    load<Wide>(u, up + t * a.us.t, n);
+    load<Wide>(dt, dp + t * a.dts.t, n);
+    rb.load(bp, a.bs.t, a.N, t0, end, tid);
+    if constexpr (!States) rc.load(cp, a.cs.t, a.N, t0, end, tid);
+  };
+  float sum = 0.f;
+  fetch(begin);
+  for (int t0 = begin; t0 < end; t0 += TT) {
+    const int64_t t = t0 + row;
+    const bool live = t < end;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      float x[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float s = dt.get(i + j) + bias[i + j], slope;
+        if (a.softplus) s = softplus(s, slope);
+        x[j] = live && i + j < n8 ? s : 0.f;
+      }
+      *reinterpret_cast<float4*>(&sdt[row][oct + i]) = make_float4(x[0], x[0] * u.get(i), x[1], x[1] * u.get(i + 1));
+    }
+    rb.stage(sB, tid);
+    if constexpr (!States) rc.stage(sC, tid);
+    Piece<InT, 8> u0 = u;
+    if constexpr (!States) {
+      if (zp) load<Wide>(z, zp + t * a.zs.t, live ? n8 : 0);
+    }
+    __syncthreads();
+    if (t0 + TT < end) fetch(t0 + TT);
+#pragma unroll 8
+    for (int k = 0; k < TT; ++k) {
+      const float2 d = sdt[k][cw];
+      float Bv[NS], Cv[NS], s = 0.f;
+      lds_floats(Bv, sB + k * NP + q * NS);
+      if constexpr (!States) lds_floats(Cv, sC + k * NP + q * NS);
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        h[i] = fmaf(__builtin_amdgcn_exp2f(d.x * a2[i]), h[i], d.y * Bv[i]);
+        if constexpr (!States) s = fmaf(Cv[i], h[i], s);
+      }
+      if constexpr (States) {
+        sum += d.x;
+      } else {
+        s = quad_sum(s);
+        if (q == 0) sy[k][cw] = s;
+      }
+    }
+    __syncthreads();
+    if constexpr (!States) {
+      if (live && n8 > 0) {
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(&sy[row][oct + i]);
+          y[i] = v.x; y[i + 1] = v.y; y[i + 2] = v.z; y[i + 3] = v.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          y[i] = fmaf(skip[i], u0.get(i), y[i]);
+          if (zp) {
+            const float x = z.get(i);
+            y[i] *= x * sigmoid(x);
+          }
+        }
+        Piece<OutT, 8> out;
+        out.set_all(y);
+        store<Wide>(out, yp + t * a.ys.t, n8);
+      }
+    }
+  }
+  const int64_t slot = static_cast<int64_t>(p.b) * a.nseg + seg;
+  if constexpr (States) {
+    store_states(h, a.hseg + ((slot + 1) * a.D + c) * a.N, a.N, q, on);
+    if (on && q == 0) a.sseg[slot * a.D + c] = sum;
+    if (seg == 0) {
+      load_states(h, a.h0 ? a.h0 + (static_cast<int64_t>(p.b) * a.D + c) * a.N : nullptr, a.N, q, on);
+      store_states(h, a.hseg + (slot * a.D + c) * a.N, a.N, q, on);
+    }
+  } else {
+    if (seg == a.nseg - 1) store_states(h, a.h_final + (static_cast<int64_t>(p.b) * a.D + c) * a.N, a.N, q, on);
+    Piece<OutT, 8> none;
+    none.zero();
+    for (int64_t t = max(begin, end) + row; t < tokens; t += TT) store<Wide>(none, yp + t * a.ys.t, n8);
+  }
+}
+
+// A few tokens, the state in place: four lanes to a channel, NS states each.
+template <typename InT, typename OutT, int NS>
+__global__ __launch_bounds__(256) void ttt_scan_decode(ScanArgs a) {
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 64 + (threadIdx.x >> 2);
+  const int q = threadIdx.x & 3;
+  const int64_t b = id / a.D;
+  const int c = static_cast<int>(id - b * a.D);
+  if (b >= a.B) return;
+  const int len = a.lens ? max(0, min(a.lens[b], a.T)) : a.T, g = c / (a.D / a.G);
+  const InT* up = static_cast<const InT*>(a.u) + b * a.us.b + c;
+  const InT* dp = static_cast<const InT*>(a.dt) + b * a.dts.b + c;
+  const InT* zp = a.z ? static_cast<const InT*>(a.z) + b * a.zs.b + c : nullptr;
+  const InT* bp = static_cast<const InT*>(a.Bm) + b * a.bs.b + g * a.bs.h;
+  const InT* cp = static_cast<const InT*>(a.Cm) + b * a.cs.b + g * a.cs.h;
+  OutT* yp = static_cast<OutT*>(a.y) + b * a.ys.b + c;
+  float* hp = a.h_final + id * a.N;
+  if (len > 0) {
+    float a2[NS], h[NS];
+    decays(a2, a, c, q, true);
+    load_states(h, hp, a.N, q, true);
+    const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, skip = a.Dskip ? a.Dskip[c] : 0.f;
+    for (int64_t t = 0; t < len; ++t) {
+      const float u = as_f32(up[t * a.us.t]);
+      float dt = as_f32(dp[t * a.dts.t]) + bias, slope;
+      if (a.softplus) dt = softplus(dt, slope);
+      float y = 0.f;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const int n = q * NS + i;
+        const float Bv = n < a.N ? as_f32(bp[t * a.bs.t + n]) : 0.f, Cv = n < a.N ? as_f32(cp[t * a.cs.t + n]) : 0.f;
+        h[i] = fmaf(__builtin_amdgcn_exp2f(dt * a2[i]), h[i], dt * u * Bv);
+        if (n < a.N) y = fmaf(Cv, h[i], y);
+      }
+      y = fmaf(skip, u, quad_sum(y));
+      if (zp) {
+        const float x = as_f32(zp[t * a.zs.t]);
+        y *= x * sigmoid(x);
+      }
+      if (q == 0) put(yp + t * a.ys.t, y);
+    }
+    store_states(h, hp, a.N, q, true);
+  }
+  for (int64_t t = len + q; t < a.T; t += 4) put(yp + t * a.ys.t, 0.f);
+}
+
+enum Which { STATES, FWD, DECODE };
+
+template <typename InT, typename OutT, int NS>
+hipError_t go(Which which, const ScanArgs& a, hipStream_t s) {
+  if (which == DECODE) {
+    const int64_t n = static_cast<int64_t>(a.B) * a.D;
+    ttt_scan_decode<InT, OutT, NS><<<static_cast<unsigned>((n + 63) / 64), 256, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  const int dg = a.D / a.G, segs = which == STATES ? a.nseg - 1 : a.nseg;
+  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.B) * a.G * ((dg + CH - 1) / CH) * segs);
+  if (which == STATES) {
+    if (a.wide) ttt_scan_fwd<InT, float, NS, true, true><<<grid, 256, 0, s>>>(a);
+    else ttt_scan_fwd<InT, float, NS, false, true><<<grid, 256, 0, s>>>(a);
+  } else {
+    if (a.wide) ttt_scan_fwd<InT, OutT, NS, true, false><<<grid, 256, 0, s>>>(a);
+    else ttt_scan_fwd<InT, OutT, NS, false, false><<<grid, 256, 0, s>>>(a);
+  }
+  return hipGetLastError();
+}
+
+template <typename InT, typename OutT>
+hipError_t go(Which which, const ScanArgs& a, hipStream_t s) {
+  switch (scan_states(a.N)) {
+    case 1: return go<InT, OutT, 1>(which, a, s);
+    case 2: return go<InT, OutT, 2>(which, a, s);
+    case 4: return go<InT, OutT, 4>(which, a, s);
+    case 8: return go<InT, OutT, 8>(which, a, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+hipError_t go(Which which, const ScanArgs& a, hipStream_t s) {
+  const bool inf = a.in_dtype == 0, outf = a.out_dtype == 0;
+  if (which == STATES) return inf ? go<float, float>(which, a, s) : go<uint16_t, float>(which, a, s);
+  if (inf && outf) return go<float, float>(which, a, s);
+  if (inf) return go<float, uint16_t>(which, a, s);
+  if (outf) return go<uint16_t, float>(which, a, s);
+  return go<uint16_t, uint16_t>(which, a, s);
+}
+
+}  // namespace
+
+int scan_states(int N) { return N < 1 ? 0 : N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 0; }
+
+hipError_t launch_scan_states(const ScanArgs& a, hipStream_t s) { return go(STATES, a, s); }
+hipError_t launch_scan_fwd(const ScanArgs& a, hipStream_t s) { return go(FWD, a, s); }
+hipError_t launch_scan_decode(const ScanArgs& a, hipStream_t s) { return go(DECODE, a, s); }
+
+}  // namespace ttt

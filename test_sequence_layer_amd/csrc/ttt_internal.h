@@ -2,6 +2,7 @@
 // family's launch arguments and entry points, for the host-side dispatch.
 #pragma once
 #include "args_attn.h"
+#include "args_block.h"
 #include "args_bwd.h"
 #include "args_linear.h"
 #include "args_mlp.h"
