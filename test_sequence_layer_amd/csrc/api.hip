@@ -2130,6 +2130,8 @@ ttt::ScanArgs make_scan_args(const ttt_selective_scan_desc* d, const ScanViews& 
   a.A = A; a.Dskip = D; a.dt_bias = bias; a.h0 = h0; a.lens = lens;
   a.us = strides2(v.u); a.dts = strides2(v.dt); a.zs = strides2(v.z); a.ys = strides2(v.y);
   a.bs = strides(v.Bm); a.cs = strides(v.Cm);
+  const int64_t four = 4 * dtype_size(d->in_dtype);
+  a.bc_wide = d->N % 4 == 0 && view_aligned(v.Bm, four) && view_aligned(v.Cm, four);
   return a;
 }
 

@@ -37,6 +37,7 @@ struct ScanArgs {
   int B, T, D, N, G;
   int in_dtype, out_dtype;
   bool softplus, wide;
+  bool bc_wide;           // B and C: N a multiple of 4, addresses and strides of 4 elements
   const void *u, *dt, *z; // [B, T, D] (z or nullptr)
   const void *Bm, *Cm;    // [B, G, T, N]
   const float* A;         // [D, N]

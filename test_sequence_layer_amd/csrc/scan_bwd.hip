@@ -17,6 +17,9 @@ namespace {
 
 using namespace scan;
 
+constexpr int TT = 16;  // tokens staged at a time: 4 channels of one to a thread, which leaves registers for the chunk
+constexpr int GS = 4;
+
 template <int NS>
 constexpr int kChunk = NS <= 4 ? 16 : 8;
 
@@ -45,13 +48,43 @@ __device__ __forceinline__ void channel_sums(float (&x)[2 * NS]) {
   }
 }
 
+// This thread's piece of the tiles: token row, channels quad .. quad + 3, and where they are.
+template <typename InT, typename OutT>
+struct Lines {
+  int row, quad, n4;  // n4 may be negative
+  const InT *u, *dt, *z;
+  const OutT* dy;
+  __device__ __forceinline__ Lines(const ScanArgs& a, const Place& p, int first, int tid) {
+    row = tid >> 4;
+    quad = (tid & 15) * 4;
+    n4 = min(4, p.nc - quad);
+    const int64_t t = first + row, c = p.c0 + quad;
+    u = static_cast<const InT*>(a.u) + p.b * a.us.b + t * a.us.t + c;
+    dt = static_cast<const InT*>(a.dt) + p.b * a.dts.b + t * a.dts.t + c;
+    z = a.z ? static_cast<const InT*>(a.z) + p.b * a.zs.b + t * a.zs.t + c : nullptr;
+    dy = static_cast<const OutT*>(a.dy) + p.b * a.ys.b + t * a.ys.t + c;
+  }
+  __device__ __forceinline__ void step(const ScanArgs& a, int dir) {
+    u += dir * TT * a.us.t;
+    dt += dir * TT * a.dts.t;
+    if (z) z += dir * TT * a.zs.t;
+    dy += dir * TT * a.ys.t;
+  }
+};
+
+template <int N>
+__device__ __forceinline__ void zero_from(float (&x)[N], int n) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = i < n ? x[i] : 0.f;
+}
+
 // What a segment adds to a zero state (hseg), its sum of dt (sseg) and what its own dy add to the gradient of the state
 // before it (gseg): g = sum_t a_1 .. a_t C_t dy_t.
 template <typename InT, typename OutT, int NS, bool Wide>
-__global__ __launch_bounds__(256) void ttt_scan_bwd_states(ScanArgs a) {
+__global__ __launch_bounds__(256, 2) void ttt_scan_bwd_states(ScanArgs a) {
   constexpr int NP = 4 * NS;
   __shared__ __align__(16) float4 tile[TT][CH];  // dt, dt u, dy
-  __shared__ __align__(16) float sB[TT * NP], sC[TT * NP];
+  __shared__ __align__(16) float bc[2 * TT * NP];
   const int tid = threadIdx.x, lane = tid & 63, q = lane & 3, cw = (tid >> 6) * 16 + (lane >> 2);
   const int seg = static_cast<int>(blockIdx.x % a.nseg);
   const Place p = place(a, blockIdx.x / a.nseg);
@@ -62,53 +95,51 @@ __global__ __launch_bounds__(256) void ttt_scan_bwd_states(ScanArgs a) {
   decays(a2, a, c, q, on);
 #pragma unroll
   for (int i = 0; i < NS; ++i) h[i] = g[i] = 0.f, prod[i] = 1.f;
-  const int row = tid >> 3, oct = (tid & 7) * 8, n8 = min(8, p.nc - oct);
-  const InT* up = static_cast<const InT*>(a.u) + p.b * a.us.b + p.c0 + oct;
-  const InT* dp = static_cast<const InT*>(a.dt) + p.b * a.dts.b + p.c0 + oct;
-  const InT* zp = a.z ? static_cast<const InT*>(a.z) + p.b * a.zs.b + p.c0 + oct : nullptr;
-  const OutT* gp = static_cast<const OutT*>(a.dy) + p.b * a.ys.b + p.c0 + oct;
-  const InT* bp = static_cast<const InT*>(a.Bm) + p.b * a.bs.b + p.g * a.bs.h;
-  const InT* cp = static_cast<const InT*>(a.Cm) + p.b * a.cs.b + p.g * a.cs.h;
-  float bias[8];
-  params<8>(bias, a.dt_bias ? a.dt_bias + p.c0 + oct : nullptr, n8, 0.f);
+  Lines<InT, OutT> at(a, p, begin, tid);
+  BcRows<InT, NS, TT> rows(a, p, begin, tid, true);
+  float bias[4];
+  params<4>(bias, a.dt_bias ? a.dt_bias + p.c0 + at.quad : nullptr, at.n4, 0.f);
   for (int t0 = begin; t0 < end; t0 += TT) {
-    const int64_t t = t0 + row;
-    const int n = t < end ? n8 : 0;
-    Piece<InT, 8> u, dt, z;
-    Piece<OutT, 8> dy;
-    Rows<InT, NS> rb, rc;
-    load<Wide>(u, up + t * a.us.t, n);
-    load<Wide>(dt, dp + t * a.dts.t, n);
-    load<Wide>(dy, gp + t * a.ys.t, n);
-    if (zp) load<Wide>(z, zp + t * a.zs.t, n);
-    rb.load(bp, a.bs.t, a.N, t0, end, tid);
-    rc.load(cp, a.cs.t, a.N, t0, end, tid);
+    const int n = t0 + at.row < end ? at.n4 : 0;
+    Piece<InT, 4> u, dt, z;
+    Piece<OutT, 4> dy;
+    load<Wide>(u, at.u, n);
+    load<Wide>(dt, at.dt, n);
+    load<Wide>(dy, at.dy, n);
+    if (at.z) load<Wide>(z, at.z, n);
+    rows.load(t0, end, 1);
+    at.step(a, 1);
     if (t0 > begin) __syncthreads();
+    float s[4], d[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float s = dt.get(i) + bias[i], d = dy.get(i), slope;
-      if (a.softplus) s = softplus(s, slope);
-      if (i >= n) s = 0.f;
-      if (zp) d *= z.get(i) * sigmoid(z.get(i));
-      tile[row][oct + i] = make_float4(s, s * u.get(i), d, 0.f);
+    for (int i = 0; i < 4; ++i) s[i] = dt.get(i) + bias[i], d[i] = dy.get(i);
+    if (a.softplus) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = softplus(s[i]);
     }
-    rb.stage(sB, tid);
-    rc.stage(sC, tid);
+    zero_from(s, n);
+    if (at.z) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[i] *= z.get(i) * sigmoid(z.get(i));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tile[at.row][at.quad + i] = make_float4(s[i], s[i] * u.get(i), d[i], 0.f);
+    rows.stage(bc);
     __syncthreads();
-#pragma unroll 8
+#pragma unroll 4
     for (int k = 0; k < TT; ++k) {
-      const float4 d = tile[k][cw];
+      const float4 x = tile[k][cw];
       float Bv[NS], Cv[NS];
-      lds_floats(Bv, sB + k * NP + q * NS);
-      lds_floats(Cv, sC + k * NP + q * NS);
+      lds_floats(Bv, bc + k * NP + q * NS);
+      lds_floats(Cv, bc + (TT + k) * NP + q * NS);
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
-        const float e = __builtin_amdgcn_exp2f(d.x * a2[i]);
-        h[i] = fmaf(e, h[i], d.y * Bv[i]);
+        const float e = __builtin_amdgcn_exp2f(x.x * a2[i]);
+        h[i] = fmaf(e, h[i], x.y * Bv[i]);
         prod[i] *= e;
-        g[i] = fmaf(prod[i], Cv[i] * d.z, g[i]);
+        g[i] = fmaf(prod[i], Cv[i] * x.z, g[i]);
       }
-      sum += d.x;
+      sum += x.x;
     }
   }
   const int64_t slot = static_cast<int64_t>(p.b) * a.nseg + seg;
@@ -122,10 +153,10 @@ __global__ __launch_bounds__(256) void ttt_scan_bwd_states(ScanArgs a) {
 }
 
 template <typename InT, typename OutT, int NS, bool Wide>
-__global__ __launch_bounds__(256) void ttt_scan_bwd(ScanArgs a) {
-  constexpr int NP = 4 * NS, CL = kChunk<NS>;
+__global__ __launch_bounds__(256, 2) void ttt_scan_bwd(ScanArgs a) {
+  constexpr int NP = 4 * NS, CL = kChunk<NS>, NV = NS > 1 ? NS / 2 : 1;
   __shared__ __align__(16) float4 tile[TT][CH];  // dt, dt u, dy; then sum g B, sum g a h A log2(e), y
-  __shared__ __align__(16) float sB[TT * NP], sC[TT * NP];
+  __shared__ __align__(16) float bc[2 * TT * NP];
   __shared__ __align__(16) float sbc[4][TT][2][NP];  // each wave's sums over its channels
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, q = lane & 3, cw = wave * 16 + (lane >> 2);
   const int seg = static_cast<int>(blockIdx.x % a.nseg);
@@ -140,46 +171,66 @@ __global__ __launch_bounds__(256) void ttt_scan_bwd(ScanArgs a) {
   if (a.nseg == 1) load_states(h, a.h0 ? a.h0 + (static_cast<int64_t>(p.b) * a.D + c) * a.N : nullptr, a.N, q, on);
   else start_state(h, a2, a, p, seg, c, q, on);
 
-  const int row = tid >> 3, oct = (tid & 7) * 8, n8 = min(8, p.nc - oct);
-  const InT* up = static_cast<const InT*>(a.u) + p.b * a.us.b + p.c0 + oct;
-  const InT* dp = static_cast<const InT*>(a.dt) + p.b * a.dts.b + p.c0 + oct;
-  const InT* zp = a.z ? static_cast<const InT*>(a.z) + p.b * a.zs.b + p.c0 + oct : nullptr;
-  const OutT* gp = static_cast<const OutT*>(a.dy) + p.b * a.ys.b + p.c0 + oct;
-  const InT* bp = static_cast<const InT*>(a.Bm) + p.b * a.bs.b + p.g * a.bs.h;
-  const InT* cp = static_cast<const InT*>(a.Cm) + p.b * a.cs.b + p.g * a.cs.h;
-  float bias[8];
-  params<8>(bias, a.dt_bias ? a.dt_bias + p.c0 + oct : nullptr, n8, 0.f);
-  float* ck = a.ckpt + (static_cast<int64_t>(p.b) * a.chunks * a.D + c) * a.N;  // chunk j at j * D * N
+  Lines<InT, OutT> at(a, p, begin, tid);
+  BcRows<InT, NS, TT> rows(a, p, begin, tid, true);
+  float bias[4];
+  params<4>(bias, a.dt_bias ? a.dt_bias + p.c0 + at.quad : nullptr, at.n4, 0.f);
   const int64_t ckstep = static_cast<int64_t>(a.D) * a.N;
+  // the chunk's state; always by the same thread, so that it is there when it is read again
+  float* ck = a.ckpt + (static_cast<int64_t>(p.b) * a.chunks + begin / CL) * ckstep + static_cast<int64_t>(c) * a.N;
 
   // forward: the state before each chunk
+  const int last = begin + (max(end - begin, 1) - 1) / TT * TT;
+  Piece<InT, 4> u, dtr, z;
+  Piece<OutT, 4> dyr;
+  auto fetch = [&](int t0, int dir, bool back) {
+    const int n = t0 + at.row < end ? at.n4 : 0;
+    load<Wide>(u, at.u, n);
+    load<Wide>(dtr, at.dt, n);
+    if (back) {
+      load<Wide>(dyr, at.dy, n);
+      if (at.z) load<Wide>(z, at.z, n);
+    }
+    rows.load(t0, end, dir);
+    at.step(a, dir);
+  };
+  if (begin < end) fetch(begin, 1, false);
   for (int t0 = begin; t0 < end; t0 += TT) {
-    const int64_t t = t0 + row;
-    const int n = t < end ? n8 : 0;
-    Piece<InT, 8> u, dt;
-    Rows<InT, NS> rb;
-    load<Wide>(u, up + t * a.us.t, n);
-    load<Wide>(dt, dp + t * a.dts.t, n);
-    rb.load(bp, a.bs.t, a.N, t0, end, tid);
+    const int n = t0 + at.row < end ? at.n4 : 0;
+    float s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = dtr.get(i) + bias[i];
+    if (a.softplus) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = softplus(s[i]);
+    }
+    zero_from(s, n);
     if (t0 > begin) __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float s = dt.get(i) + bias[i], slope;
-      if (a.softplus) s = softplus(s, slope);
-      if (i >= n) s = 0.f;
-      *reinterpret_cast<float2*>(&tile[row][oct + i]) = make_float2(s, s * u.get(i));
-    }
-    rb.stage(sB, tid);
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<float2*>(&tile[at.row][at.quad + i]) = make_float2(s[i], s[i] * u.get(i));
+    rows.stage(bc);
     __syncthreads();
+    if (t0 < last) fetch(t0 + TT, 1, false);
+    const float* sd = &tile[0][cw].x;
+    const float* sb = bc + q * NS;
+#pragma unroll
     for (int k0 = 0; k0 < TT; k0 += CL) {
-      if (t0 + k0 < end) store_states(h, ck + (t0 + k0) / CL * ckstep, a.N, q, on);
+      store_states(h, ck, a.N, q, on && t0 + k0 < end);
+      ck += ckstep;
+      if (k0 + CL >= TT && t0 >= last) break;  // (nobody asks for the state behind the last chunk)
 #pragma unroll
-      for (int k = k0; k < k0 + CL; ++k) {
-        const float2 d = *reinterpret_cast<const float2*>(&tile[k][cw]);
-        float Bv[NS];
-        lds_floats(Bv, sB + k * NP + q * NS);
+      for (int k = k0; k < k0 + CL; k += GS) {
+        Group<NS, false, GS, TT, 4 * CH> g;
+        g.read(sd, sb, k);
+        float e[GS][NS];
 #pragma unroll
-        for (int i = 0; i < NS; ++i) h[i] = fmaf(__builtin_amdgcn_exp2f(d.x * a2[i]), h[i], d.y * Bv[i]);
+        for (int j = 0; j < GS; ++j)
+#pragma unroll
+          for (int i = 0; i < NS; ++i) e[j][i] = __builtin_amdgcn_exp2f(g.d[j].x * a2[i]);
+#pragma unroll
+        for (int j = 0; j < GS; ++j)
+#pragma unroll
+          for (int i = 0; i < NS; ++i) h[i] = fmaf(e[j][i], h[i], g.d[j].y * g.B[j][i]);
       }
     }
   }
@@ -188,141 +239,137 @@ __global__ __launch_bounds__(256) void ttt_scan_bwd(ScanArgs a) {
   float g[NS], dA[NS];
   load_states(g, a.dh_final ? a.dh_final + (static_cast<int64_t>(p.b) * a.D + c) * a.N : nullptr, a.N, q, on);
   for (int s = a.nseg - 1; s > seg; --s) {
-    const int64_t at = static_cast<int64_t>(p.b) * a.nseg + s;
-    const float sum = on ? a.sseg[at * a.D + c] : 0.f;
+    const int64_t o = static_cast<int64_t>(p.b) * a.nseg + s;
+    const float sum = on ? a.sseg[o * a.D + c] : 0.f;
     float x[NS];
-    load_states(x, a.gseg + (at * a.D + c) * a.N, a.N, q, on);
+    load_states(x, a.gseg + (o * a.D + c) * a.N, a.N, q, on);
 #pragma unroll
     for (int i = 0; i < NS; ++i) g[i] = fmaf(__builtin_amdgcn_exp2f(sum * a2[i]), g[i], x[i]);
   }
 #pragma unroll
   for (int i = 0; i < NS; ++i) dA[i] = 0.f;
 
-  OutT* dup = static_cast<OutT*>(a.du) + p.b * a.dus.b + p.c0 + oct;
-  OutT* ddp = static_cast<OutT*>(a.ddt) + p.b * a.ddts.b + p.c0 + oct;
-  OutT* dzp = zp ? static_cast<OutT*>(a.dz) + p.b * a.dzs.b + p.c0 + oct : nullptr;
-  float skip[8], dD[8], db[8];
-  params<8>(skip, a.Dskip ? a.Dskip + p.c0 + oct : nullptr, n8, 0.f);
+  const int64_t oc = p.c0 + at.quad, ot = last + at.row;
+  OutT* dup = static_cast<OutT*>(a.du) + p.b * a.dus.b + ot * a.dus.t + oc;
+  OutT* ddp = static_cast<OutT*>(a.ddt) + p.b * a.ddts.b + ot * a.ddts.t + oc;
+  OutT* dzp = at.z ? static_cast<OutT*>(a.dz) + p.b * a.dzs.b + ot * a.dzs.t + oc : nullptr;
+  float skip[4], dD[4], db[4];
+  params<4>(skip, a.Dskip ? a.Dskip + oc : nullptr, at.n4, 0.f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dD[i] = db[i] = 0.f;
-  float* part = a.bcpart + (static_cast<int64_t>(p.b) * a.G + p.g) * ((a.D / a.G + CH - 1) / CH) * a.T * 2 * a.N +
-                static_cast<int64_t>(p.tile) * a.T * 2 * a.N;
+  for (int i = 0; i < 4; ++i) dD[i] = db[i] = 0.f;
+  float* part = a.bcpart + ((static_cast<int64_t>(p.b) * a.G + p.g) * ((a.D / a.G + CH - 1) / CH) + p.tile) * a.T * 2 * a.N;
 
-  const int last = begin + (max(end - begin, 1) - 1) / TT * TT;
-  for (int t0 = last; t0 >= begin && end > begin; t0 -= TT) {
-    const int64_t t = t0 + row;
-    const int n = t < end ? n8 : 0;
-    Piece<InT, 8> u, dtr, z;
-    Piece<OutT, 8> dyr;
-    Rows<InT, NS> rb, rc;
-    load<Wide>(u, up + t * a.us.t, n);
-    load<Wide>(dtr, dp + t * a.dts.t, n);
-    load<Wide>(dyr, gp + t * a.ys.t, n);
-    if (zp) load<Wide>(z, zp + t * a.zs.t, n);
-    rb.load(bp, a.bs.t, a.N, t0, end, tid);
-    rc.load(cp, a.cs.t, a.N, t0, end, tid);
-    __syncthreads();  // the tile before (or the forward walk's last) is done with
-    float dt[8], slope[8];
+  if (begin < end) {
+    // (the forward walk left the pointers one tile behind the last)
+    at.step(a, -1);
+    rows.back();
+    fetch(last, -1, true);
+  }
+  for (int t0 = last; t0 >= begin && begin < end; t0 -= TT) {
+    const int n = t0 + at.row < end ? at.n4 : 0;
+    const Piece<InT, 4> u0 = u, z0 = z;
+    const Piece<OutT, 4> dy0 = dyr;
+    float dt[4], slope[4], d[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float d = dyr.get(i);
-      dt[i] = dtr.get(i) + bias[i];
-      slope[i] = 1.f;
-      if (a.softplus) dt[i] = softplus(dt[i], slope[i]);
-      if (i >= n) dt[i] = 0.f;
-      if (zp) d *= z.get(i) * sigmoid(z.get(i));
-      tile[row][oct + i] = make_float4(dt[i], dt[i] * u.get(i), d, 0.f);
+    for (int i = 0; i < 4; ++i) dt[i] = dtr.get(i) + bias[i], slope[i] = 1.f, d[i] = dyr.get(i);
+    if (a.softplus) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dt[i] = softplus(dt[i], slope[i]);
     }
-    rb.stage(sB, tid);
-    rc.stage(sC, tid);
+    zero_from(dt, n);
+    if (at.z) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[i] *= z0.get(i) * sigmoid(z0.get(i));
+    }
+    __syncthreads();  // the tile before (or the forward walk's last) is done with
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tile[at.row][at.quad + i] = make_float4(dt[i], dt[i] * u0.get(i), d[i], 0.f);
+    rows.stage(bc);
     __syncthreads();
+    if (t0 > begin) fetch(t0 - TT, -1, true);
+    const float* sb = bc + q * NS;
+    float* res = reinterpret_cast<float*>(&tile[0][cw]) + q;
+    float* sums = &sbc[wave][0][lane >> 5][NS > 1 ? q * NS + (lane >> 4 & 1) * (NS / 2) : q];
 #pragma unroll 1
     for (int k0 = TT - CL; k0 >= 0; k0 -= CL) {
-      if (t0 + k0 >= end) {  // nothing here: zeros for the sums
-        for (int k = k0; k < k0 + CL; ++k) {
-          reinterpret_cast<float*>(&tile[k][cw])[q] = 0.f;
-          if ((lane & 12) == 0) {
-#pragma unroll
-            for (int j = 0; j < (NS > 1 ? NS / 2 : 1); ++j)
-              sbc[wave][k][lane >> 5][NS > 1 ? q * NS + (lane >> 4 & 1) * (NS / 2) + j : q] = 0.f;
-          }
-        }
-        continue;
-      }
+      ck -= ckstep;
       float ah[CL][NS], e[CL][NS];
-      load_states(h, ck + (t0 + k0) / CL * ckstep, a.N, q, on);
+      load_states(h, ck, a.N, q, on && t0 + k0 < end);
 #pragma unroll
       for (int k = 0; k < CL; ++k) {
-        const float2 d = *reinterpret_cast<const float2*>(&tile[k0 + k][cw]);
+        const float2 x = *reinterpret_cast<const float2*>(&tile[k0 + k][cw]);
         float Bv[NS];
-        lds_floats(Bv, sB + (k0 + k) * NP + q * NS);
+        lds_floats(Bv, sb + (k0 + k) * NP);
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-          e[k][i] = __builtin_amdgcn_exp2f(d.x * a2[i]);
+          e[k][i] = __builtin_amdgcn_exp2f(x.x * a2[i]);
           ah[k][i] = e[k][i] * h[i];
-          h[i] = fmaf(d.y, Bv[i], ah[k][i]);
+          h[i] = fmaf(x.y, Bv[i], ah[k][i]);
         }
       }
 #pragma unroll
       for (int k = CL - 1; k >= 0; --k) {
-        const float4 d = tile[k0 + k][cw];
-        float Bv[NS], Cv[NS], bc[2 * NS], sb = 0.f, sa = 0.f, y = 0.f;
-        lds_floats(Bv, sB + (k0 + k) * NP + q * NS);
-        lds_floats(Cv, sC + (k0 + k) * NP + q * NS);
+        const float4 x = tile[k0 + k][cw];
+        float Bv[NS], Cv[NS], v[2 * NS], s = 0.f, sa = 0.f, y = 0.f;
+        lds_floats(Bv, sb + (k0 + k) * NP);
+        lds_floats(Cv, sb + (TT + k0 + k) * NP);
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-          g[i] = fmaf(Cv[i], d.z, g[i]);
-          const float ht = fmaf(d.y, Bv[i], ah[k][i]);
-          bc[i] = d.y * g[i];
-          bc[NS + i] = d.z * ht;
-          sb = fmaf(g[i], Bv[i], sb);
+          g[i] = fmaf(Cv[i], x.z, g[i]);
+          const float ht = fmaf(x.y, Bv[i], ah[k][i]);
+          v[i] = x.y * g[i];
+          v[NS + i] = x.z * ht;
+          s = fmaf(g[i], Bv[i], s);
           const float gh = g[i] * ah[k][i];
           sa = fmaf(gh, a2[i], sa);
-          dA[i] = fmaf(gh, d.x, dA[i]);
+          dA[i] = fmaf(gh, x.x, dA[i]);
           y = fmaf(Cv[i], ht, y);
           g[i] *= e[k][i];
         }
-        channel_sums<NS>(bc);
-        sb = quad_sum(sb);
+        channel_sums<NS>(v);
+        s = quad_sum(s);
         sa = quad_sum(sa);
         y = quad_sum(y);
-        if (q < 3) reinterpret_cast<float*>(&tile[k0 + k][cw])[q] = q == 0 ? sb : q == 1 ? sa : y;
-        if ((lane & 12) == 0) {
-#pragma unroll
-          for (int j = 0; j < (NS > 1 ? NS / 2 : 1); ++j)
-            sbc[wave][k0 + k][lane >> 5][NS > 1 ? q * NS + (lane >> 4 & 1) * (NS / 2) + j : q] = bc[j];
-        }
+        // (lanes that hold the same value write it to the same place: no branch in the walk)
+        res[(k0 + k) * 4 * CH] = q == 0 ? s : q == 1 ? sa : y;
+        if constexpr (NV == 4) *reinterpret_cast<float4*>(sums + (k0 + k) * 2 * NP) = make_float4(v[0], v[1], v[2], v[3]);
+        else if constexpr (NV == 2) *reinterpret_cast<float2*>(sums + (k0 + k) * 2 * NP) = make_float2(v[0], v[1]);
+        else sums[(k0 + k) * 2 * NP] = v[0];
       }
     }
     __syncthreads();
-    if (t < end && n8 > 0) {
-      float o[3][8];
+    float o[3][4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 v = tile[row][oct + i];
-        const float uu = u.get(i);
-        float d = dyr.get(i);
-        o[2][i] = 0.f;
-        if (zp) {
-          const float x = z.get(i), s = sigmoid(x), gate = x * s;
-          o[2][i] = d * fmaf(skip[i], uu, v.z) * fmaf(gate, 1.f - s, s);
-          d *= gate;
-        }
-        o[0][i] = fmaf(dt[i], v.x, skip[i] * d);
-        o[1][i] = fmaf(uu, v.x, v.y * (1.f / kLog2e)) * slope[i];
-        dD[i] = fmaf(d, uu, dD[i]);
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = tile[at.row][at.quad + i];
+      const float uu = u0.get(i);
+      float dd = dy0.get(i);
+      o[2][i] = 0.f;
+      if (at.z) {
+        const float x = z0.get(i), s = sigmoid(x), gate = x * s;
+        o[2][i] = dd * fmaf(skip[i], uu, v.z) * fmaf(gate, 1.f - s, s);
+        dd *= gate;
+      }
+      o[0][i] = fmaf(dt[i], v.x, skip[i] * dd);
+      o[1][i] = fmaf(uu, v.x, v.y * (1.f / kLog2e)) * slope[i];
+      if (i < n) {
+        dD[i] = fmaf(dd, uu, dD[i]);
         db[i] += o[1][i];
       }
-      Piece<OutT, 8> out;
-      out.set_all(o[0]);
-      store<Wide>(out, dup + t * a.dus.t, n8);
-      out.set_all(o[1]);
-      store<Wide>(out, ddp + t * a.ddts.t, n8);
-      if (zp) {
-        out.set_all(o[2]);
-        store<Wide>(out, dzp + t * a.dzs.t, n8);
-      }
     }
+    Piece<OutT, 4> out;
+    out.set_all(o[0]);
+    store<Wide>(out, dup, n);
+    out.set_all(o[1]);
+    store<Wide>(out, ddp, n);
+    dup -= TT * a.dus.t;
+    ddp -= TT * a.ddts.t;
+    if (at.z) {
+      out.set_all(o[2]);
+      store<Wide>(out, dzp, n);
+      dzp -= TT * a.dzs.t;
+    }
+#pragma unroll
     for (int x = tid; x < TT * 2 * NP; x += 256) {
       const int k = x / (2 * NP), w = x / NP % 2, m = x % NP;
       if (t0 + k < end && m < a.N)
@@ -330,26 +377,27 @@ __global__ __launch_bounds__(256) void ttt_scan_bwd(ScanArgs a) {
             (sbc[0][k][w][m] + sbc[1][k][w][m]) + (sbc[2][k][w][m] + sbc[3][k][w][m]);
     }
   }
-  Piece<OutT, 8> none;
+  Piece<OutT, 4> none;
   none.zero();
-  for (int64_t t = max(begin, end) + row; t < tokens; t += TT) {
-    store<Wide>(none, dup + t * a.dus.t, n8);
-    store<Wide>(none, ddp + t * a.ddts.t, n8);
-    if (zp) store<Wide>(none, dzp + t * a.dzs.t, n8);
+  for (int64_t t = max(begin, end) + at.row; t < tokens; t += TT) {
+    store<Wide>(none, static_cast<OutT*>(a.du) + p.b * a.dus.b + t * a.dus.t + oc, at.n4);
+    store<Wide>(none, static_cast<OutT*>(a.ddt) + p.b * a.ddts.b + t * a.ddts.t + oc, at.n4);
+    if (at.z) store<Wide>(none, static_cast<OutT*>(a.dz) + p.b * a.dzs.b + t * a.dzs.t + oc, at.n4);
   }
   if (seg == 0 && a.dh0) store_states(g, a.dh0 + (static_cast<int64_t>(p.b) * a.D + c) * a.N, a.N, q, on);
   float* sums = a.part + slot * (static_cast<int64_t>(a.D) * (a.N + 2));
   store_states(dA, sums + static_cast<int64_t>(c) * a.N, a.N, q, on);
-  // dD and ddt_bias: over the 32 token rows
+  // dD and ddt_bias: over the token rows
   __syncthreads();
-  float2* rows = reinterpret_cast<float2*>(&tile[0][0]);
+  float2* lines = reinterpret_cast<float2*>(&tile[0][0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) rows[row * CH + oct + i] = make_float2(dD[i], db[i]);
+  for (int i = 0; i < 4; ++i) lines[at.row * CH + at.quad + i] = make_float2(dD[i], db[i]);
   __syncthreads();
   if (tid < p.nc) {
-    float2 s = rows[tid];
+    float2 s = lines[tid];
+#pragma unroll
     for (int r = 1; r < TT; ++r) {
-      const float2 x = rows[r * CH + tid];
+      const float2 x = lines[r * CH + tid];
       s.x += x.x;
       s.y += x.y;
     }

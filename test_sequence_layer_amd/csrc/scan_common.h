@@ -5,7 +5,7 @@
 // A workgroup of four waves holds 64 channels of one sequence; a wave 16 of them, four lanes to a channel, each with NS
 // = N / 4 states in registers for the whole walk.  Tokens go through LDS 32 at a time, where each thread has prepared 8
 // channels of one token (softplus once per token and channel, not once per state); B and C, which all channels of a group
-// share, lie there as fp32.
+// share, lie there as fp32, C behind B.
 #pragma once
 #include "block_common.h"
 
@@ -14,7 +14,7 @@ namespace scan {
 
 using namespace block;
 
-constexpr int CH = kScanCh, TT = kScanTile;
+constexpr int CH = kScanCh;
 
 // The channels of a workgroup and its sequence.
 struct Place {
@@ -80,23 +80,68 @@ __device__ __forceinline__ void lds_floats(float (&x)[NS], const float* p) {
   }
 }
 
-// B or C of a tile as a thread holds it between the load and LDS: elements tid, tid + 256, ... of [TT][4 NS].
-template <typename T, int NS>
-struct Rows {
-  static constexpr int kN = 4 * NS, kEach = TT * kN / 256 > 0 ? TT * kN / 256 : 1;
-  T v[kEach];
-  __device__ __forceinline__ void load(const T* p, int64_t stride, int N, int t0, int t1, int tid) {
+// A thread's pieces of a tile's B and C, four states of a token each, between the load and LDS.  Piece id is B's or C's
+// (id / (NS TT)) of token id / NS % TT, states 4 (id % NS) on.
+template <typename T, int NS, int TT>
+struct BcRows {
+  static constexpr int kEach = (2 * TT * NS + 255) / 256;
+  Piece<T, 4> v[kEach];
+  const T* p[kEach];
+  int64_t step[kEach];  // elements from a tile to the next
+  int t[kEach], n[kEach], lds[kEach];
+  bool wide;
+  __device__ __forceinline__ BcRows(const ScanArgs& a, const Place& at, int first, int tid, bool with_c) {
+    wide = a.bc_wide;
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
-      const int e = tid + 256 * k, t = t0 + e / kN, n = e % kN;
-      v[k] = e < TT * kN && t < t1 && n < N ? p[t * stride + n] : T(0);
+      const int id = tid + 256 * k, w = id / (NS * TT), m = id % NS;
+      t[k] = id / NS % TT;
+      n[k] = w > (with_c ? 1 : 0) ? 0 : min(4, a.N - 4 * m);  // (may be negative)
+      lds[k] = w > 1 ? -1 : (w * TT + t[k]) * 4 * NS + 4 * m;
+      const T* base = static_cast<const T*>(w ? a.Cm : a.Bm) + (w ? at.b * a.cs.b + at.g * a.cs.h : at.b * a.bs.b + at.g * a.bs.h);
+      const int64_t row = w ? a.cs.t : a.bs.t;
+      p[k] = base + (first + t[k]) * row + 4 * m;
+      step[k] = row * TT;
     }
   }
-  __device__ __forceinline__ void stage(float* lds, int tid) const {
+  // the tile that begins at token first, as far as end; then on to the next tile (dir 1) or the one before (-1)
+  __device__ __forceinline__ void load(int first, int end, int dir) {
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
-      const int e = tid + 256 * k;
-      if (e < TT * kN) lds[e] = as_f32(v[k]);
+      const int m = first + t[k] < end ? n[k] : 0;
+      if (wide) {
+        if (m > 0) v[k].load(p[k]);
+        else v[k].zero();
+      } else {
+        v[k].load_some(p[k], m);
+      }
+      p[k] += dir * step[k];
+    }
+  }
+  __device__ __forceinline__ void back() {
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) p[k] -= step[k];
+  }
+  __device__ __forceinline__ void stage(float* bc) const {
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+      if (256 * (k + 1) <= 2 * TT * NS || lds[k] >= 0)
+        *reinterpret_cast<float4*>(bc + lds[k]) = make_float4(v[k].get(0), v[k].get(1), v[k].get(2), v[k].get(3));
+  }
+};
+
+// A group of GS tokens as a lane reads it: dt and dt u of its channel (a pair every ROW floats of its tokens), B and C of its
+// states.
+template <int NS, bool C_, int GS, int TT, int ROW>
+struct Group {
+  float2 d[GS];
+  float B[GS][NS], C[C_ ? GS : 1][NS];
+  __device__ __forceinline__ void read(const float* sd, const float* bc, int k) {
+#pragma unroll
+    for (int j = 0; j < GS; ++j) {
+      d[j] = *reinterpret_cast<const float2*>(sd + (k + j) * ROW);
+      lds_floats(B[j], bc + (k + j) * 4 * NS);
+      if constexpr (C_) lds_floats(C[j], bc + (TT + k + j) * 4 * NS);
     }
   }
 };

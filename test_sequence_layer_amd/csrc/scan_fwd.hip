@@ -12,14 +12,25 @@ namespace {
 
 using namespace scan;
 
+constexpr int TT = kScanTile;
+constexpr int GS = 4;  // tokens whose LDS reads, exps and sums go together
+// Sums over the four lanes of a channel (16 apart) of four tokens' values: lane row r gets token r's.
+__device__ __forceinline__ float row_sums(const float (&y)[4]) {
+  const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(y[0]), __float_as_uint(y[2]), false, false);
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(y[1]), __float_as_uint(y[3]), false, false);
+  const float a = __uint_as_float(p[0]) + __uint_as_float(p[1]), b = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+
 // States: only what the segment adds to a zero state and the sum of its dt.
 template <typename InT, typename OutT, int NS, bool Wide, bool States>
-__global__ __launch_bounds__(256) void ttt_scan_fwd(ScanArgs a) {
+__global__ __launch_bounds__(256, 2) void ttt_scan_fwd(ScanArgs a) {
   constexpr int NP = 4 * NS;
   __shared__ __align__(16) float2 sdt[TT][CH];  // dt, dt u
-  __shared__ __align__(16) float sB[TT * NP], sC[States ? 4 : TT * NP];
+  __shared__ __align__(16) float bc[2 * TT * NP];
   __shared__ __align__(16) float sy[States ? 1 : TT][CH];
-  const int tid = threadIdx.x, lane = tid & 63, q = lane & 3, cw = (tid >> 6) * 16 + (lane >> 2);
+  const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, cw = (tid >> 6) * 16 + (lane & 15);
   const int segs = States ? a.nseg - 1 : a.nseg;
   const int seg = static_cast<int>(blockIdx.x % segs);
   const Place p = place(a, blockIdx.x / segs);
@@ -38,89 +49,98 @@ __global__ __launch_bounds__(256) void ttt_scan_fwd(ScanArgs a) {
   // this thread's piece of a tile: token row, channels oct .. oct + 7
   const int row = tid >> 3, oct = (tid & 7) * 8;
   const int n8 = min(8, p.nc - oct);  // (may be negative)
-  const InT* up = static_cast<const InT*>(a.u) + p.b * a.us.b + p.c0 + oct;
-  const InT* dp = static_cast<const InT*>(a.dt) + p.b * a.dts.b + p.c0 + oct;
-  const InT* zp = a.z ? static_cast<const InT*>(a.z) + p.b * a.zs.b + p.c0 + oct : nullptr;
-  const InT* bp = static_cast<const InT*>(a.Bm) + p.b * a.bs.b + p.g * a.bs.h;
-  const InT* cp = static_cast<const InT*>(a.Cm) + p.b * a.cs.b + p.g * a.cs.h;
-  OutT* yp = static_cast<OutT*>(a.y) + p.b * a.ys.b + p.c0 + oct;
+  const int64_t first = begin + row;
+  const InT* up = static_cast<const InT*>(a.u) + p.b * a.us.b + first * a.us.t + p.c0 + oct;
+  const InT* dp = static_cast<const InT*>(a.dt) + p.b * a.dts.b + first * a.dts.t + p.c0 + oct;
+  const InT* zp = a.z ? static_cast<const InT*>(a.z) + p.b * a.zs.b + first * a.zs.t + p.c0 + oct : nullptr;
+  OutT* yp = static_cast<OutT*>(a.y) + p.b * a.ys.b + first * a.ys.t + p.c0 + oct;
   float bias[8], skip[8];
   params<8>(bias, a.dt_bias ? a.dt_bias + p.c0 + oct : nullptr, n8, 0.f);
   if constexpr (!States) params<8>(skip, a.Dskip ? a.Dskip + p.c0 + oct : nullptr, n8, 0.f);
 
   Piece<InT, 8> u, dt, z;
-  Rows<InT, NS> rb, rc;
+  BcRows<InT, NS, TT> rows(a, p, begin, tid, !States);
   auto fetch = [&](int t0) {
-    const int64_t t = t0 + row;
-    const int n = t < end ? n8 : 0;
-    load<Wide>(u, up + t * a.us.t, n);
-    load<Wide>(dt, dp + t * a.dts.t, n);
-    rb.load(bp, a.bs.t, a.N, t0, end, tid);
-    if constexpr (!States) rc.load(cp, a.cs.t, a.N, t0, end, tid);
+    const int n = t0 + row < end ? n8 : 0;
+    load<Wide>(u, up, n);
+    load<Wide>(dt, dp, n);
+    up += TT * a.us.t;
+    dp += TT * a.dts.t;
+    rows.load(t0, end, 1);
   };
   float sum = 0.f;
   fetch(begin);
   for (int t0 = begin; t0 < end; t0 += TT) {
-    const int64_t t = t0 + row;
-    const bool live = t < end;
+    const int n = t0 + row < end ? n8 : 0;
+    float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      float x[2];
+    for (int i = 0; i < 8; ++i) x[i] = dt.get(i) + bias[i];
+    if (a.softplus) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float s = dt.get(i + j) + bias[i + j], slope;
-        if (a.softplus) s = softplus(s, slope);
-        x[j] = live && i + j < n8 ? s : 0.f;
-      }
-      *reinterpret_cast<float4*>(&sdt[row][oct + i]) = make_float4(x[0], x[0] * u.get(i), x[1], x[1] * u.get(i + 1));
+      for (int i = 0; i < 8; ++i) x[i] = softplus(x[i]);
     }
-    rb.stage(sB, tid);
-    if constexpr (!States) rc.stage(sC, tid);
-    Piece<InT, 8> u0 = u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i >= (Wide ? (n > 0 ? 8 : 0) : n)) x[i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+      *reinterpret_cast<float4*>(&sdt[row][oct + i]) = make_float4(x[i], x[i] * u.get(i), x[i + 1], x[i + 1] * u.get(i + 1));
+    rows.stage(bc);
+    const Piece<InT, 8> u0 = u;
     if constexpr (!States) {
-      if (zp) load<Wide>(z, zp + t * a.zs.t, live ? n8 : 0);
+      if (zp) {
+        load<Wide>(z, zp, n);
+        zp += TT * a.zs.t;
+      }
     }
     __syncthreads();
     if (t0 + TT < end) fetch(t0 + TT);
-#pragma unroll 8
-    for (int k = 0; k < TT; ++k) {
-      const float2 d = sdt[k][cw];
-      float Bv[NS], Cv[NS], s = 0.f;
-      lds_floats(Bv, sB + k * NP + q * NS);
-      if constexpr (!States) lds_floats(Cv, sC + k * NP + q * NS);
+    const float* sd = &sdt[0][cw].x;
+    const float* sb = bc + q * NS;
+    // the next group's reads are on their way while this one is worked on (with 8 states registers would spill)
+    constexpr int kBuf = NS <= 4 ? 2 : 1;
+    Group<NS, !States, GS, TT, 2 * CH> g[kBuf];
+    if constexpr (kBuf == 2) g[0].read(sd, sb, 0);
+#pragma unroll 2
+    for (int k = 0; k < TT; k += GS) {
+      auto& now = g[k / GS % kBuf];
+      if constexpr (kBuf == 1) now.read(sd, sb, k);
+      else if (k + GS < TT) g[(k / GS + 1) % kBuf].read(sd, sb, k + GS);
+      float e[GS][NS], y[GS];
 #pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        h[i] = fmaf(__builtin_amdgcn_exp2f(d.x * a2[i]), h[i], d.y * Bv[i]);
-        if constexpr (!States) s = fmaf(Cv[i], h[i], s);
+      for (int j = 0; j < GS; ++j)
+#pragma unroll
+        for (int i = 0; i < NS; ++i) e[j][i] = __builtin_amdgcn_exp2f(now.d[j].x * a2[i]);
+#pragma unroll
+      for (int j = 0; j < GS; ++j) {
+        y[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          h[i] = fmaf(e[j][i], h[i], now.d[j].y * now.B[j][i]);
+          if constexpr (!States) y[j] = fmaf(now.C[j][i], h[i], y[j]);
+        }
+        if constexpr (States) sum += now.d[j].x;
       }
-      if constexpr (States) {
-        sum += d.x;
-      } else {
-        s = quad_sum(s);
-        if (q == 0) sy[k][cw] = s;
-      }
+      if constexpr (!States) sy[k + q][cw] = row_sums(y);
     }
     __syncthreads();
     if constexpr (!States) {
-      if (live && n8 > 0) {
-        float y[8];
+      float y[8];
 #pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(&sy[row][oct + i]);
-          y[i] = v.x; y[i + 1] = v.y; y[i + 2] = v.z; y[i + 3] = v.w;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          y[i] = fmaf(skip[i], u0.get(i), y[i]);
-          if (zp) {
-            const float x = z.get(i);
-            y[i] *= x * sigmoid(x);
-          }
-        }
-        Piece<OutT, 8> out;
-        out.set_all(y);
-        store<Wide>(out, yp + t * a.ys.t, n8);
+      for (int i = 0; i < 8; i += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(&sy[row][oct + i]);
+        y[i] = v.x; y[i + 1] = v.y; y[i + 2] = v.z; y[i + 3] = v.w;
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = fmaf(skip[i], u0.get(i), y[i]);
+      if (zp) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] *= z.get(i) * sigmoid(z.get(i));
+      }
+      Piece<OutT, 8> out;
+      out.set_all(y);
+      store<Wide>(out, yp, n);
+      yp += TT * a.ys.t;
     }
   }
   const int64_t slot = static_cast<int64_t>(p.b) * a.nseg + seg;
@@ -133,9 +153,11 @@ __global__ __launch_bounds__(256) void ttt_scan_fwd(ScanArgs a) {
     }
   } else {
     if (seg == a.nseg - 1) store_states(h, a.h_final + (static_cast<int64_t>(p.b) * a.D + c) * a.N, a.N, q, on);
+    // rows behind the sequence's end (those of its last tile too)
+    OutT* y0 = static_cast<OutT*>(a.y) + p.b * a.ys.b + p.c0 + oct;
     Piece<OutT, 8> none;
     none.zero();
-    for (int64_t t = max(begin, end) + row; t < tokens; t += TT) store<Wide>(none, yp + t * a.ys.t, n8);
+    for (int64_t t = max(begin, end) + row; t < tokens; t += TT) store<Wide>(none, y0 + t * a.ys.t, n8);
   }
 }
 
