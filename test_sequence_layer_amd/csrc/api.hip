@@ -2074,7 +2074,7 @@ ttt_status validate_scan_fwd(const ttt_selective_scan_desc* d, const void* u, co
   if (st != TTT_OK) return st;
   ScanPlan plan = scan_plan(d, false);
   if (decode) plan.bytes = 0;
-  if (decode ? static_cast<int64_t>(d->B) * d->D * 4 > kMaxThreads : plan.blocks * plan.nseg * 256 > kMaxThreads)
+  if (decode ? static_cast<int64_t>(d->B) * d->D * 4 > kMaxThreads : plan.blocks * plan.nseg * 512 > kMaxThreads)
     return TTT_ERR_SHAPE;
   if (d->B == 0) return TTT_OK;
   if (!A || !h) return TTT_ERR_NULL;

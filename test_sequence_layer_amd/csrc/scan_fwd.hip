@@ -24,26 +24,80 @@ __device__ __forceinline__ float row_sums(const float (&y)[4]) {
 }
 
 // States: only what the segment adds to a zero state and the sum of its dt.
-// One tile's walk, the next tile's way into LDS and the last one's way out (each a third of the instructions or less) are
-// one stretch of code without a branch: with one wave to a SIMD, which is what a few thousand channels give, there is no
-// other wave to fill the cycles that a walk's dependent steps leave.
+// Waves 0 to 3 walk a tile while waves 4 to 7 bring the next one into LDS (softplus) and take the last one out (D u, the
+// gate): with 64 channels to a workgroup a few thousand channels give one walking wave to a SIMD, and a wave alone leaves a
+// third of the issue cycles empty.  One barrier a tile.
 template <typename InT, typename OutT, int NS, bool Wide, bool States>
-__global__ __launch_bounds__(256, 2) void ttt_scan_fwd(ScanArgs a) {
+__global__ __launch_bounds__(512, 2) void ttt_scan_fwd(ScanArgs a) {
   constexpr int NP = 4 * NS;
   __shared__ __align__(16) float2 sdt[2][TT][CH];  // dt, dt u
   __shared__ __align__(16) float bc[2][2 * TT * NP];
   __shared__ __align__(16) float sy[States ? 1 : 2][States ? 1 : TT][CH];
-  __shared__ __align__(16) float par[2][CH];  // dt_bias, D
-  const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, cw = (tid >> 6) * 16 + (lane & 15);
   const int segs = States ? a.nseg - 1 : a.nseg;
   const int seg = static_cast<int>(blockIdx.x % segs);
   const Place p = place(a, blockIdx.x / segs);
-  const int c = p.c0 + cw;
-  const bool on = cw < p.nc;
   const int begin = seg * a.seglen, tokens = min(a.T, begin + a.seglen), end = min(p.len, tokens);
+  const int64_t slot = static_cast<int64_t>(p.b) * a.nseg + seg;
+
+  if (__builtin_amdgcn_readfirstlane(threadIdx.x >> 8) == 0) {
+    const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, cw = (tid >> 6) * 16 + (lane & 15);
+    const int c = p.c0 + cw;
+    const bool on = cw < p.nc;
+    float a2[NS], h[NS], sum = 0.f;
+    decays(a2, a, c, q, on);
+    if (States || a.nseg == 1) {
+      load_states(h, States || !a.h0 ? nullptr : a.h0 + (static_cast<int64_t>(p.b) * a.D + c) * a.N, a.N, q, on);
+    } else {
+      start_state(h, a2, a, p, seg, c, q, on);
+    }
+    int buf = 0;
+    for (int t0 = begin; t0 < end; t0 += TT, buf ^= 1) {
+      __syncthreads();
+      const float* sd = &sdt[buf][0][cw].x;
+      const float* sb = bc[buf] + q * NS;
+      // the next group's reads are on their way while this one is worked on (with 8 states registers would spill)
+      constexpr int kBuf = NS <= 4 ? 2 : 1;
+      Group<NS, !States, GS, TT, 2 * CH> g[kBuf];
+      if constexpr (kBuf == 2) g[0].read(sd, sb, 0);
+#pragma unroll
+      for (int k = 0; k < TT; k += GS) {
+        auto& now = g[k / GS % kBuf];
+        if constexpr (kBuf == 1) now.read(sd, sb, k);
+        else if (k + GS < TT) g[(k / GS + 1) % kBuf].read(sd, sb, k + GS);
+        float e[GS][NS], y[GS];
+#pragma unroll
+        for (int j = 0; j < GS; ++j)
+#pragma unroll
+          for (int i = 0; i < NS; ++i) e[j][i] = __builtin_amdgcn_exp2f(now.d[j].x * a2[i]);
+#pragma unroll
+        for (int j = 0; j < GS; ++j) {
+          y[j] = 0.f;
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            h[i] = fmaf(e[j][i], h[i], now.d[j].y * now.B[j][i]);
+            if constexpr (!States) y[j] = fmaf(now.C[j][i], h[i], y[j]);
+          }
+          if constexpr (States) sum += now.d[j].x;
+        }
+        if constexpr (!States) sy[buf][k + q][cw] = row_sums(y);
+      }
+    }
+    __syncthreads();
+    if constexpr (States) {
+      store_states(h, a.hseg + ((slot + 1) * a.D + c) * a.N, a.N, q, on);
+      if (on && q == 0) a.sseg[slot * a.D + c] = sum;
+      if (seg == 0) {
+        load_states(h, a.h0 ? a.h0 + (static_cast<int64_t>(p.b) * a.D + c) * a.N : nullptr, a.N, q, on);
+        store_states(h, a.hseg + (slot * a.D + c) * a.N, a.N, q, on);
+      }
+    } else {
+      if (seg == a.nseg - 1) store_states(h, a.h_final + (static_cast<int64_t>(p.b) * a.D + c) * a.N, a.N, q, on);
+    }
+    return;
+  }
 
   // this thread's piece of a tile: token row, channels oct .. oct + 7
-  const int row = tid >> 3, oct = (tid & 7) * 8;
+  const int tid = threadIdx.x & 255, row = tid >> 3, oct = (tid & 7) * 8;
   const int n8 = min(8, p.nc - oct);  // (may be negative)
   const int64_t first = begin + row;
   const InT* up = static_cast<const InT*>(a.u) + p.b * a.us.b + first * a.us.t + p.c0 + oct;
@@ -51,10 +105,9 @@ __global__ __launch_bounds__(256, 2) void ttt_scan_fwd(ScanArgs a) {
   const InT* zp = States || !a.z ? nullptr : static_cast<const InT*>(a.z) + p.b * a.zs.b + first * a.zs.t + p.c0 + oct;
   OutT* yp = static_cast<OutT*>(a.y) + p.b * a.ys.b + first * a.ys.t + p.c0 + oct;
   BcRows<InT, NS, TT> next(a, p, begin, tid, !States);
-  if (tid < 2 * CH) {
-    const float* src = tid < CH ? a.dt_bias : a.Dskip;
-    par[tid / CH][tid % CH] = src && tid % CH < p.nc ? src[p.c0 + tid % CH] : 0.f;
-  }
+  float bias[8], skip[8];
+  params<8>(bias, a.dt_bias ? a.dt_bias + p.c0 + oct : nullptr, n8, 0.f);
+  if constexpr (!States) params<8>(skip, a.Dskip ? a.Dskip + p.c0 + oct : nullptr, n8, 0.f);
   // u of the tile before, this one, the next and the one behind it; the others' as far as they are wanted
   Piece<InT, 8> u_old, u_now, u_next, u_far, dt_next, dt_far, z_old, z_now;
   auto fetch = [&](int t0) {
@@ -65,60 +118,56 @@ __global__ __launch_bounds__(256, 2) void ttt_scan_fwd(ScanArgs a) {
     dp += TT * a.dts.t;
     next.load(t0, end, 1);
   };
-  // channels i and i + 1 of the next tile's token
-  auto stage = [&](int buf, int i, int n) {
-    float x[2];
-    const float2 b = *reinterpret_cast<const float2*>(&par[0][oct + i]);
+  auto stage = [&](int buf, int n) {
+    float x[8];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      x[j] = dt_next.get(i + j) + (j ? b.y : b.x);
-      const float s = softplus(x[j]);
-      x[j] = a.softplus ? s : x[j];
-      x[j] = (Wide ? n > 0 : i + j < n) ? x[j] : 0.f;
-    }
-    *reinterpret_cast<float4*>(&sdt[buf][row][oct + i]) = make_float4(x[0], x[0] * u_next.get(i), x[1], x[1] * u_next.get(i + 1));
-  };
-  float out[8];
-  auto finish = [&](int buf, int i) {
-    const float2 s = *reinterpret_cast<const float2*>(&sy[buf][row][oct + i]);
-    const float2 k = *reinterpret_cast<const float2*>(&par[1][oct + i]);
+    for (int i = 0; i < 8; ++i) x[i] = dt_next.get(i) + bias[i];
+    if (a.softplus) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float z = z_old.get(i + j), g = z * sigmoid(z);
-      const float y = fmaf(j ? k.y : k.x, u_old.get(i + j), j ? s.y : s.x);
-      out[i + j] = y * (zp ? g : 1.f);
+      for (int i = 0; i < 8; ++i) x[i] = softplus(x[i]);
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = (Wide ? n > 0 : i < n) ? x[i] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+      *reinterpret_cast<float4*>(&sdt[buf][row][oct + i]) = make_float4(x[i], x[i] * u_next.get(i), x[i + 1], x[i + 1] * u_next.get(i + 1));
   };
-
-  float a2[NS], h[NS];
-  decays(a2, a, c, q, on);
-  if (begin < end) fetch(begin);
-  if (States || a.nseg == 1) {
-    load_states(h, States || !a.h0 ? nullptr : a.h0 + (static_cast<int64_t>(p.b) * a.D + c) * a.N, a.N, q, on);
-  } else {
-    start_state(h, a2, a, p, seg, c, q, on);
-  }
-  __syncthreads();
-  float sum = 0.f;
+  auto finish = [&](int buf, int n) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(&sy[buf][row][oct + i]);
+      y[i] = v.x; y[i + 1] = v.y; y[i + 2] = v.z; y[i + 3] = v.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = fmaf(skip[i], u_old.get(i), y[i]);
+    if (zp) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] *= z_old.get(i) * sigmoid(z_old.get(i));
+    }
+    Piece<OutT, 8> out;
+    out.set_all(y);
+    store<Wide>(out, yp, n);
+    yp += TT * a.ys.t;
+  };
   if (begin < end) {
+    fetch(begin);
     u_next = u_far;
     dt_next = dt_far;
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) stage(0, i, begin + row < end ? n8 : 0);
+    stage(0, begin + row < end ? n8 : 0);
     next.stage(bc[0]);
     if (begin + TT < end) fetch(begin + TT);
   }
-  u_now = u_old = u_next;
+  u_now = u_next;
   z_now.zero();
   int buf = 0;
   for (int t0 = begin; t0 < end; t0 += TT, buf ^= 1) {
+    __syncthreads();
     u_old = u_now;
     u_now = u_next;
     u_next = u_far;
     dt_next = dt_far;
     z_old = z_now;
-    const int n = t0 + TT + row < end ? n8 : 0;
-    __syncthreads();
     next.stage(bc[buf ^ 1]);
     if (t0 + 2 * TT < end) fetch(t0 + 2 * TT);
     if constexpr (!States) {
@@ -127,71 +176,19 @@ __global__ __launch_bounds__(256, 2) void ttt_scan_fwd(ScanArgs a) {
         zp += TT * a.zs.t;
       }
     }
-    const float* sd = &sdt[buf][0][cw].x;
-    const float* sb = bc[buf] + q * NS;
-    // the next group's reads are on their way while this one is worked on (with 8 states registers would spill)
-    constexpr int kBuf = NS <= 4 ? 2 : 1;
-    Group<NS, !States, GS, TT, 2 * CH> g[kBuf];
-    if constexpr (kBuf == 2) g[0].read(sd, sb, 0);
-#pragma unroll
-    for (int k = 0; k < TT; k += GS) {
-      auto& now = g[k / GS % kBuf];
-      if constexpr (kBuf == 1) now.read(sd, sb, k);
-      else if (k + GS < TT) g[(k / GS + 1) % kBuf].read(sd, sb, k + GS);
-      float e[GS][NS], y[GS];
-#pragma unroll
-      for (int j = 0; j < GS; ++j)
-#pragma unroll
-        for (int i = 0; i < NS; ++i) e[j][i] = __builtin_amdgcn_exp2f(now.d[j].x * a2[i]);
-      if (k / GS % 2 == 0) {
-        stage(buf ^ 1, k / GS, n);
-      } else if constexpr (!States) {
-        finish(buf ^ 1, k / GS - 1);
-      }
-#pragma unroll
-      for (int j = 0; j < GS; ++j) {
-        y[j] = 0.f;
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          h[i] = fmaf(e[j][i], h[i], now.d[j].y * now.B[j][i]);
-          if constexpr (!States) y[j] = fmaf(now.C[j][i], h[i], y[j]);
-        }
-        if constexpr (States) sum += now.d[j].x;
-      }
-      if constexpr (!States) sy[buf][k + q][cw] = row_sums(y);
-    }
+    stage(buf ^ 1, t0 + TT + row < end ? n8 : 0);
     if constexpr (!States) {
-      if (t0 > begin) {
-        Piece<OutT, 8> o;
-        o.set_all(out);
-        store<Wide>(o, yp, n8);
-        yp += TT * a.ys.t;
-      }
+      if (t0 > begin) finish(buf ^ 1, n8);
     }
   }
+  __syncthreads();
   if constexpr (!States) {
-    __syncthreads();
     if (begin < end) {
       u_old = u_now;
       z_old = z_now;
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) finish(buf ^ 1, i);
-      Piece<OutT, 8> o;
-      o.set_all(out);
       const int last = begin + (end - begin - 1) / TT * TT;
-      store<Wide>(o, yp, last + row < end ? n8 : 0);
+      finish(buf ^ 1, last + row < end ? n8 : 0);
     }
-  }
-  const int64_t slot = static_cast<int64_t>(p.b) * a.nseg + seg;
-  if constexpr (States) {
-    store_states(h, a.hseg + ((slot + 1) * a.D + c) * a.N, a.N, q, on);
-    if (on && q == 0) a.sseg[slot * a.D + c] = sum;
-    if (seg == 0) {
-      load_states(h, a.h0 ? a.h0 + (static_cast<int64_t>(p.b) * a.D + c) * a.N : nullptr, a.N, q, on);
-      store_states(h, a.hseg + (slot * a.D + c) * a.N, a.N, q, on);
-    }
-  } else {
-    if (seg == a.nseg - 1) store_states(h, a.h_final + (static_cast<int64_t>(p.b) * a.D + c) * a.N, a.N, q, on);
     // rows behind the sequence's end (those of its last tile too)
     OutT* y0 = static_cast<OutT*>(a.y) + p.b * a.ys.b + p.c0 + oct;
     Piece<OutT, 8> none;
@@ -257,11 +254,11 @@ hipError_t go(Which which, const ScanArgs& a, hipStream_t s) {
   const int dg = a.D / a.G, segs = which == STATES ? a.nseg - 1 : a.nseg;
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.B) * a.G * ((dg + CH - 1) / CH) * segs);
   if (which == STATES) {
-    if (a.wide) ttt_scan_fwd<InT, float, NS, true, true><<<grid, 256, 0, s>>>(a);
-    else ttt_scan_fwd<InT, float, NS, false, true><<<grid, 256, 0, s>>>(a);
+    if (a.wide) ttt_scan_fwd<InT, float, NS, true, true><<<grid, 512, 0, s>>>(a);
+    else ttt_scan_fwd<InT, float, NS, false, true><<<grid, 512, 0, s>>>(a);
   } else {
-    if (a.wide) ttt_scan_fwd<InT, OutT, NS, true, false><<<grid, 256, 0, s>>>(a);
-    else ttt_scan_fwd<InT, OutT, NS, false, false><<<grid, 256, 0, s>>>(a);
+    if (a.wide) ttt_scan_fwd<InT, OutT, NS, true, false><<<grid, 512, 0, s>>>(a);
+    else ttt_scan_fwd<InT, OutT, NS, false, false><<<grid, 512, 0, s>>>(a);
   }
   return hipGetLastError();
 }
