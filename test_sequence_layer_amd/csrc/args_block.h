@@ -104,7 +104,7 @@ struct RowSumArgs {
 constexpr int kScanCh = 64;     // channels of a workgroup
 constexpr int kScanTile = 32;   // tokens staged at a time
 
-int scan_states(int N);         // states a thread holds; 0: not supported
+int scan_states(int N, int lanes);  // states a lane holds with so many lanes to a channel; 0: not supported
 int scan_chunk(int N);          // tokens between checkpoints
 hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t s);
 hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t s);

@@ -110,13 +110,9 @@ constexpr float kLog2e = 1.44269504088896340736f;
 
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
-// 1 / (1 + e^-x), from e^-|x| so that neither end loses digits.  v_exp_f32 and v_rcp_f32 are good to 1 ulp; x log2(e) is
-// rounded, which shows where |x| is large: |x| 2^-24 of the result.
-__device__ __forceinline__ float sigmoid(float x) {
-  const float e = fast_exp(-fabsf(x));
-  const float r = __builtin_amdgcn_rcpf(1.f + e);
-  return x >= 0.f ? r : e * r;
-}
+// 1 / (1 + e^-x).  v_exp_f32 and v_rcp_f32 are good to 1 ulp; x log2(e) is rounded, which shows where the result is e^x:
+// |x| 2^-24 of it.  Below x = -88 e^-x is infinite and the result 0.
+__device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * x)); }
 
 // log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x| <= 1, and its slope, the sigmoid.  log(1 + e) = 2 artanh(s) with
 // s = e / (2 + e) <= 1/3, and 2 artanh(s) / s a polynomial of degree 4 in s^2 (its interpolation at Chebyshev points of

@@ -96,7 +96,7 @@ __global__ __launch_bounds__(256, 2) void ttt_scan_bwd_states(ScanArgs a) {
 #pragma unroll
   for (int i = 0; i < NS; ++i) h[i] = g[i] = 0.f, prod[i] = 1.f;
   Lines<InT, OutT> at(a, p, begin, tid);
-  BcRows<InT, NS, TT> rows(a, p, begin, tid, true);
+  BcRows<InT, NP, TT> rows(a, p, begin, tid, true);
   float bias[4];
   params<4>(bias, a.dt_bias ? a.dt_bias + p.c0 + at.quad : nullptr, at.n4, 0.f);
   for (int t0 = begin; t0 < end; t0 += TT) {
@@ -172,7 +172,7 @@ __global__ __launch_bounds__(256, 2) void ttt_scan_bwd(ScanArgs a) {
   else start_state(h, a2, a, p, seg, c, q, on);
 
   Lines<InT, OutT> at(a, p, begin, tid);
-  BcRows<InT, NS, TT> rows(a, p, begin, tid, true);
+  BcRows<InT, NP, TT> rows(a, p, begin, tid, true);
   float bias[4];
   params<4>(bias, a.dt_bias ? a.dt_bias + p.c0 + at.quad : nullptr, at.n4, 0.f);
   const int64_t ckstep = static_cast<int64_t>(a.D) * a.N;
@@ -220,7 +220,7 @@ __global__ __launch_bounds__(256, 2) void ttt_scan_bwd(ScanArgs a) {
       if (k0 + CL >= TT && t0 >= last) break;  // (nobody asks for the state behind the last chunk)
 #pragma unroll
       for (int k = k0; k < k0 + CL; k += GS) {
-        Group<NS, false, GS, TT, 4 * CH> g;
+        Group<NS, false, GS, TT, NP, 4 * CH> g;
         g.read(sd, sb, k);
         float e[GS][NS];
 #pragma unroll
@@ -444,7 +444,7 @@ hipError_t go(bool states, const ScanArgs& a, hipStream_t s) {
 
 template <typename InT, typename OutT>
 hipError_t go(bool states, const ScanArgs& a, hipStream_t s) {
-  switch (scan_states(a.N)) {
+  switch (scan_states(a.N, 4)) {
     case 1: return go<InT, OutT, 1>(states, a, s);
     case 2: return go<InT, OutT, 2>(states, a, s);
     case 4: return go<InT, OutT, 4>(states, a, s);
@@ -463,7 +463,7 @@ hipError_t go(bool states, const ScanArgs& a, hipStream_t s) {
 
 }  // namespace
 
-int scan_chunk(int N) { return scan_states(N) <= 4 ? kChunk<4> : kChunk<8>; }
+int scan_chunk(int N) { return scan_states(N, 4) <= 4 ? kChunk<4> : kChunk<8>; }
 
 hipError_t launch_scan_bwd_states(const ScanArgs& a, hipStream_t s) { return go(true, a, s); }
 hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t s) { return go(false, a, s); }

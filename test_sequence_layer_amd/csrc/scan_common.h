@@ -2,10 +2,10 @@
 //
 //   h_t[c,n] = exp(dt_t[c] A[c,n]) h_{t-1}[c,n] + dt_t[c] B_t[n] u_t[c],   y_t[c] = sum_n C_t[n] h_t[c,n] + D[c] u_t[c]
 //
-// A workgroup of four waves holds 64 channels of one sequence; a wave 16 of them, four lanes to a channel, each with NS
-// = N / 4 states in registers for the whole walk.  Tokens go through LDS 32 at a time, where each thread has prepared 8
-// channels of one token (softplus once per token and channel, not once per state); B and C, which all channels of a group
-// share, lie there as fp32, C behind B.
+// A workgroup holds 64 channels of one sequence, several lanes to a channel, each with NS states in registers for the whole
+// walk.  Tokens go through LDS a tile at a time, where each thread has prepared some channels of one token (softplus once
+// per token and channel, not once per state); B and C, which all channels of a group share, lie there as fp32, C behind B,
+// NP states each, zeros from N on.
 #pragma once
 #include "block_common.h"
 
@@ -81,10 +81,10 @@ __device__ __forceinline__ void lds_floats(float (&x)[NS], const float* p) {
 }
 
 // A thread's pieces of a tile's B and C, four states of a token each, between the load and LDS.  Piece id is B's or C's
-// (id / (NS TT)) of token id / NS % TT, states 4 (id % NS) on.
-template <typename T, int NS, int TT>
+// (id / (NQ TT)) of token id / NQ % TT, states 4 (id % NQ) on, for 256 threads.
+template <typename T, int NP, int TT>
 struct BcRows {
-  static constexpr int kEach = (2 * TT * NS + 255) / 256;
+  static constexpr int NQ = NP / 4, kEach = (2 * TT * NQ + 255) / 256;
   Piece<T, 4> v[kEach];
   const T* p[kEach];
   int64_t step[kEach];  // elements from a tile to the next
@@ -94,10 +94,10 @@ struct BcRows {
     wide = a.bc_wide;
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
-      const int id = tid + 256 * k, w = id / (NS * TT), m = id % NS;
-      t[k] = id / NS % TT;
+      const int id = tid + 256 * k, w = id / (NQ * TT), m = id % NQ;
+      t[k] = id / NQ % TT;
       n[k] = w > (with_c ? 1 : 0) ? 0 : min(4, a.N - 4 * m);  // (may be negative)
-      lds[k] = w > 1 ? -1 : (w * TT + t[k]) * 4 * NS + 4 * m;
+      lds[k] = w > 1 ? -1 : (w * TT + t[k]) * NP + 4 * m;
       const T* base = static_cast<const T*>(w ? a.Cm : a.Bm) + (w ? at.b * a.cs.b + at.g * a.cs.h : at.b * a.bs.b + at.g * a.bs.h);
       const int64_t row = w ? a.cs.t : a.bs.t;
       p[k] = base + (first + t[k]) * row + 4 * m;
@@ -125,14 +125,14 @@ struct BcRows {
   __device__ __forceinline__ void stage(float* bc) const {
 #pragma unroll
     for (int k = 0; k < kEach; ++k)
-      if (256 * (k + 1) <= 2 * TT * NS || lds[k] >= 0)
+      if (256 * (k + 1) <= 2 * TT * NQ || lds[k] >= 0)
         *reinterpret_cast<float4*>(bc + lds[k]) = make_float4(v[k].get(0), v[k].get(1), v[k].get(2), v[k].get(3));
   }
 };
 
 // A group of GS tokens as a lane reads it: dt and dt u of its channel (a pair every ROW floats of its tokens), B and C of its
-// states.
-template <int NS, bool C_, int GS, int TT, int ROW>
+// NS states.
+template <int NS, bool C_, int GS, int TT, int NP, int ROW>
 struct Group {
   float2 d[GS];
   float B[GS][NS], C[C_ ? GS : 1][NS];
@@ -140,8 +140,8 @@ struct Group {
 #pragma unroll
     for (int j = 0; j < GS; ++j) {
       d[j] = *reinterpret_cast<const float2*>(sd + (k + j) * ROW);
-      lds_floats(B[j], bc + (k + j) * 4 * NS);
-      if constexpr (C_) lds_floats(C[j], bc + (TT + k + j) * 4 * NS);
+      lds_floats(B[j], bc + (k + j) * NP);
+      if constexpr (C_) lds_floats(C[j], bc + (TT + k + j) * NP);
     }
   }
 };

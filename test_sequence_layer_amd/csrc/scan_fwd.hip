@@ -5,6 +5,8 @@
 //
 // Per token, channel and state one exp, two products and two multiply-adds: 24 issue cycles a wave of 64 (v_exp_f32 takes 8,
 // measured), against (with N = 16) half a byte: vector issue is the bound.
+#include <utility>
+
 #include "scan_common.h"
 
 namespace ttt {
@@ -13,7 +15,11 @@ namespace {
 using namespace scan;
 
 constexpr int TT = kScanTile;
-constexpr int GS = 4;  // tokens whose LDS reads, exps and sums go together
+constexpr int LANES = 4;                      // to a channel
+constexpr int WALKERS = CH * LANES;           // threads that walk
+constexpr int THREADS = WALKERS + 256;        // and those that bring the tiles in and out
+constexpr int GS = 4;                         // tokens whose decays and sums go together
+
 // Sums over the four lanes of a channel (16 apart) of four tokens' values: lane row r gets token r's.
 __device__ __forceinline__ float row_sums(const float (&y)[4]) {
   const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(y[0]), __float_as_uint(y[2]), false, false);
@@ -23,13 +29,26 @@ __device__ __forceinline__ float row_sums(const float (&y)[4]) {
   return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
 
+// f(0) .. f(N - 1) with constants for arguments
+template <typename F, int... I>
+__device__ __forceinline__ void each(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F&& f) {
+  each(f, std::make_integer_sequence<int, N>{});
+}
+
 // States: only what the segment adds to a zero state and the sum of its dt.
 // Waves 0 to 3 walk a tile while waves 4 to 7 bring the next one into LDS (softplus) and take the last one out (D u, the
-// gate): with 64 channels to a workgroup a few thousand channels give one walking wave to a SIMD, and a wave alone leaves a
-// third of the issue cycles empty.  One barrier a tile.
+// gate), one barrier a tile: a wave by itself issues a vector instruction every 5 cycles and one that needs the last one's
+// result every 8 (measured; two waves to a SIMD every 4), and 64 channels to a workgroup often leave one workgroup to a CU.
+// The 16 channels of a lane row share their B, so that a lane reads one state of one token, and all of the row take it from
+// there by a broadcast inside the multiplication (DPP): four states of B and C for each token and lane kept LDS busy for more
+// than half of the time.
 template <typename InT, typename OutT, int NS, bool Wide, bool States>
-__global__ __launch_bounds__(512, 2) void ttt_scan_fwd(ScanArgs a) {
-  constexpr int NP = 4 * NS;
+__global__ __launch_bounds__(THREADS, 2) void ttt_scan_fwd(ScanArgs a) {
+  constexpr int NP = LANES * NS;
   __shared__ __align__(16) float2 sdt[2][TT][CH];  // dt, dt u
   __shared__ __align__(16) float bc[2][2 * TT * NP];
   __shared__ __align__(16) float sy[States ? 1 : 2][States ? 1 : TT][CH];
@@ -39,7 +58,7 @@ __global__ __launch_bounds__(512, 2) void ttt_scan_fwd(ScanArgs a) {
   const int begin = seg * a.seglen, tokens = min(a.T, begin + a.seglen), end = min(p.len, tokens);
   const int64_t slot = static_cast<int64_t>(p.b) * a.nseg + seg;
 
-  if (__builtin_amdgcn_readfirstlane(threadIdx.x >> 8) == 0) {
+  if (__builtin_amdgcn_readfirstlane(threadIdx.x) < WALKERS) {
     const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, cw = (tid >> 6) * 16 + (lane & 15);
     const int c = p.c0 + cw;
     const bool on = cw < p.nc;
@@ -53,34 +72,44 @@ __global__ __launch_bounds__(512, 2) void ttt_scan_fwd(ScanArgs a) {
     int buf = 0;
     for (int t0 = begin; t0 < end; t0 += TT, buf ^= 1) {
       __syncthreads();
-      const float* sd = &sdt[buf][0][cw].x;
-      const float* sb = bc[buf] + q * NS;
-      // the next group's reads are on their way while this one is worked on (with 8 states registers would spill)
-      constexpr int kBuf = NS <= 4 ? 2 : 1;
-      Group<NS, !States, GS, TT, 2 * CH> g[kBuf];
-      if constexpr (kBuf == 2) g[0].read(sd, sb, 0);
+      constexpr int RB = 16 / NS;  // tokens whose B lies in a row's lanes: state lane % NS of token lane / NS
+      const float* sb = bc[buf] + (lane & 15) / NS * NP + q * NS + (lane & 15) % NS;
+      float Br[TT / RB];
 #pragma unroll
-      for (int k = 0; k < TT; k += GS) {
-        auto& now = g[k / GS % kBuf];
-        if constexpr (kBuf == 1) now.read(sd, sb, k);
-        else if (k + GS < TT) g[(k / GS + 1) % kBuf].read(sd, sb, k + GS);
+      for (int k = 0; k < TT / RB; ++k) Br[k] = sb[k * RB * NP];
+      // dt, dt u and C of a group of tokens: the next one's are on their way while this one is worked on
+      float2 d[2][GS];
+      float C[2][GS][NS];
+      auto read = [&](int buf2, int k) {
+#pragma unroll
+        for (int j = 0; j < GS; ++j) {
+          d[buf2][j] = sdt[buf][k + j][cw];
+          if constexpr (!States) lds_floats(C[buf2][j], bc[buf] + (TT + k + j) * NP + q * NS);
+        }
+      };
+      read(0, 0);
+      each<TT / GS>([&](auto group) {
+        constexpr int k = group * GS;
+        if constexpr (k + GS < TT) read((group + 1) & 1, k + GS);
         float e[GS][NS], y[GS];
 #pragma unroll
         for (int j = 0; j < GS; ++j)
 #pragma unroll
-          for (int i = 0; i < NS; ++i) e[j][i] = __builtin_amdgcn_exp2f(now.d[j].x * a2[i]);
-#pragma unroll
-        for (int j = 0; j < GS; ++j) {
-          y[j] = 0.f;
-#pragma unroll
-          for (int i = 0; i < NS; ++i) {
-            h[i] = fmaf(e[j][i], h[i], now.d[j].y * now.B[j][i]);
-            if constexpr (!States) y[j] = fmaf(now.C[j][i], h[i], y[j]);
-          }
-          if constexpr (States) sum += now.d[j].x;
-        }
+          for (int i = 0; i < NS; ++i) e[j][i] = __builtin_amdgcn_exp2f(d[group & 1][j].x * a2[i]);
+        each<GS>([&](auto j) {
+          constexpr int t = k + j;
+          const float2 x = d[group & 1][j];
+          float s = 0.f;
+          each<NS>([&](auto i) {
+            constexpr int from = 0x150 + t % RB * NS + i;  // row_newbcast
+            h[i] = fmaf(e[j][i], h[i], mfma::dpp_mov<from>(Br[t / RB]) * x.y);
+            if constexpr (!States) s = fmaf(C[group & 1][j][i], h[i], s);
+          });
+          if constexpr (States) sum += x.x;
+          y[j] = s;
+        });
         if constexpr (!States) sy[buf][k + q][cw] = row_sums(y);
-      }
+      });
     }
     __syncthreads();
     if constexpr (States) {
@@ -97,14 +126,14 @@ __global__ __launch_bounds__(512, 2) void ttt_scan_fwd(ScanArgs a) {
   }
 
   // this thread's piece of a tile: token row, channels oct .. oct + 7
-  const int tid = threadIdx.x & 255, row = tid >> 3, oct = (tid & 7) * 8;
+  const int tid = threadIdx.x - WALKERS, row = tid >> 3, oct = (tid & 7) * 8;
   const int n8 = min(8, p.nc - oct);  // (may be negative)
   const int64_t first = begin + row;
   const InT* up = static_cast<const InT*>(a.u) + p.b * a.us.b + first * a.us.t + p.c0 + oct;
   const InT* dp = static_cast<const InT*>(a.dt) + p.b * a.dts.b + first * a.dts.t + p.c0 + oct;
   const InT* zp = States || !a.z ? nullptr : static_cast<const InT*>(a.z) + p.b * a.zs.b + first * a.zs.t + p.c0 + oct;
   OutT* yp = static_cast<OutT*>(a.y) + p.b * a.ys.b + first * a.ys.t + p.c0 + oct;
-  BcRows<InT, NS, TT> next(a, p, begin, tid, !States);
+  BcRows<InT, NP, TT> next(a, p, begin, tid, !States);
   float bias[8], skip[8];
   params<8>(bias, a.dt_bias ? a.dt_bias + p.c0 + oct : nullptr, n8, 0.f);
   if constexpr (!States) params<8>(skip, a.Dskip ? a.Dskip + p.c0 + oct : nullptr, n8, 0.f);
@@ -118,7 +147,8 @@ __global__ __launch_bounds__(512, 2) void ttt_scan_fwd(ScanArgs a) {
     dp += TT * a.dts.t;
     next.load(t0, end, 1);
   };
-  auto stage = [&](int buf, int n) {
+  // (u is zero where there is no token; its dt has to be)
+  auto stage = [&](int buf, int n, bool whole) {
     float x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = dt_next.get(i) + bias[i];
@@ -126,8 +156,10 @@ __global__ __launch_bounds__(512, 2) void ttt_scan_fwd(ScanArgs a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = softplus(x[i]);
     }
+    if (!Wide || !whole) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = (Wide ? n > 0 : i < n) ? x[i] : 0.f;
+      for (int i = 0; i < 8; ++i) x[i] = i < n ? x[i] : 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < 8; i += 2)
       *reinterpret_cast<float4*>(&sdt[buf][row][oct + i]) = make_float4(x[i], x[i] * u_next.get(i), x[i + 1], x[i + 1] * u_next.get(i + 1));
@@ -154,7 +186,7 @@ __global__ __launch_bounds__(512, 2) void ttt_scan_fwd(ScanArgs a) {
     fetch(begin);
     u_next = u_far;
     dt_next = dt_far;
-    stage(0, begin + row < end ? n8 : 0);
+    stage(0, begin + row < end ? n8 : 0, begin + TT <= end && p.nc == CH);
     next.stage(bc[0]);
     if (begin + TT < end) fetch(begin + TT);
   }
@@ -176,7 +208,7 @@ __global__ __launch_bounds__(512, 2) void ttt_scan_fwd(ScanArgs a) {
         zp += TT * a.zs.t;
       }
     }
-    stage(buf ^ 1, t0 + TT + row < end ? n8 : 0);
+    stage(buf ^ 1, t0 + TT + row < end ? n8 : 0, t0 + 2 * TT <= end && p.nc == CH);
     if constexpr (!States) {
       if (t0 > begin) finish(buf ^ 1, n8);
     }
@@ -245,31 +277,42 @@ __global__ __launch_bounds__(256) void ttt_scan_decode(ScanArgs a) {
 enum Which { STATES, FWD, DECODE };
 
 template <typename InT, typename OutT, int NS>
-hipError_t go(Which which, const ScanArgs& a, hipStream_t s) {
-  if (which == DECODE) {
-    const int64_t n = static_cast<int64_t>(a.B) * a.D;
-    ttt_scan_decode<InT, OutT, NS><<<static_cast<unsigned>((n + 63) / 64), 256, 0, s>>>(a);
-    return hipGetLastError();
-  }
-  const int dg = a.D / a.G, segs = which == STATES ? a.nseg - 1 : a.nseg;
+hipError_t walk(bool states, const ScanArgs& a, hipStream_t s) {
+  const int dg = a.D / a.G, segs = states ? a.nseg - 1 : a.nseg;
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.B) * a.G * ((dg + CH - 1) / CH) * segs);
-  if (which == STATES) {
-    if (a.wide) ttt_scan_fwd<InT, float, NS, true, true><<<grid, 512, 0, s>>>(a);
-    else ttt_scan_fwd<InT, float, NS, false, true><<<grid, 512, 0, s>>>(a);
+  if (states) {
+    if (a.wide) ttt_scan_fwd<InT, float, NS, true, true><<<grid, THREADS, 0, s>>>(a);
+    else ttt_scan_fwd<InT, float, NS, false, true><<<grid, THREADS, 0, s>>>(a);
   } else {
-    if (a.wide) ttt_scan_fwd<InT, OutT, NS, true, false><<<grid, 512, 0, s>>>(a);
-    else ttt_scan_fwd<InT, OutT, NS, false, false><<<grid, 512, 0, s>>>(a);
+    if (a.wide) ttt_scan_fwd<InT, OutT, NS, true, false><<<grid, THREADS, 0, s>>>(a);
+    else ttt_scan_fwd<InT, OutT, NS, false, false><<<grid, THREADS, 0, s>>>(a);
   }
+  return hipGetLastError();
+}
+
+template <typename InT, typename OutT, int NS>
+hipError_t token(const ScanArgs& a, hipStream_t s) {
+  const int64_t n = static_cast<int64_t>(a.B) * a.D;
+  ttt_scan_decode<InT, OutT, NS><<<static_cast<unsigned>((n + 63) / 64), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <typename InT, typename OutT>
 hipError_t go(Which which, const ScanArgs& a, hipStream_t s) {
-  switch (scan_states(a.N)) {
-    case 1: return go<InT, OutT, 1>(which, a, s);
-    case 2: return go<InT, OutT, 2>(which, a, s);
-    case 4: return go<InT, OutT, 4>(which, a, s);
-    case 8: return go<InT, OutT, 8>(which, a, s);
+  if (which == DECODE) {
+    switch (scan_states(a.N, 4)) {
+      case 1: return token<InT, OutT, 1>(a, s);
+      case 2: return token<InT, OutT, 2>(a, s);
+      case 4: return token<InT, OutT, 4>(a, s);
+      case 8: return token<InT, OutT, 8>(a, s);
+      default: return hipErrorInvalidValue;
+    }
+  }
+  switch (scan_states(a.N, LANES)) {
+    case 1: return walk<InT, OutT, 1>(which == STATES, a, s);
+    case 2: return walk<InT, OutT, 2>(which == STATES, a, s);
+    case 4: return walk<InT, OutT, 4>(which == STATES, a, s);
+    case 8: return walk<InT, OutT, 8>(which == STATES, a, s);
     default: return hipErrorInvalidValue;
   }
 }
@@ -285,7 +328,11 @@ hipError_t go(Which which, const ScanArgs& a, hipStream_t s) {
 
 }  // namespace
 
-int scan_states(int N) { return N < 1 ? 0 : N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 0; }
+int scan_states(int N, int lanes) {
+  for (int n = 1; n * lanes <= 32; n *= 2)
+    if (N >= 1 && N <= n * lanes) return n;
+  return 0;
+}
 
 hipError_t launch_scan_states(const ScanArgs& a, hipStream_t s) { return go(STATES, a, s); }
 hipError_t launch_scan_fwd(const ScanArgs& a, hipStream_t s) { return go(FWD, a, s); }
