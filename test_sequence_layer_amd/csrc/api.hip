@@ -2097,7 +2097,7 @@ ttt_status validate_scan_bwd(const ttt_selective_scan_desc* d, const void* u, co
   ttt_status st = check_scan_desc(d);
   if (st != TTT_OK) return st;
   const ScanPlan plan = scan_plan(d, true);
-  if (plan.blocks * plan.nseg * 256 > kMaxThreads) return TTT_ERR_SHAPE;
+  if (plan.blocks * plan.nseg * 512 > kMaxThreads) return TTT_ERR_SHAPE;
   if (static_cast<int64_t>(d->B) * d->G * d->T * 2 * d->N > kMaxThreads) return TTT_ERR_SHAPE;  // the sums
   if (static_cast<int64_t>(d->D) * (d->N + 2) > kMaxThreads / 16) return TTT_ERR_SHAPE;
   if (!A || !dA) return TTT_ERR_NULL;

@@ -64,11 +64,11 @@ struct Lines {
     z = a.z ? static_cast<const InT*>(a.z) + p.b * a.zs.b + t * a.zs.t + c : nullptr;
     dy = static_cast<const OutT*>(a.dy) + p.b * a.ys.b + t * a.ys.t + c;
   }
-  __device__ __forceinline__ void step(const ScanArgs& a, int dir) {
-    u += dir * TT * a.us.t;
-    dt += dir * TT * a.dts.t;
-    if (z) z += dir * TT * a.zs.t;
-    dy += dir * TT * a.ys.t;
+  __device__ __forceinline__ void step(const ScanArgs& a) {
+    u += TT * a.us.t;
+    dt += TT * a.dts.t;
+    if (z) z += TT * a.zs.t;
+    dy += TT * a.ys.t;
   }
 };
 
@@ -108,7 +108,7 @@ __global__ __launch_bounds__(256, 2) void ttt_scan_bwd_states(ScanArgs a) {
     load<Wide>(dy, at.dy, n);
     if (at.z) load<Wide>(z, at.z, n);
     rows.load(t0, end, 1);
-    at.step(a, 1);
+    at.step(a);
     if (t0 > begin) __syncthreads();
     float s[4], d[4];
 #pragma unroll
@@ -152,244 +152,280 @@ __global__ __launch_bounds__(256, 2) void ttt_scan_bwd_states(ScanArgs a) {
   }
 }
 
+// Waves 0 to 3 walk, 16 channels each; waves 4 to 7 bring the tiles into LDS one step ahead of them and take them out one
+// step behind (see the forward): first the forward walk's tiles, then the same backward.  Step s works on buffer s % 2.
 template <typename InT, typename OutT, int NS, bool Wide>
-__global__ __launch_bounds__(256, 2) void ttt_scan_bwd(ScanArgs a) {
+__global__ __launch_bounds__(512, 1) void ttt_scan_bwd(ScanArgs a) {
   constexpr int NP = 4 * NS, CL = kChunk<NS>, NV = NS > 1 ? NS / 2 : 1;
-  __shared__ __align__(16) float4 tile[TT][CH];  // dt, dt u, dy; then sum g B, sum g a h A log2(e), y
-  __shared__ __align__(16) float bc[2 * TT * NP];
-  __shared__ __align__(16) float sbc[4][TT][2][NP];  // each wave's sums over its channels
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, q = lane & 3, cw = wave * 16 + (lane >> 2);
+  __shared__ __align__(16) float4 tile[2][TT][CH];  // dt, dt u, dy; then sum g B, sum g a h A log2(e), y
+  __shared__ __align__(16) float bc[2][2 * TT * NP];
+  __shared__ __align__(16) float sbc[2][4][TT][2][NP];  // each wave's sums over its channels
   const int seg = static_cast<int>(blockIdx.x % a.nseg);
   const Place p = place(a, blockIdx.x / a.nseg);
-  const int c = p.c0 + cw;
-  const bool on = cw < p.nc;
   const int begin = seg * a.seglen, tokens = min(a.T, begin + a.seglen), end = min(p.len, tokens);
   const int64_t slot = static_cast<int64_t>(p.b) * a.nseg + seg;
+  const int tiles = begin < end ? (end - begin + TT - 1) / TT : 0;
+  float* sums = a.part + slot * (static_cast<int64_t>(a.D) * (a.N + 2));
 
-  float a2[NS], h[NS];
-  decays(a2, a, c, q, on);
-  if (a.nseg == 1) load_states(h, a.h0 ? a.h0 + (static_cast<int64_t>(p.b) * a.D + c) * a.N : nullptr, a.N, q, on);
-  else start_state(h, a2, a, p, seg, c, q, on);
-
-  Lines<InT, OutT> at(a, p, begin, tid);
-  BcRows<InT, NP, TT> rows(a, p, begin, tid, true);
-  float bias[4];
-  params<4>(bias, a.dt_bias ? a.dt_bias + p.c0 + at.quad : nullptr, at.n4, 0.f);
-  const int64_t ckstep = static_cast<int64_t>(a.D) * a.N;
-  // the chunk's state; always by the same thread, so that it is there when it is read again
-  float* ck = a.ckpt + (static_cast<int64_t>(p.b) * a.chunks + begin / CL) * ckstep + static_cast<int64_t>(c) * a.N;
-
-  // forward: the state before each chunk
-  const int last = begin + (max(end - begin, 1) - 1) / TT * TT;
-  Piece<InT, 4> u, dtr, z;
-  Piece<OutT, 4> dyr;
-  auto fetch = [&](int t0, int dir, bool back) {
-    const int n = t0 + at.row < end ? at.n4 : 0;
-    load<Wide>(u, at.u, n);
-    load<Wide>(dtr, at.dt, n);
-    if (back) {
-      load<Wide>(dyr, at.dy, n);
-      if (at.z) load<Wide>(z, at.z, n);
-    }
-    rows.load(t0, end, dir);
-    at.step(a, dir);
-  };
-  if (begin < end) fetch(begin, 1, false);
-  for (int t0 = begin; t0 < end; t0 += TT) {
-    const int n = t0 + at.row < end ? at.n4 : 0;
-    float s[4];
+  if (__builtin_amdgcn_readfirstlane(threadIdx.x) < 256) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, q = lane & 3, cw = wave * 16 + (lane >> 2);
+    const int c = p.c0 + cw;
+    const bool on = cw < p.nc;
+    float a2[NS], h[NS];
+    decays(a2, a, c, q, on);
+    if (a.nseg == 1) load_states(h, a.h0 ? a.h0 + (static_cast<int64_t>(p.b) * a.D + c) * a.N : nullptr, a.N, q, on);
+    else start_state(h, a2, a, p, seg, c, q, on);
+    const int64_t ckstep = static_cast<int64_t>(a.D) * a.N;
+    // the chunk's state; always by the same thread, so that it is there when it is read again
+    float* ck = a.ckpt + (static_cast<int64_t>(p.b) * a.chunks + begin / CL) * ckstep + static_cast<int64_t>(c) * a.N;
+    int buf = 0;
+    // forward: the state before each chunk
+    for (int k = 0; k < tiles; ++k, buf ^= 1) {
+      __syncthreads();
+      const float* sd = &tile[buf][0][cw].x;
+      const float* sb = bc[buf] + q * NS;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] = dtr.get(i) + bias[i];
-    if (a.softplus) {
+      for (int k0 = 0; k0 < TT; k0 += CL) {
+        store_states(h, ck, a.N, q, on && begin + k * TT + k0 < end);
+        ck += ckstep;
+        if (k0 + CL >= TT && k == tiles - 1) break;  // (nobody asks for the state behind the last chunk)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = softplus(s[i]);
-    }
-    zero_from(s, n);
-    if (t0 > begin) __syncthreads();
+        for (int j0 = k0; j0 < k0 + CL; j0 += GS) {
+          Group<NS, false, GS, TT, NP, 4 * CH> g;
+          g.read(sd, sb, j0);
+          float e[GS][NS];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<float2*>(&tile[at.row][at.quad + i]) = make_float2(s[i], s[i] * u.get(i));
-    rows.stage(bc);
-    __syncthreads();
-    if (t0 < last) fetch(t0 + TT, 1, false);
-    const float* sd = &tile[0][cw].x;
-    const float* sb = bc + q * NS;
+          for (int j = 0; j < GS; ++j)
 #pragma unroll
-    for (int k0 = 0; k0 < TT; k0 += CL) {
-      store_states(h, ck, a.N, q, on && t0 + k0 < end);
-      ck += ckstep;
-      if (k0 + CL >= TT && t0 >= last) break;  // (nobody asks for the state behind the last chunk)
+            for (int i = 0; i < NS; ++i) e[j][i] = __builtin_amdgcn_exp2f(g.d[j].x * a2[i]);
 #pragma unroll
-      for (int k = k0; k < k0 + CL; k += GS) {
-        Group<NS, false, GS, TT, NP, 4 * CH> g;
-        g.read(sd, sb, k);
-        float e[GS][NS];
+          for (int j = 0; j < GS; ++j)
 #pragma unroll
-        for (int j = 0; j < GS; ++j)
-#pragma unroll
-          for (int i = 0; i < NS; ++i) e[j][i] = __builtin_amdgcn_exp2f(g.d[j].x * a2[i]);
-#pragma unroll
-        for (int j = 0; j < GS; ++j)
-#pragma unroll
-          for (int i = 0; i < NS; ++i) h[i] = fmaf(e[j][i], h[i], g.d[j].y * g.B[j][i]);
+            for (int i = 0; i < NS; ++i) h[i] = fmaf(e[j][i], h[i], g.d[j].y * g.B[j][i]);
+        }
       }
     }
+    // the gradient of the state behind the segment
+    float g[NS], dA[NS];
+    load_states(g, a.dh_final ? a.dh_final + (static_cast<int64_t>(p.b) * a.D + c) * a.N : nullptr, a.N, q, on);
+    for (int s = a.nseg - 1; s > seg; --s) {
+      const int64_t o = static_cast<int64_t>(p.b) * a.nseg + s;
+      const float sum = on ? a.sseg[o * a.D + c] : 0.f;
+      float x[NS];
+      load_states(x, a.gseg + (o * a.D + c) * a.N, a.N, q, on);
+#pragma unroll
+      for (int i = 0; i < NS; ++i) g[i] = fmaf(__builtin_amdgcn_exp2f(sum * a2[i]), g[i], x[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NS; ++i) dA[i] = 0.f;
+
+    float next[NS];  // the state before the chunk that comes next
+    load_states(next, ck - ckstep, a.N, q, on && tiles > 0 && begin + tiles * TT - CL < end);
+    for (int k = tiles - 1; k >= 0; --k, buf ^= 1) {
+      __syncthreads();
+      const float4* td = &tile[buf][0][cw];
+      const float* sb = bc[buf] + q * NS;
+      float* res = reinterpret_cast<float*>(&tile[buf][0][cw]) + q;
+      float* out = &sbc[buf][wave][0][lane >> 5][NS > 1 ? q * NS + (lane >> 4 & 1) * (NS / 2) : q];
+#pragma unroll 1
+      for (int k0 = TT - CL; k0 >= 0; k0 -= CL) {
+        float ah[CL][NS], e[CL][NS];
+        ck -= ckstep;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) h[i] = next[i];
+        const int before = begin + k * TT + k0 - CL;
+        load_states(next, ck - ckstep, a.N, q, on && before >= begin && before < end);
+#pragma unroll
+        for (int j = 0; j < CL; ++j) {
+          const float2 x = *reinterpret_cast<const float2*>(td + (k0 + j) * CH);
+          float Bv[NS];
+          lds_floats(Bv, sb + (k0 + j) * NP);
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            e[j][i] = __builtin_amdgcn_exp2f(x.x * a2[i]);
+            ah[j][i] = e[j][i] * h[i];
+            h[i] = fmaf(x.y, Bv[i], ah[j][i]);
+          }
+        }
+#pragma unroll
+        for (int j = CL - 1; j >= 0; --j) {
+          const float4 x = td[(k0 + j) * CH];
+          float Bv[NS], Cv[NS], v[2 * NS], s = 0.f, sa = 0.f, y = 0.f;
+          lds_floats(Bv, sb + (k0 + j) * NP);
+          lds_floats(Cv, sb + (TT + k0 + j) * NP);
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            g[i] = fmaf(Cv[i], x.z, g[i]);
+            const float ht = fmaf(x.y, Bv[i], ah[j][i]);
+            v[i] = x.y * g[i];
+            v[NS + i] = x.z * ht;
+            const float gh = g[i] * ah[j][i];
+            s = i ? fmaf(g[i], Bv[i], s) : g[i] * Bv[i];
+            sa = i ? fmaf(gh, a2[i], sa) : gh * a2[i];
+            y = i ? fmaf(Cv[i], ht, y) : Cv[i] * ht;
+            dA[i] = fmaf(gh, x.x, dA[i]);
+            g[i] *= e[j][i];
+          }
+          channel_sums<NS>(v);
+          s = quad_sum(s);
+          sa = quad_sum(sa);
+          y = quad_sum(y);
+          // (lanes that hold the same value write it to the same place: no branch in the walk)
+          res[(k0 + j) * 4 * CH] = q == 0 ? s : q == 1 ? sa : y;
+          if constexpr (NV == 4) *reinterpret_cast<float4*>(out + (k0 + j) * 2 * NP) = make_float4(v[0], v[1], v[2], v[3]);
+          else if constexpr (NV == 2) *reinterpret_cast<float2*>(out + (k0 + j) * 2 * NP) = make_float2(v[0], v[1]);
+          else out[(k0 + j) * 2 * NP] = v[0];
+        }
+      }
+    }
+    __syncthreads();
+    if (seg == 0 && a.dh0) store_states(g, a.dh0 + (static_cast<int64_t>(p.b) * a.D + c) * a.N, a.N, q, on);
+    store_states(dA, sums + static_cast<int64_t>(c) * a.N, a.N, q, on);
+    __syncthreads();
+    return;
   }
 
-  // the gradient of the state behind the segment
-  float g[NS], dA[NS];
-  load_states(g, a.dh_final ? a.dh_final + (static_cast<int64_t>(p.b) * a.D + c) * a.N : nullptr, a.N, q, on);
-  for (int s = a.nseg - 1; s > seg; --s) {
-    const int64_t o = static_cast<int64_t>(p.b) * a.nseg + s;
-    const float sum = on ? a.sseg[o * a.D + c] : 0.f;
-    float x[NS];
-    load_states(x, a.gseg + (o * a.D + c) * a.N, a.N, q, on);
-#pragma unroll
-    for (int i = 0; i < NS; ++i) g[i] = fmaf(__builtin_amdgcn_exp2f(sum * a2[i]), g[i], x[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < NS; ++i) dA[i] = 0.f;
-
-  const int64_t oc = p.c0 + at.quad, ot = last + at.row;
-  OutT* dup = static_cast<OutT*>(a.du) + p.b * a.dus.b + ot * a.dus.t + oc;
-  OutT* ddp = static_cast<OutT*>(a.ddt) + p.b * a.ddts.b + ot * a.ddts.t + oc;
-  OutT* dzp = at.z ? static_cast<OutT*>(a.dz) + p.b * a.dzs.b + ot * a.dzs.t + oc : nullptr;
-  float skip[4], dD[4], db[4];
+  const int tid = threadIdx.x - 256;
+  const Lines<InT, OutT> at(a, p, begin, tid);
+  BcRows<InT, NP, TT> rows(a, p, begin, tid, true);
+  const int64_t oc = p.c0 + at.quad;
+  float bias[4], skip[4], dD[4], db[4];
+  params<4>(bias, a.dt_bias ? a.dt_bias + oc : nullptr, at.n4, 0.f);
   params<4>(skip, a.Dskip ? a.Dskip + oc : nullptr, at.n4, 0.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) dD[i] = db[i] = 0.f;
+  OutT* dup = static_cast<OutT*>(a.du) + p.b * a.dus.b + oc;
+  OutT* ddp = static_cast<OutT*>(a.ddt) + p.b * a.ddts.b + oc;
+  OutT* dzp = at.z ? static_cast<OutT*>(a.dz) + p.b * a.dzs.b + oc : nullptr;
   float* part = a.bcpart + ((static_cast<int64_t>(p.b) * a.G + p.g) * ((a.D / a.G + CH - 1) / CH) + p.tile) * a.T * 2 * a.N;
 
-  if (begin < end) {
-    // (the forward walk left the pointers one tile behind the last)
-    at.step(a, -1);
-    rows.back();
-    fetch(last, -1, true);
-  }
-  for (int t0 = last; t0 >= begin && begin < end; t0 -= TT) {
-    const int n = t0 + at.row < end ? at.n4 : 0;
-    const Piece<InT, 4> u0 = u, z0 = z;
-    const Piece<OutT, 4> dy0 = dyr;
-    float dt[4], slope[4], d[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) dt[i] = dtr.get(i) + bias[i], slope[i] = 1.f, d[i] = dyr.get(i);
-    if (a.softplus) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) dt[i] = softplus(dt[i], slope[i]);
+  // a tile's inputs of this thread; dt and its slope once they are known
+  struct Held {
+    Piece<InT, 4> u, z;
+    Piece<OutT, 4> dy;
+    float dt[4], slope[4];
+  };
+  Held old, now, next;  // of the tile behind the walk, in the walk, before it
+  Piece<InT, 4> u_far, dt_far, z_far, dt_next;
+  Piece<OutT, 4> dy_far;
+  const int steps = 2 * tiles;
+  auto token = [&](int s) { return begin + (s < tiles ? s : steps - 1 - s) * TT; };
+  auto fetch = [&](int s) {
+    const int t0 = token(s), n = t0 + at.row < end ? at.n4 : 0;
+    const int64_t o = t0 - begin;
+    load<Wide>(u_far, at.u + o * a.us.t, n);
+    load<Wide>(dt_far, at.dt + o * a.dts.t, n);
+    if (s >= tiles) {
+      load<Wide>(dy_far, at.dy + o * a.ys.t, n);
+      if (at.z) load<Wide>(z_far, at.z + o * a.zs.t, n);
     }
-    zero_from(dt, n);
-    if (at.z) {
+    rows.load(t0, end, s + 1 < tiles ? 1 : s + 1 == tiles ? 0 : -1);
+  };
+  auto stage = [&](int s) {
+    const int n = token(s) + at.row < end ? at.n4 : 0;
+    float4* to = &tile[s & 1][at.row][at.quad];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) d[i] *= z0.get(i) * sigmoid(z0.get(i));
-    }
-    __syncthreads();  // the tile before (or the forward walk's last) is done with
+    for (int i = 0; i < 4; ++i) next.dt[i] = dt_next.get(i) + bias[i], next.slope[i] = 1.f;
+    if (s < tiles) {
+      if (a.softplus) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) tile[at.row][at.quad + i] = make_float4(dt[i], dt[i] * u0.get(i), d[i], 0.f);
-    rows.stage(bc);
-    __syncthreads();
-    if (t0 > begin) fetch(t0 - TT, -1, true);
-    const float* sb = bc + q * NS;
-    float* res = reinterpret_cast<float*>(&tile[0][cw]) + q;
-    float* sums = &sbc[wave][0][lane >> 5][NS > 1 ? q * NS + (lane >> 4 & 1) * (NS / 2) : q];
-#pragma unroll 1
-    for (int k0 = TT - CL; k0 >= 0; k0 -= CL) {
-      ck -= ckstep;
-      float ah[CL][NS], e[CL][NS];
-      load_states(h, ck, a.N, q, on && t0 + k0 < end);
+        for (int i = 0; i < 4; ++i) next.dt[i] = softplus(next.dt[i]);
+      }
+      zero_from(next.dt, n);
 #pragma unroll
-      for (int k = 0; k < CL; ++k) {
-        const float2 x = *reinterpret_cast<const float2*>(&tile[k0 + k][cw]);
-        float Bv[NS];
-        lds_floats(Bv, sb + (k0 + k) * NP);
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<float2*>(to + i) = make_float2(next.dt[i], next.dt[i] * next.u.get(i));
+    } else {
+      float d[4];
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          e[k][i] = __builtin_amdgcn_exp2f(x.x * a2[i]);
-          ah[k][i] = e[k][i] * h[i];
-          h[i] = fmaf(x.y, Bv[i], ah[k][i]);
-        }
+      for (int i = 0; i < 4; ++i) d[i] = next.dy.get(i);
+      if (a.softplus) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) next.dt[i] = softplus(next.dt[i], next.slope[i]);
+      }
+      zero_from(next.dt, n);
+      if (at.z) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] *= next.z.get(i) * sigmoid(next.z.get(i));
       }
 #pragma unroll
-      for (int k = CL - 1; k >= 0; --k) {
-        const float4 x = tile[k0 + k][cw];
-        float Bv[NS], Cv[NS], v[2 * NS], s = 0.f, sa = 0.f, y = 0.f;
-        lds_floats(Bv, sb + (k0 + k) * NP);
-        lds_floats(Cv, sb + (TT + k0 + k) * NP);
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          g[i] = fmaf(Cv[i], x.z, g[i]);
-          const float ht = fmaf(x.y, Bv[i], ah[k][i]);
-          v[i] = x.y * g[i];
-          v[NS + i] = x.z * ht;
-          s = fmaf(g[i], Bv[i], s);
-          const float gh = g[i] * ah[k][i];
-          sa = fmaf(gh, a2[i], sa);
-          dA[i] = fmaf(gh, x.x, dA[i]);
-          y = fmaf(Cv[i], ht, y);
-          g[i] *= e[k][i];
-        }
-        channel_sums<NS>(v);
-        s = quad_sum(s);
-        sa = quad_sum(sa);
-        y = quad_sum(y);
-        // (lanes that hold the same value write it to the same place: no branch in the walk)
-        res[(k0 + k) * 4 * CH] = q == 0 ? s : q == 1 ? sa : y;
-        if constexpr (NV == 4) *reinterpret_cast<float4*>(sums + (k0 + k) * 2 * NP) = make_float4(v[0], v[1], v[2], v[3]);
-        else if constexpr (NV == 2) *reinterpret_cast<float2*>(sums + (k0 + k) * 2 * NP) = make_float2(v[0], v[1]);
-        else sums[(k0 + k) * 2 * NP] = v[0];
-      }
+      for (int i = 0; i < 4; ++i) to[i] = make_float4(next.dt[i], next.dt[i] * next.u.get(i), d[i], 0.f);
     }
-    __syncthreads();
+    rows.stage(bc[s & 1]);
+  };
+  auto finish = [&](int s) {
+    const int t0 = token(s), n = t0 + at.row < end ? at.n4 : 0;
     float o[3][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 v = tile[at.row][at.quad + i];
-      const float uu = u0.get(i);
-      float dd = dy0.get(i);
+      const float4 v = tile[s & 1][at.row][at.quad + i];
+      const float uu = old.u.get(i);
+      float dd = old.dy.get(i);
       o[2][i] = 0.f;
       if (at.z) {
-        const float x = z0.get(i), s = sigmoid(x), gate = x * s;
-        o[2][i] = dd * fmaf(skip[i], uu, v.z) * fmaf(gate, 1.f - s, s);
+        const float x = old.z.get(i), sg = sigmoid(x), gate = x * sg;
+        o[2][i] = dd * fmaf(skip[i], uu, v.z) * fmaf(gate, 1.f - sg, sg);
         dd *= gate;
       }
-      o[0][i] = fmaf(dt[i], v.x, skip[i] * dd);
-      o[1][i] = fmaf(uu, v.x, v.y * (1.f / kLog2e)) * slope[i];
+      o[0][i] = fmaf(old.dt[i], v.x, skip[i] * dd);
+      o[1][i] = fmaf(uu, v.x, v.y * (1.f / kLog2e)) * old.slope[i];
       if (i < n) {
         dD[i] = fmaf(dd, uu, dD[i]);
         db[i] += o[1][i];
       }
     }
+    const int64_t t = t0 + at.row;
     Piece<OutT, 4> out;
     out.set_all(o[0]);
-    store<Wide>(out, dup, n);
+    store<Wide>(out, dup + t * a.dus.t, n);
     out.set_all(o[1]);
-    store<Wide>(out, ddp, n);
-    dup -= TT * a.dus.t;
-    ddp -= TT * a.ddts.t;
+    store<Wide>(out, ddp + t * a.ddts.t, n);
     if (at.z) {
       out.set_all(o[2]);
-      store<Wide>(out, dzp, n);
-      dzp -= TT * a.dzs.t;
+      store<Wide>(out, dzp + t * a.dzs.t, n);
     }
 #pragma unroll
     for (int x = tid; x < TT * 2 * NP; x += 256) {
       const int k = x / (2 * NP), w = x / NP % 2, m = x % NP;
+      const float* v = &sbc[s & 1][0][0][0][0] + x;
+      constexpr int W = TT * 2 * NP;
       if (t0 + k < end && m < a.N)
-        part[(static_cast<int64_t>(t0 + k) * 2 + w) * a.N + m] =
-            (sbc[0][k][w][m] + sbc[1][k][w][m]) + (sbc[2][k][w][m] + sbc[3][k][w][m]);
+        part[(static_cast<int64_t>(t0 + k) * 2 + w) * a.N + m] = (v[0] + v[W]) + (v[2 * W] + v[3 * W]);
     }
+  };
+  if (steps) {
+    fetch(0);
+    next.u = u_far;
+    dt_next = dt_far;
+    stage(0);
+    fetch(1);
+  }
+  for (int s = 0; s < steps; ++s) {
+    __syncthreads();
+    old = now;
+    now = next;
+    next.u = u_far;
+    next.z = z_far;
+    next.dy = dy_far;
+    dt_next = dt_far;
+    if (s > tiles) finish(s - 1);
+    if (s + 1 < steps) stage(s + 1);
+    if (s + 2 < steps) fetch(s + 2);
+  }
+  __syncthreads();
+  if (steps) {
+    old = now;
+    finish(steps - 1);
   }
   Piece<OutT, 4> none;
   none.zero();
   for (int64_t t = max(begin, end) + at.row; t < tokens; t += TT) {
-    store<Wide>(none, static_cast<OutT*>(a.du) + p.b * a.dus.b + t * a.dus.t + oc, at.n4);
-    store<Wide>(none, static_cast<OutT*>(a.ddt) + p.b * a.ddts.b + t * a.ddts.t + oc, at.n4);
-    if (at.z) store<Wide>(none, static_cast<OutT*>(a.dz) + p.b * a.dzs.b + t * a.dzs.t + oc, at.n4);
+    store<Wide>(none, dup + t * a.dus.t, at.n4);
+    store<Wide>(none, ddp + t * a.ddts.t, at.n4);
+    if (at.z) store<Wide>(none, dzp + t * a.dzs.t, at.n4);
   }
-  if (seg == 0 && a.dh0) store_states(g, a.dh0 + (static_cast<int64_t>(p.b) * a.D + c) * a.N, a.N, q, on);
-  float* sums = a.part + slot * (static_cast<int64_t>(a.D) * (a.N + 2));
-  store_states(dA, sums + static_cast<int64_t>(c) * a.N, a.N, q, on);
   // dD and ddt_bias: over the token rows
-  __syncthreads();
-  float2* lines = reinterpret_cast<float2*>(&tile[0][0]);
+  float2* lines = reinterpret_cast<float2*>(&tile[0][0][0]);
+  if (steps == 0 || ((steps - 1) & 1) == 0) lines = reinterpret_cast<float2*>(&tile[1][0][0]);  // (finish may still be reading the other)
 #pragma unroll
   for (int i = 0; i < 4; ++i) lines[at.row * CH + at.quad + i] = make_float2(dD[i], db[i]);
   __syncthreads();
@@ -436,8 +472,8 @@ hipError_t go(bool states, const ScanArgs& a, hipStream_t s) {
     if (a.wide) ttt_scan_bwd_states<InT, OutT, NS, true><<<grid, 256, 0, s>>>(a);
     else ttt_scan_bwd_states<InT, OutT, NS, false><<<grid, 256, 0, s>>>(a);
   } else {
-    if (a.wide) ttt_scan_bwd<InT, OutT, NS, true><<<grid, 256, 0, s>>>(a);
-    else ttt_scan_bwd<InT, OutT, NS, false><<<grid, 256, 0, s>>>(a);
+    if (a.wide) ttt_scan_bwd<InT, OutT, NS, true><<<grid, 512, 0, s>>>(a);
+    else ttt_scan_bwd<InT, OutT, NS, false><<<grid, 512, 0, s>>>(a);
   }
   return hipGetLastError();
 }

@@ -104,7 +104,7 @@ struct BcRows {
       step[k] = row * TT;
     }
   }
-  // the tile that begins at token first, as far as end; then on to the next tile (dir 1) or the one before (-1)
+  // the tile that begins at token first, as far as end; then on to the next tile (dir 1), the one before (-1) or none (0)
   __device__ __forceinline__ void load(int first, int end, int dir) {
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
@@ -115,12 +115,9 @@ struct BcRows {
       } else {
         v[k].load_some(p[k], m);
       }
-      p[k] += dir * step[k];
+      if (dir > 0) p[k] += step[k];
+      else if (dir < 0) p[k] -= step[k];
     }
-  }
-  __device__ __forceinline__ void back() {
-#pragma unroll
-    for (int k = 0; k < kEach; ++k) p[k] -= step[k];
   }
   __device__ __forceinline__ void stage(float* bc) const {
 #pragma unroll
