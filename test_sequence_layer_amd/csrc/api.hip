@@ -2131,7 +2131,8 @@ ttt::ScanArgs make_scan_args(const ttt_selective_scan_desc* d, const ScanViews& 
   a.us = strides2(v.u); a.dts = strides2(v.dt); a.zs = strides2(v.z); a.ys = strides2(v.y);
   a.bs = strides(v.Bm); a.cs = strides(v.Cm);
   const int64_t four = 4 * dtype_size(d->in_dtype);
-  a.bc_wide = d->N % 4 == 0 && view_aligned(v.Bm, four) && view_aligned(v.Cm, four);
+  a.wide = d->D / d->G % 8 == 0 && d->N % 4 == 0 && view_aligned(v.Bm, four) && view_aligned(v.Cm, four) &&
+           all_wide({v.u, v.dt, v.z, v.y});
   return a;
 }
 
@@ -2335,7 +2336,6 @@ ttt_status ttt_selective_scan_fwd(const ttt_selective_scan_desc* desc, const voi
   const ScanPlan plan = scan_plan(desc, false);
   const ScanViews v = scan_views(desc, u, dt, A, Bm, Cm, D, z, dt_bias, h0, lens, y);
   ttt::ScanArgs a = make_scan_args(desc, v, u, dt, A, Bm, Cm, D, z, dt_bias, h0, lens);
-  a.wide = desc->D / desc->G % 8 == 0 && all_wide({v.u, v.dt, v.z, v.y});
   a.y = y; a.h_final = h_final;
   a.nseg = plan.nseg; a.seglen = plan.seglen;
   char* ws = static_cast<char*>(workspace);
@@ -2391,7 +2391,7 @@ ttt_status ttt_selective_scan_bwd(const ttt_selective_scan_desc* desc, const voi
   const View vdu = rows_view(du, desc->B, desc->T, desc->D, desc->du, desc->out_dtype);
   const View vddt = rows_view(ddt, desc->B, desc->T, desc->D, desc->ddt, desc->out_dtype);
   const View vdz = rows_view(dz, desc->B, desc->T, desc->D, desc->dz, desc->out_dtype);
-  a.wide = desc->D / desc->G % 8 == 0 && all_wide({v.u, v.dt, v.z, v.y, vdu, vddt, vdz});
+  a.wide = a.wide && all_wide({vdu, vddt, vdz});
   a.dy = dy; a.dh_final = dh_final;
   a.du = du; a.ddt = ddt; a.dz = dz; a.dh0 = dh0;
   a.dus = strides2(vdu); a.ddts = strides2(vddt); a.dzs = strides2(vdz);

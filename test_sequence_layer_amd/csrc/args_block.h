@@ -36,8 +36,8 @@ struct ConvArgs {
 struct ScanArgs {
   int B, T, D, N, G;
   int in_dtype, out_dtype;
-  bool softplus, wide;
-  bool bc_wide;           // B and C: N a multiple of 4, addresses and strides of 4 elements
+  bool softplus;
+  bool wide;              // rows in pieces of 8 (or 4) elements: channels of a group and addresses fit, B and C in pieces of 4
   const void *u, *dt, *z; // [B, T, D] (z or nullptr)
   const void *Bm, *Cm;    // [B, G, T, N]
   const float* A;         // [D, N]

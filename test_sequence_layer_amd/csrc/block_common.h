@@ -80,6 +80,7 @@ struct Piece {
   }
 };
 
+// The first n of N elements, the others zero.  Wide: all or none of them.
 template <bool Wide, typename T, int N>
 __device__ __forceinline__ void load(Piece<T, N>& v, const T* p, int n) {
   if constexpr (Wide) {
@@ -87,6 +88,22 @@ __device__ __forceinline__ void load(Piece<T, N>& v, const T* p, int n) {
     else v.zero();
   } else {
     v.load_some(p, n);
+  }
+}
+
+// The same for loads that stay on their way over other work.  Wide: p is always good to read and ``keep`` drops what should
+// not have been: with a branch around a load the compiler waits for all that is on its way, stores too, before it uses one.
+template <bool Wide, typename T, int N>
+__device__ __forceinline__ void load_ahead(Piece<T, N>& v, const T* p, int n) {
+  if constexpr (Wide) v.load(p);
+  else v.load_some(p, n);
+}
+
+template <bool Wide, typename T, int N>
+__device__ __forceinline__ void keep(Piece<T, N>& v, int n) {
+  if constexpr (Wide) {
+#pragma unroll
+    for (int i = 0; i < Piece<T, N>::kWords; ++i) v.w[i] = n > 0 ? v.w[i] : 0;
   }
 }
 

@@ -10,6 +10,8 @@
 //   ddt_t = sum_n g_t a_t h_{t-1} A + u_t sum_n g_t B_t
 // The walk goes forward first and writes the state before each chunk of CL tokens, then backward chunk by chunk: the chunk's
 // a_t and a_t h_{t-1} are computed again into registers and used from the last token on.
+#include <limits.h>
+
 #include "scan_common.h"
 
 namespace ttt {
@@ -58,7 +60,7 @@ struct Lines {
     row = tid >> 4;
     quad = (tid & 15) * 4;
     n4 = min(4, p.nc - quad);
-    const int64_t t = first + row, c = p.c0 + quad;
+    const int64_t t = first + row, c = p.c0 + (n4 > 0 ? quad : 0);
     u = static_cast<const InT*>(a.u) + p.b * a.us.b + t * a.us.t + c;
     dt = static_cast<const InT*>(a.dt) + p.b * a.dts.b + t * a.dts.t + c;
     z = a.z ? static_cast<const InT*>(a.z) + p.b * a.zs.b + t * a.zs.t + c : nullptr;
@@ -67,7 +69,7 @@ struct Lines {
   __device__ __forceinline__ void step(const ScanArgs& a) {
     u += TT * a.us.t;
     dt += TT * a.dts.t;
-    if (z) z += TT * a.zs.t;
+    if (a.z) z += TT * a.zs.t;
     dy += TT * a.ys.t;
   }
 };
@@ -96,7 +98,7 @@ __global__ __launch_bounds__(256, 2) void ttt_scan_bwd_states(ScanArgs a) {
 #pragma unroll
   for (int i = 0; i < NS; ++i) h[i] = g[i] = 0.f, prod[i] = 1.f;
   Lines<InT, OutT> at(a, p, begin, tid);
-  BcRows<InT, NP, TT> rows(a, p, begin, tid, true);
+  BcRows<InT, NP, TT, Wide> rows(a, p, begin, tid, true);
   float bias[4];
   params<4>(bias, a.dt_bias ? a.dt_bias + p.c0 + at.quad : nullptr, at.n4, 0.f);
   for (int t0 = begin; t0 < end; t0 += TT) {
@@ -106,8 +108,9 @@ __global__ __launch_bounds__(256, 2) void ttt_scan_bwd_states(ScanArgs a) {
     load<Wide>(u, at.u, n);
     load<Wide>(dt, at.dt, n);
     load<Wide>(dy, at.dy, n);
-    if (at.z) load<Wide>(z, at.z, n);
-    rows.load(t0, end, 1);
+    if (a.z) load<Wide>(z, at.z, n);
+    typename BcRows<InT, NP, TT, Wide>::Values v;
+    rows.load(v, t0, end, 1);
     at.step(a);
     if (t0 > begin) __syncthreads();
     float s[4], d[4];
@@ -118,13 +121,13 @@ __global__ __launch_bounds__(256, 2) void ttt_scan_bwd_states(ScanArgs a) {
       for (int i = 0; i < 4; ++i) s[i] = softplus(s[i]);
     }
     zero_from(s, n);
-    if (at.z) {
+    if (a.z) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) d[i] *= z.get(i) * sigmoid(z.get(i));
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) tile[at.row][at.quad + i] = make_float4(s[i], s[i] * u.get(i), d[i], 0.f);
-    rows.stage(bc);
+    rows.stage(v, bc, t0, end);
     __syncthreads();
 #pragma unroll 4
     for (int k = 0; k < TT; ++k) {
@@ -164,7 +167,7 @@ __global__ __launch_bounds__(512, 1) void ttt_scan_bwd(ScanArgs a) {
   const Place p = place(a, blockIdx.x / a.nseg);
   const int begin = seg * a.seglen, tokens = min(a.T, begin + a.seglen), end = min(p.len, tokens);
   const int64_t slot = static_cast<int64_t>(p.b) * a.nseg + seg;
-  const int tiles = begin < end ? (end - begin + TT - 1) / TT : 0;
+  const int tiles = begin < end ? (end - begin + 2 * TT - 1) / (2 * TT) * 2 : 0;  // (an even number: two steps at a time)
   float* sums = a.part + slot * (static_cast<int64_t>(a.D) * (a.N + 2));
 
   if (__builtin_amdgcn_readfirstlane(threadIdx.x) < 256) {
@@ -235,46 +238,80 @@ __global__ __launch_bounds__(512, 1) void ttt_scan_bwd(ScanArgs a) {
         for (int i = 0; i < NS; ++i) h[i] = next[i];
         const int before = begin + k * TT + k0 - CL;
         load_states(next, ck - ckstep, a.N, q, on && before >= begin && before < end);
+        {
+          Group<NS, false, GS, TT, NP, 4 * CH> in[2];
+          in[0].read(&td->x, sb, k0);
 #pragma unroll
-        for (int j = 0; j < CL; ++j) {
-          const float2 x = *reinterpret_cast<const float2*>(td + (k0 + j) * CH);
-          float Bv[NS];
-          lds_floats(Bv, sb + (k0 + j) * NP);
+          for (int m = 0; m < CL; m += GS) {
+            if (m + GS < CL) in[(m / GS + 1) & 1].read(&td->x, sb, k0 + m + GS);
+            __builtin_amdgcn_sched_barrier(0);  // (the reads stay ahead)
+            const auto& now = in[m / GS & 1];
 #pragma unroll
-          for (int i = 0; i < NS; ++i) {
-            e[j][i] = __builtin_amdgcn_exp2f(x.x * a2[i]);
-            ah[j][i] = e[j][i] * h[i];
-            h[i] = fmaf(x.y, Bv[i], ah[j][i]);
+            for (int j = 0; j < GS; ++j)
+#pragma unroll
+              for (int i = 0; i < NS; ++i) e[m + j][i] = __builtin_amdgcn_exp2f(now.d[j].x * a2[i]);
+#pragma unroll
+            for (int j = 0; j < GS; ++j)
+#pragma unroll
+              for (int i = 0; i < NS; ++i) {
+                ah[m + j][i] = e[m + j][i] * h[i];
+                h[i] = fmaf(now.d[j].y, now.B[j][i], ah[m + j][i]);
+              }
           }
         }
+        // two tokens at a time, the next two's reads ahead of this two's writes (which the compiler cannot tell apart)
+        float4 x[2][2];
+        float Bv[2][2][NS], Cv[2][2][NS];
+        auto read = [&](int to, int j) {
 #pragma unroll
-        for (int j = CL - 1; j >= 0; --j) {
-          const float4 x = td[(k0 + j) * CH];
-          float Bv[NS], Cv[NS], v[2 * NS], s = 0.f, sa = 0.f, y = 0.f;
-          lds_floats(Bv, sb + (k0 + j) * NP);
-          lds_floats(Cv, sb + (TT + k0 + j) * NP);
-#pragma unroll
-          for (int i = 0; i < NS; ++i) {
-            g[i] = fmaf(Cv[i], x.z, g[i]);
-            const float ht = fmaf(x.y, Bv[i], ah[j][i]);
-            v[i] = x.y * g[i];
-            v[NS + i] = x.z * ht;
-            const float gh = g[i] * ah[j][i];
-            s = i ? fmaf(g[i], Bv[i], s) : g[i] * Bv[i];
-            sa = i ? fmaf(gh, a2[i], sa) : gh * a2[i];
-            y = i ? fmaf(Cv[i], ht, y) : Cv[i] * ht;
-            dA[i] = fmaf(gh, x.x, dA[i]);
-            g[i] *= e[j][i];
+          for (int r = 0; r < 2; ++r) {
+            x[to][r] = td[(k0 + j - r) * CH];
+            lds_floats(Bv[to][r], sb + (k0 + j - r) * NP);
+            lds_floats(Cv[to][r], sb + (TT + k0 + j - r) * NP);
           }
-          channel_sums<NS>(v);
-          s = quad_sum(s);
-          sa = quad_sum(sa);
-          y = quad_sum(y);
-          // (lanes that hold the same value write it to the same place: no branch in the walk)
-          res[(k0 + j) * 4 * CH] = q == 0 ? s : q == 1 ? sa : y;
-          if constexpr (NV == 4) *reinterpret_cast<float4*>(out + (k0 + j) * 2 * NP) = make_float4(v[0], v[1], v[2], v[3]);
-          else if constexpr (NV == 2) *reinterpret_cast<float2*>(out + (k0 + j) * 2 * NP) = make_float2(v[0], v[1]);
-          else out[(k0 + j) * 2 * NP] = v[0];
+        };
+        read(CL / 2 & 1, CL - 1);
+#pragma unroll
+        for (int m = CL / 2; m > 0; --m) {
+          if (m > 1) read(m - 1 & 1, 2 * m - 3);
+          __builtin_amdgcn_sched_barrier(0);
+          float v[2][2 * NS], s[2], sa[2], y[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int j = 2 * m - 1 - r;
+            const float4 xt = x[m & 1][r];
+            const float(&Bt)[NS] = Bv[m & 1][r], (&Ct)[NS] = Cv[m & 1][r];
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+              g[i] = fmaf(Ct[i], xt.z, g[i]);
+              const float ht = fmaf(xt.y, Bt[i], ah[j][i]);
+              v[r][i] = xt.y * g[i];
+              v[r][NS + i] = xt.z * ht;
+              const float gh = g[i] * ah[j][i];
+              s[r] = i ? fmaf(g[i], Bt[i], s[r]) : g[i] * Bt[i];
+              sa[r] = i ? fmaf(gh, a2[i], sa[r]) : gh * a2[i];
+              y[r] = i ? fmaf(Ct[i], ht, y[r]) : Ct[i] * ht;
+              dA[i] = fmaf(gh, xt.x, dA[i]);
+              g[i] *= e[j][i];
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            channel_sums<NS>(v[r]);
+            s[r] = quad_sum(s[r]);
+            sa[r] = quad_sum(sa[r]);
+            y[r] = quad_sum(y[r]);
+          }
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int j = 2 * m - 1 - r;
+            // (lanes that hold the same value write it to the same place: no branch in the walk)
+            res[(k0 + j) * 4 * CH] = q == 0 ? s[r] : q == 1 ? sa[r] : y[r];
+            float* to = out + (k0 + j) * 2 * NP;
+            if constexpr (NV == 4) *reinterpret_cast<float4*>(to) = make_float4(v[r][0], v[r][1], v[r][2], v[r][3]);
+            else if constexpr (NV == 2) *reinterpret_cast<float2*>(to) = make_float2(v[r][0], v[r][1]);
+            else to[0] = v[r][0];
+          }
         }
       }
     }
@@ -286,46 +323,95 @@ __global__ __launch_bounds__(512, 1) void ttt_scan_bwd(ScanArgs a) {
   }
 
   const int tid = threadIdx.x - 256;
-  const Lines<InT, OutT> at(a, p, begin, tid);
-  BcRows<InT, NP, TT> rows(a, p, begin, tid, true);
+  Lines<InT, OutT> at(a, p, begin, tid);
+  BcRows<InT, NP, TT, Wide> rows(a, p, begin, tid, true);
+  const int last = begin + max(tiles - 1, 0) * TT;
   const int64_t oc = p.c0 + at.quad;
   float bias[4], skip[4], dD[4], db[4];
   params<4>(bias, a.dt_bias ? a.dt_bias + oc : nullptr, at.n4, 0.f);
   params<4>(skip, a.Dskip ? a.Dskip + oc : nullptr, at.n4, 0.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) dD[i] = db[i] = 0.f;
-  OutT* dup = static_cast<OutT*>(a.du) + p.b * a.dus.b + oc;
-  OutT* ddp = static_cast<OutT*>(a.ddt) + p.b * a.ddts.b + oc;
-  OutT* dzp = at.z ? static_cast<OutT*>(a.dz) + p.b * a.dzs.b + oc : nullptr;
-  float* part = a.bcpart + ((static_cast<int64_t>(p.b) * a.G + p.g) * ((a.D / a.G + CH - 1) / CH) + p.tile) * a.T * 2 * a.N;
+  OutT* dup = static_cast<OutT*>(a.du) + p.b * a.dus.b + (last + at.row) * a.dus.t + oc;
+  OutT* ddp = static_cast<OutT*>(a.ddt) + p.b * a.ddts.b + (last + at.row) * a.ddts.t + oc;
+  OutT* dzp = a.z ? static_cast<OutT*>(a.dz) + p.b * a.dzs.b + (last + at.row) * a.dzs.t + oc : nullptr;
+  // its sums over the four waves: element tid + 256 k of a tile's [TT][2][NP]
+  constexpr int kSums = (TT * 2 * NP + 255) / 256;
+  float* part[kSums];
+  int sum_t[kSums];  // the token in the tile; beyond any where there is no such element
+#pragma unroll
+  for (int k = 0; k < kSums; ++k) {
+    const int x = tid + 256 * k, t = x / (2 * NP), w = x / NP % 2, m = x % NP;
+    sum_t[k] = x < TT * 2 * NP && m < a.N ? t : INT_MAX / 2;
+    part[k] = a.bcpart + ((static_cast<int64_t>(p.b) * a.G + p.g) * ((a.D / a.G + CH - 1) / CH) + p.tile) * a.T * 2 * a.N +
+              (static_cast<int64_t>(last + t) * 2 + w) * a.N + m;
+  }
 
-  // a tile's inputs of this thread; dt and its slope once they are known
+  // a tile's inputs of this thread as they come, two steps before they go into LDS (a step of the forward walk is shorter
+  // than a load)
+  struct Raw {
+    Piece<InT, 4> u, dt, z;
+    Piece<OutT, 4> dy;
+    typename BcRows<InT, NP, TT, Wide>::Values bc;
+  };
+  Raw far[2];
+  // what the way out wants of them
   struct Held {
     Piece<InT, 4> u, z;
     Piece<OutT, 4> dy;
     float dt[4], slope[4];
   };
   Held old, now, next;  // of the tile behind the walk, in the walk, before it
-  Piece<InT, 4> u_far, dt_far, z_far, dt_next;
-  Piece<OutT, 4> dy_far;
   const int steps = 2 * tiles;
   auto token = [&](int s) { return begin + (s < tiles ? s : steps - 1 - s) * TT; };
-  auto fetch = [&](int s) {
-    const int t0 = token(s), n = t0 + at.row < end ? at.n4 : 0;
-    const int64_t o = t0 - begin;
-    load<Wide>(u_far, at.u + o * a.us.t, n);
-    load<Wide>(dt_far, at.dt + o * a.dts.t, n);
-    if (s >= tiles) {
-      load<Wide>(dy_far, at.dy + o * a.ys.t, n);
-      if (at.z) load<Wide>(z_far, at.z + o * a.zs.t, n);
+  // Without a branch around the loads (see load_ahead): behind the last step the last one's again, and for the forward walk
+  // the last tile's dy and z, which are wanted first (z: or u), and are at hand from then on.
+  const OutT* gp = at.dy + (last - begin) * a.ys.t;
+  const int64_t zstride = a.z ? a.zs.t : a.us.t;
+  const InT* zp = (a.z ? at.z : at.u) + (last - begin) * zstride;
+  auto fetch = [&](Raw& r, int step) {
+    const int s = min(step, steps - 1), t0 = token(s), n = t0 + at.row < end ? at.n4 : 0;
+    const InT *u = at.u, *dt = at.dt, *z = zp;
+    const OutT* dy = gp;
+    if (Wide && t0 + TT > end) {  // rows behind the end: the last one instead
+      const int over = max(0, t0 + at.row - (end - 1));
+      u -= over * a.us.t;
+      dt -= over * a.dts.t;
     }
-    rows.load(t0, end, s + 1 < tiles ? 1 : s + 1 == tiles ? 0 : -1);
+    if (Wide && (s < tiles || t0 + TT > end)) {
+      const int over = max(0, (s < tiles ? last : t0) + at.row - (end - 1));
+      z -= over * zstride;
+      dy -= over * a.ys.t;
+    }
+    load_ahead<Wide>(r.u, u, n);
+    load_ahead<Wide>(r.dt, dt, n);
+    load_ahead<Wide>(r.dy, dy, s < tiles ? 0 : n);
+    load_ahead<Wide>(r.z, z, s < tiles ? 0 : n);
+    const int dir = step + 1 < tiles ? 1 : step + 1 == tiles || step + 1 >= steps ? 0 : -1;
+    rows.load(r.bc, t0, end, dir);
+    if (dir > 0) {
+      at.u += TT * a.us.t;
+      at.dt += TT * a.dts.t;
+    } else if (dir < 0) {
+      at.u -= TT * a.us.t;
+      at.dt -= TT * a.dts.t;
+      zp -= TT * zstride;
+      gp -= TT * a.ys.t;
+    }
   };
-  auto stage = [&](int s) {
-    const int n = token(s) + at.row < end ? at.n4 : 0;
+  auto stage = [&](Raw& r, int s) {
+    const int t0 = token(s), n = t0 + at.row < end ? at.n4 : 0;
+    if (t0 + TT > end || p.nc < CH) {
+      keep<Wide>(r.u, n);
+      keep<Wide>(r.dy, n);
+      keep<Wide>(r.z, n);
+    }
+    next.u = r.u;
+    next.z = r.z;
+    next.dy = r.dy;
     float4* to = &tile[s & 1][at.row][at.quad];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) next.dt[i] = dt_next.get(i) + bias[i], next.slope[i] = 1.f;
+    for (int i = 0; i < 4; ++i) next.dt[i] = r.dt.get(i) + bias[i], next.slope[i] = 1.f;
     if (s < tiles) {
       if (a.softplus) {
 #pragma unroll
@@ -343,14 +429,14 @@ __global__ __launch_bounds__(512, 1) void ttt_scan_bwd(ScanArgs a) {
         for (int i = 0; i < 4; ++i) next.dt[i] = softplus(next.dt[i], next.slope[i]);
       }
       zero_from(next.dt, n);
-      if (at.z) {
+      if (a.z) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[i] *= next.z.get(i) * sigmoid(next.z.get(i));
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) to[i] = make_float4(next.dt[i], next.dt[i] * next.u.get(i), d[i], 0.f);
     }
-    rows.stage(bc[s & 1]);
+    rows.stage(r.bc, bc[s & 1], t0, end);
   };
   auto finish = [&](int s) {
     const int t0 = token(s), n = t0 + at.row < end ? at.n4 : 0;
@@ -361,55 +447,53 @@ __global__ __launch_bounds__(512, 1) void ttt_scan_bwd(ScanArgs a) {
       const float uu = old.u.get(i);
       float dd = old.dy.get(i);
       o[2][i] = 0.f;
-      if (at.z) {
+      if (a.z) {
         const float x = old.z.get(i), sg = sigmoid(x), gate = x * sg;
         o[2][i] = dd * fmaf(skip[i], uu, v.z) * fmaf(gate, 1.f - sg, sg);
         dd *= gate;
       }
       o[0][i] = fmaf(old.dt[i], v.x, skip[i] * dd);
       o[1][i] = fmaf(uu, v.x, v.y * (1.f / kLog2e)) * old.slope[i];
-      if (i < n) {
-        dD[i] = fmaf(dd, uu, dD[i]);
-        db[i] += o[1][i];
-      }
+      dD[i] = fmaf(dd, uu, dD[i]);
+      db[i] += i < n ? o[1][i] : 0.f;
     }
-    const int64_t t = t0 + at.row;
-    Piece<OutT, 4> out;
-    out.set_all(o[0]);
-    store<Wide>(out, dup + t * a.dus.t, n);
-    out.set_all(o[1]);
-    store<Wide>(out, ddp + t * a.ddts.t, n);
-    if (at.z) {
-      out.set_all(o[2]);
-      store<Wide>(out, dzp + t * a.dzs.t, n);
-    }
+    Piece<OutT, 4> out[3];
 #pragma unroll
-    for (int x = tid; x < TT * 2 * NP; x += 256) {
-      const int k = x / (2 * NP), w = x / NP % 2, m = x % NP;
-      const float* v = &sbc[s & 1][0][0][0][0] + x;
+    for (int k = 0; k < 3; ++k) out[k].set_all(o[k]);
+    if (n > 0) {
+      store<Wide>(out[0], dup, n);
+      store<Wide>(out[1], ddp, n);
+      if (a.z) store<Wide>(out[2], dzp, n);
+    }
+    dup -= TT * a.dus.t;
+    ddp -= TT * a.ddts.t;
+    dzp -= TT * a.dzs.t;
+#pragma unroll
+    for (int k = 0; k < kSums; ++k) {
       constexpr int W = TT * 2 * NP;
-      if (t0 + k < end && m < a.N)
-        part[(static_cast<int64_t>(t0 + k) * 2 + w) * a.N + m] = (v[0] + v[W]) + (v[2 * W] + v[3 * W]);
+      const float* v = &sbc[s & 1][0][0][0][0] + (W < 256 ? tid % W : tid + 256 * k);
+      const float sum = (v[0] + v[W]) + (v[2 * W] + v[3 * W]);
+      if (t0 + sum_t[k] < end) *part[k] = sum;
+      part[k] -= TT * 2 * a.N;
     }
   };
   if (steps) {
-    fetch(0);
-    next.u = u_far;
-    dt_next = dt_far;
-    stage(0);
-    fetch(1);
+    fetch(far[0], 0);
+    fetch(far[1], 1);
+    stage(far[0], 0);
+    fetch(far[0], 2);
   }
-  for (int s = 0; s < steps; ++s) {
+  auto step = [&](Raw& r, int s) {
     __syncthreads();
     old = now;
     now = next;
-    next.u = u_far;
-    next.z = z_far;
-    next.dy = dy_far;
-    dt_next = dt_far;
     if (s > tiles) finish(s - 1);
-    if (s + 1 < steps) stage(s + 1);
-    if (s + 2 < steps) fetch(s + 2);
+    if (s + 1 < steps) stage(r, s + 1);
+    fetch(r, s + 3);
+  };
+  for (int s = 0; s < steps; s += 2) {
+    step(far[1], s);
+    step(far[0], s + 1);
   }
   __syncthreads();
   if (steps) {
@@ -419,9 +503,9 @@ __global__ __launch_bounds__(512, 1) void ttt_scan_bwd(ScanArgs a) {
   Piece<OutT, 4> none;
   none.zero();
   for (int64_t t = max(begin, end) + at.row; t < tokens; t += TT) {
-    store<Wide>(none, dup + t * a.dus.t, at.n4);
-    store<Wide>(none, ddp + t * a.ddts.t, at.n4);
-    if (at.z) store<Wide>(none, dzp + t * a.dzs.t, at.n4);
+    store<Wide>(none, static_cast<OutT*>(a.du) + p.b * a.dus.b + t * a.dus.t + oc, at.n4);
+    store<Wide>(none, static_cast<OutT*>(a.ddt) + p.b * a.ddts.b + t * a.ddts.t + oc, at.n4);
+    if (a.z) store<Wide>(none, static_cast<OutT*>(a.dz) + p.b * a.dzs.b + t * a.dzs.t + oc, at.n4);
   }
   // dD and ddt_bias: over the token rows
   float2* lines = reinterpret_cast<float2*>(&tile[0][0][0]);
@@ -443,10 +527,10 @@ __global__ __launch_bounds__(512, 1) void ttt_scan_bwd(ScanArgs a) {
   }
 }
 
-// dB and dC: the sum over the tiles of channels, in their order.
-template <typename OutT>
+// dB and dC: the sum over the tiles of channels, in their order; V neighbouring states of a token a thread.
+template <typename OutT, int V>
 __global__ __launch_bounds__(256) void ttt_scan_bc_sum(ScanBcSumArgs a) {
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, each = static_cast<int64_t>(a.T) * 2 * a.N;
+  const int64_t id = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * V, each = static_cast<int64_t>(a.T) * 2 * a.N;
   const int64_t bg = id / each;
   const int64_t e = id - bg * each;
   const int b = static_cast<int>(bg / a.G), g = static_cast<int>(bg % a.G);
@@ -454,14 +538,25 @@ __global__ __launch_bounds__(256) void ttt_scan_bc_sum(ScanBcSumArgs a) {
   const int64_t t = e / (2 * a.N);
   const int w = static_cast<int>(e / a.N % 2), n = static_cast<int>(e % a.N);
   const int len = a.lens ? max(0, min(a.lens[b], a.T)) : a.T;
-  float s = 0.f;
+  float s[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) s[i] = 0.f;
   if (t < len) {
     const float* p = a.part + bg * a.tiles * each + e;
-    for (int k = 0; k < a.tiles; ++k) s += p[k * each];
+#pragma unroll 8
+    for (int k = 0; k < a.tiles; ++k) {
+      if constexpr (V == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p + k * each);
+        s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
+      } else {
+        s[0] += p[k * each];
+      }
+    }
   }
   OutT* o = w ? static_cast<OutT*>(a.dC) + b * a.dcs.b + g * a.dcs.h + t * a.dcs.t
               : static_cast<OutT*>(a.dB) + b * a.dbs.b + g * a.dbs.h + t * a.dbs.t;
-  put(o + n, s);
+#pragma unroll
+  for (int i = 0; i < V; ++i) put(o + n + i, s[i]);
 }
 
 template <typename InT, typename OutT, int NS>
@@ -507,9 +602,15 @@ hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t s) { return go(false, 
 hipError_t launch_scan_bc_sum(const ScanBcSumArgs& a, hipStream_t s) {
   const int64_t n = static_cast<int64_t>(a.B) * a.G * a.T * 2 * a.N;
   if (n == 0) return hipSuccess;
-  const unsigned grid = static_cast<unsigned>((n + 255) / 256);
-  if (a.out_dtype == 0) ttt_scan_bc_sum<float><<<grid, 256, 0, s>>>(a);
-  else ttt_scan_bc_sum<uint16_t><<<grid, 256, 0, s>>>(a);
+  const bool four = a.N % 4 == 0;
+  const unsigned grid = static_cast<unsigned>((n / (four ? 4 : 1) + 255) / 256);
+  if (a.out_dtype == 0) {
+    if (four) ttt_scan_bc_sum<float, 4><<<grid, 256, 0, s>>>(a);
+    else ttt_scan_bc_sum<float, 1><<<grid, 256, 0, s>>>(a);
+  } else {
+    if (four) ttt_scan_bc_sum<uint16_t, 4><<<grid, 256, 0, s>>>(a);
+    else ttt_scan_bc_sum<uint16_t, 1><<<grid, 256, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 

@@ -82,16 +82,14 @@ __device__ __forceinline__ void lds_floats(float (&x)[NS], const float* p) {
 
 // A thread's pieces of a tile's B and C, four states of a token each, between the load and LDS.  Piece id is B's or C's
 // (id / (NQ TT)) of token id / NQ % TT, states 4 (id % NQ) on, for 256 threads.
-template <typename T, int NP, int TT>
+template <typename T, int NP, int TT, bool Wide>
 struct BcRows {
   static constexpr int NQ = NP / 4, kEach = (2 * TT * NQ + 255) / 256;
-  Piece<T, 4> v[kEach];
+  typedef Piece<T, 4> Values[kEach];
   const T* p[kEach];
-  int64_t step[kEach];  // elements from a tile to the next
+  int64_t row[kEach];  // elements from a token to the next
   int t[kEach], n[kEach], lds[kEach];
-  bool wide;
   __device__ __forceinline__ BcRows(const ScanArgs& a, const Place& at, int first, int tid, bool with_c) {
-    wide = a.bc_wide;
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
       const int id = tid + 256 * k, w = id / (NQ * TT), m = id % NQ;
@@ -99,31 +97,28 @@ struct BcRows {
       n[k] = w > (with_c ? 1 : 0) ? 0 : min(4, a.N - 4 * m);  // (may be negative)
       lds[k] = w > 1 ? -1 : (w * TT + t[k]) * NP + 4 * m;
       const T* base = static_cast<const T*>(w ? a.Cm : a.Bm) + (w ? at.b * a.cs.b + at.g * a.cs.h : at.b * a.bs.b + at.g * a.bs.h);
-      const int64_t row = w ? a.cs.t : a.bs.t;
-      p[k] = base + (first + t[k]) * row + 4 * m;
-      step[k] = row * TT;
+      row[k] = w ? a.cs.t : a.bs.t;
+      p[k] = base + (first + t[k]) * row[k] + (Wide && n[k] <= 0 ? 0 : 4 * m);
     }
   }
-  // the tile that begins at token first, as far as end; then on to the next tile (dir 1), the one before (-1) or none (0)
-  __device__ __forceinline__ void load(int first, int end, int dir) {
+  // the tile that begins at token first, as far as end (> first); then on to the next tile (dir 1), the one before (-1) or none
+  __device__ __forceinline__ void load(Values& v, int first, int end, int dir) {
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
-      const int m = first + t[k] < end ? n[k] : 0;
-      if (wide) {
-        if (m > 0) v[k].load(p[k]);
-        else v[k].zero();
-      } else {
-        v[k].load_some(p[k], m);
-      }
-      if (dir > 0) p[k] += step[k];
-      else if (dir < 0) p[k] -= step[k];
+      const T* src = p[k];
+      if (Wide && first + TT > end) src -= max(0, first + t[k] - (end - 1)) * row[k];  // (the last token instead)
+      load_ahead<Wide>(v[k], src, first + t[k] < end ? n[k] : 0);
+      if (dir > 0) p[k] += row[k] * TT;
+      else if (dir < 0) p[k] -= row[k] * TT;
     }
   }
-  __device__ __forceinline__ void stage(float* bc) const {
+  __device__ __forceinline__ void stage(Values& v, float* bc, int first, int end) const {
 #pragma unroll
-    for (int k = 0; k < kEach; ++k)
+    for (int k = 0; k < kEach; ++k) {
+      if (first + TT > end || n[k] <= 0) keep<Wide>(v[k], first + t[k] < end ? n[k] : 0);
       if (256 * (k + 1) <= 2 * TT * NQ || lds[k] >= 0)
         *reinterpret_cast<float4*>(bc + lds[k]) = make_float4(v[k].get(0), v[k].get(1), v[k].get(2), v[k].get(3));
+    }
   }
 };
 

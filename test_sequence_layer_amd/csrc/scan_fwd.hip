@@ -128,27 +128,36 @@ __global__ __launch_bounds__(THREADS, 2) void ttt_scan_fwd(ScanArgs a) {
   // this thread's piece of a tile: token row, channels oct .. oct + 7
   const int tid = threadIdx.x - WALKERS, row = tid >> 3, oct = (tid & 7) * 8;
   const int n8 = min(8, p.nc - oct);  // (may be negative)
-  const int64_t first = begin + row;
-  const InT* up = static_cast<const InT*>(a.u) + p.b * a.us.b + first * a.us.t + p.c0 + oct;
-  const InT* dp = static_cast<const InT*>(a.dt) + p.b * a.dts.b + first * a.dts.t + p.c0 + oct;
-  const InT* zp = States || !a.z ? nullptr : static_cast<const InT*>(a.z) + p.b * a.zs.b + first * a.zs.t + p.c0 + oct;
-  OutT* yp = static_cast<OutT*>(a.y) + p.b * a.ys.b + first * a.ys.t + p.c0 + oct;
-  BcRows<InT, NP, TT> next(a, p, begin, tid, !States);
+  const int64_t first = begin + row, oc = p.c0 + (Wide && n8 <= 0 ? 0 : oct);
+  const InT* up = static_cast<const InT*>(a.u) + p.b * a.us.b + first * a.us.t + oc;
+  const InT* dp = static_cast<const InT*>(a.dt) + p.b * a.dts.b + first * a.dts.t + oc;
+  const InT* zp = States || !a.z ? nullptr : static_cast<const InT*>(a.z) + p.b * a.zs.b + first * a.zs.t + oc;
+  OutT* yp = static_cast<OutT*>(a.y) + p.b * a.ys.b + first * a.ys.t + oc;
+  BcRows<InT, NP, TT, Wide> rows(a, p, begin, tid, !States);
+  typename BcRows<InT, NP, TT, Wide>::Values bc_far;
   float bias[8], skip[8];
   params<8>(bias, a.dt_bias ? a.dt_bias + p.c0 + oct : nullptr, n8, 0.f);
   if constexpr (!States) params<8>(skip, a.Dskip ? a.Dskip + p.c0 + oct : nullptr, n8, 0.f);
   // u of the tile before, this one, the next and the one behind it; the others' as far as they are wanted
   Piece<InT, 8> u_old, u_now, u_next, u_far, dt_next, dt_far, z_old, z_now;
+  auto count = [&](int t0) { return t0 + row < end ? n8 : 0; };  // of this thread's 8 channels in the tile at t0
   auto fetch = [&](int t0) {
-    const int n = t0 + row < end ? n8 : 0;
-    load<Wide>(u_far, up, n);
-    load<Wide>(dt_far, dp, n);
+    const int n = count(t0);
+    const InT *u = up, *d = dp;
+    if (Wide && t0 + TT > end) {  // rows behind the end: the last one instead
+      const int over = max(0, t0 + row - (end - 1));
+      u -= over * a.us.t;
+      d -= over * a.dts.t;
+    }
+    load_ahead<Wide>(u_far, u, n);
+    load_ahead<Wide>(dt_far, d, n);
     up += TT * a.us.t;
     dp += TT * a.dts.t;
-    next.load(t0, end, 1);
+    rows.load(bc_far, t0, end, 1);
   };
-  // (u is zero where there is no token; its dt has to be)
-  auto stage = [&](int buf, int n, bool whole) {
+  // (u is zero where there is no token, and so has its dt to be)
+  auto stage = [&](int buf, int t0) {
+    const int n = count(t0);
     float x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = dt_next.get(i) + bias[i];
@@ -156,7 +165,8 @@ __global__ __launch_bounds__(THREADS, 2) void ttt_scan_fwd(ScanArgs a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = softplus(x[i]);
     }
-    if (!Wide || !whole) {
+    if (!Wide || t0 + TT > end || p.nc < CH) {
+      keep<Wide>(u_next, n);
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = i < n ? x[i] : 0.f;
     }
@@ -173,7 +183,7 @@ __global__ __launch_bounds__(THREADS, 2) void ttt_scan_fwd(ScanArgs a) {
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = fmaf(skip[i], u_old.get(i), y[i]);
-    if (zp) {
+    if (a.z) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] *= z_old.get(i) * sigmoid(z_old.get(i));
     }
@@ -186,8 +196,8 @@ __global__ __launch_bounds__(THREADS, 2) void ttt_scan_fwd(ScanArgs a) {
     fetch(begin);
     u_next = u_far;
     dt_next = dt_far;
-    stage(0, begin + row < end ? n8 : 0, begin + TT <= end && p.nc == CH);
-    next.stage(bc[0]);
+    rows.stage(bc_far, bc[0], begin, end);
+    stage(0, begin);
     if (begin + TT < end) fetch(begin + TT);
   }
   u_now = u_next;
@@ -200,15 +210,17 @@ __global__ __launch_bounds__(THREADS, 2) void ttt_scan_fwd(ScanArgs a) {
     u_next = u_far;
     dt_next = dt_far;
     z_old = z_now;
-    next.stage(bc[buf ^ 1]);
+    rows.stage(bc_far, bc[buf ^ 1], t0 + TT, end);
     if (t0 + 2 * TT < end) fetch(t0 + 2 * TT);
     if constexpr (!States) {
-      if (zp) {
-        load<Wide>(z_now, zp, t0 + row < end ? n8 : 0);
+      if (a.z) {
+        const InT* z = zp;
+        if (Wide && t0 + TT > end) z -= max(0, t0 + row - (end - 1)) * a.zs.t;
+        load_ahead<Wide>(z_now, z, count(t0));
         zp += TT * a.zs.t;
       }
     }
-    stage(buf ^ 1, t0 + TT + row < end ? n8 : 0, t0 + 2 * TT <= end && p.nc == CH);
+    stage(buf ^ 1, t0 + TT);  // (zeros behind the last tile)
     if constexpr (!States) {
       if (t0 > begin) finish(buf ^ 1, n8);
     }
@@ -218,8 +230,7 @@ __global__ __launch_bounds__(THREADS, 2) void ttt_scan_fwd(ScanArgs a) {
     if (begin < end) {
       u_old = u_now;
       z_old = z_now;
-      const int last = begin + (end - begin - 1) / TT * TT;
-      finish(buf ^ 1, last + row < end ? n8 : 0);
+      finish(buf ^ 1, count(begin + (end - begin - 1) / TT * TT));
     }
     // rows behind the sequence's end (those of its last tile too)
     OutT* y0 = static_cast<OutT*>(a.y) + p.b * a.ys.b + p.c0 + oct;
@@ -263,7 +274,7 @@ __global__ __launch_bounds__(256) void ttt_scan_decode(ScanArgs a) {
         if (n < a.N) y = fmaf(Cv, h[i], y);
       }
       y = fmaf(skip, u, quad_sum(y));
-      if (zp) {
+      if (a.z) {
         const float x = as_f32(zp[t * a.zs.t]);
         y *= x * sigmoid(x);
       }
