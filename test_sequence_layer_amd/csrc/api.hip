@@ -1946,8 +1946,8 @@ ttt_status validate_conv_fwd(const ttt_short_conv_desc* d, const void* X, const 
                              const void* state, const int32_t* lens, const void* Y, const void* state_final, bool decode) {
   ttt_status st = check_conv_desc(d);
   if (st != TTT_OK) return st;
-  const int64_t pieces = ceil_div(d->D, d->in_dtype == TTT_BF16 ? 8 : 4);
-  if (static_cast<int64_t>(d->B) * (decode ? 1 : ceil_div(d->T, 8) + 1) * pieces > kMaxThreads) return TTT_ERR_SHAPE;
+  const int64_t blocks = ceil_div(d->D, d->in_dtype == TTT_BF16 ? 8 * 64 : 4 * 64);  // waves of a row
+  if (static_cast<int64_t>(d->B) * (decode ? 1 : ceil_div(d->T, 8) + 1) * blocks * 64 > kMaxThreads) return TTT_ERR_SHAPE;
   if (d->B == 0) return TTT_OK;
   if (!w || (decode && !state_final)) return TTT_ERR_NULL;
   if (d->T > 0 && (!X || !Y)) return TTT_ERR_NULL;
@@ -2074,7 +2074,7 @@ ttt_status validate_scan_fwd(const ttt_selective_scan_desc* d, const void* u, co
   if (st != TTT_OK) return st;
   ScanPlan plan = scan_plan(d, false);
   if (decode) plan.bytes = 0;
-  if (decode ? static_cast<int64_t>(d->B) * d->D * 4 > kMaxThreads : plan.blocks * plan.nseg * 512 > kMaxThreads)
+  if (decode ? static_cast<int64_t>(d->B) * ceil_div(d->D, 16) * 64 > kMaxThreads : plan.blocks * plan.nseg * 512 > kMaxThreads)
     return TTT_ERR_SHAPE;
   if (d->B == 0) return TTT_OK;
   if (!A || !h) return TTT_ERR_NULL;
@@ -2362,6 +2362,8 @@ ttt_status ttt_selective_scan_decode(const ttt_selective_scan_desc* desc, const 
   if (desc->B == 0 || desc->T == 0) return TTT_OK;
   const ScanViews v = scan_views(desc, u, dt, A, Bm, Cm, D, z, dt_bias, nullptr, lens, y);
   ttt::ScanArgs a = make_scan_args(desc, v, u, dt, A, Bm, Cm, D, z, dt_bias, nullptr, lens);
+  const int64_t four = 4 * dtype_size(desc->in_dtype);
+  a.wide = desc->N % 4 == 0 && view_aligned(v.Bm, four) && view_aligned(v.Cm, four) && all_aligned({A, h}, 16);
   a.y = y; a.h_final = h;
   return hip_status(ttt::launch_scan_decode(a, static_cast<hipStream_t>(stream)));
 }

@@ -34,14 +34,19 @@ __device__ __forceinline__ Place place(const ScanArgs& a, int64_t blk) {
   return p;
 }
 
-// A log2(e) of a lane's states, finite: -inf keeps nothing, and exp(0 A) of a token that is not there is 1.
+// A log2(e), finite: -inf keeps nothing, and exp(0 A) of a token that is not there is 1.
+__device__ __forceinline__ float scaled_decay(float A) {
+  const float x = A * kLog2e;
+  return x != x ? x : fminf(fmaxf(x, -3.0e38f), 3.0e38f);
+}
+
+// of a lane's states
 template <int NS>
 __device__ __forceinline__ void decays(float (&a2)[NS], const ScanArgs& a, int c, int q, bool on) {
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
     const int n = q * NS + i;
-    const float x = on && n < a.N ? a.A[static_cast<int64_t>(c) * a.N + n] * kLog2e : 0.f;
-    a2[i] = x != x ? x : fminf(fmaxf(x, -3.0e38f), 3.0e38f);
+    a2[i] = scaled_decay(on && n < a.N ? a.A[static_cast<int64_t>(c) * a.N + n] : 0.f);
   }
 }
 

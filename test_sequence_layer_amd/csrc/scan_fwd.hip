@@ -240,49 +240,107 @@ __global__ __launch_bounds__(THREADS, 2) void ttt_scan_fwd(ScanArgs a) {
   }
 }
 
-// A few tokens, the state in place: four lanes to a channel, NS states each.
-template <typename InT, typename OutT, int NS>
+// NS states from q NS on, in fours where N and the addresses allow it.
+template <bool Wide, int NS>
+__device__ __forceinline__ void token_states(float (&x)[NS], const float* p, int N, int q) {
+  if constexpr (Wide && NS >= 4) {
+#pragma unroll
+    for (int i = 0; i < NS; i += 4) {
+      const float4 v = q * NS + i < N ? *reinterpret_cast<const float4*>(p + q * NS + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+      x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+    }
+  } else {
+    load_states(x, p, N, q, true);
+  }
+}
+
+template <bool Wide, typename T, int NS>
+__device__ __forceinline__ void token_row(float (&x)[NS], const T* p, int N, int q) {
+  if constexpr (Wide && NS >= 4) {
+#pragma unroll
+    for (int i = 0; i < NS; i += 4) {
+      Piece<T, 4> v;
+      if (q * NS + i < N) v.load(p + q * NS + i);
+      else v.zero();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[i + j] = v.get(j);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) x[i] = q * NS + i < N ? as_f32(p[q * NS + i]) : 0.f;
+  }
+}
+
+// A few tokens, the state in place: four lanes to a channel, NS states each, S sequences to a thread, which share the
+// channel's parameters and whose loads are on their way together.  8 N bytes of state a channel against 5 N flops: a copy of
+// the state with the arithmetic on the way.
+template <typename InT, typename OutT, int NS, int S, bool Wide>
 __global__ __launch_bounds__(256) void ttt_scan_decode(ScanArgs a) {
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 64 + (threadIdx.x >> 2);
-  const int q = threadIdx.x & 3;
-  const int64_t b = id / a.D;
-  const int c = static_cast<int>(id - b * a.D);
-  if (b >= a.B) return;
-  const int len = a.lens ? max(0, min(a.lens[b], a.T)) : a.T, g = c / (a.D / a.G);
-  const InT* up = static_cast<const InT*>(a.u) + b * a.us.b + c;
-  const InT* dp = static_cast<const InT*>(a.dt) + b * a.dts.b + c;
-  const InT* zp = a.z ? static_cast<const InT*>(a.z) + b * a.zs.b + c : nullptr;
-  const InT* bp = static_cast<const InT*>(a.Bm) + b * a.bs.b + g * a.bs.h;
-  const InT* cp = static_cast<const InT*>(a.Cm) + b * a.cs.b + g * a.cs.h;
-  OutT* yp = static_cast<OutT*>(a.y) + b * a.ys.b + c;
-  float* hp = a.h_final + id * a.N;
-  if (len > 0) {
-    float a2[NS], h[NS];
-    decays(a2, a, c, q, true);
-    load_states(h, hp, a.N, q, true);
-    const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, skip = a.Dskip ? a.Dskip[c] : 0.f;
-    for (int64_t t = 0; t < len; ++t) {
-      const float u = as_f32(up[t * a.us.t]);
-      float dt = as_f32(dp[t * a.dts.t]) + bias, slope;
-      if (a.softplus) dt = softplus(dt, slope);
-      float y = 0.f;
+  const uint32_t blocks = (static_cast<uint32_t>(a.D) + 15) / 16;  // 16 channels to a wave
+  const uint32_t id = blockIdx.x * 4u + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = threadIdx.x & 3, c = static_cast<int>(id % blocks * 16 + (threadIdx.x >> 2 & 15));
+  const int64_t b0 = static_cast<int64_t>(id / blocks) * S;
+  if (b0 >= a.B || c >= a.D) return;
+  const int g = c / (a.D / a.G);
+  float h[S][NS], a2[NS];
+  int len[S], most = 0;
+  int64_t bs[S];
+#pragma unroll
+  for (int r = 0; r < S; ++r) {
+    bs[r] = min(b0 + r, static_cast<int64_t>(a.B) - 1);  // (behind the last sequence: nothing of it is written)
+    len[r] = b0 + r >= a.B ? 0 : a.lens ? max(0, min(a.lens[bs[r]], a.T)) : a.T;
+    most = max(most, len[r]);
+    token_states<Wide>(h[r], a.h_final + (bs[r] * a.D + c) * a.N, a.N, q);
+  }
+  token_states<Wide>(a2, a.A + static_cast<int64_t>(c) * a.N, a.N, q);
+#pragma unroll
+  for (int i = 0; i < NS; ++i) a2[i] = scaled_decay(a2[i]);
+  const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, skip = a.Dskip ? a.Dskip[c] : 0.f;
+  for (int64_t t = 0; t < most; ++t) {
+    float u[S], dt[S], z[S], Bv[S][NS], Cv[S][NS];
+#pragma unroll
+    for (int r = 0; r < S; ++r) {
+      const int64_t at = t < len[r] ? t : 0, b = bs[r];  // (its first token instead)
+      const bool any = len[r] > 0;
+      u[r] = any ? as_f32(static_cast<const InT*>(a.u)[b * a.us.b + at * a.us.t + c]) : 0.f;
+      dt[r] = any ? as_f32(static_cast<const InT*>(a.dt)[b * a.dts.b + at * a.dts.t + c]) : 0.f;
+      z[r] = any && a.z ? as_f32(static_cast<const InT*>(a.z)[b * a.zs.b + at * a.zs.t + c]) : 0.f;
+      if (any) {
+        token_row<Wide>(Bv[r], static_cast<const InT*>(a.Bm) + b * a.bs.b + g * a.bs.h + at * a.bs.t, a.N, q);
+        token_row<Wide>(Cv[r], static_cast<const InT*>(a.Cm) + b * a.cs.b + g * a.cs.h + at * a.cs.t, a.N, q);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < S; ++r) {
+      if (t >= len[r]) continue;
+      float step = dt[r] + bias, y = 0.f;
+      if (a.softplus) step = softplus(step);
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
-        const int n = q * NS + i;
-        const float Bv = n < a.N ? as_f32(bp[t * a.bs.t + n]) : 0.f, Cv = n < a.N ? as_f32(cp[t * a.cs.t + n]) : 0.f;
-        h[i] = fmaf(__builtin_amdgcn_exp2f(dt * a2[i]), h[i], dt * u * Bv);
-        if (n < a.N) y = fmaf(Cv, h[i], y);
+        h[r][i] = fmaf(__builtin_amdgcn_exp2f(step * a2[i]), h[r][i], step * u[r] * Bv[r][i]);
+        if (Wide || q * NS + i < a.N) y = fmaf(Cv[r][i], h[r][i], y);
       }
-      y = fmaf(skip, u, quad_sum(y));
-      if (a.z) {
-        const float x = as_f32(zp[t * a.zs.t]);
-        y *= x * sigmoid(x);
-      }
-      if (q == 0) put(yp + t * a.ys.t, y);
+      y = fmaf(skip, u[r], quad_sum(y));
+      if (a.z) y *= z[r] * sigmoid(z[r]);
+      if (q == 0) put(static_cast<OutT*>(a.y) + bs[r] * a.ys.b + t * a.ys.t + c, y);
     }
-    store_states(h, hp, a.N, q, true);
   }
-  for (int64_t t = len + q; t < a.T; t += 4) put(yp + t * a.ys.t, 0.f);
+#pragma unroll
+  for (int r = 0; r < S; ++r) {
+    if (len[r] > 0) {
+      float* to = a.h_final + (bs[r] * a.D + c) * a.N;
+      if constexpr (Wide && NS >= 4) {
+#pragma unroll
+        for (int i = 0; i < NS; i += 4)
+          if (q * NS + i < a.N)
+            *reinterpret_cast<float4*>(to + q * NS + i) = make_float4(h[r][i], h[r][i + 1], h[r][i + 2], h[r][i + 3]);
+      } else {
+        store_states(h[r], to, a.N, q, true);
+      }
+    }
+    if (b0 + r < a.B)
+      for (int64_t t = len[r] + q; t < a.T; t += 4) put(static_cast<OutT*>(a.y) + bs[r] * a.ys.b + t * a.ys.t + c, 0.f);
+  }
 }
 
 enum Which { STATES, FWD, DECODE };
@@ -301,11 +359,22 @@ hipError_t walk(bool states, const ScanArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <typename InT, typename OutT, int NS, int S>
+hipError_t token(const ScanArgs& a, hipStream_t s) {
+  const int64_t waves = static_cast<int64_t>((a.B + S - 1) / S) * ((a.D + 15) / 16);
+  const unsigned grid = static_cast<unsigned>((waves + 3) / 4);
+  if (a.wide) ttt_scan_decode<InT, OutT, NS, S, true><<<grid, 256, 0, s>>>(a);
+  else ttt_scan_decode<InT, OutT, NS, S, false><<<grid, 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+// Four sequences to a thread where that still leaves 2^17 threads, a wave for every place that the card has.
 template <typename InT, typename OutT, int NS>
 hipError_t token(const ScanArgs& a, hipStream_t s) {
-  const int64_t n = static_cast<int64_t>(a.B) * a.D;
-  ttt_scan_decode<InT, OutT, NS><<<static_cast<unsigned>((n + 63) / 64), 256, 0, s>>>(a);
-  return hipGetLastError();
+  if constexpr (NS < 8) {  // (of 32 states the registers would not do)
+    if (static_cast<int64_t>(a.B) * a.D >= 1 << 17) return token<InT, OutT, NS, 4>(a, s);
+  }
+  return token<InT, OutT, NS, 1>(a, s);
 }
 
 template <typename InT, typename OutT>

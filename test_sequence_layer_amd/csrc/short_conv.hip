@@ -5,6 +5,8 @@
 //
 //   y_t = act(bias + sum_j w_j x_{t-K+1+j}),   K = 2, 3, 4, act the identity or silu
 // 2 K flops a token and channel against 4 bytes: memory is the bound.
+#include <type_traits>
+
 #include "block_common.h"
 
 namespace ttt {
@@ -15,7 +17,33 @@ using namespace block;
 template <typename T>
 constexpr int kVec = 16 / static_cast<int>(sizeof(T));
 
-constexpr int kTok = 16;  // tokens of a thread in the forward
+// w and bias of a piece of channels
+template <int K, bool Wide, int V>
+__device__ __forceinline__ void taps(float (&w)[K][V], float (&bias)[V], const ConvArgs& a, int c, int n) {
+  if constexpr (Wide) {
+    Piece<float, V * K> all;
+    all.load(a.w + static_cast<int64_t>(c) * K);
+    Piece<float, V> b;
+    if (a.bias) b.load(a.bias + c);
+    else b.zero();
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      bias[i] = b.get(i);
+#pragma unroll
+      for (int j = 0; j < K; ++j) w[j][i] = all.get(i * K + j);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      bias[i] = a.bias && i < n ? a.bias[c + i] : 0.f;
+#pragma unroll
+      for (int j = 0; j < K; ++j) w[j][i] = i < n ? a.w[static_cast<int64_t>(c + i) * K + j] : 0.f;
+    }
+  }
+}
+
+// The wave's number in the launch, as a scalar: what is the same for a wave is computed once.
+__device__ __forceinline__ uint32_t wave_id() { return blockIdx.x * 4u + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
 __device__ __forceinline__ int length(const int32_t* lens, int b, int T) { return lens ? max(0, min(lens[b], T)) : T; }
 
@@ -27,14 +55,14 @@ __device__ __forceinline__ void row(Piece<T, V>& x, const ConvArgs& a, const T* 
   else x.zero();
 }
 
-template <typename InT, typename OutT, int K, bool Wide>
-__global__ __launch_bounds__(256) void ttt_conv_fwd(ConvArgs a, int pieces, int tiles) {
+// kTok tokens of a piece of channels to a thread, all of its rows on their way at once.
+template <typename InT, typename OutT, int K, bool Wide, int kTok>
+__global__ __launch_bounds__(256) void ttt_conv_fwd(ConvArgs a, int blocks, int tiles) {
   constexpr int V = kVec<InT>;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t line = id / pieces;
-  const int c = static_cast<int>(id - line * pieces) * V;
-  if (line >= static_cast<int64_t>(a.B) * tiles) return;
+  const uint32_t id = wave_id(), line = id / blocks;  // 64 pieces of channels to a wave
+  const int c = static_cast<int>((id % blocks) * 64 + (threadIdx.x & 63)) * V;
   const int b = static_cast<int>(line / tiles), tile = static_cast<int>(line % tiles);
+  if (b >= a.B || c >= a.D) return;
   const int n = min(V, a.D - c), len = length(a.lens, b, a.T), t0 = tile * kTok;
   const InT* xp = static_cast<const InT*>(a.X) + b * a.xs.b;
   const InT* st = a.state ? static_cast<const InT*>(a.state) + static_cast<int64_t>(b) * (K - 1) * a.D : nullptr;
@@ -42,18 +70,20 @@ __global__ __launch_bounds__(256) void ttt_conv_fwd(ConvArgs a, int pieces, int 
 
   Piece<InT, V> x[kTok + K - 1];
 #pragma unroll
-  for (int i = 0; i < kTok + K - 1; ++i) {
+  for (int i = 0; i < K - 1; ++i) {
     const int64_t r = t0 - (K - 1) + i;
     if (r < len) row<Wide, K>(x[i], a, xp, st, r, c, n);
     else x[i].zero();
   }
-  float w[K][V], bias[V];
+  if (Wide && t0 + kTok <= len) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    bias[i] = a.bias && i < n ? a.bias[c + i] : 0.f;
+    for (int i = 0; i < kTok; ++i) x[K - 1 + i].load(xp + (t0 + i) * a.xs.t + c);
+  } else {
 #pragma unroll
-    for (int j = 0; j < K; ++j) w[j][i] = i < n ? a.w[static_cast<int64_t>(c + i) * K + j] : 0.f;
+    for (int i = 0; i < kTok; ++i) load<Wide>(x[K - 1 + i], xp + (t0 + i) * a.xs.t + c, t0 + i < len ? n : 0);
   }
+  float w[K][V], bias[V];
+  taps<K, Wide>(w, bias, a, c, n);
 #pragma unroll
   for (int t = 0; t < kTok; ++t) {
     if (t0 + t >= a.T) break;
@@ -81,51 +111,62 @@ __global__ __launch_bounds__(256) void ttt_conv_fwd(ConvArgs a, int pieces, int 
   }
 }
 
-// A few tokens from the state, which goes on in place: one thread walks a piece of channels.
-template <typename InT, typename OutT, int K, bool Wide>
-__global__ __launch_bounds__(256) void ttt_conv_decode(ConvArgs a, int pieces) {
+// A few tokens from the state, which goes on in place: a thread walks a piece of channels of S sequences, which share the taps
+// and whose loads are on their way together.
+template <typename InT, typename OutT, int K, bool Wide, int S>
+__global__ __launch_bounds__(256) void ttt_conv_decode(ConvArgs a, int blocks) {
   constexpr int V = kVec<InT>;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t b = id / pieces;
-  const int c = static_cast<int>(id - b * pieces) * V;
-  if (b >= a.B) return;
-  const int n = min(V, a.D - c), len = length(a.lens, static_cast<int>(b), a.T);
-  const InT* xp = static_cast<const InT*>(a.X) + b * a.xs.b + c;
-  InT* st = static_cast<InT*>(a.state_out) + b * (K - 1) * a.D + c;
-  OutT* yp = static_cast<OutT*>(a.Y) + b * a.ys.b + c;
-  Piece<InT, V> x[K];
+  const uint32_t id = wave_id();
+  const int64_t b0 = static_cast<int64_t>(id / blocks) * S;
+  const int c = static_cast<int>((id % blocks) * 64 + (threadIdx.x & 63)) * V;
+  if (b0 >= a.B || c >= a.D) return;
+  const int n = min(V, a.D - c);
+  Piece<InT, V> x[S][K];
+  int len[S], most = 0;
 #pragma unroll
-  for (int j = 0; j < K - 1; ++j) load<Wide>(x[j], st + static_cast<int64_t>(j) * a.D, n);
+  for (int r = 0; r < S; ++r) {
+    len[r] = b0 + r < a.B ? length(a.lens, static_cast<int>(b0 + r), a.T) : 0;
+    most = max(most, len[r]);
+    const InT* st = static_cast<const InT*>(a.state_out) + (b0 + r) * (K - 1) * a.D + c;
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) load<Wide>(x[r][j], st + static_cast<int64_t>(j) * a.D, len[r] > 0 ? n : 0);
+  }
   float w[K][V], bias[V];
+  taps<K, Wide>(w, bias, a, c, n);
+  for (int64_t t = 0; t < most; ++t) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    bias[i] = a.bias && i < n ? a.bias[c + i] : 0.f;
+    for (int r = 0; r < S; ++r)
+      load<Wide>(x[r][K - 1], static_cast<const InT*>(a.X) + (b0 + r) * a.xs.b + t * a.xs.t + c, t < len[r] ? n : 0);
 #pragma unroll
-    for (int j = 0; j < K; ++j) w[j][i] = i < n ? a.w[static_cast<int64_t>(c + i) * K + j] : 0.f;
-  }
-  for (int t = 0; t < len; ++t) {
-    load<Wide>(x[K - 1], xp + t * a.xs.t, n);
-    float y[V];
+    for (int r = 0; r < S; ++r) {
+      if (t >= len[r]) continue;
+      float y[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float s = bias[i];
+      for (int i = 0; i < V; ++i) {
+        float s = bias[i];
 #pragma unroll
-      for (int j = 0; j < K; ++j) s = fmaf(w[j][i], x[j].get(i), s);
-      y[i] = a.silu ? s * sigmoid(s) : s;
+        for (int j = 0; j < K; ++j) s = fmaf(w[j][i], x[r][j].get(i), s);
+        y[i] = a.silu ? s * sigmoid(s) : s;
+      }
+      Piece<OutT, V> out;
+      out.set_all(y);
+      store<Wide>(out, static_cast<OutT*>(a.Y) + (b0 + r) * a.ys.b + t * a.ys.t + c, n);
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) x[r][j] = x[r][j + 1];
     }
-    Piece<OutT, V> out;
-    out.set_all(y);
-    store<Wide>(out, yp + t * a.ys.t, n);
-#pragma unroll
-    for (int j = 0; j < K - 1; ++j) x[j] = x[j + 1];
-  }
-  if (len > 0) {
-#pragma unroll
-    for (int j = 0; j < K - 1; ++j) store<Wide>(x[j], st + static_cast<int64_t>(j) * a.D, n);
   }
   Piece<OutT, V> none;
   none.zero();
-  for (int t = len; t < a.T; ++t) store<Wide>(none, yp + t * a.ys.t, n);
+#pragma unroll
+  for (int r = 0; r < S; ++r) {
+    if (b0 + r >= a.B) break;
+    if (len[r] > 0) {
+      InT* st = static_cast<InT*>(a.state_out) + (b0 + r) * (K - 1) * a.D + c;
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) store<Wide>(x[r][j], st + static_cast<int64_t>(j) * a.D, n);
+    }
+    for (int64_t t = len[r]; t < a.T; ++t) store<Wide>(none, static_cast<OutT*>(a.Y) + (b0 + r) * a.ys.b + t * a.ys.t + c, n);
+  }
 }
 
 // Backward.  With g_t = dy_t act'(pre_t), pre_t the sum before the activation:
@@ -141,11 +182,10 @@ __global__ __launch_bounds__(256) void ttt_conv_bwd(ConvArgs a, int cblocks) {
   constexpr int NP = K + 1;
   __shared__ float sums[kWalks][NP][kLanes * V + 4];
   const int lane = threadIdx.x % kLanes, walk = threadIdx.x / kLanes;
-  const int64_t blk = blockIdx.x;
-  const int cb = static_cast<int>(blk % cblocks);
-  const int64_t line = blk / cblocks;
-  const int p = static_cast<int>(line % a.nparts);
-  const int64_t b = line / a.nparts;
+  const int cb = static_cast<int>(blockIdx.x % static_cast<uint32_t>(cblocks));
+  const uint32_t line = blockIdx.x / static_cast<uint32_t>(cblocks);
+  const int p = static_cast<int>(line % static_cast<uint32_t>(a.nparts));
+  const int64_t b = line / static_cast<uint32_t>(a.nparts);
   const int c = (cb * kLanes + lane) * V;
   const int n = min(V, a.D - c);  // (may be negative)
   const int len = length(a.lens, static_cast<int>(b), a.T);
@@ -158,14 +198,11 @@ __global__ __launch_bounds__(256) void ttt_conv_bwd(ConvArgs a, int cblocks) {
   const OutT* ds = a.dstate_out ? static_cast<const OutT*>(a.dstate_out) + b * (K - 1) * a.D + c : nullptr;
 
   float w[K][V], bias[V], dw[NP][V];
+  taps<K, Wide>(w, bias, a, n > 0 ? c : 0, n);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    bias[i] = a.bias && i < n ? a.bias[c + i] : 0.f;
-#pragma unroll
-    for (int j = 0; j < K; ++j) w[j][i] = i < n ? a.w[static_cast<int64_t>(c + i) * K + j] : 0.f;
+  for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int j = 0; j < NP; ++j) dw[j][i] = 0.f;
-  }
   if (n > 0 && (t0 < a.T || seg == 0)) {  // (without tokens the state's gradient is still handed on)
     const int64_t t1 = min(static_cast<int64_t>(a.T), t0 + a.seg), end = min(t1, static_cast<int64_t>(len));
     Piece<InT, V> x[K];   // x_{t-K+1} .. x_t
@@ -260,14 +297,23 @@ enum Which { FWD, BWD, DECODE };
 template <typename InT, typename OutT, int K, bool Wide>
 hipError_t go(Which which, const ConvArgs& a, hipStream_t s) {
   constexpr int V = kVec<InT>;
-  const int pieces = (a.D + V - 1) / V;
+  const int pieces = (a.D + V - 1) / V, blocks = (pieces + 63) / 64;
   if (which == FWD) {
-    const int tiles = a.T > 0 ? (a.T + kTok - 1) / kTok : 1;  // (without tokens the state is still handed on)
-    const int64_t n = static_cast<int64_t>(a.B) * tiles * pieces;
-    ttt_conv_fwd<InT, OutT, K, Wide><<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(a, pieces, tiles);
+    // long walks read fewer rows twice; short ones are more threads: from 2^18 of the long ones on there are enough
+    auto run = [&](auto tok) {
+      const int tiles = a.T > 0 ? (a.T + tok - 1) / tok : 1;  // (without tokens the state is still handed on)
+      const int64_t waves = static_cast<int64_t>(a.B) * tiles * blocks;
+      ttt_conv_fwd<InT, OutT, K, Wide, tok><<<static_cast<unsigned>((waves + 3) / 4), 256, 0, s>>>(a, blocks, tiles);
+    };
+    if (static_cast<int64_t>(a.B) * (a.T / 32) * pieces >= 1 << 18) run(std::integral_constant<int, 32>{});
+    else run(std::integral_constant<int, 8>{});
   } else if (which == DECODE) {
-    const int64_t n = static_cast<int64_t>(a.B) * pieces;
-    ttt_conv_decode<InT, OutT, K, Wide><<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(a, pieces);
+    // four sequences to a thread where that leaves 2^15 threads, two waves to a SIMD in half of the card
+    const bool four = static_cast<int64_t>(a.B) * pieces >= 1 << 17;
+    const int64_t waves = static_cast<int64_t>(four ? (a.B + 3) / 4 : a.B) * blocks;
+    const unsigned grid = static_cast<unsigned>((waves + 3) / 4);
+    if (four) ttt_conv_decode<InT, OutT, K, Wide, 4><<<grid, 256, 0, s>>>(a, blocks);
+    else ttt_conv_decode<InT, OutT, K, Wide, 1><<<grid, 256, 0, s>>>(a, blocks);
   } else {
     const int cblocks = (pieces + kLanes - 1) / kLanes;
     const int64_t n = static_cast<int64_t>(a.B) * a.nparts * cblocks;
