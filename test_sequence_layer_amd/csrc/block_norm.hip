@@ -7,6 +7,8 @@
 //   s = res + alpha v,                    y = NORM(s) gamma_pre + beta_pre
 // NORM divides by the root of the mean square plus eps, the layer norm after taking the mean off.  Each row is read once,
 // kept in registers and written once: memory is the bound.
+#include <type_traits>
+
 #include "block_common.h"
 
 namespace ttt {
@@ -16,56 +18,100 @@ using namespace block;
 
 __device__ __forceinline__ float wave_sum(float x) { return mfma::sum_rows(mfma::sum16(x)); }
 
-// Sums over the W waves of a row's team.  Each sum has a slot of its own, and two rows in a row two sets of them, so that
-// one barrier a sum is enough.
+__device__ __forceinline__ double wave_sum(double x) {
+  auto step = [&](auto ctrl) {
+    const uint64_t v = __double_as_longlong(x);
+    const uint32_t lo = __builtin_amdgcn_mov_dpp(static_cast<int>(v), decltype(ctrl)::value, 0xf, 0xf, true);
+    const uint32_t hi = __builtin_amdgcn_mov_dpp(static_cast<int>(v >> 32), decltype(ctrl)::value, 0xf, 0xf, true);
+    x += __longlong_as_double(static_cast<uint64_t>(hi) << 32 | lo);
+  };
+  step(std::integral_constant<int, 0xB1>{});   // quad_perm [1,0,3,2]
+  step(std::integral_constant<int, 0x4E>{});   // quad_perm [2,3,0,1]
+  step(std::integral_constant<int, 0x141>{});  // row_half_mirror
+  step(std::integral_constant<int, 0x140>{});  // row_mirror
+  auto pair = [&](auto swap) {
+    const uint64_t v = __double_as_longlong(x);
+    const auto lo = swap(static_cast<uint32_t>(v)), hi = swap(static_cast<uint32_t>(v >> 32));
+    x = __longlong_as_double(static_cast<uint64_t>(hi[0]) << 32 | lo[0]) + __longlong_as_double(static_cast<uint64_t>(hi[1]) << 32 | lo[1]);
+  };
+  pair([](uint32_t v) { return __builtin_amdgcn_permlane16_swap(v, v, false, false); });
+  pair([](uint32_t v) { return __builtin_amdgcn_permlane32_swap(v, v, false, false); });
+  return x;
+}
+
+// Sums over the W waves of a row's team.  Each sum has a slot of its own, eight of them in turn, so that one barrier a sum is
+// enough: who writes a slot again is seven barriers further on than who still reads it could be.
 template <int W>
 struct Team {
-  float (*slots)[W][2];  // [slot][wave][2] of this team
+  double (*slots)[W][2];  // [slot][wave][2] of this team
   int wave, next;
-  __device__ __forceinline__ float2 sum2(float a, float b) {
+  static constexpr int kSlots = 8;
+  template <typename F>
+  __device__ __forceinline__ void sum2(F& a, F& b) {
     a = wave_sum(a);
     b = wave_sum(b);
     if constexpr (W > 1) {
-      float (*s)[2] = slots[next];
+      double (*s)[2] = slots[next];
       next = next + 1 == kSlots ? 0 : next + 1;
       if ((threadIdx.x & 63) == 0) {
         s[wave][0] = a;
         s[wave][1] = b;
       }
       __syncthreads();
-      a = s[0][0];
-      b = s[0][1];
+      a = static_cast<F>(s[0][0]);
+      b = static_cast<F>(s[0][1]);
 #pragma unroll
       for (int i = 1; i < W; ++i) {
-        a += s[i][0];
-        b += s[i][1];
+        a += static_cast<F>(s[i][0]);
+        b += static_cast<F>(s[i][1]);
       }
     }
-    return make_float2(a, b);
   }
-  static constexpr int kSlots = 8;
 };
 
-// mean (0 for the root-mean-square norm) and 1 / sqrt(var + eps) of a row of D elements, NE of them in a thread (zeros
-// behind the row's end).  The mean comes first, then the squares of what is left: no cancellation.
+// mean (0 for the root-mean-square norm) and 1 / sqrt(var + eps) of a row of 1 / inv elements, NE of them in a thread (zeros
+// behind the row's end).  The layer norm's two sums go in 64 bits, so that one pass is enough: nothing cancels in
+// sum x^2 - D mean^2 that 32 bits would have kept.
 template <int W, int NE>
-__device__ __forceinline__ float2 stats(const float (&x)[NE], int valid, int D, bool layer, float eps, Team<W>& team) {
-  float mean = 0.f;
+__device__ __forceinline__ float2 stats(const float (&x)[NE], int valid, double inv, bool layer, float eps, Team<W>& team) {
   if (layer) {
-    float s = 0.f;
+    double s = 0.0, ss = 0.0;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) s += x[i];
-    mean = team.sum2(s, 0.f).x / static_cast<float>(D);
+    for (int i = 0; i < NE; ++i) {
+      const double v = i < valid ? static_cast<double>(x[i]) : 0.0;
+      s += v;
+      ss = fma(v, v, ss);
+    }
+    team.sum2(s, ss);
+    const double mean = s * inv;
+    const float var = static_cast<float>(fmax(fma(ss, inv, -mean * mean), 0.0));
+    return make_float2(static_cast<float>(mean), __builtin_amdgcn_rsqf(var + eps));
   }
-  float s = 0.f;
+  float s = 0.f, none = 0.f;
 #pragma unroll
-  for (int i = 0; i < NE; ++i) {
-    const float d = i < valid ? x[i] - mean : 0.f;
-    s = fmaf(d, d, s);
-  }
-  const float var = team.sum2(s, 0.f).x / static_cast<float>(D) + eps;
-  return make_float2(mean, 1.f / sqrtf(var));
+  for (int i = 0; i < NE; ++i) s = i < valid ? fmaf(x[i], x[i], s) : s;
+  team.sum2(s, none);
+  return make_float2(0.f, __builtin_amdgcn_rsqf(fmaf(s, static_cast<float>(inv), eps)));
 }
+
+// A row's sequence and token, and the one that is ``step`` rows further on.
+struct Walk {
+  int64_t b, t, T, db, dt;
+  __device__ __forceinline__ Walk(int64_t line, int64_t step, int64_t T_) : T(T_) {
+    b = line / T;
+    t = line - b * T;
+    db = step / T;
+    dt = step - db * T;
+  }
+  __device__ __forceinline__ void advance() {
+    b += db;
+    t += dt;
+    if (t >= T) {
+      t -= T;
+      ++b;
+    }
+  }
+};
 
 // A thread's elements of a row: NC pieces of 8, piece i at 8 (i R + r); element by element instead at i R + r.
 template <int R, int NC, bool Wide>
@@ -136,13 +182,15 @@ __device__ __forceinline__ bool dead(const NormArgs& a, int64_t b, int64_t t) {
 template <typename T, typename RT, int R, int NC, bool Wide>
 __global__ __launch_bounds__(R) void ttt_norm_fwd(NormArgs a) {
   constexpr int W = R / 64, NE = 8 * NC;
-  __shared__ float slots[Team<W>::kSlots][W][2];
+  __shared__ double slots[Team<W>::kSlots][W][2];
   Team<W> team{slots, static_cast<int>(threadIdx.x >> 6), 0};
   const Cols<R, NC, Wide> cols{static_cast<int>(threadIdx.x), a.D};
   const int valid = cols.valid();
+  const double inv = 1.0 / static_cast<double>(a.D);
   const int64_t rows = static_cast<int64_t>(a.B) * a.T;
-  for (int64_t line = blockIdx.x; line < rows; line += gridDim.x) {
-    const int64_t b = line / a.T, t = line - b * a.T;
+  Walk at(blockIdx.x, gridDim.x, a.T);
+  for (int64_t line = blockIdx.x; line < rows; line += gridDim.x, at.advance()) {
+    const int64_t b = at.b, t = at.t;
     RT* sp = a.S ? static_cast<RT*>(a.S) + b * a.ss.b + t * a.ss.t : nullptr;
     T* yp = a.Y ? static_cast<T*>(a.Y) + b * a.ys.b + t * a.ys.t : nullptr;
     float v[NE], w[NE];
@@ -166,7 +214,7 @@ __global__ __launch_bounds__(R) void ttt_norm_fwd(NormArgs a) {
       }
     }
     if (a.gamma_post) {
-      const float2 st = stats<W>(v, valid, a.D, a.layer, a.eps, team);
+      const float2 st = stats<W>(v, valid, inv, a.layer, a.eps, team);
       cols.param(w, a.gamma_post, 1.f);
 #pragma unroll
       for (int i = 0; i < NE; ++i) v[i] = (v[i] - st.x) * st.y * w[i];
@@ -191,7 +239,7 @@ __global__ __launch_bounds__(R) void ttt_norm_fwd(NormArgs a) {
     }
     if (sp) cols.store(v, sp);
     if (yp) {
-      const float2 st = stats<W>(v, valid, a.D, a.layer, a.eps, team);
+      const float2 st = stats<W>(v, valid, inv, a.layer, a.eps, team);
       cols.param(w, a.gamma_pre, 1.f);
 #pragma unroll
       for (int i = 0; i < NE; ++i) v[i] = (v[i] - st.x) * st.y * w[i];
@@ -207,7 +255,7 @@ __global__ __launch_bounds__(R) void ttt_norm_fwd(NormArgs a) {
 
 // The gradient through unit = (x - mean) rstd, in place: h holds the gradient of unit.
 template <int W, int NE>
-__device__ __forceinline__ void norm_back(float (&h)[NE], const float (&unit)[NE], float rstd, int valid, int D, bool layer,
+__device__ __forceinline__ void norm_back(float (&h)[NE], const float (&unit)[NE], float rstd, int valid, float inv, bool layer,
                                           Team<W>& team) {
   float s = 0.f, m = 0.f;
 #pragma unroll
@@ -216,8 +264,8 @@ __device__ __forceinline__ void norm_back(float (&h)[NE], const float (&unit)[NE
     s = fmaf(h[i], unit[i], s);
     m += h[i];
   }
-  const float2 sums = team.sum2(s, layer ? m : 0.f);
-  const float cs = sums.x / static_cast<float>(D), cm = sums.y / static_cast<float>(D);
+  team.sum2(s, m);
+  const float cs = s * inv, cm = layer ? m * inv : 0.f;
 #pragma unroll
   for (int i = 0; i < NE; ++i) h[i] = (h[i] - cm - unit[i] * cs) * rstd;
 }
@@ -227,34 +275,87 @@ __device__ __forceinline__ void norm_back(float (&h)[NE], const float (&unit)[NE
 template <typename T, typename RT, int R, int NC, bool Wide>
 __global__ __launch_bounds__(R < 256 ? 256 : R) void ttt_norm_bwd(NormArgs a) {
   constexpr int W = R / 64, NE = 8 * NC, TEAMS = R < 256 ? 256 / R : 1;
-  __shared__ float slots[TEAMS][Team<W>::kSlots][W][2];
+  __shared__ double slots[TEAMS][Team<W>::kSlots][W][2];
   __shared__ float sums[TEAMS > 1 ? 256 : 1][TEAMS > 1 ? 9 : 1];
-  const int who = threadIdx.x / R, r = threadIdx.x % R;
+  const int who = R < 256 ? __builtin_amdgcn_readfirstlane(threadIdx.x / R) : 0, r = threadIdx.x % R;
   Team<W> team{slots[who], r >> 6, 0};
   const Cols<R, NC, Wide> cols{r, a.D};
   const int valid = cols.valid();
+  const double inv = 1.0 / static_cast<double>(a.D);
   const int64_t rows = static_cast<int64_t>(a.B) * a.T;
+  // the columns' parameters stay in registers too (teams of 1024: there are none left)
+  constexpr bool kHeld = R < 1024;
+  float wa[NE], wp[NE], wb[NE], wn[NE];
+  auto fill = [&] {
+    cols.param(wa, a.alpha, 1.f);
+    cols.param(wp, a.gamma_post, 1.f);
+    cols.param(wb, a.beta_post, 0.f);
+    cols.param(wn, a.gamma_pre, 1.f);
+  };
+  if constexpr (kHeld) fill();
   float acc[5][NE];
 #pragma unroll
   for (int k = 0; k < 5; ++k)
 #pragma unroll
     for (int i = 0; i < NE; ++i) acc[k][i] = 0.f;
   const int64_t step = static_cast<int64_t>(gridDim.x) * TEAMS;
-  for (int64_t first = static_cast<int64_t>(blockIdx.x) * TEAMS; first < rows; first += step) {
-    const int64_t line = min(first + who, rows - 1);
-    const int64_t b = line / a.T, t = line - b * a.T;
-    const bool off = first + who >= rows, none = off || dead(a, b, t);
-    // (a team without a row goes along on zeros: the others wait for it at the sums)
-    float x[NE], z[NE], u1[NE], v[NE], u2[NE], g[NE], w[NE];
-    float gate[NE], slope[NE];
+  int64_t first = static_cast<int64_t>(blockIdx.x) * TEAMS;
+  Walk at(first + who, step, max(a.T, 1)), ahead = at;
+  // the row's pieces as they lie in memory, on their way a row ahead; what is not there is read from the workspace and dropped
+  struct Raw {
+    Piece<T, 8> x[NC], z[NC], dy[NC];
+    Piece<RT, 8> res[NC], ds[NC];
+  } raw;
+  auto fetch = [&](int64_t line) {
+    const int64_t b = line < rows ? ahead.b : 0, t = line < rows ? ahead.t : 0;
+    auto get = [&](auto& v, const auto* p, int64_t o) {
+      typedef std::remove_const_t<std::remove_pointer_t<decltype(p)>> E;
+      const E* from = p ? p + o : reinterpret_cast<const E*>(a.part);
 #pragma unroll
-    for (int i = 0; i < NE; ++i) x[i] = z[i] = g[i] = u2[i] = v[i] = 0.f;
-    if (!none) {
-      cols.load(x, static_cast<const T*>(a.X) + b * a.xs.b + t * a.xs.t);
-      if (a.Z) cols.load(z, static_cast<const T*>(a.Z) + b * a.zs.b + t * a.zs.t);
-      if (a.res) cols.load(u2, static_cast<const RT*>(a.res) + b * a.rs.b + t * a.rs.t);
-      if (a.dS) cols.load(v, static_cast<const RT*>(a.dS) + b * a.ss.b + t * a.ss.t);
-      if (a.dY) cols.load(g, static_cast<const T*>(a.dY) + b * a.ys.b + t * a.ys.t);
+      for (int i = 0; i < NC; ++i) v[i].load(from + (8 * (i * R + r) < a.D ? 8 * (i * R + r) : 0));
+    };
+    get(raw.x, static_cast<const T*>(a.X), b * a.xs.b + t * a.xs.t);
+    get(raw.z, static_cast<const T*>(a.Z), b * a.zs.b + t * a.zs.t);
+    get(raw.res, static_cast<const RT*>(a.res), b * a.rs.b + t * a.rs.t);
+    get(raw.ds, static_cast<const RT*>(a.dS), b * a.ss.b + t * a.ss.t);
+    get(raw.dy, static_cast<const T*>(a.dY), b * a.ys.b + t * a.ys.t);
+  };
+  if constexpr (Wide) {
+    if (first < rows) fetch(first + who);
+  }
+  for (; first < rows; first += step) {
+    const int64_t b = at.b, t = at.t;
+    const bool off = first + who >= rows, none = off || dead(a, b, t);
+    at.advance();
+    // (a team without a row goes along on zeros: the others wait for it at the sums)
+    float x[NE], z[NE], u1[NE], v[NE], u2[NE], g[NE];
+    float gate[NE], slope[NE];
+    if constexpr (Wide) {
+      auto take = [&](float (&to)[NE], auto& from, bool on) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const bool here = on && !none && 8 * (i * R + r) < a.D;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) to[8 * i + j] = here ? from[i].get(j) : 0.f;
+        }
+      };
+      take(x, raw.x, true);
+      take(z, raw.z, a.Z != nullptr);
+      take(u2, raw.res, a.res != nullptr);
+      take(v, raw.ds, a.dS != nullptr);
+      take(g, raw.dy, a.dY != nullptr);
+      ahead.advance();
+      if (first + step < rows) fetch(first + step + who);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) x[i] = z[i] = g[i] = u2[i] = v[i] = 0.f;
+      if (!none) {
+        cols.load(x, static_cast<const T*>(a.X) + b * a.xs.b + t * a.xs.t);
+        if (a.Z) cols.load(z, static_cast<const T*>(a.Z) + b * a.zs.b + t * a.zs.t);
+        if (a.res) cols.load(u2, static_cast<const RT*>(a.res) + b * a.rs.b + t * a.rs.t);
+        if (a.dS) cols.load(v, static_cast<const RT*>(a.dS) + b * a.ss.b + t * a.ss.t);
+        if (a.dY) cols.load(g, static_cast<const T*>(a.dY) + b * a.ys.b + t * a.ys.t);
+      }
     }
     float ds[NE], n1[NE];
 #pragma unroll
@@ -273,29 +374,24 @@ __global__ __launch_bounds__(R < 256 ? 256 : R) void ttt_norm_bwd(NormArgs a) {
     }
     float rstd1 = 1.f;
     if (a.gamma_post) {
-      const float2 st = stats<W>(u1, valid, a.D, a.layer, a.eps, team);
+      const float2 st = stats<W>(u1, valid, inv, a.layer, a.eps, team);
       rstd1 = st.y;
-      cols.param(w, a.gamma_post, 1.f);
+      if constexpr (!kHeld) fill();
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
         u1[i] = i < valid ? (u1[i] - st.x) * st.y : 0.f;
-        n1[i] = u1[i] * w[i];
-      }
-      if (a.beta_post) {
-        cols.param(w, a.beta_post, 0.f);
-#pragma unroll
-        for (int i = 0; i < NE; ++i) n1[i] += w[i];
+        n1[i] = fmaf(u1[i], wp[i], wb[i]);
       }
     }
-    cols.param(w, a.alpha, 1.f);
+    if constexpr (!kHeld) cols.param(wa, a.alpha, 1.f);
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
       v[i] = a.gate_first ? n1[i] : n1[i] * gate[i];
-      u2[i] = fmaf(w[i], v[i], u2[i]);
+      u2[i] = fmaf(wa[i], v[i], u2[i]);
     }
     if (a.dY) {
-      const float2 st = stats<W>(u2, valid, a.D, a.layer, a.eps, team);
-      cols.param(w, a.gamma_pre, 1.f);
+      const float2 st = stats<W>(u2, valid, inv, a.layer, a.eps, team);
+      if constexpr (!kHeld) cols.param(wn, a.gamma_pre, 1.f);
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
         u2[i] = i < valid ? (u2[i] - st.x) * st.y : 0.f;
@@ -303,9 +399,9 @@ __global__ __launch_bounds__(R < 256 ? 256 : R) void ttt_norm_bwd(NormArgs a) {
           acc[3][i] = fmaf(g[i], u2[i], acc[3][i]);
           acc[4][i] += g[i];
         }
-        g[i] *= w[i];
+        g[i] *= wn[i];
       }
-      norm_back<W>(g, u2, st.y, valid, a.D, a.layer, team);
+      norm_back<W>(g, u2, st.y, valid, static_cast<float>(inv), a.layer, team);
 #pragma unroll
       for (int i = 0; i < NE; ++i) ds[i] += g[i];
     }
@@ -314,25 +410,25 @@ __global__ __launch_bounds__(R < 256 ? 256 : R) void ttt_norm_bwd(NormArgs a) {
       for (int i = 0; i < NE; ++i) ds[i] = 0.f;
     }
     if (a.dres && !off) cols.store(ds, static_cast<RT*>(a.dres) + b * a.drs.b + t * a.drs.t);
-    cols.param(w, a.alpha, 1.f);
+    if constexpr (!kHeld) cols.param(wa, a.alpha, 1.f);
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
       if (!none) acc[0][i] = fmaf(ds[i], v[i], acc[0][i]);
-      g[i] = ds[i] * w[i];                                   // dv
+      g[i] = ds[i] * wa[i];                                  // dv
       z[i] = a.gate_first ? 0.f : g[i] * n1[i] * slope[i];   // dz
       if (!a.gate_first) g[i] *= gate[i];                    // dn
     }
     if (a.gamma_post) {
-      cols.param(w, a.gamma_post, 1.f);
+      if constexpr (!kHeld) cols.param(wp, a.gamma_post, 1.f);
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
         if (!none) {
           acc[1][i] = fmaf(g[i], u1[i], acc[1][i]);
           acc[2][i] += g[i];
         }
-        g[i] *= w[i];
+        g[i] *= wp[i];
       }
-      norm_back<W>(g, u1, rstd1, valid, a.D, a.layer, team);
+      norm_back<W>(g, u1, rstd1, valid, static_cast<float>(inv), a.layer, team);
     }
     if (a.gate_first) {
 #pragma unroll
