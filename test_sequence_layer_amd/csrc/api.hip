@@ -3,6 +3,7 @@
 #include <limits.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <initializer_list>
 #include <mutex>
 
@@ -2011,17 +2012,42 @@ struct ScanPlan {
   int64_t hseg, sseg, gseg, ckpt, bcpart, part, bytes;
 };
 
+// Tokens of a segment: those that take the least time by a model of it.  One workgroup runs on each of the 256 CUs, 64
+// channels of one segment, and a launch takes as many rounds as that gives.  One segment of 2048 tokens takes 133 us, its
+// gradients 635 to 687: 0.07 and 0.35 us a token.  More than one walk the tokens once more for their start states; what that
+// costs (0.85 and 0.3 of a token, 8 us and 0.25 us a segment) is no measurement of its own but was set so that the choice
+// comes near the best of 1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48 and 64 segments.  Measured, us, bf16, N = 16:
+//   blocks, tokens          8, 2048   24, 2048   24, 8192   48, 2048   96, 2048   128, 2048   144, 2048   288, 2048
+//   forward, one segment        133        132        513        133        133         134         136         268
+//   forward, chosen              33         41        142         80        111         124         135         268
+//   forward, best                31         44        126         70        110         126         136         268
+//   gradients, one              635        653       2562        654        658         687         682        1362
+//   gradients, chosen            63        146        377        203        349         523         574        1006
+//   gradients, best              64        143        373        203        346         466         568        1006
+int64_t scan_seglen(int64_t blocks, int64_t T, bool backward) {
+  const double token = backward ? 0.35 : 0.07, twice = backward ? 1.3 : 1.85;
+  int64_t best = 0;
+  double least = 0.0;
+  for (int64_t n = 1; n <= 64 && (n == 1 || (n - 1) * 64 < T); ++n) {
+    // segments are whole tiles, so n of them may come out as fewer
+    const int64_t len = ceil_div(std::max<int64_t>(ceil_div(T, n), n > 1 ? 64 : 1), ttt::kScanTile) * ttt::kScanTile;
+    const int64_t count = std::max<int64_t>(ceil_div(T, len), 1);
+    const double rounds = static_cast<double>(ceil_div(blocks * count, 256));
+    const double cost =
+        rounds * static_cast<double>(len) * token * (count > 1 ? twice : 1.0) + (count > 1 ? 8.0 + 0.25 * count : 0.0);
+    if (best == 0 || cost < least) {
+      least = cost;
+      best = len;
+    }
+  }
+  return best;
+}
+
 ScanPlan scan_plan(const ttt_selective_scan_desc* d, bool backward) {
   ScanPlan p;
   p.tiles = ceil_div(d->D / d->G, ttt::kScanCh);
   p.blocks = static_cast<int64_t>(d->B) * d->G * p.tiles;
-  int64_t n = 1;
-  if (p.blocks > 0 && p.blocks < 160) n = ceil_div(512, p.blocks);
-  if (n > ceil_div(d->T, 64)) n = ceil_div(d->T, 64);
-  if (n > 64) n = 64;
-  if (n < 1) n = 1;
-  p.seglen = static_cast<int>(ceil_div(ceil_div(d->T, n), ttt::kScanTile) * ttt::kScanTile);
-  if (p.seglen < ttt::kScanTile) p.seglen = ttt::kScanTile;
+  p.seglen = static_cast<int>(scan_seglen(p.blocks, d->T, backward));
   p.nseg = static_cast<int>(d->T > 0 ? ceil_div(d->T, p.seglen) : 1);
   p.chunks = static_cast<int>(ceil_div(d->T, ttt::scan_chunk(d->N)));
   int64_t at = 0;
