@@ -3,8 +3,10 @@
 // Pages: [TTT] = news article "大模型最强架构TTT问世！斯坦福UCSD等5年磨一剑，一夜推翻Transformer"
 // (aharts.cn / itmax.cn), part 04 (the Mamba layer that TTT is compared with).
 //
-// Per token, channel and state one exp, two products and two multiply-adds: 24 issue cycles a wave of 64 (v_exp_f32 takes 8,
-// measured), against (with N = 16) half a byte: vector issue is the bound.
+// Per token, channel and state one exp, two products and two multiply-adds: 21 issue cycles a wave of 64 (measured with two
+// waves to a SIMD: v_exp_f32 8.3, a multiply-add 4, a product 2.5), against (with N = 16) half a byte: vector issue is the bound.
+// 4 x 8192 tokens, 4096 channels, N = 16, bf16: 527 us, 2.0 TB/s; by that count 313 us, by its bytes 203 at the 5.3 TB/s of a
+// large copy.
 #include <utility>
 
 #include "scan_common.h"
@@ -271,76 +273,53 @@ __device__ __forceinline__ void token_row(float (&x)[NS], const T* p, int N, int
   }
 }
 
-// A few tokens, the state in place: four lanes to a channel, NS states each, S sequences to a thread, which share the
-// channel's parameters and whose loads are on their way together.  8 N bytes of state a channel against 5 N flops: a copy of
-// the state with the arithmetic on the way.
-template <typename InT, typename OutT, int NS, int S, bool Wide>
+// A few tokens, the state in place: four lanes to a channel, NS states each.  8 N bytes of state a channel against 5 N flops: a
+// copy of the state with the arithmetic on the way.  512 sequences of 4096 channels, N = 16, bf16, one token: 69 us, 4.1 TB/s.
+// Four sequences to a thread, which share the channel's parameters, took 90 (16 sequences 6.6 against 4.4, 1024 sequences 176
+// against 142, four tokens of them 442 against 266; in fp32 1024 sequences 118 against 128, four tokens 231 against 224).
+template <typename InT, typename OutT, int NS, bool Wide>
 __global__ __launch_bounds__(256) void ttt_scan_decode(ScanArgs a) {
   const uint32_t blocks = (static_cast<uint32_t>(a.D) + 15) / 16;  // 16 channels to a wave
   const uint32_t id = blockIdx.x * 4u + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = threadIdx.x & 3, c = static_cast<int>(id % blocks * 16 + (threadIdx.x >> 2 & 15));
-  const int64_t b0 = static_cast<int64_t>(id / blocks) * S;
-  if (b0 >= a.B || c >= a.D) return;
-  const int g = c / (a.D / a.G);
-  float h[S][NS], a2[NS];
-  int len[S], most = 0;
-  int64_t bs[S];
-#pragma unroll
-  for (int r = 0; r < S; ++r) {
-    bs[r] = min(b0 + r, static_cast<int64_t>(a.B) - 1);  // (behind the last sequence: nothing of it is written)
-    len[r] = b0 + r >= a.B ? 0 : a.lens ? max(0, min(a.lens[bs[r]], a.T)) : a.T;
-    most = max(most, len[r]);
-    token_states<Wide>(h[r], a.h_final + (bs[r] * a.D + c) * a.N, a.N, q);
-  }
+  const int64_t b = id / blocks;
+  if (b >= a.B || c >= a.D) return;
+  const int g = c / (a.D / a.G), len = a.lens ? max(0, min(a.lens[b], a.T)) : a.T;
+  float* const state = a.h_final + (b * a.D + c) * a.N;
+  float h[NS], a2[NS];
+  token_states<Wide>(h, state, a.N, q);
   token_states<Wide>(a2, a.A + static_cast<int64_t>(c) * a.N, a.N, q);
 #pragma unroll
   for (int i = 0; i < NS; ++i) a2[i] = scaled_decay(a2[i]);
   const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, skip = a.Dskip ? a.Dskip[c] : 0.f;
-  for (int64_t t = 0; t < most; ++t) {
-    float u[S], dt[S], z[S], Bv[S][NS], Cv[S][NS];
+  for (int64_t t = 0; t < len; ++t) {
+    float Bv[NS], Cv[NS], y = 0.f;
+    const float u = as_f32(static_cast<const InT*>(a.u)[b * a.us.b + t * a.us.t + c]);
+    const float dt = as_f32(static_cast<const InT*>(a.dt)[b * a.dts.b + t * a.dts.t + c]);
+    const float z = a.z ? as_f32(static_cast<const InT*>(a.z)[b * a.zs.b + t * a.zs.t + c]) : 0.f;
+    token_row<Wide>(Bv, static_cast<const InT*>(a.Bm) + b * a.bs.b + g * a.bs.h + t * a.bs.t, a.N, q);
+    token_row<Wide>(Cv, static_cast<const InT*>(a.Cm) + b * a.cs.b + g * a.cs.h + t * a.cs.t, a.N, q);
+    float step = dt + bias;
+    if (a.softplus) step = softplus(step);
 #pragma unroll
-    for (int r = 0; r < S; ++r) {
-      const int64_t at = t < len[r] ? t : 0, b = bs[r];  // (its first token instead)
-      const bool any = len[r] > 0;
-      u[r] = any ? as_f32(static_cast<const InT*>(a.u)[b * a.us.b + at * a.us.t + c]) : 0.f;
-      dt[r] = any ? as_f32(static_cast<const InT*>(a.dt)[b * a.dts.b + at * a.dts.t + c]) : 0.f;
-      z[r] = any && a.z ? as_f32(static_cast<const InT*>(a.z)[b * a.zs.b + at * a.zs.t + c]) : 0.f;
-      if (any) {
-        token_row<Wide>(Bv[r], static_cast<const InT*>(a.Bm) + b * a.bs.b + g * a.bs.h + at * a.bs.t, a.N, q);
-        token_row<Wide>(Cv[r], static_cast<const InT*>(a.Cm) + b * a.cs.b + g * a.cs.h + at * a.cs.t, a.N, q);
-      }
+    for (int i = 0; i < NS; ++i) {
+      h[i] = fmaf(__builtin_amdgcn_exp2f(step * a2[i]), h[i], step * u * Bv[i]);
+      if (Wide || q * NS + i < a.N) y = fmaf(Cv[i], h[i], y);
     }
+    y = fmaf(skip, u, quad_sum(y));
+    if (a.z) y *= z * sigmoid(z);
+    if (q == 0) put(static_cast<OutT*>(a.y) + b * a.ys.b + t * a.ys.t + c, y);
+  }
+  if (len > 0) {
+    if constexpr (Wide && NS >= 4) {
 #pragma unroll
-    for (int r = 0; r < S; ++r) {
-      if (t >= len[r]) continue;
-      float step = dt[r] + bias, y = 0.f;
-      if (a.softplus) step = softplus(step);
-#pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        h[r][i] = fmaf(__builtin_amdgcn_exp2f(step * a2[i]), h[r][i], step * u[r] * Bv[r][i]);
-        if (Wide || q * NS + i < a.N) y = fmaf(Cv[r][i], h[r][i], y);
-      }
-      y = fmaf(skip, u[r], quad_sum(y));
-      if (a.z) y *= z[r] * sigmoid(z[r]);
-      if (q == 0) put(static_cast<OutT*>(a.y) + bs[r] * a.ys.b + t * a.ys.t + c, y);
+      for (int i = 0; i < NS; i += 4)
+        if (q * NS + i < a.N) *reinterpret_cast<float4*>(state + q * NS + i) = make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
+    } else {
+      store_states(h, state, a.N, q, true);
     }
   }
-#pragma unroll
-  for (int r = 0; r < S; ++r) {
-    if (len[r] > 0) {
-      float* to = a.h_final + (bs[r] * a.D + c) * a.N;
-      if constexpr (Wide && NS >= 4) {
-#pragma unroll
-        for (int i = 0; i < NS; i += 4)
-          if (q * NS + i < a.N)
-            *reinterpret_cast<float4*>(to + q * NS + i) = make_float4(h[r][i], h[r][i + 1], h[r][i + 2], h[r][i + 3]);
-      } else {
-        store_states(h[r], to, a.N, q, true);
-      }
-    }
-    if (b0 + r < a.B)
-      for (int64_t t = len[r] + q; t < a.T; t += 4) put(static_cast<OutT*>(a.y) + bs[r] * a.ys.b + t * a.ys.t + c, 0.f);
-  }
+  for (int64_t t = len + q; t < a.T; t += 4) put(static_cast<OutT*>(a.y) + b * a.ys.b + t * a.ys.t + c, 0.f);
 }
 
 enum Which { STATES, FWD, DECODE };
@@ -359,22 +338,13 @@ hipError_t walk(bool states, const ScanArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename InT, typename OutT, int NS, int S>
-hipError_t token(const ScanArgs& a, hipStream_t s) {
-  const int64_t waves = static_cast<int64_t>((a.B + S - 1) / S) * ((a.D + 15) / 16);
-  const unsigned grid = static_cast<unsigned>((waves + 3) / 4);
-  if (a.wide) ttt_scan_decode<InT, OutT, NS, S, true><<<grid, 256, 0, s>>>(a);
-  else ttt_scan_decode<InT, OutT, NS, S, false><<<grid, 256, 0, s>>>(a);
-  return hipGetLastError();
-}
-
-// Four sequences to a thread where that still leaves 2^17 threads, a wave for every place that the card has.
 template <typename InT, typename OutT, int NS>
 hipError_t token(const ScanArgs& a, hipStream_t s) {
-  if constexpr (NS < 8) {  // (of 32 states the registers would not do)
-    if (static_cast<int64_t>(a.B) * a.D >= 1 << 17) return token<InT, OutT, NS, 4>(a, s);
-  }
-  return token<InT, OutT, NS, 1>(a, s);
+  const int64_t waves = static_cast<int64_t>(a.B) * ((a.D + 15) / 16);
+  const unsigned grid = static_cast<unsigned>((waves + 3) / 4);
+  if (a.wide) ttt_scan_decode<InT, OutT, NS, true><<<grid, 256, 0, s>>>(a);
+  else ttt_scan_decode<InT, OutT, NS, false><<<grid, 256, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 template <typename InT, typename OutT>

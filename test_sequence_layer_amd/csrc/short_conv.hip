@@ -4,7 +4,8 @@
 // (aharts.cn / itmax.cn), part 04 (the Mamba backbone the layer is measured in).
 //
 //   y_t = act(bias + sum_j w_j x_{t-K+1+j}),   K = 2, 3, 4, act the identity or silu
-// 2 K flops a token and channel against 4 bytes: memory is the bound.
+// 2 K flops a token and channel against 4 bytes: memory is the bound.  bf16, K = 4: 4 x 8192 tokens of 4096 channels 111 us, 4.9
+// TB/s; gradients of 8 x 2048 of 1536 54 us, 2.8 TB/s; one token of 512 x 4096 9.3 us.
 #include <type_traits>
 
 #include "block_common.h"
@@ -55,8 +56,12 @@ __device__ __forceinline__ void row(Piece<T, V>& x, const ConvArgs& a, const T* 
   else x.zero();
 }
 
-// kTok tokens of a piece of channels to a thread, all of its rows on their way at once.
-template <typename InT, typename OutT, int K, bool Wide, int kTok>
+// kTok tokens of a piece of channels to a thread, all of its rows on their way at once.  32 tokens read fewer rows twice but were
+// slower throughout (bf16, rows of 4096: 4 x 2048 tokens 29.2 us against 28.1, 4 x 8192 tokens 115 against 108, of a wider row 123
+// against 111).
+constexpr int kTok = 8;
+
+template <typename InT, typename OutT, int K, bool Wide>
 __global__ __launch_bounds__(256) void ttt_conv_fwd(ConvArgs a, int blocks, int tiles) {
   constexpr int V = kVec<InT>;
   const uint32_t id = wave_id(), line = id / blocks;  // 64 pieces of channels to a wave
@@ -299,17 +304,13 @@ hipError_t go(Which which, const ConvArgs& a, hipStream_t s) {
   constexpr int V = kVec<InT>;
   const int pieces = (a.D + V - 1) / V, blocks = (pieces + 63) / 64;
   if (which == FWD) {
-    // long walks read fewer rows twice; short ones are more threads: from 2^18 of the long ones on there are enough
-    auto run = [&](auto tok) {
-      const int tiles = a.T > 0 ? (a.T + tok - 1) / tok : 1;  // (without tokens the state is still handed on)
-      const int64_t waves = static_cast<int64_t>(a.B) * tiles * blocks;
-      ttt_conv_fwd<InT, OutT, K, Wide, tok><<<static_cast<unsigned>((waves + 3) / 4), 256, 0, s>>>(a, blocks, tiles);
-    };
-    if (static_cast<int64_t>(a.B) * (a.T / 32) * pieces >= 1 << 18) run(std::integral_constant<int, 32>{});
-    else run(std::integral_constant<int, 8>{});
+    const int tiles = a.T > 0 ? (a.T + kTok - 1) / kTok : 1;  // (without tokens the state is still handed on)
+    const int64_t waves = static_cast<int64_t>(a.B) * tiles * blocks;
+    ttt_conv_fwd<InT, OutT, K, Wide><<<static_cast<unsigned>((waves + 3) / 4), 256, 0, s>>>(a, blocks, tiles);
   } else if (which == DECODE) {
-    // four sequences to a thread where that leaves 2^15 threads, two waves to a SIMD in half of the card
-    const bool four = static_cast<int64_t>(a.B) * pieces >= 1 << 17;
+    // four sequences to a thread from 2^18 pieces on; one against four, rows of 4096 in bf16: 256 sequences (2^17) 5.7 and 6.1 us,
+    // 512 9.5 and 8.0, 2048 27.3 and 21.6
+    const bool four = static_cast<int64_t>(a.B) * pieces >= 1 << 18;
     const int64_t waves = static_cast<int64_t>(four ? (a.B + 3) / 4 : a.B) * blocks;
     const unsigned grid = static_cast<unsigned>((waves + 3) / 4);
     if (four) ttt_conv_decode<InT, OutT, K, Wide, 4><<<grid, 256, 0, s>>>(a, blocks);
