@@ -721,7 +721,9 @@ const char* ttt_rotary_kernel_name(const ttt_rotary_desc* desc, const ttt_rope* 
  *    (bi, t, c) is at bi*b + t*t' + c of its ttt_strides {b, h, t'} (h is not looked
  *    at).  Strides as for linear attention (>= 0, outputs' elements apart).  Any
  *    address and stride of whole elements will do; where all are multiples of 16
- *    bytes and the channels (of a group) of 8 elements, rows go in 16-byte pieces.
+ *    bytes and the channels (of a group) of 8 elements, rows go in 16-byte pieces
+ *    (the scan's prompts and gradients: where N is a multiple of 4 and B and C are
+ *    aligned to 4 elements too).
  *  - Outputs share no element with an input or another output (TTT_ERR_ALIAS) except
  *    where said; slices of the same rows ([B, T, 2 D] halves, [B, T, N + N]) pass.
  *  - lens: [B] int32 on the device, the tokens of each sequence (taken into [0, T]),
