@@ -45,6 +45,17 @@ def test_scan_tokens(ttt, case):
     small.test_scan_tokens(ttt, case)
 
 
+# lengths where the gradients go from one segment to two, three, ..., and where the last has one token
+@pytest.mark.parametrize("T", [63, 64, 65, 95, 96, 97, 127, 128, 129, 160, 161, 192, 193, 257])
+def test_scan_segments(ttt, T):
+    case = (2, T, 40, 16, 1, F32, F32, True, True, True, True, True, None, "dense")
+    small.test_scan_forward(ttt, case)
+    small.test_scan_backward(ttt, case)
+    ends = (6, T, 8, 4, 1, F32, F32, True, True, True, True, True, "late", "dense")
+    small.test_scan_forward(ttt, ends)
+    small.test_scan_backward(ttt, ends)
+
+
 @pytest.mark.parametrize("case", [
     (6, 1501, 136, BF, F32, "layer", True, False, True, True, True, True, True, True, "late", "dense"),
     (6, 1501, 520, BF, BF, "rms", True, True, True, False, True, True, False, True, "early", "slice"),
