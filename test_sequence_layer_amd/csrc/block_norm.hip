@@ -7,7 +7,7 @@
 //   s = res + alpha v,                    y = NORM(s) gamma_pre + beta_pre
 // NORM divides by the root of the mean square plus eps, the layer norm after taking the mean off.  Each row is read once,
 // kept in registers and written once: memory is the bound.
-// 4 x 8192 rows of 2048, bf16 with an fp32 residual stream: 197 us, 4.8 TB/s.  Gradients of 8 x 2048 rows of 768: 83 us, two launches.
+// 4 x 8192 rows of 2048, bf16 with an fp32 residual stream: 197 to 207 us, 4.5 to 4.8 TB/s.  Gradients of 8 x 2048 rows of 768: 83 us, two launches.
 #include <type_traits>
 
 #include "block_common.h"
