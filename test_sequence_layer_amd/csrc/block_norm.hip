@@ -84,9 +84,9 @@ __device__ __forceinline__ float2 stats(const float (&x)[NE], int valid, double 
       ss = fma(v, v, ss);
     }
     team.sum2(s, ss);
-    const double mean = s * inv;
-    const float var = static_cast<float>(fmax(fma(ss, inv, -mean * mean), 0.0));
-    return make_float2(static_cast<float>(mean), __builtin_amdgcn_rsqf(var + eps));
+    const double mean = s * inv, var = fma(ss, inv, -mean * mean);
+    // (a row with an infinity has inf - inf here, and the NaN has to stay: fmax would drop it)
+    return make_float2(static_cast<float>(mean), __builtin_amdgcn_rsqf(static_cast<float>(var < 0.0 ? 0.0 : var) + eps));
   }
   float s = 0.f, none = 0.f;
 #pragma unroll
