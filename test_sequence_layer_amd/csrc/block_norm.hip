@@ -7,7 +7,7 @@
 //   s = res + alpha v,                    y = NORM(s) gamma_pre + beta_pre
 // NORM divides by the root of the mean square plus eps, the layer norm after taking the mean off.  Each row is read once,
 // kept in registers and written once: memory is the bound.
-// 4 x 8192 rows of 2048, bf16 with an fp32 residual stream: 197 to 207 us, 4.5 to 4.8 TB/s.  Gradients of 8 x 2048 rows of 768: 83 us, two launches.
+// 4 x 8192 rows of 2048, bf16 with an fp32 residual stream: 197 to 207 us, 4.5 to 4.8 TB/s.  Gradients of 8 x 2048 rows of 768: 75 us, two launches.
 #include <type_traits>
 
 #include "block_common.h"
@@ -95,14 +95,14 @@ __device__ __forceinline__ float2 stats(const float (&x)[NE], int valid, double 
   return make_float2(0.f, __builtin_amdgcn_rsqf(fmaf(s, static_cast<float>(inv), eps)));
 }
 
-// A row's sequence and token, and the one that is ``step`` rows further on.
+// A row's sequence and token, and the one that is ``step`` rows further on (B and T are below 2^31, a step below 2^15).
 struct Walk {
-  int64_t b, t, T, db, dt;
-  __device__ __forceinline__ Walk(int64_t line, int64_t step, int64_t T_) : T(T_) {
-    b = line / T;
-    t = line - b * T;
-    db = step / T;
-    dt = step - db * T;
+  uint32_t b, t, T, db, dt;
+  __device__ __forceinline__ Walk(int64_t line, int64_t step, int T_) : T(T_) {
+    b = static_cast<uint32_t>(line / T);
+    t = static_cast<uint32_t>(line - static_cast<int64_t>(b) * T);
+    db = static_cast<uint32_t>(step) / T;
+    dt = static_cast<uint32_t>(step) - db * T;
   }
   __device__ __forceinline__ void advance() {
     b += db;
@@ -284,8 +284,9 @@ __global__ __launch_bounds__(R < 256 ? 256 : R) void ttt_norm_bwd(NormArgs a) {
   const int valid = cols.valid();
   const double inv = 1.0 / static_cast<double>(a.D);
   const int64_t rows = static_cast<int64_t>(a.B) * a.T;
-  // the columns' parameters stay in registers too (teams of 1024: there are none left)
-  constexpr bool kHeld = R < 1024;
+  // the columns' parameters stay in registers too, and the next row is on its way.  Teams of 1024 have no registers left for
+  // either: at 8 x 2048 rows of 8192, bf16, a row ahead took 1400 us, reading each row as it comes 1114
+  constexpr bool kHeld = R < 1024, kAhead = Wide && kHeld;
   float wa[NE], wp[NE], wb[NE], wn[NE];
   auto fill = [&] {
     cols.param(wa, a.alpha, 1.f);
@@ -301,37 +302,41 @@ __global__ __launch_bounds__(R < 256 ? 256 : R) void ttt_norm_bwd(NormArgs a) {
     for (int i = 0; i < NE; ++i) acc[k][i] = 0.f;
   const int64_t step = static_cast<int64_t>(gridDim.x) * TEAMS;
   int64_t first = static_cast<int64_t>(blockIdx.x) * TEAMS;
-  Walk at(first + who, step, max(a.T, 1)), ahead = at;
-  // the row's pieces as they lie in memory, on their way a row ahead; what is not there is read from the workspace and dropped
+  Walk ahead(first + who, step, max(a.T, 1));  // of the next row that is read
+  // the row's pieces as they lie in memory, on their way a row ahead.  Rows behind their sequence's last token and tensors that
+  // are not there are not read: their loads go to this workgroup's own partial sums, which it writes at its end, and are dropped
   struct Raw {
     Piece<T, 8> x[NC], z[NC], dy[NC];
     Piece<RT, 8> res[NC], ds[NC];
   } raw;
-  auto fetch = [&](int64_t line) {
-    const int64_t b = line < rows ? ahead.b : 0, t = line < rows ? ahead.t : 0;
-    auto get = [&](auto& v, const auto* p, int64_t o) {
+  float* const part = a.part + static_cast<int64_t>(blockIdx.x) * 5 * a.D;
+  auto skipped = [&](int64_t line) { return line >= rows || dead(a, ahead.b, ahead.t); };
+  auto fetch = [&](bool skip) {
+    auto get = [&](auto& v, const auto* p, const Strides2& st) {
       typedef std::remove_const_t<std::remove_pointer_t<decltype(p)>> E;
-      const E* from = p ? p + o : reinterpret_cast<const E*>(a.part);
+      const E* from = p && !skip ? p + (ahead.b * st.b + ahead.t * st.t) : reinterpret_cast<const E*>(part);
 #pragma unroll
       for (int i = 0; i < NC; ++i) v[i].load(from + (8 * (i * R + r) < a.D ? 8 * (i * R + r) : 0));
     };
-    get(raw.x, static_cast<const T*>(a.X), b * a.xs.b + t * a.xs.t);
-    get(raw.z, static_cast<const T*>(a.Z), b * a.zs.b + t * a.zs.t);
-    get(raw.res, static_cast<const RT*>(a.res), b * a.rs.b + t * a.rs.t);
-    get(raw.ds, static_cast<const RT*>(a.dS), b * a.ss.b + t * a.ss.t);
-    get(raw.dy, static_cast<const T*>(a.dY), b * a.ys.b + t * a.ys.t);
+    get(raw.x, static_cast<const T*>(a.X), a.xs);
+    get(raw.z, static_cast<const T*>(a.Z), a.zs);
+    get(raw.res, static_cast<const RT*>(a.res), a.rs);
+    get(raw.ds, static_cast<const RT*>(a.dS), a.ss);
+    get(raw.dy, static_cast<const T*>(a.dY), a.ys);
   };
-  if constexpr (Wide) {
-    if (first < rows) fetch(first + who);
+  bool next_none = skipped(first + who);
+  if constexpr (kAhead) {
+    if (first < rows) fetch(next_none);
   }
   for (; first < rows; first += step) {
-    const int64_t b = at.b, t = at.t;
-    const bool off = first + who >= rows, none = off || dead(a, b, t);
-    at.advance();
+    const int64_t b = ahead.b, t = ahead.t;
+    const bool off = first + who >= rows, none = next_none;
+    ahead.advance();
+    next_none = skipped(first + step + who);
     // (a team without a row goes along on zeros: the others wait for it at the sums)
     float x[NE], z[NE], u1[NE], v[NE], u2[NE], g[NE];
     float gate[NE], slope[NE];
-    if constexpr (Wide) {
+    if constexpr (kAhead) {
       auto take = [&](float (&to)[NE], auto& from, bool on) {
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
@@ -345,8 +350,7 @@ __global__ __launch_bounds__(R < 256 ? 256 : R) void ttt_norm_bwd(NormArgs a) {
       take(u2, raw.res, a.res != nullptr);
       take(v, raw.ds, a.dS != nullptr);
       take(g, raw.dy, a.dY != nullptr);
-      ahead.advance();
-      if (first + step < rows) fetch(first + step + who);
+      if (first + step < rows) fetch(next_none);
     } else {
 #pragma unroll
       for (int i = 0; i < NE; ++i) x[i] = z[i] = g[i] = u2[i] = v[i] = 0.f;
@@ -447,7 +451,6 @@ __global__ __launch_bounds__(R < 256 ? 256 : R) void ttt_norm_bwd(NormArgs a) {
       if (a.dZ) cols.store(z, static_cast<T*>(a.dZ) + b * a.dzs.b + t * a.dzs.t);
     }
   }
-  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 5 * a.D;
 #pragma unroll
   for (int k = 0; k < 5; ++k) {
     if constexpr (TEAMS > 1) {

@@ -3,7 +3,7 @@ import pytest
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
-F32 = torch.float32
+BF, F32 = torch.bfloat16, torch.float32
 INF = float("inf")
 
 
@@ -46,3 +46,30 @@ def test_norm_of_a_row_with_an_infinity(ttt, D, value):
     assert torch.isnan(got[1, 3]).all()
     got[1, 3] = want[1, 3]
     assert torch.equal(got, want)
+
+
+# the gradients read a row ahead, but no row behind its sequence's last token and no tensor that is not there: rows of nothing
+# between rows of tokens, several to a workgroup, with NaN in all that has no business in the result
+@pytest.mark.parametrize("D,dtype,res_dtype", [(72, BF, F32), (768, BF, BF), (2048, F32, BF), (2056, BF, F32), (4104, BF, F32)])
+@pytest.mark.parametrize("given", ["s", "y", "all"])
+def test_norm_backward_between_rows_of_nothing(ttt, D, dtype, res_dtype, given):
+    B, T = 37, 61
+    lens = torch.tensor([(0, 61, 1, 30, 60)[b % 5] for b in range(B)], dtype=torch.int32, device="cuda")
+    live = (torch.arange(T, device="cuda") < lens[:, None])[..., None]
+    rows = lambda seed, to: random((B, T, D), to, seed).where(live, float("nan"))  # noqa: E731
+    p = lambda seed: random((D,), F32, seed, 0.1, 1.0)  # noqa: E731
+    x, ds, dy = rows(1, dtype), None if given == "y" else rows(2, res_dtype), None if given == "s" else rows(3, dtype)
+    more = {} if given == "s" else dict(gamma_pre=p(4))
+    if given == "all":
+        more.update(res=rows(5, res_dtype), z=rows(6, dtype), alpha=p(7), gamma_post=p(8), beta_post=p(9), kind="layer")
+    ws = torch.full((ttt.block_norm_workspace_bytes(x) // 4,), float("nan"), device="cuda")
+    got = ttt.block_norm_bwd(x, ds, dy, lens=lens, workspace=ws, **more)
+    for g in got:
+        assert g is None or torch.isfinite(g).all()
+    cut = lambda t, b: None if t is None else t[b:b + 1, :int(lens[b])] if t.dim() == 3 else t  # noqa: E731
+    for b in (1, 2, 3, 18, 33, 36):
+        part = {k: cut(v, b) if torch.is_tensor(v) else v for k, v in more.items()}
+        alone = ttt.block_norm_bwd(cut(x, b), cut(ds, b), cut(dy, b), **part)
+        for g, a in zip(got[:3], alone[:3]):
+            if g is not None:
+                assert torch.equal(cut(g, b), a) and not g[b, int(lens[b]):].any()
