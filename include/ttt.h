@@ -900,7 +900,8 @@ typedef struct {
  *     S = res + alpha v,                    Y = NORM(S) gamma_pre + beta_pre
  * with Y from S before its rounding.  Z (no gate), res (zero), gamma_post (no norm behind
  * the block; then no beta_post either, TTT_ERR_NULL), beta_post, alpha (1), beta_pre may be
- * NULL; so may S or Y, which is then not written (gamma_pre exactly where Y is: TTT_ERR_NULL).
+ * NULL; so may S or Y (not both, TTT_ERR_NULL), which is then not written.  Y and beta_pre need
+ * gamma_pre (TTT_ERR_NULL); without Y gamma_pre and beta_pre are not looked at.
  * S may be exactly res (same address, strides and type).
  */
 ttt_status ttt_block_norm_fwd(const ttt_block_norm_desc* desc, const void* X, const void* Z, const void* res,
