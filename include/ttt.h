@@ -815,7 +815,8 @@ typedef struct {
  *     h_t = exp(step_t A) h_{t-1} + step_t Bm_t u_t
  *     y_t = (sum_n Cm_t h_t + D u_t) silu(z_t)
  * channel c reading Bm and Cm of group c / (D / G).
- *   A : [D, N]; -inf keeps nothing;  D, dt_bias : [D], each or NULL (zero)
+ *   A : [D, N]; -inf keeps nothing over a step of 1e-36 and more, and all over a step of 0
+ *       (with softplus a step below e^-87 is 0);  D, dt_bias : [D], each or NULL (zero)
  *   z : [B, T, D] or NULL (no gate);  h0 : [B, D, N] fp32 or NULL (zero)
  *   h_final : [B, D, N] fp32, the state after the last token; may be exactly h0
  *   workspace : ttt_selective_scan_workspace_bytes(desc, 0) bytes, 16-byte aligned
@@ -901,7 +902,7 @@ typedef struct {
  * with Y from S before its rounding.  Z (no gate), res (zero), gamma_post (no norm behind
  * the block; then no beta_post either, TTT_ERR_NULL), beta_post, alpha (1), beta_pre may be
  * NULL; so may S or Y (not both, TTT_ERR_NULL), which is then not written.  Y and beta_pre need
- * gamma_pre (TTT_ERR_NULL); without Y gamma_pre and beta_pre are not looked at.
+ * gamma_pre (TTT_ERR_NULL); without Y gamma_pre and beta_pre reach nothing.
  * S may be exactly res (same address, strides and type).
  */
 ttt_status ttt_block_norm_fwd(const ttt_block_norm_desc* desc, const void* X, const void* Z, const void* res,

@@ -1641,7 +1641,8 @@ def selective_scan_fwd(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, 
     u, dt, z : [B, T, D] bfloat16 or float32, channels contiguous, any strides between sequences and tokens; z may be None
                (no gate).  step = dt + dt_bias, with ``softplus`` its log(1 + exp(.))
     Bm, Cm   : [B, G, T, N] of the same dtype, 1 <= N <= 32, the N of a token contiguous; channel c reads group c // (D // G)
-    A        : [D, N] float32 (-inf keeps nothing);  D, dt_bias : [D] float32 or None (zero)
+    A        : [D, N] float32 (-inf keeps nothing over a step of 1e-36 and more, all over a step of 0; with ``softplus`` a step
+               below e^-87 is 0);  D, dt_bias : [D] float32 or None (zero)
     h0       : initial state [B, D, N] float32, or None (zero)
     lens     : [B] int32, the tokens of each sequence, or None (T each).  Rows behind them are not read and give zeros
     returns (y [B, T, D] of out_dtype (default u's), h_final [B, D, N] float32, the state after the last token).

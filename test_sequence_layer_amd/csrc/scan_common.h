@@ -34,7 +34,8 @@ __device__ __forceinline__ Place place(const ScanArgs& a, int64_t blk) {
   return p;
 }
 
-// A log2(e), finite: -inf keeps nothing, and exp(0 A) of a token that is not there is 1.
+// A log2(e), finite: exp(0 A) of a token that is not there has to be 1.  -inf becomes -3e38, which keeps nothing over steps of
+// 1e-36 and more.
 __device__ __forceinline__ float scaled_decay(float A) {
   const float x = A * kLog2e;
   return x != x ? x : fminf(fmaxf(x, -3.0e38f), 3.0e38f);

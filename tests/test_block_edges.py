@@ -3,7 +3,7 @@ from test_block_abi import NULL, OK, norm_desc, norm_fwd
 
 
 def test_norm_parameters_without_an_output():
-    assert norm_fwd(norm_desc(), y=None) == OK                       # gamma_pre and beta_pre are not looked at
+    assert norm_fwd(norm_desc(), y=None) == OK                       # gamma_pre and beta_pre reach nothing
     assert norm_fwd(norm_desc(), y=None, bn=None) == OK
     assert norm_fwd(norm_desc(), y=None, gn=None, bn=None) == OK
     assert norm_fwd(norm_desc(), gn=None) == NULL and norm_fwd(norm_desc(), gn=None, bn=None) == NULL

@@ -73,3 +73,28 @@ def test_norm_backward_between_rows_of_nothing(ttt, D, dtype, res_dtype, given):
         for g, a in zip(got[:3], alone[:3]):
             if g is not None:
                 assert torch.equal(cut(g, b), a) and not g[b, int(lens[b]):].any()
+
+
+# A = -inf: exp(step A) is 0 for a step of 1e-36 and more and 1 for a step of 0, in one segment, in several, token by token and
+# backward; with softplus steps below e^-87 count as 0
+@pytest.mark.parametrize("T", [5, 700])
+def test_a_decay_that_keeps_nothing(ttt, T):
+    steps = torch.tensor([0.0, 1e-36, 1e-20, 0.1, 0.0, 2e-36], device="cuda")
+    keeps = (steps == 0).float()
+    B, D, N = 1, len(steps), 3
+    dt = torch.zeros(B, T, D, device="cuda")
+    dt[:, T // 2] = steps  # all other steps are 0
+    u, bc = random((B, T, D), F32, 1), torch.zeros(B, 1, T, N, device="cuda")
+    A, h0, dh = torch.full((D, N), -INF, device="cuda"), random((B, D, N), F32, 2), random((B, D, N), F32, 3)
+    y, h = ttt.selective_scan_fwd(u, dt, A, bc, bc, h0=h0)
+    assert torch.equal(h, h0 * keeps[:, None]) and not y.any()
+    state = h0.clone()
+    ttt.selective_scan_decode(u, dt, A, bc, bc, state)
+    assert torch.equal(state, h)
+    got = ttt.selective_scan_bwd(u, dt, A, bc, bc, torch.zeros_like(u), h0=h0, dh_final=dh)
+    assert torch.equal(got[8], dh * keeps[:, None]) and torch.isfinite(got[2]).all()
+    raw = torch.tensor([-200.0, -80.0, -20.0, 0.0, -90.0, 50.0], device="cuda")
+    wide = torch.full((B, T, D), -200.0, device="cuda")
+    wide[:, T // 2] = raw
+    _, h = ttt.selective_scan_fwd(u, wide, A, bc, bc, h0=h0, softplus=True)
+    assert torch.equal(h, h0 * (raw < -87).float()[:, None])
