@@ -1,6 +1,9 @@
 """The short convolution, the selective scan and the block norm where a value, a length or a walk is at an end of its range."""
 import pytest
 
+import block_testutil as bt
+import test_block_gpu as small
+
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 BF, F32 = torch.bfloat16, torch.float32
@@ -98,3 +101,59 @@ def test_a_decay_that_keeps_nothing(ttt, T):
     wide[:, T // 2] = raw
     _, h = ttt.selective_scan_fwd(u, wide, A, bc, bc, h0=h0, softplus=True)
     assert torch.equal(h, h0 * (raw < -87).float()[:, None])
+
+
+# more rows than workgroups: the forward's second pass over its loop, teams whose places for sums come round again, rows of
+# nothing in between
+@pytest.mark.parametrize("case", [
+    (6, 1501, 136, BF, F32, "layer", True, False, True, True, True, True, True, True, "late", "dense"),
+    (6, 1501, 520, BF, BF, "rms", True, True, True, False, True, True, False, True, "early", "slice"),
+    (6, 1501, 500, F32, F32, "layer", True, False, True, True, True, True, True, True, "early", "odd"),
+    (6, 801, 1032, F32, BF, "layer", True, False, True, True, True, True, True, True, "late", "dense"),
+    (6, 601, 2056, BF, F32, "layer", False, False, True, True, True, True, True, True, "early", "dense"),
+    (1, 1100, 4104, BF, F32, "layer", True, True, True, True, True, True, True, True, None, "dense"),
+    (1, 1100, 4101, BF, BF, "rms", True, False, True, False, True, True, False, True, None, "odd"),
+])
+def test_norm_forward_more_rows_than_workgroups(ttt, case):
+    small.test_norm_forward(ttt, case)
+
+
+@pytest.mark.parametrize("case", [
+    (1, 700, 4104, BF, BF, "layer", True, True, True, True, True, True, True, True, None, "dense"),
+    (1, 700, 4101, F32, F32, "rms", True, False, True, False, True, True, False, True, None, "odd"),
+    (6, 301, 2056, F32, BF, "layer", True, False, True, True, True, True, True, True, "late", "slice"),
+])
+def test_norm_backward_more_rows_than_workgroups(ttt, case):
+    small.test_norm_backward(ttt, case)
+
+
+def segment(B, T, D, dtype):
+    """Tokens that a thread of the convolution's gradients walks."""
+    return min(max(T * B * -(-D // (8 if dtype == BF else 4)) >> 17, 16), 128)
+
+
+# longer walks than 16 tokens, as training has them, up to the longest of 128: dx and the state's gradient of every sequence
+# against that sequence alone, where walks are 16 tokens long; the sums over tokens against 64 bits on a few channels
+@pytest.mark.parametrize("B,T,D,K,dtype,out,silu,walk", [
+    (8, 2048, 1536, 4, BF, BF, True, 24), (6, 1501, 1540, 3, F32, F32, True, 26), (10, 5003, 2056, 4, BF, F32, False, 98),
+    (40, 3301, 1032, 2, BF, BF, True, 128)])
+def test_conv_gradients_of_long_walks(ttt, B, T, D, K, dtype, out, silu, walk):
+    assert segment(B, T, D, dtype) == walk and segment(1, T, D, dtype) == 16
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    mk = lambda *s, to=F32, std=1.0: (torch.randn(s, generator=gen, device="cuda") * std).to(to)  # noqa: E731
+    lens = torch.tensor([(T, T // 2, walk * 8 + 1, 0, T - 1, 1)[b % 6] for b in range(B)], dtype=torch.int32, device="cuda")
+    c = dict(x=mk(B, T, D, to=dtype), w=mk(D, K, std=0.5), dy=mk(B, T, D, to=out), bias=mk(D), state=mk(B, K - 1, D, to=dtype),
+             dstate_final=mk(B, K - 1, D, to=out))
+    dx, dw, db, dst = ttt.short_conv_bwd(**c, silu=silu, lens=lens)
+    for b in sorted({0, 1, 2, 3, 4, 5, B - 1}):
+        one = {k: v[b:b + 1] if k in ("x", "dy", "state", "dstate_final") else v for k, v in c.items()}
+        alone = ttt.short_conv_bwd(**one, silu=silu, lens=lens[b:b + 1])
+        assert torch.equal(dx[b:b + 1], alone[0]) and torch.equal(dst[b:b + 1], alone[3])
+    cut = slice(D - 9, D)
+    part = {k: (v[cut] if k in ("w", "bias") else v[..., cut]).cpu() for k, v in c.items()}
+    ref, size = bt.conv_grads(**part, act=silu, lens=lens.cpu())
+    deep = bt.conv(part["x"], part["w"], part["bias"], part["state"], lens=lens.cpu(), magnitudes=True)[2].max().item()
+    # as for short walks; a term goes through the rest of its walk and its workgroup's 8 walks, the last sum is in 64 bits
+    roundings = 2 * K + 8 + (20 + deep if silu else 0)
+    for n, a, r, s in zip(("dx", "dw", "dbias", "dstate"), (dx[..., cut], dw[cut], db[cut], dst[..., cut]), ref, size):
+        bt.check(n, a, r, s, roundings + (walk + 8 if n in ("dw", "dbias") else 0))
