@@ -157,3 +157,36 @@ def test_conv_gradients_of_long_walks(ttt, B, T, D, K, dtype, out, silu, walk):
     roundings = 2 * K + 8 + (20 + deep if silu else 0)
     for n, a, r, s in zip(("dx", "dw", "dbias", "dstate"), (dx[..., cut], dw[cut], db[cut], dst[..., cut]), ref, size):
         bt.check(n, a, r, s, roundings + (walk + 8 if n in ("dw", "dbias") else 0))
+
+
+# The bounds of the tests over types and layouts allow every rounding its worst; this one asks for what they come to: no further
+# from 64 bits than 8 times what plain fp32 operations are, which add the same terms in another order, and 2^-22 of the largest
+# value for results that those happen to hit
+@pytest.mark.parametrize("B,T,D,N,G,gate", [(2, 60, 24, 16, 1, True), (1, 300, 70, 16, 2, False), (3, 700, 12, 4, 1, True), (2, 333, 40, 32, 1, True)])
+def test_scan_is_as_good_as_plain_fp32(ttt, B, T, D, N, G, gate):
+    _, _, c, g = small.scan_case(B, T, D, N, G, F32, F32, True, gate, True, True, True, None, "dense", 21)
+    dy, dh = random((B, T, D), F32, 22), random((B, D, N), F32, 23)
+    names = ("u", "dt", "A", "Bm", "Cm", "D", "z", "dt_bias", "h0")
+
+    def plain(dtype):
+        p = {n: None if c[n] is None else c[n].to(dtype).requires_grad_() for n in names}
+        step = torch.nn.functional.softplus(p["dt"] + p["dt_bias"])
+        Bx, Cx = (p[n].repeat_interleave(D // G, 1) for n in ("Bm", "Cm"))
+        h, ys = p["h0"], []
+        for t in range(T):
+            h = torch.exp(step[:, t, :, None] * p["A"]) * h + (step[:, t] * p["u"][:, t])[..., None] * Bx[:, :, t]
+            ys.append((h * Cx[:, :, t]).sum(-1))
+        y = torch.stack(ys, 1) + p["D"] * p["u"]
+        if gate:
+            y = y * bt.silu(p["z"])
+        leaves = [v for v in p.values() if v is not None]
+        return [y.detach(), h.detach(), *torch.autograd.grad([y, h], leaves, [dy.cpu().to(dtype), dh.cpu().to(dtype)])]
+
+    exact, own = plain(torch.float64), plain(F32)
+    grads = ttt.selective_scan_bwd(**g, dy=dy, dh_final=dh, softplus=True)
+    order = [0, 1, 2, 3, 4, 5, 6, 7, 8] if gate else [0, 1, 2, 3, 4, 5, 7, 8]
+    got = [*ttt.selective_scan_fwd(**g, softplus=True), *(grads[i] for i in order)]
+    for n, a, r, f in zip(["y", "h", *(n for n in names if c[n] is not None)], got, exact, own):
+        off, ref = (a.cpu().double() - r).abs().max().item(), (f.double() - r).abs().max().item()
+        print(f"{n}: off {off:.2e}, plain fp32 {ref:.2e}, largest {r.abs().max().item():.1e}", flush=True)
+        assert off <= 8 * ref + 2.0 ** -22 * r.abs().max().item(), n
