@@ -2000,7 +2000,7 @@ ttt_status check_scan_desc(const ttt_selective_scan_desc* d) {
     return TTT_ERR_SHAPE;
   if (!dtype_ok(d->in_dtype) || !dtype_ok(d->out_dtype)) return TTT_ERR_DTYPE;
   if (d->flags & ~TTT_FLAG_SOFTPLUS) return TTT_ERR_FLAGS;
-  if (ttt::scan_states(d->N, 4) == 0) return TTT_ERR_UNSUPPORTED;
+  if (ttt::scan_states(d->N) == 0) return TTT_ERR_UNSUPPORTED;
   int64_t n = 1;
   if (!mul_ok(n, d->B) || !mul_ok(n, d->T > 0 ? d->T : 1) || !mul_ok(n, d->D) || !mul_ok(n, d->N)) return TTT_ERR_SHAPE;
   return TTT_OK;

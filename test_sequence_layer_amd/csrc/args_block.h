@@ -28,7 +28,7 @@ struct ConvArgs {
   void* dX;
   void* dstate;           // or nullptr
   Strides2 dxs;
-  int seg, nseg;          // tokens a thread walks; segments
+  int seg;                // tokens a thread walks
   float* part;            // [B * nparts, D * (K + 1)]: dw [D, K], then dbias [D]
   int nparts;             // partial rows a sequence
 };
@@ -104,7 +104,7 @@ struct RowSumArgs {
 constexpr int kScanCh = 64;     // channels of a workgroup
 constexpr int kScanTile = 32;   // tokens staged at a time
 
-int scan_states(int N, int lanes);  // states a lane holds with so many lanes to a channel; 0: not supported
+int scan_states(int N);         // states that each of a channel's four lanes holds; 0: not supported
 int scan_chunk(int N);          // tokens between checkpoints
 hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t s);
 hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t s);

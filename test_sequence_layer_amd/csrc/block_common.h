@@ -64,10 +64,6 @@ struct Piece {
     else if (i & 1) w[i / 2] = (w[i / 2] & 0xffffu) | static_cast<uint32_t>(x) << 16;
     else w[i / 2] = (w[i / 2] & 0xffff0000u) | x;
   }
-  __device__ __forceinline__ void set(int i, float x) {
-    if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(x);
-    else set_bits(i, f32_to_bf16_bits(x));
-  }
   __device__ __forceinline__ void set_all(const float* x) {
     if constexpr (sizeof(T) == 4) {
 #pragma unroll

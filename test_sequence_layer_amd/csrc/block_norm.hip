@@ -17,6 +17,8 @@ namespace {
 
 using namespace block;
 
+constexpr int NE = 8;  // elements of a row that a thread holds
+
 __device__ __forceinline__ float wave_sum(float x) { return mfma::sum_rows(mfma::sum16(x)); }
 
 __device__ __forceinline__ double wave_sum(double x) {
@@ -73,7 +75,7 @@ struct Team {
 // mean (0 for the root-mean-square norm) and 1 / sqrt(var + eps) of a row of 1 / inv elements, NE of them in a thread (zeros
 // behind the row's end).  The layer norm's two sums go in 64 bits, so that one pass is enough: nothing cancels in
 // sum x^2 - D mean^2 that 32 bits would have kept.
-template <int W, int NE>
+template <int W>
 __device__ __forceinline__ float2 stats(const float (&x)[NE], int valid, double inv, bool layer, float eps, Team<W>& team) {
   if (layer) {
     double s = 0.0, ss = 0.0;
@@ -114,64 +116,52 @@ struct Walk {
   }
 };
 
-// A thread's elements of a row: NC pieces of 8, piece i at 8 (i R + r); element by element instead at i R + r.
-template <int R, int NC, bool Wide>
+// A thread's elements of a row: a piece at 8 r; element by element instead at i R + r.
+template <int R, bool Wide>
 struct Cols {
   int r, D;
-  __device__ __forceinline__ int valid() const {  // of the thread's 8 NC elements, in their order
+  __device__ __forceinline__ int valid() const {  // of the thread's elements, in their order
+    if constexpr (Wide) return 8 * r < D ? 8 : 0;
+    else return r < D ? min(NE, (D - r + R - 1) / R) : 0;
+  }
+  template <typename T>
+  __device__ __forceinline__ void load(float (&x)[NE], const T* p) const {
     if constexpr (Wide) {
-      int n = 0;
+      const int c = 8 * r;
+      Piece<T, 8> v;
+      if (c < D) v.load(p + c);
+      else v.zero();
 #pragma unroll
-      for (int i = 0; i < NC; ++i) n += 8 * (i * R + r) < D ? 8 : 0;
-      return n;
+      for (int j = 0; j < 8; ++j) x[j] = v.get(j);
     } else {
-      return r < D ? min(8 * NC, (D - r + R - 1) / R) : 0;
-    }
-  }
-  template <typename T>
-  __device__ __forceinline__ void load(float (&x)[8 * NC], const T* p) const {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      if constexpr (Wide) {
-        const int c = 8 * (i * R + r);
-        Piece<T, 8> v;
-        if (c < D) v.load(p + c);
-        else v.zero();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[8 * i + j] = v.get(j);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int c = (8 * i + j) * R + r;
-          x[8 * i + j] = c < D ? as_f32(p[c]) : 0.f;
-        }
+      for (int j = 0; j < NE; ++j) {
+        const int c = j * R + r;
+        x[j] = c < D ? as_f32(p[c]) : 0.f;
       }
     }
   }
   template <typename T>
-  __device__ __forceinline__ void store(const float (&x)[8 * NC], T* p) const {
+  __device__ __forceinline__ void store(const float (&x)[NE], T* p) const {
+    if constexpr (Wide) {
+      const int c = 8 * r;
+      Piece<T, 8> v;
+      v.set_all(x);
+      if (c < D) v.store(p + c);
+    } else {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      if constexpr (Wide) {
-        const int c = 8 * (i * R + r);
-        Piece<T, 8> v;
-        v.set_all(&x[8 * i]);
-        if (c < D) v.store(p + c);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int c = (8 * i + j) * R + r;
-          if (c < D) put(p + c, x[8 * i + j]);
-        }
+      for (int j = 0; j < NE; ++j) {
+        const int c = j * R + r;
+        if (c < D) put(p + c, x[j]);
       }
     }
   }
-  __device__ __forceinline__ void param(float (&x)[8 * NC], const float* p, float none) const {
+  __device__ __forceinline__ void param(float (&x)[NE], const float* p, float none) const {
     if (p) {
       load(x, p);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8 * NC; ++i) x[i] = none;
+      for (int i = 0; i < NE; ++i) x[i] = none;
     }
   }
 };
@@ -180,12 +170,12 @@ __device__ __forceinline__ bool dead(const NormArgs& a, int64_t b, int64_t t) {
   return a.lens && t >= max(0, min(a.lens[b], a.T));
 }
 
-template <typename T, typename RT, int R, int NC, bool Wide>
+template <typename T, typename RT, int R, bool Wide>
 __global__ __launch_bounds__(R) void ttt_norm_fwd(NormArgs a) {
-  constexpr int W = R / 64, NE = 8 * NC;
+  constexpr int W = R / 64;
   __shared__ double slots[Team<W>::kSlots][W][2];
   Team<W> team{slots, static_cast<int>(threadIdx.x >> 6), 0};
-  const Cols<R, NC, Wide> cols{static_cast<int>(threadIdx.x), a.D};
+  const Cols<R, Wide> cols{static_cast<int>(threadIdx.x), a.D};
   const int valid = cols.valid();
   const double inv = 1.0 / static_cast<double>(a.D);
   const int64_t rows = static_cast<int64_t>(a.B) * a.T;
@@ -255,7 +245,7 @@ __global__ __launch_bounds__(R) void ttt_norm_fwd(NormArgs a) {
 }
 
 // The gradient through unit = (x - mean) rstd, in place: h holds the gradient of unit.
-template <int W, int NE>
+template <int W>
 __device__ __forceinline__ void norm_back(float (&h)[NE], const float (&unit)[NE], float rstd, int valid, float inv, bool layer,
                                           Team<W>& team) {
   float s = 0.f, m = 0.f;
@@ -273,14 +263,14 @@ __device__ __forceinline__ void norm_back(float (&h)[NE], const float (&unit)[NE
 
 // Backward: everything of the forward again from the row, then back through it.  A thread keeps its columns' sums of the
 // parameters' gradients over all rows of its workgroup; teams of fewer than 256 threads share a workgroup, which adds theirs up.
-template <typename T, typename RT, int R, int NC, bool Wide>
+template <typename T, typename RT, int R, bool Wide>
 __global__ __launch_bounds__(R < 256 ? 256 : R) void ttt_norm_bwd(NormArgs a) {
-  constexpr int W = R / 64, NE = 8 * NC, TEAMS = R < 256 ? 256 / R : 1;
+  constexpr int W = R / 64, TEAMS = R < 256 ? 256 / R : 1;
   __shared__ double slots[TEAMS][Team<W>::kSlots][W][2];
   __shared__ float sums[TEAMS > 1 ? 256 : 1][TEAMS > 1 ? 9 : 1];
   const int who = R < 256 ? __builtin_amdgcn_readfirstlane(threadIdx.x / R) : 0, r = threadIdx.x % R;
   Team<W> team{slots[who], r >> 6, 0};
-  const Cols<R, NC, Wide> cols{r, a.D};
+  const Cols<R, Wide> cols{r, a.D};
   const int valid = cols.valid();
   const double inv = 1.0 / static_cast<double>(a.D);
   const int64_t rows = static_cast<int64_t>(a.B) * a.T;
@@ -306,8 +296,8 @@ __global__ __launch_bounds__(R < 256 ? 256 : R) void ttt_norm_bwd(NormArgs a) {
   // the row's pieces as they lie in memory, on their way a row ahead.  Rows behind their sequence's last token and tensors that
   // are not there are not read: their loads go to this workgroup's own partial sums, which it writes at its end, and are dropped
   struct Raw {
-    Piece<T, 8> x[NC], z[NC], dy[NC];
-    Piece<RT, 8> res[NC], ds[NC];
+    Piece<T, 8> x, z, dy;
+    Piece<RT, 8> res, ds;
   } raw;
   float* const part = a.part + static_cast<int64_t>(blockIdx.x) * 5 * a.D;
   auto skipped = [&](int64_t line) { return line >= rows || dead(a, ahead.b, ahead.t); };
@@ -315,8 +305,7 @@ __global__ __launch_bounds__(R < 256 ? 256 : R) void ttt_norm_bwd(NormArgs a) {
     auto get = [&](auto& v, const auto* p, const Strides2& st) {
       typedef std::remove_const_t<std::remove_pointer_t<decltype(p)>> E;
       const E* from = p && !skip ? p + (ahead.b * st.b + ahead.t * st.t) : reinterpret_cast<const E*>(part);
-#pragma unroll
-      for (int i = 0; i < NC; ++i) v[i].load(from + (8 * (i * R + r) < a.D ? 8 * (i * R + r) : 0));
+      v.load(from + (8 * r < a.D ? 8 * r : 0));
     };
     get(raw.x, static_cast<const T*>(a.X), a.xs);
     get(raw.z, static_cast<const T*>(a.Z), a.zs);
@@ -338,12 +327,9 @@ __global__ __launch_bounds__(R < 256 ? 256 : R) void ttt_norm_bwd(NormArgs a) {
     float gate[NE], slope[NE];
     if constexpr (kAhead) {
       auto take = [&](float (&to)[NE], auto& from, bool on) {
+        const bool here = on && !none && 8 * r < a.D;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          const bool here = on && !none && 8 * (i * R + r) < a.D;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) to[8 * i + j] = here ? from[i].get(j) : 0.f;
-        }
+        for (int j = 0; j < 8; ++j) to[j] = here ? from.get(j) : 0.f;
       };
       take(x, raw.x, true);
       take(z, raw.z, a.Z != nullptr);
@@ -454,42 +440,39 @@ __global__ __launch_bounds__(R < 256 ? 256 : R) void ttt_norm_bwd(NormArgs a) {
 #pragma unroll
   for (int k = 0; k < 5; ++k) {
     if constexpr (TEAMS > 1) {
+      __syncthreads();
 #pragma unroll
-      for (int c0 = 0; c0 < NE; c0 += 8) {
-        __syncthreads();
+      for (int i = 0; i < NE; ++i) sums[threadIdx.x][i] = acc[k][i];
+      __syncthreads();
+      if (who == 0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sums[threadIdx.x][i] = acc[k][c0 + i];
-        __syncthreads();
-        if (who == 0) {
+        for (int i = 0; i < NE; ++i)
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int m = 1; m < TEAMS; ++m) acc[k][c0 + i] += sums[m * R + r][i];
-        }
+          for (int m = 1; m < TEAMS; ++m) acc[k][i] += sums[m * R + r][i];
       }
     }
     if (who == 0) {
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
-        const int c = Wide ? 8 * ((i / 8) * R + r) + i % 8 : i * R + r;
+        const int c = Wide ? 8 * r + i : i * R + r;
         if (c < a.D) part[static_cast<int64_t>(k) * a.D + c] = acc[k][i];
       }
     }
   }
 }
 
-template <typename T, typename RT, int R, int NC>
+template <typename T, typename RT, int R>
 hipError_t go(bool backward, const NormArgs& a, hipStream_t s) {
   if (backward) {
     constexpr int threads = R < 256 ? 256 : R;
     const unsigned grid = static_cast<unsigned>(a.blocks);
-    if (a.wide) ttt_norm_bwd<T, RT, R, NC, true><<<grid, threads, 0, s>>>(a);
-    else ttt_norm_bwd<T, RT, R, NC, false><<<grid, threads, 0, s>>>(a);
+    if (a.wide) ttt_norm_bwd<T, RT, R, true><<<grid, threads, 0, s>>>(a);
+    else ttt_norm_bwd<T, RT, R, false><<<grid, threads, 0, s>>>(a);
   } else {
     const int64_t rows = static_cast<int64_t>(a.B) * a.T, most = 256 * 2048 / R;  // all that run at a time
     const unsigned grid = static_cast<unsigned>(rows < most ? rows : most);
-    if (a.wide) ttt_norm_fwd<T, RT, R, NC, true><<<grid, R, 0, s>>>(a);
-    else ttt_norm_fwd<T, RT, R, NC, false><<<grid, R, 0, s>>>(a);
+    if (a.wide) ttt_norm_fwd<T, RT, R, true><<<grid, R, 0, s>>>(a);
+    else ttt_norm_fwd<T, RT, R, false><<<grid, R, 0, s>>>(a);
   }
   return hipGetLastError();
 }
@@ -497,11 +480,11 @@ hipError_t go(bool backward, const NormArgs& a, hipStream_t s) {
 // Threads of a row: the fewest whose 8 elements each hold it.
 template <typename T, typename RT>
 hipError_t go(bool backward, const NormArgs& a, hipStream_t s) {
-  if (a.D <= 512) return go<T, RT, 64, 1>(backward, a, s);
-  if (a.D <= 1024) return go<T, RT, 128, 1>(backward, a, s);
-  if (a.D <= 2048) return go<T, RT, 256, 1>(backward, a, s);
-  if (a.D <= 4096) return go<T, RT, 512, 1>(backward, a, s);
-  if (a.D <= 8192) return go<T, RT, 1024, 1>(backward, a, s);
+  if (a.D <= 512) return go<T, RT, 64>(backward, a, s);
+  if (a.D <= 1024) return go<T, RT, 128>(backward, a, s);
+  if (a.D <= 2048) return go<T, RT, 256>(backward, a, s);
+  if (a.D <= 4096) return go<T, RT, 512>(backward, a, s);
+  if (a.D <= 8192) return go<T, RT, 1024>(backward, a, s);
   return hipErrorInvalidValue;
 }
 

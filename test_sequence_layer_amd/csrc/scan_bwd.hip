@@ -196,7 +196,7 @@ __global__ __launch_bounds__(512, 1) void ttt_scan_bwd(ScanArgs a) {
         if (k0 + CL >= TT && k == tiles - 1) break;  // (nobody asks for the state behind the last chunk)
 #pragma unroll
         for (int j0 = k0; j0 < k0 + CL; j0 += GS) {
-          Group<NS, false, GS, TT, NP, 4 * CH> g;
+          Group<NS, GS, NP, 4 * CH> g;
           g.read(sd, sb, j0);
           float e[GS][NS];
 #pragma unroll
@@ -241,7 +241,7 @@ __global__ __launch_bounds__(512, 1) void ttt_scan_bwd(ScanArgs a) {
         const int before = begin + k * TT + k0 - CL;
         load_states(next, ck - ckstep, a.N, q, on && before >= begin && before < end);
         {
-          Group<NS, false, GS, TT, NP, 4 * CH> in[2];
+          Group<NS, GS, NP, 4 * CH> in[2];
           in[0].read(&td->x, sb, k0);
 #pragma unroll
           for (int m = 0; m < CL; m += GS) {
@@ -577,7 +577,7 @@ hipError_t go(bool states, const ScanArgs& a, hipStream_t s) {
 
 template <typename InT, typename OutT>
 hipError_t go(bool states, const ScanArgs& a, hipStream_t s) {
-  switch (scan_states(a.N, 4)) {
+  switch (scan_states(a.N)) {
     case 1: return go<InT, OutT, 1>(states, a, s);
     case 2: return go<InT, OutT, 2>(states, a, s);
     case 4: return go<InT, OutT, 4>(states, a, s);
@@ -596,7 +596,7 @@ hipError_t go(bool states, const ScanArgs& a, hipStream_t s) {
 
 }  // namespace
 
-int scan_chunk(int N) { return scan_states(N, 4) <= 4 ? kChunk<4> : kChunk<8>; }
+int scan_chunk(int N) { return scan_states(N) <= 4 ? kChunk<4> : kChunk<8>; }
 
 hipError_t launch_scan_bwd_states(const ScanArgs& a, hipStream_t s) { return go(true, a, s); }
 hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t s) { return go(false, a, s); }

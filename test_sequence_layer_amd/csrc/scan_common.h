@@ -128,18 +128,17 @@ struct BcRows {
   }
 };
 
-// A group of GS tokens as a lane reads it: dt and dt u of its channel (a pair every ROW floats of its tokens), B and C of its
-// NS states.
-template <int NS, bool C_, int GS, int TT, int NP, int ROW>
+// A group of GS tokens as a lane reads it: dt and dt u of its channel (a pair every ROW floats of its tokens), B of its NS
+// states.
+template <int NS, int GS, int NP, int ROW>
 struct Group {
   float2 d[GS];
-  float B[GS][NS], C[C_ ? GS : 1][NS];
+  float B[GS][NS];
   __device__ __forceinline__ void read(const float* sd, const float* bc, int k) {
 #pragma unroll
     for (int j = 0; j < GS; ++j) {
       d[j] = *reinterpret_cast<const float2*>(sd + (k + j) * ROW);
       lds_floats(B[j], bc + (k + j) * NP);
-      if constexpr (C_) lds_floats(C[j], bc + (TT + k + j) * NP);
     }
   }
 };

@@ -325,10 +325,17 @@ __global__ __launch_bounds__(256) void ttt_scan_decode(ScanArgs a) {
 enum Which { STATES, FWD, DECODE };
 
 template <typename InT, typename OutT, int NS>
-hipError_t walk(bool states, const ScanArgs& a, hipStream_t s) {
-  const int dg = a.D / a.G, segs = states ? a.nseg - 1 : a.nseg;
+hipError_t go(Which which, const ScanArgs& a, hipStream_t s) {
+  if (which == DECODE) {
+    const int64_t waves = static_cast<int64_t>(a.B) * ((a.D + 15) / 16);
+    const unsigned grid = static_cast<unsigned>((waves + 3) / 4);
+    if (a.wide) ttt_scan_decode<InT, OutT, NS, true><<<grid, 256, 0, s>>>(a);
+    else ttt_scan_decode<InT, OutT, NS, false><<<grid, 256, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  const int dg = a.D / a.G, segs = which == STATES ? a.nseg - 1 : a.nseg;
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.B) * a.G * ((dg + CH - 1) / CH) * segs);
-  if (states) {
+  if (which == STATES) {
     if (a.wide) ttt_scan_fwd<InT, float, NS, true, true><<<grid, THREADS, 0, s>>>(a);
     else ttt_scan_fwd<InT, float, NS, false, true><<<grid, THREADS, 0, s>>>(a);
   } else {
@@ -338,31 +345,13 @@ hipError_t walk(bool states, const ScanArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename InT, typename OutT, int NS>
-hipError_t token(const ScanArgs& a, hipStream_t s) {
-  const int64_t waves = static_cast<int64_t>(a.B) * ((a.D + 15) / 16);
-  const unsigned grid = static_cast<unsigned>((waves + 3) / 4);
-  if (a.wide) ttt_scan_decode<InT, OutT, NS, true><<<grid, 256, 0, s>>>(a);
-  else ttt_scan_decode<InT, OutT, NS, false><<<grid, 256, 0, s>>>(a);
-  return hipGetLastError();
-}
-
 template <typename InT, typename OutT>
 hipError_t go(Which which, const ScanArgs& a, hipStream_t s) {
-  if (which == DECODE) {
-    switch (scan_states(a.N, 4)) {
-      case 1: return token<InT, OutT, 1>(a, s);
-      case 2: return token<InT, OutT, 2>(a, s);
-      case 4: return token<InT, OutT, 4>(a, s);
-      case 8: return token<InT, OutT, 8>(a, s);
-      default: return hipErrorInvalidValue;
-    }
-  }
-  switch (scan_states(a.N, LANES)) {
-    case 1: return walk<InT, OutT, 1>(which == STATES, a, s);
-    case 2: return walk<InT, OutT, 2>(which == STATES, a, s);
-    case 4: return walk<InT, OutT, 4>(which == STATES, a, s);
-    case 8: return walk<InT, OutT, 8>(which == STATES, a, s);
+  switch (scan_states(a.N)) {
+    case 1: return go<InT, OutT, 1>(which, a, s);
+    case 2: return go<InT, OutT, 2>(which, a, s);
+    case 4: return go<InT, OutT, 4>(which, a, s);
+    case 8: return go<InT, OutT, 8>(which, a, s);
     default: return hipErrorInvalidValue;
   }
 }
@@ -378,9 +367,9 @@ hipError_t go(Which which, const ScanArgs& a, hipStream_t s) {
 
 }  // namespace
 
-int scan_states(int N, int lanes) {
-  for (int n = 1; n * lanes <= 32; n *= 2)
-    if (N >= 1 && N <= n * lanes) return n;
+int scan_states(int N) {
+  for (int n = 1; n <= 8; n *= 2)
+    if (N >= 1 && N <= 4 * n) return n;
   return 0;
 }
 
