@@ -904,6 +904,8 @@ typedef struct {
  * NULL; so may S or Y (not both, TTT_ERR_NULL), which is then not written.  Y and beta_pre need
  * gamma_pre (TTT_ERR_NULL); without Y gamma_pre and beta_pre reach nothing.
  * S may be exactly res (same address, strides and type).
+ * A token's mean square or variance plus eps is an fp32 number: between 1e-37 and 1e38 it is
+ * good to fp32's rounding; below, with a tiny eps, and above it is not what the formula gives.
  */
 ttt_status ttt_block_norm_fwd(const ttt_block_norm_desc* desc, const void* X, const void* Z, const void* res,
                               const float* alpha, const float* gamma_post, const float* beta_post,

@@ -1793,6 +1793,7 @@ def block_norm_fwd(x, res=None, z=None, alpha=None, gamma_post=None, beta_post=N
     gamma_post, beta_post : [D] float32, the norm behind the block, or None (none)
     gamma_pre, beta_pre   : [D] float32, the norm before the next block; without gamma_pre there is no y
     kind  : "rms" (mean square) or "layer" (mean and variance);  gate_first : NORM(x silu(z)) instead of NORM(x) silu(z)
+    eps   : added to the mean square or variance, which together are an fp32 number, good between 1e-37 and 1e38
     lens  : [B] int32, the tokens of each sequence, or None (T each).  Rows behind them are not read and give zeros
     keep  : whether s is wanted;  ``s`` may be ``res`` itself
     returns (s [B, T, D] of res's dtype (without res: res_dtype, default x's) or None, y [B, T, D] of x's dtype or None).

@@ -190,3 +190,16 @@ def test_scan_is_as_good_as_plain_fp32(ttt, B, T, D, N, G, gate):
         off, ref = (a.cpu().double() - r).abs().max().item(), (f.double() - r).abs().max().item()
         print(f"{n}: off {off:.2e}, plain fp32 {ref:.2e}, largest {r.abs().max().item():.1e}", flush=True)
         assert off <= 8 * ref + 2.0 ** -22 * r.abs().max().item(), n
+
+
+# small and large rows without eps: as far as mean squares of 1e-37 and 1e38 the result does not depend on their size
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("scale", [2.0 ** -60, 2.0 ** -20, 1.0, 2.0 ** 60])
+def test_norm_of_small_and_large_rows(ttt, kind, scale):
+    x, ga, dy = random((2, 3, 200), F32, 1), random((200,), F32, 2, 0.1, 1.0), random((2, 3, 200), F32, 3)
+    _, y = ttt.block_norm_fwd(x * scale, gamma_pre=ga, kind=kind, eps=0.0)
+    ref = bt.norm_rounded(x.cpu(), None, None, None, None, None, ga.cpu(), None, kind, 0.0, False)[1]
+    bt.check_rounded("y", y, ref)
+    dx = ttt.block_norm_bwd(x * scale, None, dy, gamma_pre=ga, kind=kind, eps=0.0)[0]
+    ref = bt.norm_rounded(x.cpu(), None, None, None, None, None, ga.cpu(), None, kind, 0.0, False, dy=dy.cpu())[0]
+    bt.check_rounded("dx", dx * scale, ref)
