@@ -62,6 +62,17 @@ KERNEL_SOURCES = {
     "ttt_attn_sum": ["attn_bwd.hip", "attn_common.h", "mfma_common.h", "args_attn.h", "ttt_common.h"],
     "ttt_attn_decode": ["attn_decode.hip", "rope.h", "mfma_common.h", "args_attn.h", "ttt_common.h"],
     "ttt_rotary": ["rotary.hip", "rope.h", "mfma_common.h", "args_attn.h", "ttt_common.h"],
+    "ttt_scan_fwd": ["scan_fwd.hip", "scan_common.h", "block_common.h", "mfma_common.h", "args_block.h", "args_attn.h", "ttt_common.h"],
+    "ttt_scan_decode": ["scan_fwd.hip", "scan_common.h", "block_common.h", "mfma_common.h", "args_block.h", "args_attn.h", "ttt_common.h"],
+    "ttt_scan_bwd": ["scan_bwd.hip", "scan_common.h", "block_common.h", "mfma_common.h", "args_block.h", "args_attn.h", "ttt_common.h"],
+    "ttt_scan_bwd_states": ["scan_bwd.hip", "scan_common.h", "block_common.h", "mfma_common.h", "args_block.h", "args_attn.h", "ttt_common.h"],
+    "ttt_scan_bc_sum": ["scan_bwd.hip", "scan_common.h", "block_common.h", "mfma_common.h", "args_block.h", "args_attn.h", "ttt_common.h"],
+    "ttt_conv_fwd": ["short_conv.hip", "block_common.h", "mfma_common.h", "args_block.h", "args_attn.h", "ttt_common.h"],
+    "ttt_conv_decode": ["short_conv.hip", "block_common.h", "mfma_common.h", "args_block.h", "args_attn.h", "ttt_common.h"],
+    "ttt_conv_bwd": ["short_conv.hip", "block_common.h", "mfma_common.h", "args_block.h", "args_attn.h", "ttt_common.h"],
+    "ttt_norm_fwd": ["block_norm.hip", "block_common.h", "mfma_common.h", "args_block.h", "args_attn.h", "ttt_common.h"],
+    "ttt_norm_bwd": ["block_norm.hip", "block_common.h", "mfma_common.h", "args_block.h", "args_attn.h", "ttt_common.h"],
+    "ttt_row_sum": ["block_sum.hip", "block_common.h", "mfma_common.h", "args_block.h", "args_attn.h", "ttt_common.h"],
 }
 
 
