@@ -7,7 +7,9 @@
 //   s = res + alpha v,                    y = NORM(s) gamma_pre + beta_pre
 // NORM divides by the root of the mean square plus eps, the layer norm after taking the mean off.  Each row is read once,
 // kept in registers and written once: memory is the bound.
-// 4 x 8192 rows of 2048, bf16 with an fp32 residual stream: 197 to 207 us, 4.5 to 4.8 TB/s.  Gradients of 8 x 2048 rows of 768: 75 us, two launches.
+// 4 x 8192 rows of 2048, bf16 with an fp32 residual stream: 206 us, 4.6 TB/s (fp32 throughout 268, 4.9 TB/s).  Gradients of
+// 8 x 2048 rows of 768: 76 us, two launches.  Rows over 4096 keep values in scratch in the gradients (96 bytes a lane, 350 element
+// by element) and element by element in the forward (44): 8 x 2048 rows of 8192 in bf16 take 370 and 1117 us, of 8188 1112 and 3037.
 #include <type_traits>
 
 #include "block_common.h"

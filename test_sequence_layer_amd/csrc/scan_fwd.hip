@@ -3,10 +3,12 @@
 // Pages: [TTT] = news article "大模型最强架构TTT问世！斯坦福UCSD等5年磨一剑，一夜推翻Transformer"
 // (aharts.cn / itmax.cn), part 04 (the Mamba layer that TTT is compared with).
 //
-// Per token, channel and state one exp, two products and two multiply-adds: 21 issue cycles a wave of 64 (measured with two
-// waves to a SIMD: v_exp_f32 8.3, a multiply-add 4, a product 2.5), against (with N = 16) half a byte: vector issue is the bound.
-// 4 x 8192 tokens, 4096 channels, N = 16, bf16: 527 us, 2.0 TB/s; by that count 313 us, by its bytes 203 at the 5.3 TB/s of a
-// large copy.
+// Per token, channel and state one exp, two products and two multiply-adds, against (with N = 16) half a byte: vector issue is
+// the bound.  4 x 8192 tokens, 4096 channels, N = 16, bf16: 525 us, 2.0 TB/s, at a clock of 2.42 GHz (590 in the first launches
+// after a pause, before the clock has risen); by its bytes 203 at the 5.3 TB/s of a large copy.  Those five instructions by
+// themselves, from registers, take 356 us for as many states with one wave to a SIMD, 329 with two and 315 with eight.  They are
+// 1.68e8 of the kernel's 2.54e8 vector instructions (the others: softplus, skip, gate, conversions, sums over lanes, addresses),
+// which keep the vector unit busy in 93% of the cycles.
 #include <utility>
 
 #include "scan_common.h"

@@ -5,7 +5,7 @@
 //
 //   y_t = act(bias + sum_j w_j x_{t-K+1+j}),   K = 2, 3, 4, act the identity or silu
 // 2 K flops a token and channel against 4 bytes: memory is the bound.  bf16, K = 4: 4 x 8192 tokens of 4096 channels 111 us, 4.9
-// TB/s; gradients of 8 x 2048 of 1536 54 us, 2.8 TB/s; one token of 512 x 4096 9.3 us.
+// TB/s (fp32 192, 5.6); gradients of 8 x 2048 of 1536 54 us, 2.8 TB/s (fp32 77); one token of 512 x 4096 9.3 us.
 #include <type_traits>
 
 #include "block_common.h"
